@@ -27,7 +27,7 @@ EXPORTED = (
     "sage_quantize_workspace_bytes", "sage_quantize_smooth", "sage_fwd_workspace_bytes",
     "sage_attn_fwd", "sage_bwd_workspace_bytes", "sage_attn_bwd", "sage_dump_bytes",
     "sage_device_status", "sage_status_string", "sage_version", "sage_quantize_smooth_qknorm",
-    "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4",
+    "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4", "sage_rope",
 )
 
 
@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
     L.sage_quantize_noalloc_partials_needed.restype = sz
     L.sage_quantize_smooth_noalloc.argtypes = [P] + [vp] * 12
     L.sage_quantize_smooth_noalloc.restype = ci
+    L.sage_rope.argtypes = [vp] * 7
+    L.sage_rope.restype = ci
     _lib = L
     return L
 

@@ -9,6 +9,10 @@
  *   sage_attn_fwd         tiled online-softmax forward with per-token P codes; writes O and L
  *   sage_attn_bwd         backward with 16-bit dP and per-tile INT8 P / dS codes; writes dQ, dK, dV
  *
+ * and, for positions in the text,
+ *
+ *   sage_rope             rotary positions with several axes, and their gradient
+ *
  * Conventions shared by every entry point
  *   - Tensors are contiguous, row-major (B, H, N, d): token n of head (b, h) starts at element
  *     ((b * H + h) * N + n) * d.  Per-block scales are float32 (B, H, N / 64).
@@ -49,6 +53,7 @@ extern "C" {
 /* Element types of the 16-bit tensors (Q, K, V, dO, O). */
 #define SAGE_FP16 0
 #define SAGE_BF16 1
+#define SAGE_FP32 2             /* sage_rope only: the gradients sage_attn_bwd writes           */
 
 /* Flags. */
 #define SAGE_FLAG_DUMP 1u       /* debug: write the integer block products and the in-kernel
@@ -327,6 +332,40 @@ SAGE_API int sage_qat_bwd(const sage_params *p, const void *Qf, const void *Kf, 
                           const float *Op, const float *L, const float *R, const void *dO,
                           float *dQ, float *dK, float *dV, void *workspace, size_t workspace_bytes,
                           sage_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ *
+ * Rotary positions with several axes (for example time, height and width of a video token).
+ *
+ * Pair j of a token's `rotary` / 2 pairs turns by theta = pos[a(j)] freq[j]:
+ *   y0 = x0 cos(theta) - x1 sin(theta),  y1 = x0 sin(theta) + x1 cos(theta),
+ * with (x0, x1) = channels (j, j + rotary / 2), or (2j, 2j + 1) when `interleaved`.  Axis a(j) is
+ * the first with sections[0] + ... + sections[a] > j.  Channels from `rotary` on pass through.
+ * `inverse` turns by -theta: the rotation is orthogonal, so this is also the gradient
+ * (dX from dY).  float32 arithmetic, rounded once; theta mod 2 pi is formed in 64-bit fixed
+ * point from freq[j] / 2 pi in float64, so far positions keep their angle.
+ *
+ * In:  Q (B,H,N,d), K (B,Hk,N,d) of `dtype` (K NULL when Hk = 0);
+ *      pos (axes,pos_batch,N) int32, pos_batch = B or 1 (the same positions in every sequence).
+ * Out: Qo, Ko like Q, K; Qo may be Q and Ko may be K (in place), no other overlap.
+ * rotary: a multiple of 16, 16 <= rotary <= d.  freq (rotary / 2 entries, |freq| <= 1e15) and
+ * sections (axes entries >= 0 that sum to rotary / 2) are HOST arrays, read before the call
+ * returns.  N is any positive number of tokens; pos needs 4-byte alignment only.
+ * ------------------------------------------------------------------------------------------ */
+#define SAGE_ROPE_MAX_AXES 8
+typedef struct sage_rope_params {
+    int B, H, Hk, N, d;      /* Hk may be 0; d 64 or 128                                         */
+    int dtype;               /* SAGE_FP16, SAGE_BF16 or SAGE_FP32                                */
+    int axes;                /* 1 .. SAGE_ROPE_MAX_AXES                                          */
+    int pos_batch;           /* B, or 1                                                          */
+    int rotary;              /* channels that turn                                               */
+    int interleaved;         /* 0: halves, 1: neighbours                                         */
+    int inverse;             /* 0: forward, 1: inverse (gradient)                                */
+    const int *sections;     /* host, (axes)                                                     */
+    const double *freq;      /* host, (rotary / 2): radians a position                           */
+} sage_rope_params;
+
+SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, const int *pos,
+                       void *Qo, void *Ko, sage_stream_t stream);
 
 /* Bytes the SAGE_FLAG_DUMP buffer needs for a forward (which = 0) or backward (which = 1). */
 SAGE_API size_t sage_dump_bytes(const sage_params *p, int which);
