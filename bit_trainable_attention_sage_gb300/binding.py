@@ -27,7 +27,8 @@ EXPORTED = (
     "sage_quantize_workspace_bytes", "sage_quantize_smooth", "sage_fwd_workspace_bytes",
     "sage_attn_fwd", "sage_bwd_workspace_bytes", "sage_attn_bwd", "sage_dump_bytes",
     "sage_device_status", "sage_status_string", "sage_version", "sage_quantize_smooth_qknorm",
-    "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4", "sage_rope",
+    "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4", "sage_rope", "sage_kv_append",
+    "sage_decode_workspace_bytes", "sage_attn_decode", "sage_evict_workspace_bytes", "sage_kv_evict",
 )
 
 
@@ -110,6 +111,16 @@ def lib() -> ctypes.CDLL:
     L.sage_quantize_smooth_noalloc.restype = ci
     L.sage_rope.argtypes = [vp] * 7
     L.sage_rope.restype = ci
+    L.sage_kv_append.argtypes = [vp] * 3 + [ci] + [vp] * 5
+    L.sage_kv_append.restype = ci
+    L.sage_decode_workspace_bytes.argtypes = [vp, ci, ci]
+    L.sage_decode_workspace_bytes.restype = sz
+    L.sage_attn_decode.argtypes = [vp, ci] + [vp] * 4 + [ci, vp, sz, vp]
+    L.sage_attn_decode.restype = ci
+    L.sage_evict_workspace_bytes.argtypes = [vp, ci]
+    L.sage_evict_workspace_bytes.restype = sz
+    L.sage_kv_evict.argtypes = [vp] * 3 + [ci, ci] + [vp] * 2 + [sz, vp]
+    L.sage_kv_evict.restype = ci
     _lib = L
     return L
 

@@ -28,8 +28,8 @@ VARIANTS = {
                      defines=["-DSAGE_WAIT_CYCLES=200000000ull", "-DSAGE_TEST_SKIP_Q_ARRIVAL=1"]),
 }
 SOURCES = ["sage_quant.cu", "sage_fwd.cu", "sage_bwd.cu", "sage_capi.cu", "sage_noalloc.cu",
-           "sage_rope.cu"]
-HEADERS = ["sage_device.cuh", "sage_internal.h"]
+           "sage_rope.cu", "sage_kv.cu", "sage_decode.cu"]
+HEADERS = ["sage_device.cuh", "sage_internal.h", "sage_kv.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + os.path.join(ROOT, "include")]

@@ -558,8 +558,9 @@ int sage_device_status(sage_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SAGE_ERR_CUDA;
     const unsigned int e = take_fwd_error() | take_bwd_error() | take_quant_error();
+    const unsigned int index = take_kv_error() | take_decode_error();
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
-    return e ? SAGE_ERR_TIMEOUT : SAGE_OK;
+    return e ? SAGE_ERR_TIMEOUT : index ? SAGE_ERR_INDEX : SAGE_OK;
 }
 
 const char *sage_status_string(int status) {
@@ -571,6 +572,7 @@ const char *sage_status_string(int status) {
         case SAGE_ERR_CUDA: return "CUDA launch or runtime error";
         case SAGE_ERR_TIMEOUT: return "device-side bounded wait expired";
         case SAGE_ERR_WORKSPACE: return "workspace missing or too small";
+        case SAGE_ERR_INDEX: return "cache page, length or slot out of range";
         default: return "unknown status";
     }
 }

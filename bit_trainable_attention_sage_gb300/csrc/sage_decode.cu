@@ -1,0 +1,855 @@
+// sage_decode.cu -- attention of one new token a sequence over the paged key-value cache.
+//
+//   s_t = q . K_t / sqrt(d),  O = sum_t softmax(s)_t V_t,  L = log sum_t exp s_t,  t < lens[b].
+//
+// Work.  Each cached row is read once from HBM for the whole group of query heads that shares it,
+// so the kernel is bound by memory bandwidth: 2 d values (and 8 bytes of scales in 8 bits) a
+// token and kv head, against 4 d multiply-adds a token and query head.
+//
+// Split.  The work is cut into tiles of 64 tokens of one (sequence, kv head, group of query
+// heads), numbered in that order, and each of a fixed number of CTAs takes an equal run of them
+// whatever the lengths are: a run can cover the end of one pair, several whole pairs and the
+// start of another.  Lengths stay on the device; every CTA adds them up itself.  A pair that lies
+// in one CTA's run is finished there; the others leave their unnormalised sums, maxima and sums
+// of exponentials in the workspace (two places a CTA: a run's first and last pair), and a second
+// kernel joins them in order, so results do not depend on the order in which CTAs run.
+//
+// Inside a CTA four warps each take 16 of a tile's 64 tokens and never wait for one another: each
+// keeps its own ring of cp.async stages in shared memory, its own running maximum, sum and output
+// accumulators, and the four are joined once at the end of a pair.
+//
+// Products.  m16n8k16 tensor-core products with the query heads as the 16 rows.  The kernel
+// needs a fraction of their rate, and both operands come from registers, where 8-bit rows can be
+// widened on the way; tcgen05 would want the widened rows back in shared memory.
+//   - 16-bit pool: K by ldmatrix, V by its transposing form.
+//   - 8-bit pool: codes are exact in fp16.  The products run over channels (or tokens) in any
+//     order as long as both operands agree, so a lane takes 16 consecutive bytes of a row with
+//     one load and assigns them to the products' positions itself; no transposition is needed.
+//     q is scaled by a power of two a row to stay in fp16's range: exact to 2^-39 of its largest
+//     value.  sK multiplies the logit; sV the probability, over a running power of two `vref` that
+//     keeps the product in fp16's range.
+//   - The probabilities enter as hi + lo of two 16-bit values, at least 16 bits: one rounding to
+//     bf16 would show in the output.  With at most 8 query heads a group, hi takes rows 0-7 and
+//     lo rows 8-15 of one product, which the padding to 16 rows would waste otherwise.
+#include "sage_kv.cuh"
+
+namespace sage {
+
+__device__ unsigned int g_decode_err = 0;   // 1: a page or length was out of range
+
+constexpr int kTile = 64;                    // tokens a unit of work
+constexpr int kGran = 16;                    // tokens a warp takes of it
+constexpr int kDecWarps = kTile / kGran;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kSMs = 152;
+
+// pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3
+template <int D, int KIND>
+struct DecodeShape {
+    static constexpr int ES = KIND < 2 ? 2 : 1;
+    static constexpr int ROW = D * ES;                       // bytes
+    static constexpr int CPR = ROW / 16;                     // 16-byte chunks a row: 4, 8 or 16
+    static constexpr int SCALES = KIND < 2 ? 0 : 2 * kGran * 4;
+    static constexpr int STAGE = 2 * kGran * ROW + SCALES;
+    static constexpr int STAGES = ROW == 256 ? 3 : ROW == 128 ? 4 : 6;
+    static constexpr int SMEM = kDecWarps * STAGES * STAGE;
+    static constexpr int CTAS = ROW == 256 ? 2 : 3;          // resident CTAs an SM
+};
+
+struct DecodeArgs {
+    KvView c;
+    const void *Q;
+    void *O;
+    float *L;
+    const int *lens;
+    int Hq, G, chunks;       // query heads, heads a kv head, groups of at most MR heads a kv head
+    int ctas;                // CTAs that share the work (gridDim.x)
+    int bf16;                // type of q and O
+    float sl2;               // log2(e) / sqrt(d)
+    float *part_O;           // (ctas, 2, MR, d) unnormalised sums
+    float *part_ml;          // (ctas, 2, MR, 2) maxima (log2 units) and sums of exponentials
+    float *row_ml;           // (B, Hq, 2) the same of finished rows, with scores only
+    float *logits;           // (B, Hq, cap) log2-unit logits, with scores only
+};
+
+// ---- shared-memory and tensor-core pieces ----------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Place of 16-byte chunk c of row r in a granule.  Rows of 128 and 256 bytes in 16 bits: the 8
+// rows an ldmatrix reads at one chunk fall into the 8 different 16-byte bank groups.  In 8 bits
+// a quarter-warp reads chunks 0-3 of rows (2i, 2i + 1), or chunks (2i, 2i + 1) of rows 0, 2, 4, 6
+// (1, 3, 5, 7): the XORs put either set into 8 different bank groups.
+template <int D, int KIND>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    using S = DecodeShape<D, KIND>;
+    if constexpr (KIND < 2) return static_cast<uint32_t>(r * S::CPR + (c ^ (r & 7))) * 16u;
+    else if constexpr (D == 128) return static_cast<uint32_t>(r * 8 + (c ^ ((r & 6) ^ ((r & 1) << 2)))) * 16u;
+    else return static_cast<uint32_t>((r >> 1) * 8 + ((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1))) * 16u;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Bytes (0,1) and (2,3) of w as fp16 pairs.  INT8: byte ^ 0x80 under 0x64 is 1024 + 128 + code
+// in fp16, less 1152 the code; E4M3 by the conversion instruction.  All exact.
+template <int KIND>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (KIND == 2) {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
+        const uint32_t k = 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(k));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(k));
+    } else {
+        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+    }
+}
+
+// (x0, x1) as hi + lo pairs of the product's 16-bit type
+template <bool BF16>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    } else {
+        const __half2 h = __floats2half2_rn(x0, x1);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+
+// ---- the cut of the work ---------------------------------------------------------------------
+// The number of units; where unit u lies: its sequence and that sequence's first unit.  Called by
+// a whole CTA of NT threads; `find` gives u from the total (a u outside [0, total) is not looked
+// for).
+struct WorkAt {
+    long long total, u, first;
+    int b;
+};
+template <int NT, typename F>
+__device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find) {
+    __shared__ long long s_sum[NT / 32];
+    __shared__ long long s_first;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.c.B + NT - 1) / NT;
+    const int b0 = min(tid * per, a.c.B), b1 = min(b0 + per, a.c.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + kTile - 1) / kTile) * pairs;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const long long u = find(total);
+    long long at = before + incl - mine;
+    if (u >= at && u < at + mine) {
+        int b = b0;
+        for (;; ++b) {
+            const long long k = static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + kTile - 1) / kTile) * pairs;
+            if (u < at + k) break;
+            at += k;
+        }
+        s_first = at;
+        s_b = b;
+    }
+    __syncthreads();
+    return WorkAt{total, u, s_first, s_b};
+}
+
+// Runs that share `total` units (none of them empty), the first unit of run c, and the run that
+// holds unit u.
+__device__ __forceinline__ int runs_of(const DecodeArgs &a, long long total) {
+    return static_cast<int>(min(static_cast<long long>(a.ctas), total));
+}
+__device__ __forceinline__ long long run_start(long long total, int c, int runs) { return total * c / runs; }
+__device__ __forceinline__ int run_of(long long total, long long u, int runs) {
+    return static_cast<int>(((u + 1) * runs - 1) / total);
+}
+
+__device__ __forceinline__ void store_out(const DecodeArgs &a, size_t at, float x, float y) {
+    uint32_t w;
+    if (a.bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        w = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        w = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    reinterpret_cast<uint32_t *>(a.O)[at / 2] = w;
+}
+
+// m + log2 l in natural units
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
+
+// ---- main kernel ------------------------------------------------------------------------------
+template <int D, int KIND, int MR>
+__global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using S = DecodeShape<D, KIND>;
+    constexpr bool BF16 = KIND == 1;                 // type of the products
+    constexpr int KS = D / 16, NT = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q = lane & 3;
+    const int pairs = a.c.H * a.chunks;
+    const int cta = blockIdx.x;
+    const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
+        const int n = runs_of(a, total);
+        return cta < n ? run_start(total, cta, n) : total;
+    });
+    const int runs = runs_of(a, w.total);
+    if (cta >= runs) return;
+    const long long u1 = run_start(w.total, cta + 1, runs);
+    const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * S::STAGE);
+
+    long long u = w.u, first = w.first;
+    int b = w.b;
+    bool run_first = true;
+    while (u < u1) {
+        const int len = kv_len(a.c, a.lens, b, &g_decode_err);
+        const int tiles = (len + kTile - 1) / kTile;
+        if (u - first >= static_cast<long long>(tiles) * pairs) {
+            first += static_cast<long long>(tiles) * pairs;
+            ++b;
+            continue;
+        }
+        const int pair = static_cast<int>((u - first) / tiles);
+        const int t0 = static_cast<int>((u - first) - static_cast<long long>(pair) * tiles);
+        const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + (u1 - u)));
+        const int hk = pair / a.chunks, ch = pair - hk * a.chunks;
+        const int head0 = hk * a.G + ch * MR;                    // first query head of the group
+        const int heads = min(MR, a.G - ch * MR);
+
+        // granules of this warp: tokens tau * 64 + warp * 16, tau in [t0, t1), while below len
+        const int tok0 = t0 * kTile + warp * kGran;
+        const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + kTile - 1) / kTile);
+        uint32_t bad = 0;                                        // stages whose page is not one
+        auto load = [&](int j) {
+            const int stage = j % S::STAGES;
+            const int tok = tok0 + j * kTile;
+            const int page = kv_page(a.c, b, tok, &g_decode_err);
+            const int nv = page < 0 ? 0 : min(kGran, len - tok);
+            bad = (bad & ~(1u << stage)) | (page < 0 ? 1u << stage : 0u);
+            const size_t row = page < 0 ? 0 : kv_row(a.c, page, hk, tok);
+            const uint8_t *k = static_cast<const uint8_t *>(a.c.K) + row * S::ROW;
+            const uint8_t *v = static_cast<const uint8_t *>(a.c.V) + row * S::ROW;
+            const uint32_t dst = ring + stage * S::STAGE;
+#pragma unroll
+            for (int i = 0; i < kGran * S::CPR / 32; ++i) {
+                const int idx = i * 32 + lane, r = idx / S::CPR, c = idx % S::CPR;
+                const uint32_t off = r < nv ? static_cast<uint32_t>(idx) * 16u : 0u;
+                const uint32_t at = chunk_at<D, KIND>(r, c);
+                cp_async16(dst + at, k + off, r < nv);
+                cp_async16(dst + kGran * S::ROW + at, v + off, r < nv);
+            }
+            if constexpr (KIND >= 2) {
+                const int r = lane & 15;
+                const float *s = (lane < 16 ? a.c.sK : a.c.sV) + row;
+                cp_async4(dst + 2 * kGran * S::ROW + lane * 4, s + (r < nv ? r : 0), r < nv);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < S::STAGES - 1; ++j) {
+            if (j < ng) load(j);
+            cp_commit();
+        }
+
+        // q: rows g and g + 8 of the products' first operand
+        uint32_t qa[KS][4];
+        float qs[2] = {a.sl2, a.sl2};
+        {
+            const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
+            auto word = [&](int ks, int half) {                  // channels of k = 2q (+ 8 half), in pairs
+                if constexpr (KIND < 2) return ks * 8 + q + half * 4;
+                else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
+            };
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    qa[ks][2 * half] = g < heads ? __ldg(Q + g * (D / 2) + word(ks, half)) : 0u;
+                    qa[ks][2 * half + 1] = MR == 16 && g + 8 < heads ? __ldg(Q + (g + 8) * (D / 2) + word(ks, half)) : 0u;
+                }
+            if constexpr (KIND >= 2) {
+                // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15)
+#pragma unroll
+                for (int r = 0; r < (MR == 16 ? 2 : 1); ++r) {
+                    float mx = 0.0f;
+                    auto pair_of = [&](uint32_t x) {
+                        return a.bf16 ? __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x))
+                                      : __half22float2(*reinterpret_cast<__half2 *>(&x));
+                    };
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const float2 f = pair_of(qa[ks][2 * half + r]);
+                            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    // exponent of the largest, held to [-100, 127] so that both factors are normal
+                    const int e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+                    const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+                    qs[r] = a.sl2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const float2 f = pair_of(qa[ks][2 * half + r]);
+                            qa[ks][2 * half + r] = pack_half2(f.x * up, f.y * up);
+                        }
+                }
+            }
+        }
+
+        float acc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float vref = 1.1754943508222875e-38f;                    // 2^-126
+
+        for (int j = 0; j < ng; ++j) {
+            cp_wait<S::STAGES - 2>();
+            __syncwarp();
+            if (j + S::STAGES - 1 < ng) load(j + S::STAGES - 1);
+            cp_commit();
+            const int stage = j % S::STAGES;
+            const uint32_t sk = ring + stage * S::STAGE, sv = sk + kGran * S::ROW;
+            const int tok = tok0 + j * kTile;
+            const int nv = (bad >> stage) & 1u ? 0 : min(kGran, len - tok);
+
+            // S = q K^T: columns (tokens) nt * 8 + 2 q + {0, 1}
+            float s[2][4] = {};
+            if constexpr (KIND < 2) {
+                const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t kb[4];
+                    ldsm4(sk + chunk_at<D, KIND>(r, 2 * ks + c), kb);
+                    mma16816<BF16>(s[0], qa[ks], kb[0], kb[1]);
+                    mma16816<BF16>(s[1], qa[ks], kb[2], kb[3]);
+                }
+            } else {
+#pragma unroll
+                for (int jj = 0; jj < D / 64; ++jj)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint4 kk = lds_u4(sk + chunk_at<D, KIND>(nt * 8 + g, q + 4 * jj));
+                        const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t b0, b1;
+                            widen4<KIND>(kw[i], b0, b1);
+                            mma16816<false>(s[nt], qa[4 * jj + i], b0, b1);
+                        }
+                    }
+            }
+            float2 fv[2];                                        // sV of the lane's tokens
+            if constexpr (KIND >= 2) {
+                const uint32_t sc = sk + 2 * kGran * S::ROW;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float2 fk = lds_f2(sc + (nt * 8 + 2 * q) * 4);
+                    fv[nt] = lds_f2(sc + (kGran + nt * 8 + 2 * q) * 4);
+                    s[nt][0] *= fk.x; s[nt][1] *= fk.y;
+                    s[nt][2] *= fk.x; s[nt][3] *= fk.y;
+                }
+            }
+            // log2 units; tokens past the end of the sequence do not exist
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = nt * 8 + 2 * q + (i & 1) < nv;
+                    s[nt][i] = in ? s[nt][i] * qs[i >> 1] : -INFINITY;
+                }
+            if (a.logits) {
+#pragma unroll
+                for (int r = 0; r < (MR == 16 ? 2 : 1); ++r)
+                    if (g + 8 * r < heads) {
+                        float *to = a.logits + (static_cast<size_t>(b) * a.Hq + head0 + g + 8 * r) * a.c.cap + tok + 2 * q;
+                        *reinterpret_cast<float2 *>(to) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
+                        *reinterpret_cast<float2 *>(to + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+                    }
+            }
+            float alpha[2] = {1.0f, 1.0f};
+#pragma unroll
+            for (int r = 0; r < (MR == 16 ? 2 : 1); ++r) {
+                float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[r], mx);
+                const float ref = mn == -INFINITY ? 0.0f : mn;   // nothing seen yet: all terms are 0
+                alpha[r] = ex2_approx(m[r] - ref);
+                m[r] = mn;
+                float sum = 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = s[nt][2 * r + i];
+                        x = ex2_approx(x - ref);
+                        sum += x;
+                    }
+                l[r] = l[r] * alpha[r] + sum;
+            }
+            if constexpr (KIND >= 2) {
+                // the largest sV so far, as a power of two above it
+                float mv = fmaxf(fmaxf(fv[0].x, fv[0].y), fmaxf(fv[1].x, fv[1].y));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 2));
+                if (mv > vref) {
+                    const float up = __uint_as_float(min((__float_as_uint(mv) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
+                    const float f = vref / up;
+                    vref = up;
+                    alpha[0] *= f;
+                    alpha[1] *= f;
+                }
+                const float iv = __uint_as_float(0x7F000000u - __float_as_uint(vref));   // 1 / vref
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float x = fv[nt].x * iv, y = fv[nt].y * iv;
+                    s[nt][0] *= x; s[nt][1] *= y;
+                    s[nt][2] *= x; s[nt][3] *= y;
+                }
+            }
+            if (MR == 8) alpha[1] = alpha[0];                    // rows 8-15 hold the lo terms of 0-7
+            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) {
+                    acc[jn][0] *= alpha[0]; acc[jn][1] *= alpha[0];
+                    acc[jn][2] *= alpha[1]; acc[jn][3] *= alpha[1];
+                }
+            }
+            uint32_t ph[4], pl[4];
+            if constexpr (MR == 8) {
+                split2<BF16>(s[0][0], s[0][1], ph[0], ph[1]);
+                split2<BF16>(s[1][0], s[1][1], ph[2], ph[3]);
+            } else {
+                split2<BF16>(s[0][0], s[0][1], ph[0], pl[0]);
+                split2<BF16>(s[0][2], s[0][3], ph[1], pl[1]);
+                split2<BF16>(s[1][0], s[1][1], ph[2], pl[2]);
+                split2<BF16>(s[1][2], s[1][3], ph[3], pl[3]);
+            }
+            auto pv = [&](int jn, uint32_t b0, uint32_t b1) {
+                mma16816<BF16>(acc[jn], ph, b0, b1);
+                if constexpr (MR == 16) mma16816<BF16>(acc[jn], pl, b0, b1);
+            };
+            if constexpr (KIND < 2) {
+                const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
+#pragma unroll
+                for (int jj = 0; jj < D / 16; ++jj) {
+                    uint32_t vb[4];
+                    ldsm4t(sv + chunk_at<D, KIND>(r, 2 * jj + c), vb);
+                    pv(2 * jj, vb[0], vb[1]);
+                    pv(2 * jj + 1, vb[2], vb[3]);
+                }
+            } else {
+                // tokens 2q, 2q + 1, 2q + 8, 2q + 9; channels NT * g + jn of products jn = 0 .. NT - 1
+                constexpr int W = NT / 4;
+                uint32_t x[4][W];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int r = 2 * q + (t & 1) + 8 * (t >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 v = lds_u4(sv + chunk_at<D, KIND>(r, g));
+                        x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
+                    } else {
+                        const uint2 v = lds_u2(sv + chunk_at<D, KIND>(r, g >> 1) + (g & 1) * 8);
+                        x[t][0] = v.x; x[t][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    uint32_t p[4], r[4];
+                    widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), p[0], p[1]);
+                    widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), p[2], p[3]);
+                    widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), r[0], r[1]);
+                    widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), r[2], r[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pv(4 * i + e, p[e], r[e]);
+                }
+            }
+        }
+        cp_wait<0>();
+
+        // join the four warps, in their order
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        if (q == 0) {
+            s_m[warp][g] = m[0];
+            s_l[warp][g] = l[0];
+            if constexpr (MR == 16) {
+                s_m[warp][g + 8] = m[1];
+                s_l[warp][g + 8] = l[1];
+            }
+        }
+        __syncthreads();                                         // every warp's stages are idle from here
+        float *so = reinterpret_cast<float *>(smem);             // (warps, MR, D)
+#pragma unroll
+        for (int jn = 0; jn < NT; ++jn)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int ch_d = KIND < 2 ? jn * 8 + 2 * q + e : NT * (2 * q + e) + jn;
+                const float sc = KIND < 2 ? 1.0f : vref;
+                if constexpr (MR == 8) {
+                    so[(warp * MR + g) * D + ch_d] = (acc[jn][e] + acc[jn][2 + e]) * sc;
+                } else {
+                    so[(warp * MR + g) * D + ch_d] = acc[jn][e] * sc;
+                    so[(warp * MR + g + 8) * D + ch_d] = acc[jn][2 + e] * sc;
+                }
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == tiles;
+        // a run's first pair that began in an earlier run goes to place 0, one that goes on to place 1
+        const int place = run_first && t0 > 0 ? 0 : 1;
+        for (int idx = tid; idx < heads * (D / 2); idx += kDecThreads) {
+            const int r = idx / (D / 2), c = (idx % (D / 2)) * 2;
+            float M = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kDecWarps; ++x) M = fmaxf(M, s_m[x][r]);
+            const float ref = M == -INFINITY ? 0.0f : M;
+            float o0 = 0.0f, o1 = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kDecWarps; ++x) {
+                const float f = ex2_approx(s_m[x][r] - ref);
+                const float2 v = *reinterpret_cast<const float2 *>(so + (x * MR + r) * D + c);
+                o0 += f * v.x;
+                o1 += f * v.y;
+                sum += f * s_l[x][r];
+            }
+            const size_t head = static_cast<size_t>(b) * a.Hq + head0 + r;
+            if (whole) {
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                store_out(a, head * D + c, o0 * inv, o1 * inv);
+                if (c == 0) {
+                    a.L[head] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+                    if (a.row_ml) {
+                        a.row_ml[2 * head] = M;
+                        a.row_ml[2 * head + 1] = sum;
+                    }
+                }
+            } else {
+                const size_t at = (static_cast<size_t>(cta) * 2 + place) * MR + r;
+                *reinterpret_cast<float2 *>(a.part_O + at * D + c) = make_float2(o0, o1);
+                if (c == 0) {
+                    a.part_ml[2 * at] = M;
+                    a.part_ml[2 * at + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();                                         // before the stages are filled again
+        u += t1 - t0;
+        run_first = false;
+    }
+}
+
+// ---- join -------------------------------------------------------------------------------------
+// grid: (pairs of all sequences, heads of a group).  A pair that several runs share is the sum of
+// their parts, each under 2^(m_part - M); rows without a token get O = 0, L = -inf.
+constexpr int kJoinThreads = 256;
+
+template <int D, int MR>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
+    __shared__ float4 s_o[GROUPS][VEC];
+    __shared__ float s_red[2][kJoinThreads / 32];
+    __shared__ long long s_n[2][kJoinThreads / 32];
+    const int pairs = a.c.H * a.chunks;
+    const int b = blockIdx.x / pairs, pair = blockIdx.x - b * pairs;
+    const int hk = pair / a.chunks, ch = pair - hk * a.chunks, r = blockIdx.y;
+    if (ch * MR + r >= a.G) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t head = static_cast<size_t>(b) * a.Hq + hk * a.G + ch * MR + r;
+    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
+    if (len == 0) {
+        for (int c = tid * 2; c < D; c += kJoinThreads * 2) store_out(a, head * D + c, 0.0f, 0.0f);
+        if (tid == 0) {
+            a.L[head] = -INFINITY;
+            if (a.row_ml) {
+                a.row_ml[2 * head] = -INFINITY;
+                a.row_ml[2 * head + 1] = 0.0f;
+            }
+        }
+        return;
+    }
+    // this sequence's first unit, and the total
+    const int tiles = (len + kTile - 1) / kTile;
+    long long lo = 0, total = 0;
+    for (int i = tid; i < a.c.B; i += kJoinThreads) {
+        const long long k = static_cast<long long>((kv_len(a.c, a.lens, i, &g_decode_err) + kTile - 1) / kTile) * pairs;
+        total += k;
+        if (i < b) lo += k;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    }
+    if (lane == 0) {
+        s_n[0][warp] = total;
+        s_n[1][warp] = lo;
+    }
+    __syncthreads();
+    total = lo = 0;
+#pragma unroll
+    for (int x = 0; x < kJoinThreads / 32; ++x) {
+        total += s_n[0][x];
+        lo += s_n[1][x];
+    }
+    const long long p0 = lo + static_cast<long long>(pair) * tiles;
+    const int runs = runs_of(a, total);
+    const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
+    if (c0 == c1) return;
+    // part i of CTA c0 + i: place 1 of the first, place 0 of the others
+    auto part = [&](int i) { return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * MR + r; };
+    const int parts = c1 - c0 + 1;
+    float M = -INFINITY;
+    for (int i = tid; i < parts; i += kJoinThreads) M = fmaxf(M, a.part_ml[2 * part(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) s_red[0][warp] = M;
+    __syncthreads();
+    M = s_red[0][0];
+#pragma unroll
+    for (int x = 1; x < kJoinThreads / 32; ++x) M = fmaxf(M, s_red[0][x]);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    float sum = 0.0f;
+    for (int i = tid; i < parts; i += kJoinThreads) sum += ex2_approx(a.part_ml[2 * part(i)] - ref) * a.part_ml[2 * part(i) + 1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_red[1][warp] = sum;
+    const int v = tid % VEC, grp = tid / VEC;
+    float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = grp; i < parts; i += GROUPS) {
+        const size_t at = part(i);
+        const float f = ex2_approx(a.part_ml[2 * at] - ref);
+        const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
+        o4.x += f * x.x; o4.y += f * x.y; o4.z += f * x.z; o4.w += f * x.w;
+    }
+    s_o[grp][v] = o4;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kJoinThreads / 32; ++x) sum += s_red[1][x];
+    if (tid < VEC) {
+        o4 = s_o[0][tid];
+#pragma unroll
+        for (int x = 1; x < GROUPS; ++x) {
+            const float4 y = s_o[x][tid];
+            o4.x += y.x; o4.y += y.y; o4.z += y.z; o4.w += y.w;
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        store_out(a, head * D + tid * 4, o4.x * inv, o4.y * inv);
+        store_out(a, head * D + tid * 4 + 2, o4.z * inv, o4.w * inv);
+        if (tid == 0) {
+            a.L[head] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+            if (a.row_ml) {
+                a.row_ml[2 * head] = M;
+                a.row_ml[2 * head + 1] = sum;
+            }
+        }
+    }
+}
+
+// ---- scores -----------------------------------------------------------------------------------
+// score[b][hk][t] += sum over the group's heads of 2^(logit - m) / l, from the logits that the main
+// kernel kept: one thread a token, heads in order.
+__global__ void __launch_bounds__(256) decode_score_kernel(const __grid_constant__ DecodeArgs a) {
+    const int bh = blockIdx.y, b = bh / a.c.H, hk = bh - b * a.c.H;
+    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
+    const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
+    for (int t = blockIdx.x * 256 + threadIdx.x; t < len; t += gridDim.x * 256) {
+        float w = 0.0f;
+        for (int i = 0; i < a.G; ++i) {
+            const float m = __ldg(a.row_ml + 2 * (head0 + i)), l = __ldg(a.row_ml + 2 * (head0 + i) + 1);
+            const float x = __ldg(a.logits + (head0 + i) * a.c.cap + t);
+            if (l > 0.0f) w += ex2_approx(x - m) / l;
+        }
+        a.c.score[static_cast<size_t>(bh) * a.c.cap + t] += w;
+    }
+}
+
+unsigned int take_decode_error() {
+    unsigned int v = 0, zero = 0;
+    cudaMemcpyFromSymbol(&v, g_decode_err, sizeof(v));
+    cudaMemcpyToSymbol(g_decode_err, &zero, sizeof(zero));
+    return v;
+}
+
+// ---- host -------------------------------------------------------------------------------------
+struct DecodePlan {
+    int mr, chunks, ctas;
+    size_t off_ml, off_rows, off_logits, bytes;
+};
+
+static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
+    DecodePlan p;
+    const int G = Hq / c.H;
+    p.mr = G <= 8 ? 8 : 16;
+    p.chunks = (G + p.mr - 1) / p.mr;
+    const int row = c.d * (c.kind == SAGE_KV_16 ? 2 : 1);
+    // one resident wave; never more CTAs than there can be tiles
+    long long n = kSMs * (row == 256 ? 2 : 3);
+    const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + kTile - 1) / kTile);
+    if (n > tiles) n = tiles;
+    p.ctas = static_cast<int>(n);
+    auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const size_t parts = static_cast<size_t>(p.ctas) * 2 * p.mr;
+    const size_t heads = static_cast<size_t>(c.B) * Hq;
+    p.off_ml = up(parts * c.d * sizeof(float));
+    p.off_rows = p.off_ml + up(parts * 2 * sizeof(float));
+    p.off_logits = p.off_rows + (add_score ? up(heads * 2 * sizeof(float)) : 0);
+    p.bytes = p.off_logits + (add_score ? heads * c.max_pages * c.page * sizeof(float) : 0);
+    return p;
+}
+
+static int check_decode(const sage_kv *c, int Hq, int add_score) {
+    const int st = check_kv(c, false);
+    if (st != SAGE_OK) return st;
+    if (Hq <= 0 || Hq % c->H != 0 || (add_score & ~1)) return SAGE_ERR_ARG;
+    if (static_cast<long long>(c->B) * Hq > (1 << 24)) return SAGE_ERR_UNSUPPORTED;
+    return SAGE_OK;
+}
+
+template <int D, int KIND, int MR>
+static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
+    using S = DecodeShape<D, KIND>;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KIND, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    decode_kernel<D, KIND, MR><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = static_cast<unsigned>(a.c.B) * a.c.H * a.chunks;
+    decode_join_kernel<D, MR><<<dim3(pairs, a.G < MR ? a.G : MR), kJoinThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.logits) return e;
+    const unsigned rows = static_cast<unsigned>(a.c.B) * a.c.H;
+    const unsigned x = (a.c.cap + 1023) / 1024;
+    decode_score_kernel<<<dim3(x, rows), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, int KIND>
+static cudaError_t launch_decode_m(const DecodeArgs &a, int mr, cudaStream_t st) {
+    return mr == 8 ? launch_decode_k<D, KIND, 8>(a, st) : launch_decode_k<D, KIND, 16>(a, st);
+}
+
+template <int KIND>
+static cudaError_t launch_decode_d(const DecodeArgs &a, int d, int mr, cudaStream_t st) {
+    return d == 64 ? launch_decode_m<64, KIND>(a, mr, st) : launch_decode_m<128, KIND>(a, mr, st);
+}
+
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score) {
+    if (check_decode(c, Hq, add_score) != SAGE_OK) return 0;
+    return decode_plan(*c, Hq, add_score).bytes;
+}
+
+int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, void *O, float *L, int add_score,
+                     void *workspace, size_t workspace_bytes, sage_stream_t stream) {
+    int st = check_decode(c, Hq, add_score);
+    if (st != SAGE_OK) return st;
+    st = check_kv(c, true);
+    if (st != SAGE_OK) return st;
+    if (!Q || !lens || !O || !L || (add_score && !c->score)) return SAGE_ERR_ARG;
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(L, 16) || misaligned(lens, 4)) return SAGE_ERR_ALIGN;
+    const DecodePlan p = decode_plan(*c, Hq, add_score);
+    if (!workspace || workspace_bytes < p.bytes) return SAGE_ERR_WORKSPACE;
+    if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    DecodeArgs a;
+    a.c = kv_view(*c);
+    a.Q = Q; a.O = O; a.L = L; a.lens = lens;
+    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas;
+    a.bf16 = c->dtype == SAGE_BF16;
+    a.sl2 = scale_log2(c->d);
+    a.part_O = reinterpret_cast<float *>(w);
+    a.part_ml = reinterpret_cast<float *>(w + p.off_ml);
+    a.row_ml = add_score ? reinterpret_cast<float *>(w + p.off_rows) : nullptr;
+    a.logits = add_score ? reinterpret_cast<float *>(w + p.off_logits) : nullptr;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (c->kind == SAGE_KV_INT8) e = launch_decode_d<2>(a, c->d, p.mr, s);
+    else if (c->kind == SAGE_KV_FP8) e = launch_decode_d<3>(a, c->d, p.mr, s);
+    else if (a.bf16) e = launch_decode_d<1>(a, c->d, p.mr, s);
+    else e = launch_decode_d<0>(a, c->d, p.mr, s);
+    return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,9 +1,11 @@
-"""Thin ctypes binding of the position and cache calls of libsage_gb300.so (include/sage.h).
+"""Thin ctypes binding of the position and cache calls of libsage_gb300.so (include/sage.h):
+rotary positions, the paged key-value cache, attention of one new token over it, eviction.
 
 As in binding.py, every function has the name of the C entry point it wraps, checks and marshals
 its arguments, and takes outputs and workspaces from PyTorch; nothing is computed here.  Calls run
 on ``stream`` or else on the current stream of the tensors' device; what a call allocates belongs
-to that stream.
+to that stream.  Lengths, page tables and positions are device int32 and are not read by the host:
+a page, length or slot out of range is skipped and reported by sage_device_status().
 """
 from __future__ import annotations
 
@@ -12,10 +14,19 @@ import ctypes
 
 import torch
 
-from .binding import SAGE_BF16, SAGE_FP16, _check, lib
+from .binding import SAGE_BF16, SAGE_FP16, _check, _ptr, lib
 
 SAGE_FP32 = 2
+SAGE_KV_16, SAGE_KV_INT8, SAGE_KV_FP8 = 0, 1, 2
+_KINDS = {torch.float16: SAGE_KV_16, torch.bfloat16: SAGE_KV_16, torch.int8: SAGE_KV_INT8,
+          torch.float8_e4m3fn: SAGE_KV_FP8}
 _DTYPES = {torch.float16: SAGE_FP16, torch.bfloat16: SAGE_BF16, torch.float32: SAGE_FP32}
+
+
+class SageKv(ctypes.Structure):
+    """struct sage_kv (include/sage.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "d", "dtype", "kind", "page", "pages", "max_pages")] + \
+               [(n, ctypes.c_void_p) for n in ("K", "V", "sK", "sV", "table", "score", "pos")]
 
 
 class SageRopeParams(ctypes.Structure):
@@ -117,3 +128,144 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
         _check("sage_rope", lib().sage_rope(ctypes.byref(p), Q.data_ptr(), None if K is None else K.data_ptr(),
                                             positions.data_ptr(), Qo.data_ptr(), None if K is None else Ko.data_ptr(), st))
     return Qo, Ko
+
+
+# ---- paged key-value cache ------------------------------------------------------------------
+
+
+class KvCache:
+    """A paged key-value cache over tensors of the caller (struct sage_kv).
+
+    K, V (pages,H,page,d): fp16 or bf16 values, or int8 / float8_e4m3fn codes with sK, sV
+    (pages,H,page) float32, one scale a row.  table (B,max_pages) int32: the pages of each
+    sequence; entries behind its last page are not read.  score (B,H,max_pages*page) float32 and
+    pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict.  The tensors
+    are fixed for the life of the object; their contents are the caller's and the calls'."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None):
+        if K.dtype not in _KINDS or K.dim() != 4 or table.dim() != 2:
+            raise ValueError("K must be (pages,H,page,d) in fp16, bf16, int8 or float8_e4m3fn, table (B,max_pages)")
+        pages, H, page, d = K.shape
+        B, max_pages = table.shape
+        dev = K.device
+        _need(K, "K", K.dtype, K.shape, dev)
+        _need(V, "V", K.dtype, K.shape, dev)
+        _need(table, "table", torch.int32, table.shape, dev)
+        self.kind = _KINDS[K.dtype]
+        if (self.kind == SAGE_KV_16) != (sK is None) or (sK is None) != (sV is None):
+            raise ValueError("sK and sV belong to int8 and float8_e4m3fn pools, and only to them")
+        for name, t in (("sK", sK), ("sV", sV)):
+            if t is not None:
+                _need(t, name, torch.float32, (pages, H, page), dev)
+        self.capacity = max_pages * page
+        for name, t, dt in (("score", score, torch.float32), ("pos", pos, torch.int32)):
+            if t is not None:
+                _need(t, name, dt, (B, H, self.capacity), dev)
+        self.K, self.V, self.sK, self.sV, self.table, self.score, self.pos = K, V, sK, sV, table, score, pos
+        self.B, self.H, self.d, self.page, self.pages, self.device = B, H, d, page, pages, dev
+        self._c = {dt: SageKv(B, H, d, dt, self.kind, page, pages, max_pages, K.data_ptr(), V.data_ptr(), _ptr(sK), _ptr(sV),
+                              table.data_ptr(), _ptr(score), _ptr(pos)) for dt in (SAGE_FP16, SAGE_BF16)}
+        self._bytes = {}        # workspace sizes by what they depend on
+
+    def _struct(self, t: torch.Tensor, what: str):
+        """The struct for a call on 16-bit tensors like ``t``."""
+        if t.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"{what}: SageBwd takes fp16 or bf16 tensors, got {t.dtype}")
+        if self.kind == SAGE_KV_16 and t.dtype != self.K.dtype:
+            raise TypeError(f"{what}: the cache holds {self.K.dtype}, got {t.dtype}")
+        return ctypes.byref(self._c[_DTYPES[t.dtype]])
+
+
+def make_kv_cache(B: int, H: int, d: int, capacity: int, *, dtype=torch.int8, page: int = 64, score: bool = False,
+                  device="cuda") -> KvCache:
+    """A cache for B sequences of up to ``capacity`` tokens, each with pages of its own; ``score``
+    adds what eviction needs.  dtype: fp16, bf16, int8 or float8_e4m3fn."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    m = max(1, -(-capacity // page))
+    table = torch.arange(B * m, dtype=torch.int32, device=device).view(B, m)
+    shape = (B * m, H, page, d)
+    K, V = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    eight = dtype in (torch.int8, torch.float8_e4m3fn)
+    sK, sV = (torch.zeros(shape[:3], device=device) if eight else None for _ in range(2))
+    extra = [torch.zeros((B, H, m * page), dtype=t, device=device) if score else None for t in (torch.float32, torch.int32)]
+    return KvCache(K, V, table, sK=sK, sV=sV, score=extra[0], pos=extra[1])
+
+
+def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor, *, count=None, mu=None,
+                   pos=None, stream=None) -> None:
+    """Writes tokens 0 .. count[b] - 1 (None: all T) of K, V (B,H,T,d) to slots start[b] + t of the
+    cache, in its form.  ``mu`` (B,H,d) float32 (8-bit caches): K-smoothing, codes of K - mu.
+    ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot)."""
+    B, H, T, d = K.shape
+    dev = cache.device
+    c = cache._struct(K, "K")
+    _need(K, "K", K.dtype, (cache.B, cache.H, T, cache.d), dev)
+    _need(V, "V", K.dtype, K.shape, dev)
+    _need(start, "start", torch.int32, (B,), dev)
+    if count is not None:
+        _need(count, "count", torch.int32, (B,), dev)
+    if mu is not None:
+        _need(mu, "mu", torch.float32, (B, H, d), dev)
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (B,), dev)
+    with _on(stream, dev) as st:
+        _check("sage_kv_append", lib().sage_kv_append(c, K.data_ptr(), V.data_ptr(), T, start.data_ptr(), _ptr(count),
+                                                      _ptr(mu), _ptr(pos), st))
+
+
+def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, score: bool = False, out=None, lse=None,
+                     workspace=None, stream=None):
+    """Attention of one new token a sequence, Q (B,Hq,1,d), over its lens[b] cached slots; Hq is a
+    multiple of the cache's heads.  ``score`` adds the attention weights to cache.score.
+    Returns (O (B,Hq,1,d) in Q's type, L (B,Hq,1) float32); a sequence of no slots gives 0 and -inf."""
+    dev = cache.device
+    c = cache._struct(Q, "Q")
+    Hq = Q.shape[1]
+    _need(Q, "Q", Q.dtype, (cache.B, Hq, 1, cache.d), dev)
+    _need(lens, "lens", torch.int32, (cache.B,), dev)
+    if score and cache.score is None:
+        raise ValueError("score=True needs a cache with score")
+    nbytes = cache._bytes.get((Hq, score))
+    if nbytes is None:
+        nbytes = cache._bytes[Hq, score] = lib().sage_decode_workspace_bytes(c, Hq, int(score))
+    with _on(stream, dev) as st:
+        if out is not None:
+            _need(out, "out", Q.dtype, Q.shape, dev)
+        if lse is not None:
+            _need(lse, "lse", torch.float32, (cache.B, Hq, 1), dev)
+        O = torch.empty_like(Q) if out is None else out
+        L = torch.empty((cache.B, Hq, 1), dtype=torch.float32, device=dev) if lse is None else lse
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check("sage_attn_decode", lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(),
+                                                          int(score), ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    return O, L
+
+
+def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, budget: int, recent: int = 0, out=None,
+                  workspace=None, stream=None) -> torch.Tensor:
+    """Cuts every sequence of more than ``budget`` slots to the ``budget`` slots of the largest
+    accumulated weight (cache.score), those at positions >= seen[b] - recent first; each head for
+    itself, rows moved into the freed slots.  Returns the new lengths (B) int32."""
+    dev = cache.device
+    if cache.score is None or cache.pos is None:
+        raise ValueError("eviction needs a cache with score and pos")
+    if not 0 <= recent <= budget or budget < 1:
+        raise ValueError(f"budget {budget}, recent {recent}: 0 <= recent <= budget and budget >= 1 are wanted")
+    budget = min(budget, cache.capacity)     # no length exceeds it
+    recent = min(recent, budget)
+    _need(lens, "lens", torch.int32, (cache.B,), dev)
+    _need(seen, "seen", torch.int32, (cache.B,), dev)
+    c = ctypes.byref(cache._c[SAGE_BF16 if cache.K.dtype == torch.bfloat16 else SAGE_FP16])
+    nbytes = cache._bytes.get(budget)
+    if nbytes is None:
+        nbytes = cache._bytes[budget] = lib().sage_evict_workspace_bytes(c, budget)
+    with _on(stream, dev) as st:
+        if out is not None:
+            _need(out, "out", torch.int32, (cache.B,), dev)
+        new = torch.empty_like(lens) if out is None else out
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check("sage_kv_evict", lib().sage_kv_evict(c, lens.data_ptr(), seen.data_ptr(), budget, recent, new.data_ptr(),
+                                                    ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    return new

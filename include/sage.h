@@ -9,9 +9,12 @@
  *   sage_attn_fwd         tiled online-softmax forward with per-token P codes; writes O and L
  *   sage_attn_bwd         backward with 16-bit dP and per-tile INT8 P / dS codes; writes dQ, dK, dV
  *
- * and, for positions in the text,
+ * and, for positions in the text and for answering with what was trained,
  *
  *   sage_rope             rotary positions with several axes, and their gradient
+ *   sage_kv_append        new tokens' K and V into a paged cache (16-bit, INT8 or E4M3)
+ *   sage_attn_decode      attention of one new token a sequence over that cache
+ *   sage_kv_evict         eviction from the cache by accumulated attention weight
  *
  * Conventions shared by every entry point
  *   - Tensors are contiguous, row-major (B, H, N, d): token n of head (b, h) starts at element
@@ -49,6 +52,8 @@ extern "C" {
 #define SAGE_ERR_CUDA 4         /* a kernel launch or CUDA runtime call failed                 */
 #define SAGE_ERR_TIMEOUT 5      /* a bounded device-side wait expired (see sage_device_status) */
 #define SAGE_ERR_WORKSPACE 6    /* workspace missing or smaller than the query says            */
+#define SAGE_ERR_INDEX 7        /* a page, length or slot read on the device was out of range
+                                   (cache calls; see sage_device_status)                       */
 
 /* Element types of the 16-bit tensors (Q, K, V, dO, O). */
 #define SAGE_FP16 0
@@ -367,11 +372,85 @@ typedef struct sage_rope_params {
 SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, const int *pos,
                        void *Qo, void *Ko, sage_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------ *
+ * Paged key-value cache.
+ *
+ * The pool holds `pages` pages of `page` tokens for all H kv heads, (pages,H,page,d) each for K
+ * and V.  Slot s of sequence b lies in row s % page of page table[b][s / page].  Entries of a
+ * table row behind a sequence's last page are not read.  A page may stand in several rows (a
+ * shared prefix) as long as no call writes to it: what sage_kv_append and sage_kv_evict write
+ * must belong to one sequence only, or what the page then holds is undefined.
+ *   SAGE_KV_16    rows in the 16-bit `dtype`.
+ *   SAGE_KV_INT8  INT8 codes with one scale a row: delta = fl32(max|x| / 127), codes round half
+ *                 to even of fl32(x / delta), all zero where delta = 0.
+ *   SAGE_KV_FP8   the same with 448 and the nearest E4M3 code.
+ * Lengths, starts, counts, positions and tables are device int32 (4-byte alignment).  A page that
+ * is not in [0, pages), or a length or slot outside [0, max_pages * page], is not followed: such
+ * rows are skipped (append, evict) or masked (decode; lengths are held to the range), and
+ * sage_device_status() returns SAGE_ERR_INDEX.
+ * Calls on one cache are ordered by their stream; none allocates, and all can be captured.
+ * ------------------------------------------------------------------------------------------ */
+#define SAGE_KV_16 0
+#define SAGE_KV_INT8 1
+#define SAGE_KV_FP8 2
+
+typedef struct sage_kv {
+    int B;              /* sequences (rows of the table)                                         */
+    int H;              /* kv heads                                                              */
+    int d;              /* 64 or 128                                                             */
+    int dtype;          /* SAGE_FP16 or SAGE_BF16: K, V, q, O of the calls (and a 16-bit pool)   */
+    int kind;           /* SAGE_KV_*                                                             */
+    int page;           /* tokens a page, a multiple of 16                                       */
+    int pages;          /* pages in the pool                                                     */
+    int max_pages;      /* table entries a sequence; capacity = max_pages * page < 2^30          */
+    void *K, *V;        /* (pages,H,page,d)                                                      */
+    float *sK, *sV;     /* (pages,H,page), 8-bit kinds only, else NULL                           */
+    const int *table;   /* (B,max_pages)                                                         */
+    float *score;       /* (B,H,capacity) accumulated weight of each slot, or NULL               */
+    int *pos;           /* (B,H,capacity) position of each slot's token in the text, or NULL     */
+} sage_kv;
+
+/* sage_kv_append -- tokens 0 .. count[b] - 1 of K, V (B,H,T,d) go to slots start[b] + t.
+ * count NULL: T for every sequence; count[b] < T: the rest of a padded row is not written.
+ * mu (B,H,d) float32, 8-bit kinds only, nullable: K-smoothing, the codes are those of
+ * fl32(K - mu); attention over keys that share one mu does not change (L does, by q . mu /
+ * sqrt(d)).  sage_quantize_smooth's muK of the prompt is such a mu.
+ * Where the cache has score: score[slot] = 0.  Where it has pos: pos[slot] = pos0[b] + t, with
+ * pos0 NULL: the slot itself. */
+SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int T, const int *start,
+                            const int *count, const float *mu, const int *pos0,
+                            sage_stream_t stream);
+
+/* sage_attn_decode -- one new token a sequence over its `lens[b]` cached slots (its own included,
+ * if it has been appended): s_t = q . K_t / sqrt(d), O = sum_t softmax(s)_t V_t,
+ * L = log sum_t exp s_t.  Query head h reads kv head h / (Hq / H).  lens[b] = 0: O = 0, L = -inf.
+ * In:  Q (B,Hq,1,d).  Out: O (B,Hq,1,d), L (B,Hq,1) float32.
+ * add_score = 1: score[b][kv head][t] += the sum over its query heads of softmax(s)_t.
+ * Sums and statistics are float32; the probabilities enter the second product as two 16-bit
+ * terms (16 or more significant bits).  Results do not depend on the order in which the GPU runs
+ * its blocks.  O and L may not overlap the inputs or the cache. */
+SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score);
+SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, void *O,
+                              float *L, int add_score, void *workspace, size_t workspace_bytes,
+                              sage_stream_t stream);
+
+/* sage_kv_evict -- cuts every sequence with lens[b] > budget to `budget` slots, each kv head for
+ * itself.  First rank the slots with pos >= seen[b] - recent (seen[b]: the tokens of the text so
+ * far), then the others by score, NaN last; ties go to the lower slot.  The first `budget` stay.
+ * Those of them in slots >= budget move to the freed slots < budget, in slot order, with their
+ * scales, score and pos; all other slots keep what they hold.  lens_out[b] = min(lens[b], budget).
+ * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not be lens. */
+SAGE_API size_t sage_evict_workspace_bytes(const sage_kv *c, int budget);
+SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget, int recent,
+                           int *lens_out, void *workspace, size_t workspace_bytes,
+                           sage_stream_t stream);
+
 /* Bytes the SAGE_FLAG_DUMP buffer needs for a forward (which = 0) or backward (which = 1). */
 SAGE_API size_t sage_dump_bytes(const sage_params *p, int which);
 
 /* Waits for `stream`, then reads and clears the device-side error word of the current device:
- * SAGE_OK, or SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call. */
+ * SAGE_OK, SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call, or else
+ * SAGE_ERR_INDEX if a cache call met a page, length or slot out of range. */
 SAGE_API int sage_device_status(sage_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
