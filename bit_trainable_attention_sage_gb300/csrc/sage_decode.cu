@@ -6,7 +6,7 @@
 // so the kernel is bound by memory bandwidth: 2 d values (and 8 bytes of scales in 8 bits) a
 // token and kv head, against 4 d multiply-adds a token and query head.
 //
-// Split.  The work is cut into tiles of 64 tokens of one (sequence, kv head, group of query
+// Split.  The work is cut into tiles of 64 or 128 tokens of one (sequence, kv head, group of query
 // heads), numbered in that order, and each of a fixed number of CTAs takes an equal run of them
 // whatever the lengths are: a run can cover the end of one pair, several whole pairs and the
 // start of another.  Lengths stay on the device; every CTA adds them up itself.  A pair that lies
@@ -14,9 +14,9 @@
 // of exponentials in the workspace (two places a CTA: a run's first and last pair), and a second
 // kernel joins them in order, so results do not depend on the order in which CTAs run.
 //
-// Inside a CTA four warps each take 16 of a tile's 64 tokens and never wait for one another: each
-// keeps its own ring of cp.async stages in shared memory, its own running maximum, sum and output
-// accumulators, and the four are joined once at the end of a pair.
+// Inside a CTA four warps each take a quarter of a tile (a granule) and never wait for one another:
+// each keeps its own ring of cp.async stages in shared memory, its own running maximum, sum and
+// output accumulators, and the four are joined once at the end of a pair.
 //
 // Products.  m16n8k16 tensor-core products with the query heads as the 16 rows.  The kernel
 // needs a fraction of their rate, and both operands come from registers, where 8-bit rows can be
@@ -31,15 +31,15 @@
 //   - The probabilities enter as hi + lo of two 16-bit values, at least 16 bits: one rounding to
 //     bf16 would show in the output.  With at most 8 query heads a group, hi takes rows 0-7 and
 //     lo rows 8-15 of one product, which the padding to 16 rows would waste otherwise.
+#include <utility>
+
 #include "sage_kv.cuh"
 
 namespace sage {
 
 __device__ unsigned int g_decode_err = 0;   // 1: a page or length was out of range
 
-constexpr int kTile = 64;                    // tokens a unit of work
-constexpr int kGran = 16;                    // tokens a warp takes of it
-constexpr int kDecWarps = kTile / kGran;
+constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kSMs = 152;
 
@@ -49,12 +49,18 @@ struct DecodeShape {
     static constexpr int ES = KIND < 2 ? 2 : 1;
     static constexpr int ROW = D * ES;                       // bytes
     static constexpr int CPR = ROW / 16;                     // 16-byte chunks a row: 4, 8 or 16
-    static constexpr int SCALES = KIND < 2 ? 0 : 2 * kGran * 4;
-    static constexpr int STAGE = 2 * kGran * ROW + SCALES;
-    static constexpr int STAGES = ROW == 256 ? 3 : ROW == 128 ? 4 : 6;
-    static constexpr int SMEM = kDecWarps * STAGES * STAGE;
-    static constexpr int CTAS = ROW == 256 ? 2 : 3;          // resident CTAs an SM
+    // tokens a warp takes at a time: the maximum, the rescaling and the loads' addresses are paid
+    // once a granule, and its products are independent chains
+    static constexpr int GRAN = ROW == 256 ? 16 : 32;
+    static constexpr int TILE = GRAN * kDecWarps;
+    static constexpr int SCALES = KIND < 2 ? 0 : 2 * GRAN * 4;
+    static constexpr int STAGE = 2 * GRAN * ROW + SCALES;
+    static constexpr int STAGES = ROW == 64 ? 4 : 3;
+    static constexpr int CTAS = ROW == 64 ? 3 : 2;           // resident CTAs an SM
+    static constexpr int ALIGN = 512;                        // of the ring, so that its addresses can be XORed
+    static constexpr int SMEM = kDecWarps * STAGES * STAGE + ALIGN;
 };
+constexpr int decode_tile(int row_bytes) { return (row_bytes == 256 ? 16 : 32) * kDecWarps; }
 
 struct DecodeArgs {
     KvView c;
@@ -64,6 +70,7 @@ struct DecodeArgs {
     const int *lens;
     int Hq, G, chunks;       // query heads, heads a kv head, groups of at most MR heads a kv head
     int ctas;                // CTAs that share the work (gridDim.x)
+    int tile, tile_shift;    // tokens a unit of work, 64 or 128, and their log2
     int bf16;                // type of q and O
     float sl2;               // log2(e) / sqrt(d)
     float *part_O;           // (ctas, 2, MR, d) unnormalised sums
@@ -73,6 +80,10 @@ struct DecodeArgs {
 };
 
 // ---- shared-memory and tensor-core pieces ----------------------------------------------------
+template <int DST, int SRC>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -93,22 +104,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (BF16)
@@ -121,16 +116,27 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Place of 16-byte chunk c of row r in a granule.  Rows of 128 and 256 bytes in 16 bits: the 8
+// Place of 16-byte chunk c of row r in half a granule (16 rows; the other half follows).  Rows of 128 and 256 bytes in 16 bits: the 8
 // rows an ldmatrix reads at one chunk fall into the 8 different 16-byte bank groups.  In 8 bits
 // a quarter-warp reads chunks 0-3 of rows (2i, 2i + 1), or chunks (2i, 2i + 1) of rows 0, 2, 4, 6
 // (1, 3, 5, 7): the XORs put either set into 8 different bank groups.
 template <int D, int KIND>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+__host__ __device__ constexpr uint32_t chunk_at(int r, int c) {
     using S = DecodeShape<D, KIND>;
     if constexpr (KIND < 2) return static_cast<uint32_t>(r * S::CPR + (c ^ (r & 7))) * 16u;
     else if constexpr (D == 128) return static_cast<uint32_t>(r * 8 + (c ^ ((r & 6) ^ ((r & 1) << 2)))) * 16u;
     else return static_cast<uint32_t>((r >> 1) * 8 + ((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1))) * 16u;
+}
+
+// Half a granule's K and V rows, all 16 of them there: 32 lanes take 512 consecutive bytes at a
+// time.  Place i of a lane is that of its first 512 bytes XOR a constant, plus 512 i.
+template <int D, int KIND, int... I>
+__device__ __forceinline__ void load_half(uint32_t k_dst, uint32_t v_dst, const uint8_t *k, const uint8_t *v,
+                                          std::integer_sequence<int, I...>) {
+    using S = DecodeShape<D, KIND>;
+    constexpr int RPI = 32 / S::CPR;
+    (cp_async16_at<I * 512, I * 512>(k_dst ^ (chunk_at<D, KIND>(I * RPI, 0) - I * 512u), k), ...);
+    (cp_async16_at<I * 512, I * 512>(v_dst ^ (chunk_at<D, KIND>(I * RPI, 0) - I * 512u), v), ...);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
@@ -187,7 +193,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     const int b0 = min(tid * per, a.c.B), b1 = min(b0 + per, a.c.B);
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + kTile - 1) / kTile) * pairs;
+        mine += static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -207,7 +213,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     if (u >= at && u < at + mine) {
         int b = b0;
         for (;; ++b) {
-            const long long k = static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + kTile - 1) / kTile) * pairs;
+            const long long k = static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
             if (u < at + k) break;
             at += k;
         }
@@ -248,14 +254,20 @@ template <int D, int KIND, int MR>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND>;
     constexpr bool BF16 = KIND == 1;                 // type of the products
-    constexpr int KS = D / 16, NT = D / 8;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int KS = D / 16, NT = D / 8;           // 16-channel steps of q K^T, 8-channel columns of P V
+    constexpr int GT = S::GRAN / 8, HALVES = S::GRAN / 16;
+    constexpr int R = MR == 16 ? 2 : 1;              // rows of a lane that are heads
+    constexpr int HALF = 16 * S::ROW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & (S::ALIGN - 1));
     __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int pairs = a.c.H * a.chunks;
     const int cta = blockIdx.x;
+    // the join may take its place on the GPU; it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
         const int n = runs_of(a, total);
         return cta < n ? run_start(total, cta, n) : total;
@@ -263,14 +275,16 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
     const int runs = runs_of(a, w.total);
     if (cta >= runs) return;
     const long long u1 = run_start(w.total, cta + 1, runs);
-    const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * S::STAGE);
+    // a warp's ring: stages of K rows, V rows, then (8 bits) K scales, V scales
+    uint8_t *ring = smem + warp * (S::STAGES * S::STAGE);
+    const uint32_t load_lane = smem_u32(ring) + chunk_at<D, KIND>(lane / S::CPR, lane % S::CPR);
 
     long long u = w.u, first = w.first;
     int b = w.b;
     bool run_first = true;
     while (u < u1) {
         const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-        const int tiles = (len + kTile - 1) / kTile;
+        const int tiles = (len + S::TILE - 1) / S::TILE;
         if (u - first >= static_cast<long long>(tiles) * pairs) {
             first += static_cast<long long>(tiles) * pairs;
             ++b;
@@ -283,37 +297,50 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
         const int head0 = hk * a.G + ch * MR;                    // first query head of the group
         const int heads = min(MR, a.G - ch * MR);
 
-        // granules of this warp: tokens tau * 64 + warp * 16, tau in [t0, t1), while below len
-        const int tok0 = t0 * kTile + warp * kGran;
-        const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + kTile - 1) / kTile);
-        uint32_t bad = 0;                                        // stages whose page is not one
-        auto load = [&](int j) {
-            const int stage = j % S::STAGES;
-            const int tok = tok0 + j * kTile;
-            const int page = kv_page(a.c, b, tok, &g_decode_err);
-            const int nv = page < 0 ? 0 : min(kGran, len - tok);
-            bad = (bad & ~(1u << stage)) | (page < 0 ? 1u << stage : 0u);
-            const size_t row = page < 0 ? 0 : kv_row(a.c, page, hk, tok);
-            const uint8_t *k = static_cast<const uint8_t *>(a.c.K) + row * S::ROW;
-            const uint8_t *v = static_cast<const uint8_t *>(a.c.V) + row * S::ROW;
-            const uint32_t dst = ring + stage * S::STAGE;
+        // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
+        const int tok0 = t0 * S::TILE + warp * S::GRAN;
+        const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
+        uint32_t bad = 0;                                        // halves (2 bits a stage) whose page is not one
+        auto load = [&](int j, int stage) {
+            const int tok = tok0 + j * S::TILE;
 #pragma unroll
-            for (int i = 0; i < kGran * S::CPR / 32; ++i) {
-                const int idx = i * 32 + lane, r = idx / S::CPR, c = idx % S::CPR;
-                const uint32_t off = r < nv ? static_cast<uint32_t>(idx) * 16u : 0u;
-                const uint32_t at = chunk_at<D, KIND>(r, c);
-                cp_async16(dst + at, k + off, r < nv);
-                cp_async16(dst + kGran * S::ROW + at, v + off, r < nv);
-            }
-            if constexpr (KIND >= 2) {
-                const int r = lane & 15;
-                const float *s = (lane < 16 ? a.c.sK : a.c.sV) + row;
-                cp_async4(dst + 2 * kGran * S::ROW + lane * 4, s + (r < nv ? r : 0), r < nv);
+            for (int hf = 0; hf < HALVES; ++hf) {
+                const int t = tok + hf * 16;
+                const int left = len - t;
+                const int page = left > 0 ? kv_page(a.c, b, t, &g_decode_err) : 0;
+                const int nv = page < 0 ? 0 : max(0, min(16, left));
+                const uint32_t bit = 1u << (stage * 2 + hf);
+                bad = page < 0 ? bad | bit : bad & ~bit;
+                const size_t row = nv == 0 ? 0 : kv_row(a.c, page, hk, t);
+                const uint8_t *k = static_cast<const uint8_t *>(a.c.K) + row * S::ROW + lane * 16;
+                const uint8_t *v = static_cast<const uint8_t *>(a.c.V) + row * S::ROW + lane * 16;
+                const uint32_t dst = load_lane + stage * S::STAGE + hf * HALF;
+                if (nv == 16) {
+                    load_half<D, KIND>(dst, dst + S::GRAN * S::ROW, k, v, std::make_integer_sequence<int, HALF / 512>());
+                } else {
+                    // rows past the end are zeros: what the pool holds there is never looked at
+                    const uint32_t k0 = smem_u32(ring) + stage * S::STAGE + hf * HALF;
+#pragma unroll
+                    for (int i = 0; i < HALF / 512; ++i) {
+                        const int r = i * (32 / S::CPR) + lane / S::CPR;
+                        const uint32_t at = k0 + chunk_at<D, KIND>(r, lane % S::CPR);
+                        const uint8_t *ks = r < nv ? k + i * 512 : static_cast<const uint8_t *>(a.c.K);
+                        const uint8_t *vs = r < nv ? v + i * 512 : static_cast<const uint8_t *>(a.c.V);
+                        cp_async16(at, ks, r < nv);
+                        cp_async16(at + S::GRAN * S::ROW, vs, r < nv);
+                    }
+                }
+                if constexpr (KIND >= 2) {
+                    const int r = lane & 15;
+                    const float *sc = (lane < 16 ? a.c.sK : a.c.sV) + row;
+                    const uint32_t at = smem_u32(ring) + stage * S::STAGE + 2 * S::GRAN * S::ROW + ((lane >> 4) * S::GRAN + hf * 16 + r) * 4;
+                    cp_async4(at, sc + (r < nv ? r : 0), r < nv);
+                }
             }
         };
 #pragma unroll
         for (int j = 0; j < S::STAGES - 1; ++j) {
-            if (j < ng) load(j);
+            if (j < ng) load(j, j);
             cp_commit();
         }
 
@@ -336,7 +363,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             if constexpr (KIND >= 2) {
                 // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15)
 #pragma unroll
-                for (int r = 0; r < (MR == 16 ? 2 : 1); ++r) {
+                for (int r = 0; r < R; ++r) {
                     float mx = 0.0f;
                     auto pair_of = [&](uint32_t x) {
                         return a.bf16 ? __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x))
@@ -374,33 +401,40 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         float vref = 1.1754943508222875e-38f;                    // 2^-126
 
+        int stage = 0, ahead = S::STAGES - 1;                    // stages of granules j and j + STAGES - 1
         for (int j = 0; j < ng; ++j) {
             cp_wait<S::STAGES - 2>();
             __syncwarp();
-            if (j + S::STAGES - 1 < ng) load(j + S::STAGES - 1);
+            if (j + S::STAGES - 1 < ng) load(j + S::STAGES - 1, ahead);
             cp_commit();
-            const int stage = j % S::STAGES;
-            const uint32_t sk = ring + stage * S::STAGE, sv = sk + kGran * S::ROW;
-            const int tok = tok0 + j * kTile;
-            const int nv = (bad >> stage) & 1u ? 0 : min(kGran, len - tok);
+            const uint8_t *kst = ring + stage * S::STAGE, *vst = kst + S::GRAN * S::ROW;
+            const int tok = tok0 + j * S::TILE;
+            const uint32_t holes = (bad >> (stage * 2)) & 3u;
 
             // S = q K^T: columns (tokens) nt * 8 + 2 q + {0, 1}
-            float s[2][4] = {};
-            if constexpr (KIND < 2) {
-                const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+            float s[GT][4];
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t kb[4];
-                    ldsm4(sk + chunk_at<D, KIND>(r, 2 * ks + c), kb);
-                    mma16816<BF16>(s[0], qa[ks], kb[0], kb[1]);
-                    mma16816<BF16>(s[1], qa[ks], kb[2], kb[3]);
-                }
+            for (int nt = 0; nt < GT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+            if constexpr (KIND < 2) {
+                const uint32_t at = smem_u32(kst) + chunk_at<D, KIND>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf) {
+                        uint32_t kb[4];
+                        ldsm4((at ^ (ks * 32)) + hf * HALF, kb);
+                        mma16816<BF16>(s[2 * hf], qa[ks], kb[0], kb[1]);
+                        mma16816<BF16>(s[2 * hf + 1], qa[ks], kb[2], kb[3]);
+                    }
             } else {
+                const uint32_t at = chunk_at<D, KIND>(g, q);     // rows 8 apart are 8 * ROW apart
 #pragma unroll
                 for (int jj = 0; jj < D / 64; ++jj)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const uint4 kk = lds_u4(sk + chunk_at<D, KIND>(nt * 8 + g, q + 4 * jj));
+                    for (int nt = 0; nt < GT; ++nt) {
+                        const uint4 kk = *reinterpret_cast<const uint4 *>(kst + (at ^ (jj * 64)) + nt * 8 * S::ROW);
                         const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -410,38 +444,49 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                         }
                     }
             }
-            float2 fv[2];                                        // sV of the lane's tokens
+            float2 fv[GT];                                       // sV of the lane's tokens
             if constexpr (KIND >= 2) {
-                const uint32_t sc = sk + 2 * kGran * S::ROW;
+                const uint8_t *sc = kst + 2 * S::GRAN * S::ROW + q * 8;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const float2 fk = lds_f2(sc + (nt * 8 + 2 * q) * 4);
-                    fv[nt] = lds_f2(sc + (kGran + nt * 8 + 2 * q) * 4);
-                    s[nt][0] *= fk.x; s[nt][1] *= fk.y;
-                    s[nt][2] *= fk.x; s[nt][3] *= fk.y;
+                for (int nt = 0; nt < GT; ++nt) {
+                    const float2 fk = *reinterpret_cast<const float2 *>(sc + nt * 32);
+                    fv[nt] = *reinterpret_cast<const float2 *>(sc + S::GRAN * 4 + nt * 32);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        s[nt][2 * r] *= fk.x;
+                        s[nt][2 * r + 1] *= fk.y;
+                    }
                 }
             }
-            // log2 units; tokens past the end of the sequence do not exist
+            // log2 units; tokens past the end of the sequence, or without a page, do not exist
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < GT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = nt * 8 + 2 * q + (i & 1) < nv;
-                    s[nt][i] = in ? s[nt][i] * qs[i >> 1] : -INFINITY;
-                }
+                for (int i = 0; i < 2 * R; ++i) s[nt][i] *= qs[i >> 1];
+            if (len - tok < S::GRAN || holes) {
+#pragma unroll
+                for (int nt = 0; nt < GT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2 * R; ++i)
+                        if (nt * 8 + 2 * q + (i & 1) >= len - tok || (holes >> (nt / 2)) & 1u) s[nt][i] = -INFINITY;
+            }
             if (a.logits) {
 #pragma unroll
-                for (int r = 0; r < (MR == 16 ? 2 : 1); ++r)
+                for (int r = 0; r < R; ++r)
                     if (g + 8 * r < heads) {
                         float *to = a.logits + (static_cast<size_t>(b) * a.Hq + head0 + g + 8 * r) * a.c.cap + tok + 2 * q;
-                        *reinterpret_cast<float2 *>(to) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
-                        *reinterpret_cast<float2 *>(to + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+#pragma unroll
+                        for (int nt = 0; nt < GT; ++nt)
+                            if (nt < 2 || len - tok > 16)        // (slots up to the next multiple of 16 exist)
+                                *reinterpret_cast<float2 *>(to + nt * 8) = make_float2(s[nt][2 * r], s[nt][2 * r + 1]);
                     }
             }
             float alpha[2] = {1.0f, 1.0f};
 #pragma unroll
-            for (int r = 0; r < (MR == 16 ? 2 : 1); ++r) {
-                float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            for (int r = 0; r < R; ++r) {
+                float mx = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+#pragma unroll
+                for (int nt = 1; nt < GT; ++nt) mx = max3f(mx, s[nt][2 * r], s[nt][2 * r + 1]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(m[r], mx);
@@ -450,7 +495,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                 m[r] = mn;
                 float sum = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < GT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float &x = s[nt][2 * r + i];
@@ -461,7 +506,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             }
             if constexpr (KIND >= 2) {
                 // the largest sV so far, as a power of two above it
-                float mv = fmaxf(fmaxf(fv[0].x, fv[0].y), fmaxf(fv[1].x, fv[1].y));
+                float mv = fmaxf(fv[0].x, fv[0].y);
+#pragma unroll
+                for (int nt = 1; nt < GT; ++nt) mv = max3f(mv, fv[nt].x, fv[nt].y);
                 mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
                 mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 2));
                 if (mv > vref) {
@@ -473,10 +520,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                 }
                 const float iv = __uint_as_float(0x7F000000u - __float_as_uint(vref));   // 1 / vref
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < GT; ++nt) {
                     const float x = fv[nt].x * iv, y = fv[nt].y * iv;
-                    s[nt][0] *= x; s[nt][1] *= y;
-                    s[nt][2] *= x; s[nt][3] *= y;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        s[nt][2 * r] *= x;
+                        s[nt][2 * r + 1] *= y;
+                    }
                 }
             }
             if (MR == 8) alpha[1] = alpha[0];                    // rows 8-15 hold the lo terms of 0-7
@@ -487,55 +537,61 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     acc[jn][2] *= alpha[1]; acc[jn][3] *= alpha[1];
                 }
             }
-            uint32_t ph[4], pl[4];
-            if constexpr (MR == 8) {
-                split2<BF16>(s[0][0], s[0][1], ph[0], ph[1]);
-                split2<BF16>(s[1][0], s[1][1], ph[2], ph[3]);
-            } else {
-                split2<BF16>(s[0][0], s[0][1], ph[0], pl[0]);
-                split2<BF16>(s[0][2], s[0][3], ph[1], pl[1]);
-                split2<BF16>(s[1][0], s[1][1], ph[2], pl[2]);
-                split2<BF16>(s[1][2], s[1][3], ph[3], pl[3]);
-            }
-            auto pv = [&](int jn, uint32_t b0, uint32_t b1) {
-                mma16816<BF16>(acc[jn], ph, b0, b1);
-                if constexpr (MR == 16) mma16816<BF16>(acc[jn], pl, b0, b1);
-            };
-            if constexpr (KIND < 2) {
-                const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
 #pragma unroll
-                for (int jj = 0; jj < D / 16; ++jj) {
-                    uint32_t vb[4];
-                    ldsm4t(sv + chunk_at<D, KIND>(r, 2 * jj + c), vb);
-                    pv(2 * jj, vb[0], vb[1]);
-                    pv(2 * jj + 1, vb[2], vb[3]);
+            for (int hf = 0; hf < HALVES; ++hf) {
+                float(&s0)[4] = s[2 * hf], (&s1)[4] = s[2 * hf + 1];
+                uint32_t ph[4], pl[4];
+                if constexpr (MR == 8) {
+                    split2<BF16>(s0[0], s0[1], ph[0], ph[1]);
+                    split2<BF16>(s1[0], s1[1], ph[2], ph[3]);
+                } else {
+                    split2<BF16>(s0[0], s0[1], ph[0], pl[0]);
+                    split2<BF16>(s0[2], s0[3], ph[1], pl[1]);
+                    split2<BF16>(s1[0], s1[1], ph[2], pl[2]);
+                    split2<BF16>(s1[2], s1[3], ph[3], pl[3]);
                 }
-            } else {
-                // tokens 2q, 2q + 1, 2q + 8, 2q + 9; channels NT * g + jn of products jn = 0 .. NT - 1
-                constexpr int W = NT / 4;
-                uint32_t x[4][W];
+                auto pv = [&](int jn, uint32_t b0, uint32_t b1) {
+                    mma16816<BF16>(acc[jn], ph, b0, b1);
+                    if constexpr (MR == 16) mma16816<BF16>(acc[jn], pl, b0, b1);
+                };
+                if constexpr (KIND < 2) {
+                    const uint32_t at = smem_u32(vst) + hf * HALF + chunk_at<D, KIND>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int r = 2 * q + (t & 1) + 8 * (t >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 v = lds_u4(sv + chunk_at<D, KIND>(r, g));
-                        x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
-                    } else {
-                        const uint2 v = lds_u2(sv + chunk_at<D, KIND>(r, g >> 1) + (g & 1) * 8);
-                        x[t][0] = v.x; x[t][1] = v.y;
+                    for (int jj = 0; jj < D / 16; ++jj) {
+                        uint32_t vb[4];
+                        ldsm4t(at ^ (jj * 32), vb);
+                        pv(2 * jj, vb[0], vb[1]);
+                        pv(2 * jj + 1, vb[2], vb[3]);
+                    }
+                } else {
+                    // tokens 2q, 2q + 1, 2q + 8, 2q + 9; channels NT * g + jn of products jn = 0 .. NT - 1
+                    constexpr int W = NT / 4;
+                    uint32_t x[4][W];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint8_t *at = vst + hf * HALF + (t >> 1) * 8 * S::ROW;
+                        if constexpr (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g));
+                            x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g >> 1) + (g & 1) * 8);
+                            x[t][0] = v.x; x[t][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        uint32_t p[4], r[4];
+                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), p[0], p[1]);
+                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), p[2], p[3]);
+                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), r[0], r[1]);
+                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), r[2], r[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pv(4 * i + e, p[e], r[e]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    uint32_t p[4], r[4];
-                    widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), p[0], p[1]);
-                    widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), p[2], p[3]);
-                    widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), r[0], r[1]);
-                    widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), r[2], r[3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) pv(4 * i + e, p[e], r[e]);
-                }
             }
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+            ahead = ahead + 1 == S::STAGES ? 0 : ahead + 1;
         }
         cp_wait<0>();
 
@@ -613,40 +669,31 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
     }
 }
 
-// ---- join -------------------------------------------------------------------------------------
-// grid: (pairs of all sequences, heads of a group).  A pair that several runs share is the sum of
-// their parts, each under 2^(m_part - M); rows without a token get O = 0, L = -inf.
+// ---- join and scores ----------------------------------------------------------------------------
+// grid: (sequences * kv heads, blocks a row).  A pair that several runs share is the sum of their
+// parts, each under 2^(m_part - M), in their order; sequences without a token get O = 0, L = -inf.
+// Then score[b][hk][t] += sum over the group's heads of 2^(logit - M) / l, from the logits that the
+// main kernel kept: four tokens a thread, heads in order.  Launched while the main kernel still
+// runs (programmatic dependent launch): the lengths are added up before the wait for its end.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinHeads = 64;               // heads whose M and 1 / l are held at a time
 
 template <int D, int MR>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
+    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC, WARPS = kJoinThreads / 32;
     __shared__ float4 s_o[GROUPS][VEC];
-    __shared__ float s_red[2][kJoinThreads / 32];
-    __shared__ long long s_n[2][kJoinThreads / 32];
-    const int pairs = a.c.H * a.chunks;
-    const int b = blockIdx.x / pairs, pair = blockIdx.x - b * pairs;
-    const int hk = pair / a.chunks, ch = pair - hk * a.chunks, r = blockIdx.y;
-    if (ch * MR + r >= a.G) return;
+    __shared__ float s_M[kJoinHeads], s_inv[kJoinHeads];
+    __shared__ long long s_n[2][WARPS];
+    const int bh = blockIdx.x, b = bh / a.c.H, hk = bh - b * a.c.H;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const size_t head = static_cast<size_t>(b) * a.Hq + hk * a.G + ch * MR + r;
+    const int pairs = a.c.H * a.chunks;
+    const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
     const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-    if (len == 0) {
-        for (int c = tid * 2; c < D; c += kJoinThreads * 2) store_out(a, head * D + c, 0.0f, 0.0f);
-        if (tid == 0) {
-            a.L[head] = -INFINITY;
-            if (a.row_ml) {
-                a.row_ml[2 * head] = -INFINITY;
-                a.row_ml[2 * head + 1] = 0.0f;
-            }
-        }
-        return;
-    }
+    const int tiles = (len + a.tile - 1) >> a.tile_shift;
     // this sequence's first unit, and the total
-    const int tiles = (len + kTile - 1) / kTile;
     long long lo = 0, total = 0;
     for (int i = tid; i < a.c.B; i += kJoinThreads) {
-        const long long k = static_cast<long long>((kv_len(a.c, a.lens, i, &g_decode_err) + kTile - 1) / kTile) * pairs;
+        const long long k = static_cast<long long>((kv_len(a.c, a.lens, i, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
         total += k;
         if (i < b) lo += k;
     }
@@ -662,81 +709,115 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     __syncthreads();
     total = lo = 0;
 #pragma unroll
-    for (int x = 0; x < kJoinThreads / 32; ++x) {
+    for (int x = 0; x < WARPS; ++x) {
         total += s_n[0][x];
         lo += s_n[1][x];
     }
-    const long long p0 = lo + static_cast<long long>(pair) * tiles;
-    const int runs = runs_of(a, total);
-    const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
-    if (c0 == c1) return;
-    // part i of CTA c0 + i: place 1 of the first, place 0 of the others
-    auto part = [&](int i) { return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * MR + r; };
-    const int parts = c1 - c0 + 1;
-    float M = -INFINITY;
-    for (int i = tid; i < parts; i += kJoinThreads) M = fmaxf(M, a.part_ml[2 * part(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) s_red[0][warp] = M;
-    __syncthreads();
-    M = s_red[0][0];
-#pragma unroll
-    for (int x = 1; x < kJoinThreads / 32; ++x) M = fmaxf(M, s_red[0][x]);
-    const float ref = M == -INFINITY ? 0.0f : M;
-    float sum = 0.0f;
-    for (int i = tid; i < parts; i += kJoinThreads) sum += ex2_approx(a.part_ml[2 * part(i)] - ref) * a.part_ml[2 * part(i) + 1];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_red[1][warp] = sum;
-    const int v = tid % VEC, grp = tid / VEC;
-    float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = grp; i < parts; i += GROUPS) {
-        const size_t at = part(i);
-        const float f = ex2_approx(a.part_ml[2 * at] - ref);
-        const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
-        o4.x += f * x.x; o4.y += f * x.y; o4.z += f * x.z; o4.w += f * x.w;
-    }
-    s_o[grp][v] = o4;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kJoinThreads / 32; ++x) sum += s_red[1][x];
-    if (tid < VEC) {
-        o4 = s_o[0][tid];
-#pragma unroll
-        for (int x = 1; x < GROUPS; ++x) {
-            const float4 y = s_o[x][tid];
-            o4.x += y.x; o4.y += y.y; o4.z += y.z; o4.w += y.w;
+    // nothing of this row is this block's (block 0 always goes on to the wait)
+    if (blockIdx.y > 0 && blockIdx.y >= a.G && blockIdx.y * (kJoinThreads * 4) >= len) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (len == 0) {
+        for (int i = blockIdx.y * (kJoinThreads * 2) + tid * 2; i < a.G * D; i += gridDim.y * (kJoinThreads * 2)) {
+            store_out(a, head0 * D + i, 0.0f, 0.0f);
+            if (i % D == 0) a.L[head0 + i / D] = -INFINITY;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        store_out(a, head * D + tid * 4, o4.x * inv, o4.y * inv);
-        store_out(a, head * D + tid * 4 + 2, o4.z * inv, o4.w * inv);
-        if (tid == 0) {
-            a.L[head] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
-            if (a.row_ml) {
-                a.row_ml[2 * head] = M;
-                a.row_ml[2 * head + 1] = sum;
+        return;
+    }
+    const int runs = runs_of(a, total);
+    // the four tokens of this thread
+    const int t = (blockIdx.y * kJoinThreads + tid) * 4;
+    float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int h0 = 0; h0 < a.G; h0 += kJoinHeads) {
+        const int n = min(kJoinHeads, a.G - h0);
+        // M and l of every head, a warp each
+        for (int i = warp; i < n; i += WARPS) {
+            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
+            const long long p0 = lo + (static_cast<long long>(hk) * a.chunks + ch) * tiles;
+            const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
+            float M, sum;
+            if (c0 == c1) {
+                M = sum = 0.0f;
+                if (a.row_ml) {
+                    M = a.row_ml[2 * (head0 + h)];
+                    sum = a.row_ml[2 * (head0 + h) + 1];
+                    if (M == -INFINITY) M = 0.0f;
+                }
+            } else {
+                // part of CTA c: place 1 of the first, place 0 of the others
+                auto part = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r; };
+                M = -INFINITY;
+                for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[2 * part(c)]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                const float ref = M == -INFINITY ? 0.0f : M;
+                sum = 0.0f;
+                for (int c = c0 + lane; c <= c1; c += 32) sum += ex2_approx(a.part_ml[2 * part(c)] - ref) * a.part_ml[2 * part(c) + 1];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0 && h % gridDim.y == blockIdx.y) a.L[head0 + h] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+                M = ref;
+            }
+            if (lane == 0) {
+                s_M[i] = M;
+                s_inv[i] = sum > 0.0f ? 1.0f / sum : 0.0f;
             }
         }
-    }
-}
-
-// ---- scores -----------------------------------------------------------------------------------
-// score[b][hk][t] += sum over the group's heads of 2^(logit - m) / l, from the logits that the main
-// kernel kept: one thread a token, heads in order.
-__global__ void __launch_bounds__(256) decode_score_kernel(const __grid_constant__ DecodeArgs a) {
-    const int bh = blockIdx.y, b = bh / a.c.H, hk = bh - b * a.c.H;
-    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-    const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
-    for (int t = blockIdx.x * 256 + threadIdx.x; t < len; t += gridDim.x * 256) {
-        float w = 0.0f;
-        for (int i = 0; i < a.G; ++i) {
-            const float m = __ldg(a.row_ml + 2 * (head0 + i)), l = __ldg(a.row_ml + 2 * (head0 + i) + 1);
-            const float x = __ldg(a.logits + (head0 + i) * a.c.cap + t);
-            if (l > 0.0f) w += ex2_approx(x - m) / l;
+        __syncthreads();
+        // this block's heads of the shared pairs
+        const int v = tid % VEC, grp = tid / VEC;
+        for (int i = 0; i < n; ++i) {
+            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
+            if (h % gridDim.y != blockIdx.y) continue;
+            const long long p0 = lo + (static_cast<long long>(hk) * a.chunks + ch) * tiles;
+            const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
+            if (c0 == c1) continue;
+            float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = c0 + grp; c <= c1; c += GROUPS) {
+                const size_t at = (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r;
+                const float f = ex2_approx(a.part_ml[2 * at] - s_M[i]);
+                const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
+                o4.x += f * x.x; o4.y += f * x.y; o4.z += f * x.z; o4.w += f * x.w;
+            }
+            s_o[grp][v] = o4;
+            __syncthreads();
+            if (tid < VEC) {
+                o4 = s_o[0][tid];
+#pragma unroll
+                for (int x = 1; x < GROUPS; ++x) {
+                    const float4 y = s_o[x][tid];
+                    o4.x += y.x; o4.y += y.y; o4.z += y.z; o4.w += y.w;
+                }
+                const float inv = s_inv[i];
+                store_out(a, (head0 + h) * D + tid * 4, o4.x * inv, o4.y * inv);
+                store_out(a, (head0 + h) * D + tid * 4 + 2, o4.z * inv, o4.w * inv);
+            }
+            __syncthreads();
         }
-        a.c.score[static_cast<size_t>(bh) * a.c.cap + t] += w;
+        if (a.logits && t < len) {
+            const float *x = a.logits + (head0 + h0) * a.c.cap + t;
+            for (int i = 0; i < n; ++i) {
+                const float4 y = *reinterpret_cast<const float4 *>(x + static_cast<size_t>(i) * a.c.cap);
+                const float M = s_M[i], inv = s_inv[i];
+                add.x += ex2_approx(y.x - M) * inv;
+                add.y += ex2_approx(y.y - M) * inv;
+                add.z += ex2_approx(y.z - M) * inv;
+                add.w += ex2_approx(y.w - M) * inv;
+            }
+        }
+        __syncthreads();
+    }
+    if (a.logits && t < len) {
+        float *to = a.c.score + static_cast<size_t>(bh) * a.c.cap + t;
+        if (t + 4 <= len) {
+            float4 y = *reinterpret_cast<const float4 *>(to);
+            y.x += add.x; y.y += add.y; y.z += add.z; y.w += add.w;
+            *reinterpret_cast<float4 *>(to) = y;
+        } else {                                     // slots past the end keep what they hold
+            to[0] += add.x;
+            if (t + 1 < len) to[1] += add.y;
+            if (t + 2 < len) to[2] += add.z;
+        }
     }
 }
 
@@ -749,7 +830,7 @@ unsigned int take_decode_error() {
 
 // ---- host -------------------------------------------------------------------------------------
 struct DecodePlan {
-    int mr, chunks, ctas;
+    int mr, chunks, ctas, tile;
     size_t off_ml, off_rows, off_logits, bytes;
 };
 
@@ -760,8 +841,9 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     p.chunks = (G + p.mr - 1) / p.mr;
     const int row = c.d * (c.kind == SAGE_KV_16 ? 2 : 1);
     // one resident wave; never more CTAs than there can be tiles
-    long long n = kSMs * (row == 256 ? 2 : 3);
-    const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + kTile - 1) / kTile);
+    p.tile = decode_tile(row);
+    long long n = kSMs * (row == 64 ? 3 : 2);
+    const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + p.tile - 1) / p.tile);
     if (n > tiles) n = tiles;
     p.ctas = static_cast<int>(n);
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
@@ -785,19 +867,30 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
 template <int D, int KIND, int MR>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     using S = DecodeShape<D, KIND>;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KIND, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    // the kernel's shared-memory limit, raised once a device (again is harmless)
+    static bool raised[16] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 16 || !raised[dev]) {
+        e = cudaFuncSetAttribute(decode_kernel<D, KIND, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 16) raised[dev] = true;
+    }
     decode_kernel<D, KIND, MR><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const unsigned pairs = static_cast<unsigned>(a.c.B) * a.c.H * a.chunks;
-    decode_join_kernel<D, MR><<<dim3(pairs, a.G < MR ? a.G : MR), kJoinThreads, 0, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !a.logits) return e;
-    const unsigned rows = static_cast<unsigned>(a.c.B) * a.c.H;
-    const unsigned x = (a.c.cap + 1023) / 1024;
-    decode_score_kernel<<<dim3(x, rows), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    const int y = a.logits ? (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : a.G < 16 ? a.G : 16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, y);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR>, a);
 }
 
 template <int D, int KIND>
@@ -836,7 +929,7 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
     DecodeArgs a;
     a.c = kv_view(*c);
     a.Q = Q; a.O = O; a.L = L; a.lens = lens;
-    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas;
+    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas; a.tile = p.tile; a.tile_shift = p.tile == 64 ? 6 : 7;
     a.bf16 = c->dtype == SAGE_BF16;
     a.sl2 = scale_log2(c->d);
     a.part_O = reinterpret_cast<float *>(w);

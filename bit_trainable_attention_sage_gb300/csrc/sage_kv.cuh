@@ -15,12 +15,20 @@ struct KvView {
     float *score;
     int *pos;
     int B, H, page, pages, max_pages, cap;   // cap = max_pages * page
+    uint32_t page_mul, page_shift;           // s / page = s * page_mul >> page_shift for s < 2^30
 };
+
+// s / page without a division: page_mul = ceil(2^(30 + k) / page) with 2^k >= page exceeds the
+// quotient by less than 2^k / page / 2^(30 + k) of s, so by less than 1 / page for s < 2^30: the
+// floor is exact.
+__device__ __forceinline__ int kv_page_of(const KvView &c, int s) {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(s)) * c.page_mul) >> c.page_shift);
+}
 
 // The page that holds slot s of sequence b, or -1 (and the error word raised) where the table's
 // entry is not a page of the pool.  s must be in [0, cap).
 __device__ __forceinline__ int kv_page(const KvView &c, int b, int s, unsigned int *err) {
-    const int p = __ldg(c.table + static_cast<size_t>(b) * c.max_pages + s / c.page);
+    const int p = __ldg(c.table + static_cast<size_t>(b) * c.max_pages + kv_page_of(c, s));
     if (static_cast<unsigned>(p) < static_cast<unsigned>(c.pages)) return p;
     atomicOr(err, 1u);
     return -1;
@@ -28,7 +36,7 @@ __device__ __forceinline__ int kv_page(const KvView &c, int b, int s, unsigned i
 
 // Row (of d elements) of slot s of kv head h in page p: 64-bit, pools exceed 2^31 elements.
 __device__ __forceinline__ size_t kv_row(const KvView &c, int p, int h, int s) {
-    return (static_cast<size_t>(p) * c.H + h) * c.page + s % c.page;
+    return (static_cast<size_t>(p) * c.H + h) * c.page + (s - kv_page_of(c, s) * c.page);
 }
 
 // lens[b], held to [0, cap] (and the error word raised where it is not).
@@ -40,8 +48,11 @@ __device__ __forceinline__ int kv_len(const KvView &c, const int *lens, int b, u
 }
 
 inline KvView kv_view(const sage_kv &c) {
+    uint32_t k = 0;
+    while ((1ull << k) < static_cast<uint64_t>(c.page)) ++k;
+    const uint64_t mul = ((1ull << (30 + k)) + c.page - 1) / c.page;     // at most 2^31
     return KvView{c.K, c.V, c.sK, c.sV, c.table, c.score, c.pos, c.B, c.H, c.page, c.pages,
-                  c.max_pages, c.max_pages * c.page};
+                  c.max_pages, c.max_pages * c.page, static_cast<uint32_t>(mul), 30 + k};
 }
 
 inline bool misaligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }

@@ -38,30 +38,50 @@ class SageRopeParams(ctypes.Structure):
 
 def _need(t: torch.Tensor, what: str, dtype, shape, device):
     """A contiguous tensor of this type and shape on this device."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: must be a contiguous CUDA tensor on {device}")
+    raise ValueError(f"{what}: must be a contiguous tensor on {device}")
+
+
+def _workspace_ok(ws, device):
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"workspace: must be a contiguous tensor on {device}")
+
+
+def _cuda(device):
+    if device.type != "cuda":
+        raise ValueError(f"SageBwd tensors must be CUDA tensors, these are on {device}")
+
+
+def _elsewhere(stream, device) -> bool:
+    """Whether the call has to change the current stream or device first (with _on)."""
+    return stream is not None or torch.cuda.current_device() != device.index
 
 
 @contextlib.contextmanager
 def _on(stream, device):
     """Makes ``stream`` (or the device's current stream) current, so that the launch and what is
-    allocated for it belong to the same stream and device; yields its handle."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    elif torch.cuda.current_device() != device.index:
+    allocated for it belong to the same stream and device."""
+    if stream is None:
         with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
+            yield
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     else:
-        yield torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _current(device) -> int:
+    """Handle of the device's current stream.  torch.cuda.current_stream() builds an object for it
+    (3 us on the GB300's host cores, as long as a launch); this returns the handle alone (0.1 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 # ---- rotary positions -----------------------------------------------------------------------
@@ -102,31 +122,35 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
     """Rotary positions of Q (B,H,N,d) and K (B,Hk,N,d, or None), fp16, bf16 or float32.
     ``positions`` (axes,B,N) int32, or (axes,1,N) for every sequence the same.  ``inverse`` turns
     back: the gradient.  ``out`` (Qo, Ko) may be (Q, K).  Returns (Qo, Ko)."""
-    B, H, N, d = Q.shape
-    dev = Q.device
-    if Q.dtype not in _DTYPES:
-        raise TypeError(f"sage_rope takes fp16, bf16 or float32 tensors, got {Q.dtype}")
-    _need(Q, "Q", Q.dtype, Q.shape, dev)
+    shape, dtype, dev = Q.shape, Q.dtype, Q.device
+    B, H, N, d = shape
+    if dtype not in _DTYPES:
+        raise TypeError(f"sage_rope takes fp16, bf16 or float32 tensors, got {dtype}")
+    _cuda(dev)
+    _need(Q, "Q", dtype, shape, dev)
     if d != rope.d:
         raise ValueError(f"Q has {d} channels, the rope {rope.d}")
     Hk = 0
     if K is not None:
         Hk = K.shape[1]
-        _need(K, "K", Q.dtype, (B, Hk, N, d), dev)
+        _need(K, "K", dtype, (B, Hk, N, d), dev)
     pb = 1 if positions.dim() == 3 and positions.shape[1] == 1 else B
     _need(positions, "positions", torch.int32, (rope.axes, pb, N), dev)
-    with _on(stream, dev) as st:
-        if out is None:
-            Qo, Ko = torch.empty_like(Q), None if K is None else torch.empty_like(K)
-        else:
-            Qo, Ko = out
-            _need(Qo, "out[0]", Q.dtype, Q.shape, dev)
-            if K is not None:
-                _need(Ko, "out[1]", K.dtype, K.shape, dev)
-        p = SageRopeParams(B, H, Hk, N, d, _DTYPES[Q.dtype], rope.axes, pb, rope.rotary, rope.interleaved, bool(inverse),
-                           rope._sections, rope._freq)
-        _check("sage_rope", lib().sage_rope(ctypes.byref(p), Q.data_ptr(), None if K is None else K.data_ptr(),
-                                            positions.data_ptr(), Qo.data_ptr(), None if K is None else Ko.data_ptr(), st))
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return sage_rope(Q, K, positions, rope, inverse=inverse, out=out)
+    if out is None:
+        Qo, Ko = torch.empty_like(Q), None if K is None else torch.empty_like(K)
+    else:
+        Qo, Ko = out
+        _need(Qo, "out[0]", dtype, shape, dev)
+        if K is not None:
+            _need(Ko, "out[1]", dtype, K.shape, dev)
+    p = SageRopeParams(B, H, Hk, N, d, _DTYPES[dtype], rope.axes, pb, rope.rotary, rope.interleaved, bool(inverse),
+                       rope._sections, rope._freq)
+    st = lib().sage_rope(ctypes.byref(p), Q.data_ptr(), None if K is None else K.data_ptr(), positions.data_ptr(),
+                         Qo.data_ptr(), None if K is None else Ko.data_ptr(), _current(dev))
+    _check("sage_rope", st)
     return Qo, Ko
 
 
@@ -148,6 +172,7 @@ class KvCache:
         pages, H, page, d = K.shape
         B, max_pages = table.shape
         dev = K.device
+        _cuda(dev)
         _need(K, "K", K.dtype, K.shape, dev)
         _need(V, "V", K.dtype, K.shape, dev)
         _need(table, "table", torch.int32, table.shape, dev)
@@ -198,11 +223,11 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
     """Writes tokens 0 .. count[b] - 1 (None: all T) of K, V (B,H,T,d) to slots start[b] + t of the
     cache, in its form.  ``mu`` (B,H,d) float32 (8-bit caches): K-smoothing, codes of K - mu.
     ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot)."""
-    B, H, T, d = K.shape
-    dev = cache.device
+    shape, dev = K.shape, cache.device
+    B, H, T, d = shape
     c = cache._struct(K, "K")
     _need(K, "K", K.dtype, (cache.B, cache.H, T, cache.d), dev)
-    _need(V, "V", K.dtype, K.shape, dev)
+    _need(V, "V", K.dtype, shape, dev)
     _need(start, "start", torch.int32, (B,), dev)
     if count is not None:
         _need(count, "count", torch.int32, (B,), dev)
@@ -210,9 +235,11 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
         _need(mu, "mu", torch.float32, (B, H, d), dev)
     if pos is not None:
         _need(pos, "pos", torch.int32, (B,), dev)
-    with _on(stream, dev) as st:
-        _check("sage_kv_append", lib().sage_kv_append(c, K.data_ptr(), V.data_ptr(), T, start.data_ptr(), _ptr(count),
-                                                      _ptr(mu), _ptr(pos), st))
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return sage_kv_append(cache, K, V, start, count=count, mu=mu, pos=pos)
+    st = lib().sage_kv_append(c, K.data_ptr(), V.data_ptr(), T, start.data_ptr(), _ptr(count), _ptr(mu), _ptr(pos), _current(dev))
+    _check("sage_kv_append", st)
 
 
 def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, score: bool = False, out=None, lse=None,
@@ -220,26 +247,30 @@ def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, sco
     """Attention of one new token a sequence, Q (B,Hq,1,d), over its lens[b] cached slots; Hq is a
     multiple of the cache's heads.  ``score`` adds the attention weights to cache.score.
     Returns (O (B,Hq,1,d) in Q's type, L (B,Hq,1) float32); a sequence of no slots gives 0 and -inf."""
-    dev = cache.device
+    shape, dtype, dev = Q.shape, Q.dtype, cache.device
     c = cache._struct(Q, "Q")
-    Hq = Q.shape[1]
-    _need(Q, "Q", Q.dtype, (cache.B, Hq, 1, cache.d), dev)
+    Hq = shape[1]
+    _need(Q, "Q", dtype, (cache.B, Hq, 1, cache.d), dev)
     _need(lens, "lens", torch.int32, (cache.B,), dev)
     if score and cache.score is None:
         raise ValueError("score=True needs a cache with score")
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return sage_attn_decode(Q, cache, lens, score=score, out=out, lse=lse, workspace=workspace)
     nbytes = cache._bytes.get((Hq, score))
     if nbytes is None:
         nbytes = cache._bytes[Hq, score] = lib().sage_decode_workspace_bytes(c, Hq, int(score))
-    with _on(stream, dev) as st:
-        if out is not None:
-            _need(out, "out", Q.dtype, Q.shape, dev)
-        if lse is not None:
-            _need(lse, "lse", torch.float32, (cache.B, Hq, 1), dev)
-        O = torch.empty_like(Q) if out is None else out
-        L = torch.empty((cache.B, Hq, 1), dtype=torch.float32, device=dev) if lse is None else lse
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        _check("sage_attn_decode", lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(),
-                                                          int(score), ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    if out is not None:
+        _need(out, "out", dtype, shape, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (cache.B, Hq, 1), dev)
+    _workspace_ok(workspace, dev)
+    O = torch.empty_like(Q) if out is None else out
+    L = torch.empty((cache.B, Hq, 1), dtype=torch.float32, device=dev) if lse is None else lse
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    st = lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(), int(score), ws.data_ptr(),
+                                nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
+    _check("sage_attn_decode", st)
     return O, L
 
 
@@ -261,11 +292,15 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
     nbytes = cache._bytes.get(budget)
     if nbytes is None:
         nbytes = cache._bytes[budget] = lib().sage_evict_workspace_bytes(c, budget)
-    with _on(stream, dev) as st:
-        if out is not None:
-            _need(out, "out", torch.int32, (cache.B,), dev)
-        new = torch.empty_like(lens) if out is None else out
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        _check("sage_kv_evict", lib().sage_kv_evict(c, lens.data_ptr(), seen.data_ptr(), budget, recent, new.data_ptr(),
-                                                    ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return sage_kv_evict(cache, lens, seen, budget=budget, recent=recent, out=out, workspace=workspace)
+    if out is not None:
+        _need(out, "out", torch.int32, (cache.B,), dev)
+    _workspace_ok(workspace, dev)
+    new = torch.empty_like(lens) if out is None else out
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    st = lib().sage_kv_evict(c, lens.data_ptr(), seen.data_ptr(), budget, recent, new.data_ptr(), ws.data_ptr(),
+                             nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
+    _check("sage_kv_evict", st)
     return new
