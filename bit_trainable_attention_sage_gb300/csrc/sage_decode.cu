@@ -867,16 +867,9 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
 template <int D, int KIND, int MR>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     using S = DecodeShape<D, KIND>;
-    // the kernel's shared-memory limit, raised once a device (again is harmless)
     static bool raised[16] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR>), S::SMEM, raised);
     if (e != cudaSuccess) return e;
-    if (dev >= 16 || !raised[dev]) {
-        e = cudaFuncSetAttribute(decode_kernel<D, KIND, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-        if (e != cudaSuccess) return e;
-        if (dev < 16) raised[dev] = true;
-    }
     decode_kernel<D, KIND, MR><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -41,33 +41,67 @@ __device__ __forceinline__ void unpack16(const uint4 u, float (&v)[8]) {
     }
 }
 
-// One row's 8 values of a lane -> 8 codes, and the row's scale.
-template <int KIND, int LANES>
-__device__ __forceinline__ uint2 kv_codes(const float (&x)[8], float *delta_out) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+// fl32(x / delta) for two values, r = fl32(1 / delta): Markstein's correction of a quotient
+// ("Computation of elementary functions on the IBM RISC System/6000 processor", 1990), twice.  With
+// significands x, delta in [1, 2) and u = 2^-24, r is off by at most delta u / 2 of itself and
+// q0 = fl(x r) by at most 1.5 units in the last place (ulp); the residual x - q delta is exact, so each
+// correction leaves the quotient times its error times r's, and a rounding.  After the first the
+// error is below 0.5 ulp (1 + 3 u); the second then rounds a value that is within
+// 0.5 (1 + 3 u) delta u / 2 ulp of x / delta, and x / delta is no nearer than u 2^24 / delta * u ulp to a
+// value half way between two floats (25 bits times delta's 24 never make x's 24): less for every
+// delta < 2, so it rounds as x / delta does.  Scales where a residual could underflow take the
+// division.
+__device__ __forceinline__ f2 quotient2(f2 x, float delta, float r) {
+    const f2 d{-delta, -delta}, rr{r, r};
+    f2 q = mul2(x, rr);
+    q = fma2(fma2(q, d, x), rr, q);
+    return fma2(fma2(q, d, x), rr, q);
+}
+
+// One row's 8 values of a lane, and the largest of the row -> 8 codes and the row's scale.
+template <int KIND>
+__device__ __forceinline__ uint2 kv_codes(const float (&x)[8], float m, float *delta_out) {
     const float delta = __fdiv_rn(m, KIND == SAGE_KV_INT8 ? 127.0f : 448.0f);
     *delta_out = delta;
-    if (delta == 0.0f) return make_uint2(0u, 0u);
-    uint32_t w[2] = {0u, 0u};
+    f2 y[4];
+    if (delta >= 0x1p-90f && delta <= 0x1p90f) {
+        const float r = __frcp_rn(delta);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = quotient2(f2{x[2 * i], x[2 * i + 1]}, delta, r);
+    } else if (delta == 0.0f) {
+        return make_uint2(0u, 0u);
+    } else {
+        // a subnormal delta can be rounded so far down that the quotient exceeds 127 (E4M3 saturates)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i].x = fminf(fmaxf(__fdiv_rn(x[2 * i], delta), -448.0f), 448.0f);
+            y[i].y = fminf(fmaxf(__fdiv_rn(x[2 * i + 1], delta), -448.0f), 448.0f);
+            if (KIND == SAGE_KV_INT8) {
+                y[i].x = fminf(fmaxf(y[i].x, -127.0f), 127.0f);
+                y[i].y = fminf(fmaxf(y[i].y, -127.0f), 127.0f);
+            }
+        }
+    }
+    uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if constexpr (KIND == SAGE_KV_INT8) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                int q = __float2int_rn(__fdiv_rn(x[4 * i + j], delta));
-                q = max(-127, min(127, q));                 // a subnormal delta can round down
-                w[i] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * j);
-            }
+            // y + 1.5 2^23 holds the nearest integer (ties to even) in its low bits
+            const f2 magic{12582912.0f, 12582912.0f};
+            const f2 a = add2(y[2 * i], magic), b = add2(y[2 * i + 1], magic);
+            const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+            const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+            w[i] = __byte_perm(lo, hi, 0x5410);
         } else {
-            w[i] = e4m3x2(__fdiv_rn(x[4 * i], delta), __fdiv_rn(x[4 * i + 1], delta)) |
-                   static_cast<uint32_t>(e4m3x2(__fdiv_rn(x[4 * i + 2], delta), __fdiv_rn(x[4 * i + 3], delta))) << 16;
+            w[i] = e4m3x2(y[2 * i].x, y[2 * i].y) | static_cast<uint32_t>(e4m3x2(y[2 * i + 1].x, y[2 * i + 1].y)) << 16;
         }
     }
     return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float largest8(const float (&x)[8]) {
+    return fmaxf(max3f(max3f(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]), fabsf(x[4])),
+                 max3f(fabsf(x[5]), fabsf(x[6]), fabsf(x[7])));
 }
 
 // grid: (row groups of a head, B * H).  ROWS rows of each lane group are loaded before any is
@@ -139,7 +173,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
             unpack16<T>(v[r], y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], mu[i]);
-            const uint2 ck = kv_codes<KIND, LANES>(x, &dk), cv = kv_codes<KIND, LANES>(y, &dv);
+            float mk = largest8(x), mv = largest8(y);
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) {
+                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            }
+            const uint2 ck = kv_codes<KIND>(x, mk, &dk), cv = kv_codes<KIND>(y, mv, &dv);
             if (row[r] >= 0) {
                 reinterpret_cast<uint2 *>(a.c.K)[row[r] * LANES + lane] = ck;
                 reinterpret_cast<uint2 *>(a.c.V)[row[r] * LANES + lane] = cv;
@@ -183,24 +223,30 @@ static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st
 // eviction
 //
 // Which slots stay is a selection, not a sort: the budget-th largest key of a row of n keys by
-// radix selection (four passes of 8 bits), then one pass in slot order that takes what is above it
+// radix selection (11, 11 and 10 bits), then one pass in slot order that takes what is above it
 // and the first of what is equal.  Only stayers in slots >= budget move, into the freed slots
 // below: sources and destinations are disjoint, so the moves need no order among them, and a
 // cache that is cut back by a few tokens moves a few rows instead of being compacted.
 //
-// kv_select_kernel: one CTA a (sequence, kv head); reads score and pos, writes the pairs
-// (destination, source) to the workspace.  kv_move_kernel: the moves, spread over the GPU.
+// One cluster of C CTAs a (sequence, kv head), each with a contiguous C-th of the slots: scores and
+// positions are read once, the keys stay in shared memory (CACHED; rows of more than
+// 8 * 48 K slots read them again each pass), histograms and counts are added up over the cluster
+// through distributed shared memory, and the same CTAs then move the rows.  One launch, and with
+// C up to 8 a few long rows still use many SMs.
 // ---------------------------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelMaxCluster = 8;
+constexpr int kSelMaxKeys = 48 * 1024;       // of a CTA in shared memory
 
 struct EvictArgs {
     KvView c;
     const int *lens, *seen;
     int *lens_out;
-    int *moves;          // (B*H): rows to move
     int *dst, *src;      // (B*H, max_moves)
     int budget, recent, max_moves;
+    int cluster;
 };
 
 // Larger key = stays longer.  Recent tokens above every score; scores in the order of the reals
@@ -212,157 +258,279 @@ __device__ __forceinline__ uint32_t evict_key(float s, bool recent) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);      // at most 0xFF800000 (+inf)
 }
 
-struct KeyReader {
-    const float *score;
-    const int *pos;
-    long long newest;    // positions from here on are recent
-    __device__ __forceinline__ uint32_t operator()(int s) const {
-        return evict_key(__ldg(score + s), __ldg(pos + s) >= newest);
-    }
-};
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the word at this address of CTA `rank`'s shared memory
+__device__ __forceinline__ int cluster_word(const int *p, int rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int wcount[2][kSelWarps];
-    __shared__ int s_digit, s_above;
-    const int bh = blockIdx.x, b = bh / a.c.H;
+// One row moved by ROW_BYTES / 16 lanes.
+template <int ROW_BYTES>
+__device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, int h, int first, int step, int m, int lane) {
+    constexpr int CHUNKS = ROW_BYTES / 16, UNROLL = 2;
+    const size_t list = static_cast<size_t>(bh) * a.max_moves, base = static_cast<size_t>(bh) * a.c.cap;
+    uint4 *K = static_cast<uint4 *>(a.c.K), *V = static_cast<uint4 *>(a.c.V);
+    for (int i0 = first; i0 < m; i0 += step * UNROLL) {
+        size_t rd[UNROLL], rs[UNROLL];
+        int d[UNROLL], s[UNROLL];
+        bool ok[UNROLL];
+        uint4 k[UNROLL], v[UNROLL];
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x) {
+            const int i = i0 + x * step;
+            ok[x] = i < m;
+            d[x] = ok[x] ? a.dst[list + i] : 0;
+            s[x] = ok[x] ? a.src[list + i] : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x) {
+            const int pd = ok[x] ? kv_page(a.c, b, d[x], &g_kv_err) : -1, ps = ok[x] ? kv_page(a.c, b, s[x], &g_kv_err) : -1;
+            ok[x] = pd >= 0 && ps >= 0;
+            rd[x] = ok[x] ? kv_row(a.c, pd, h, d[x]) : 0;
+            rs[x] = ok[x] ? kv_row(a.c, ps, h, s[x]) : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x)
+            if (ok[x]) {
+                k[x] = K[rs[x] * CHUNKS + lane];
+                v[x] = V[rs[x] * CHUNKS + lane];
+            }
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x)
+            if (ok[x]) {
+                K[rd[x] * CHUNKS + lane] = k[x];
+                V[rd[x] * CHUNKS + lane] = v[x];
+                if (lane == 0) {
+                    a.c.score[base + d[x]] = a.c.score[base + s[x]];
+                    a.c.pos[base + d[x]] = a.c.pos[base + s[x]];
+                    if (a.c.sK) {
+                        a.c.sK[rd[x]] = a.c.sK[rs[x]];
+                        a.c.sV[rd[x]] = a.c.sV[rs[x]];
+                    }
+                }
+            }
+    }
+}
+
+// grid: (cluster, B * H)
+template <bool CACHED, int ROW_BYTES>
+__global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
+    extern __shared__ uint32_t s_key[];
+    __shared__ int hist[3][kSelBins];
+    __shared__ int s_warp[2][kSelWarps];
+    __shared__ int s_count[4];                   // of this CTA, read by the others: equal keys; freed, movers
+    __shared__ int s_digit, s_above, s_here;
+    const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H, rank = blockIdx.x;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int n = kv_len(a.c, a.lens, b, &g_kv_err);
-    if (tid == 0 && bh - b * a.c.H == 0) a.lens_out[b] = min(n, a.budget);
-    if (n <= a.budget) {
-        if (tid == 0) a.moves[bh] = 0;
-        return;
-    }
+    if (tid == 0 && rank == 0 && h == 0) a.lens_out[b] = min(n, a.budget);
+    if (n <= a.budget) return;                   // the whole cluster alike
     const size_t base = static_cast<size_t>(bh) * a.c.cap;
-    const KeyReader key{a.c.score + base, a.c.pos + base, static_cast<long long>(__ldg(a.seen + b)) - a.recent};
-    // the budget-th largest key: `prefix` its leading digits, `need` its rank among the keys that share them
-    uint32_t prefix = 0;
-    int need = a.budget;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-        for (int s = tid; s < n; s += kSelThreads) {
-            const uint32_t k = key(s);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    const long long newest = static_cast<long long>(__ldg(a.seen + b)) - a.recent;   // recent from here on
+    // this CTA's slots [lo, lo + len), a warp's contiguous: slot lo + (warp * its + i) * 32 + lane
+    const int seg = ((n + a.cluster - 1) / a.cluster + kSelThreads - 1) / kSelThreads * kSelThreads;
+    const int lo = min(n, rank * seg), len = min(n - lo, seg), its = seg / kSelThreads;
+    const int mine = warp * its * 32 + lane;
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    // score and pos are read with plain loads: the moves below write them (after every read here)
+    auto key = [&](int i) -> uint32_t {
+        const int s = mine + i * 32;
+        if constexpr (CACHED) return s_key[s];
+        else return evict_key(a.c.score[base + lo + s], a.c.pos[base + lo + s] >= newest);
+    };
+    // first digit: 11 bits.  Recent tokens share one key: counted by the warp.
+    for (int i = 0; i < its; ++i) {
+        const int s = mine + i * 32;
+        uint32_t k = 0;
+        const bool in = s < len;
+        if (in) {
+            k = evict_key(a.c.score[base + lo + s], a.c.pos[base + lo + s] >= newest);
+            if constexpr (CACHED) s_key[s] = k;
         }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8 l .. 248 - 8 l, in descending order
-            int c[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = hist[255 - 8 * lane - i];
-                sum += c[i];
-            }
-            int incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
-            }
-            int above = incl - sum;
-            if (above < need && need <= incl) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (above < need && need <= above + c[i]) {
-                        s_digit = 255 - 8 * lane - i;
-                        s_above = above;
-                    }
-                    above += c[i];
+        const uint32_t top = __ballot_sync(0xffffffffu, in && k == 0xFFFFFFFFu);
+        if (in && k != 0xFFFFFFFFu) atomicAdd(&hist[0][k >> 21], 1);
+        if (lane == 0 && top) atomicAdd(&hist[0][kSelBins - 1], __popc(top));
+    }
+    // the budget-th largest key: `T` its leading digits, `need` its rank among the keys that share them
+    uint32_t T = 0;
+    int need = a.budget, equal = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+        if (pass > 0) {
+            const uint32_t mask = 0xFFFFFFFFu << (pass == 1 ? 21 : 10);
+            for (int i = 0; i < its; ++i) {
+                const int s = mine + i * 32;
+                const uint32_t k = s < len ? key(i) : ~T;                 // ~T shares no digit
+                const bool in = s < len && (k & mask) == T;
+                // ties: equal keys of a warp are added once
+                const uint32_t same = __ballot_sync(0xffffffffu, in);
+                if (same) {
+                    const uint32_t leader = __shfl_sync(0xffffffffu, k, __ffs(same) - 1);
+                    const uint32_t alike = __ballot_sync(0xffffffffu, in && k == leader);
+                    if (in && k != leader) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1);
+                    if (lane == __ffs(same) - 1) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], __popc(alike));
                 }
             }
         }
+        if (a.cluster > 1) cluster_sync();
+        else __syncthreads();
+        // thread t holds digits bins - 1 - 2t and bins - 2 - 2t, in descending order
+        int c[2] = {0, 0};
+        const int d0 = bins - 1 - 2 * tid;
+        if (d0 > 0) {
+            for (int r = 0; r < a.cluster; ++r) {
+                c[0] += a.cluster > 1 ? cluster_word(&hist[pass][d0], r) : hist[pass][d0];
+                c[1] += a.cluster > 1 ? cluster_word(&hist[pass][d0 - 1], r) : hist[pass][d0 - 1];
+            }
+        }
+        int incl = c[0] + c[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s_warp[0][warp] = incl;
         __syncthreads();
-        prefix |= static_cast<uint32_t>(s_digit) << shift;
+        int above = incl - c[0] - c[1];
+        for (int w = 0; w < warp; ++w) above += s_warp[0][w];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (above < need && need <= above + c[i]) {
+                s_digit = d0 - i;
+                s_above = above;
+                s_here = c[i];
+            }
+            above += c[i];
+        }
+        __syncthreads();
+        T |= static_cast<uint32_t>(s_digit) << shift;
         need -= s_above;
+        equal = s_here;
         __syncthreads();
     }
-    // slot order: warp w owns slots [w * span, (w + 1) * span), span a multiple of 32
-    const uint32_t T = prefix;
-    const int span = ((n + kSelThreads - 1) / kSelThreads) * 32;
-    const int s0 = min(n, warp * span), s1 = min(n, s0 + span);
-    int eq = 0;
-    for (int s = s0; s < s1; s += 32) {
-        const bool in = s + lane < s1;
-        eq += __popc(__ballot_sync(0xffffffffu, in && key(s + lane) == T));
+    // Of the `equal` keys equal to T, the first `need` in slot order stay.  How many lie before this
+    // warp's slots matters only when not all of them do.
+    int eq0 = 0;
+    if (equal > need) {
+        int eq = 0;
+        for (int i = 0; i < its; ++i) eq += __popc(__ballot_sync(0xffffffffu, mine + i * 32 < len && key(i) == T));
+        if (lane == 0) s_warp[0][warp] = eq;
+        __syncthreads();
+        if (tid == 0) {
+            int sum = 0;
+            for (int w = 0; w < kSelWarps; ++w) sum += s_warp[0][w];
+            s_count[0] = sum;
+        }
+        if (a.cluster > 1) cluster_sync();
+        else __syncthreads();
+        for (int r = 0; r < rank; ++r) eq0 += cluster_word(&s_count[0], r);
+        for (int w = 0; w < warp; ++w) eq0 += s_warp[0][w];
+        __syncthreads();
     }
-    if (lane == 0) wcount[0][warp] = eq;
-    __syncthreads();
-    int eq0 = 0;                                      // equal keys in the slots before this warp's
-    for (int w = 0; w < warp; ++w) eq0 += wcount[0][w];
-    __syncthreads();
     // freed slots below the budget and stayers from it on, counted, then numbered
     const uint32_t before = (1u << lane) - 1u;
-    int at[2] = {0, 0};
+    int at[2] = {0, 0}, moves = 0;
     for (int pass = 0; pass < 2; ++pass) {
         int e = eq0, freed = at[0], moved = at[1];
-        for (int s = s0; s < s1; s += 32) {
-            const bool in = s + lane < s1;
-            const uint32_t k = in ? key(s + lane) : 0u;
+        for (int i = 0; i < its; ++i) {
+            const int s = mine + i * 32, slot = lo + s;
+            const bool in = s < len;
+            const uint32_t k = in ? key(i) : 0u;
             const bool iseq = in && k == T;
             const uint32_t beq = __ballot_sync(0xffffffffu, iseq);
-            const bool stays = in && (k > T || (iseq && e + __popc(beq & before) < need));
+            const bool stays = in && (k > T || (iseq && (equal <= need || e + __popc(beq & before) < need)));
             e += __popc(beq);
-            const bool f = in && !stays && s + lane < a.budget, m = stays && s + lane >= a.budget;
+            const bool f = in && !stays && slot < a.budget, m = stays && slot >= a.budget;
             const uint32_t bf = __ballot_sync(0xffffffffu, f), bm = __ballot_sync(0xffffffffu, m);
             if (pass == 1) {
                 const size_t o = static_cast<size_t>(bh) * a.max_moves;
-                if (f) a.dst[o + freed + __popc(bf & before)] = s + lane;
-                if (m) a.src[o + moved + __popc(bm & before)] = s + lane;
+                if (f) a.dst[o + freed + __popc(bf & before)] = slot;
+                if (m) a.src[o + moved + __popc(bm & before)] = slot;
             }
             freed += __popc(bf);
             moved += __popc(bm);
         }
         if (pass == 0) {
             if (lane == 0) {
-                wcount[0][warp] = freed;
-                wcount[1][warp] = moved;
+                s_warp[0][warp] = freed;
+                s_warp[1][warp] = moved;
             }
             __syncthreads();
+            if (tid < 2) {
+                int sum = 0;
+                for (int w = 0; w < kSelWarps; ++w) sum += s_warp[tid][w];
+                s_count[2 + tid] = sum;
+            }
+            if (a.cluster > 1) cluster_sync();
+            else __syncthreads();
+            for (int r = 0; r < a.cluster; ++r) {
+                const int f = cluster_word(&s_count[2], r), m = cluster_word(&s_count[3], r);
+                if (r < rank) {
+                    at[0] += f;
+                    at[1] += m;
+                }
+                moves += m;
+            }
             for (int w = 0; w < warp; ++w) {
-                at[0] += wcount[0][w];
-                at[1] += wcount[1][w];
+                at[0] += s_warp[0][w];
+                at[1] += s_warp[1][w];
             }
-            if (tid == kSelThreads - 1) a.moves[bh] = at[1] + wcount[1][warp];
         }
     }
-}
-
-// grid: (blocks a row, B * H); ROW_BYTES / 16 lanes a move.
-template <int ROW_BYTES>
-__global__ void __launch_bounds__(256) kv_move_kernel(const EvictArgs a) {
-    constexpr int CHUNKS = ROW_BYTES / 16;                   // 4, 8 or 16
-    constexpr int GROUPS = 256 / CHUNKS;
-    const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
-    const int m = a.moves[bh];
-    const int lane = threadIdx.x % CHUNKS;
-    for (int i = blockIdx.x * GROUPS + threadIdx.x / CHUNKS; i < m; i += gridDim.x * GROUPS) {
-        const size_t o = static_cast<size_t>(bh) * a.max_moves + i;
-        const int d = a.dst[o], s = a.src[o];
-        const int pd = kv_page(a.c, b, d, &g_kv_err), ps = kv_page(a.c, b, s, &g_kv_err);
-        if (pd < 0 || ps < 0) continue;
-        const size_t rd = kv_row(a.c, pd, h, d), rs = kv_row(a.c, ps, h, s);
-        uint4 *K = static_cast<uint4 *>(a.c.K), *V = static_cast<uint4 *>(a.c.V);
-        const uint4 k = K[rs * CHUNKS + lane], v = V[rs * CHUNKS + lane];
-        K[rd * CHUNKS + lane] = k;
-        V[rd * CHUNKS + lane] = v;
-        if (lane == 0) {
-            if (a.c.sK) {
-                a.c.sK[rd] = a.c.sK[rs];
-                a.c.sV[rd] = a.c.sV[rs];
-            }
-            const size_t base = static_cast<size_t>(bh) * a.c.cap;
-            a.c.score[base + d] = a.c.score[base + s];
-            a.c.pos[base + d] = a.c.pos[base + s];
-        }
-    }
+    // every CTA's part of the lists is written, every read of another's shared memory done
+    if (a.cluster > 1) cluster_sync();
+    else __syncthreads();
+    constexpr int CHUNKS = ROW_BYTES / 16, GROUPS = kSelThreads / CHUNKS;
+    evict_moves<ROW_BYTES>(a, bh, b, h, rank * GROUPS + tid / CHUNKS, a.cluster * GROUPS, moves, tid % CHUNKS);
 }
 
 static int evict_max_moves(const sage_kv &c, int budget) {
     const int cap = c.max_pages * c.page;
     const int m = budget < cap - budget ? budget : cap - budget;
     return m < 0 ? 0 : (m + 3) & ~3;
+}
+
+// Clusters as large as 8192 slots a CTA ask for, but no more than give every SM a CTA.
+template <bool CACHED, int ROW_BYTES>
+static cudaError_t launch_evict_c(const EvictArgs &a, int rows, size_t smem, cudaStream_t st) {
+    if (CACHED) {
+        static bool raised[16] = {false};
+        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(kv_evict_kernel<CACHED, ROW_BYTES>),
+                                         kSelMaxKeys * sizeof(uint32_t), raised);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.cluster, rows);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.cluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_evict_kernel<CACHED, ROW_BYTES>, a);
+}
+
+template <int ROW_BYTES>
+static cudaError_t launch_evict(EvictArgs a, int rows, cudaStream_t st) {
+    int c = 1;
+    while (c < kSelMaxCluster && c * 8192 < a.c.cap) c *= 2;
+    while (c > 1 && static_cast<long long>(rows) * c > 152 && c / 2 * kSelMaxKeys >= a.c.cap) c /= 2;
+    a.cluster = c;
+    // keys of a CTA, rounded as the kernel rounds its share of the longest row
+    const size_t keys = ((static_cast<size_t>(a.c.cap) + c - 1) / c + kSelThreads - 1) / kSelThreads * kSelThreads;
+    if (keys <= kSelMaxKeys) return launch_evict_c<true, ROW_BYTES>(a, rows, keys * sizeof(uint32_t), st);
+    return launch_evict_c<false, ROW_BYTES>(a, rows, 0, st);
 }
 
 unsigned int take_kv_error() {
@@ -395,8 +563,8 @@ int sage_kv_append(const sage_kv *c, const void *K, const void *V, int T, const 
 
 size_t sage_evict_workspace_bytes(const sage_kv *c, int budget) {
     if (check_kv(c, false) != SAGE_OK || budget <= 0) return 0;
-    const size_t rows = static_cast<size_t>(c->B) * c->H;
-    return (rows + 2 * rows * evict_max_moves(*c, budget)) * sizeof(int);
+    const size_t n = 2 * static_cast<size_t>(c->B) * c->H * evict_max_moves(*c, budget);
+    return (n ? n : 4) * sizeof(int);
 }
 
 int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget, int recent, int *lens_out,
@@ -415,23 +583,14 @@ int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget
     a.lens = lens; a.seen = seen; a.lens_out = lens_out;
     a.budget = budget; a.recent = recent;
     a.max_moves = evict_max_moves(*c, budget);
-    a.moves = static_cast<int *>(workspace);
-    a.dst = a.moves + rows;
+    a.dst = static_cast<int *>(workspace);
     a.src = a.dst + static_cast<size_t>(rows) * a.max_moves;
-    kv_select_kernel<<<rows, kSelThreads, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
-    if (a.max_moves == 0) return SAGE_OK;
-    // enough CTAs that the GPU is full whatever the number of rows, and no more than the moves fill
     const int row_bytes = c->d * (c->kind == SAGE_KV_16 ? 2 : 1);
-    const int groups = 256 / (row_bytes / 16);
-    int x = (152 * 8 + rows - 1) / rows;
-    const int most = (a.max_moves + groups - 1) / groups;
-    if (x > most) x = most;
-    const dim3 grid(x, rows);
-    if (row_bytes == 64) kv_move_kernel<64><<<grid, 256, 0, s>>>(a);
-    else if (row_bytes == 128) kv_move_kernel<128><<<grid, 256, 0, s>>>(a);
-    else kv_move_kernel<256><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+    cudaError_t e;
+    if (row_bytes == 64) e = launch_evict<64>(a, rows, s);
+    else if (row_bytes == 128) e = launch_evict<128>(a, rows, s);
+    else e = launch_evict<256>(a, rows, s);
+    return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -55,6 +55,16 @@ inline KvView kv_view(const sage_kv &c) {
                   c.max_pages, c.max_pages * c.page, static_cast<uint32_t>(mul), 30 + k};
 }
 
+// A kernel's dynamic shared-memory limit, raised once a device (`raised`; again is harmless).
+inline cudaError_t raise_smem(const void *kernel, size_t bytes, bool (&raised)[16]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 16 && raised[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev < 16) raised[dev] = true;
+    return e;
+}
+
 inline bool misaligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 // The rules of struct sage_kv (`pointers` false: sizes only, for the workspace queries).

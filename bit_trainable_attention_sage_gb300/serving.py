@@ -95,6 +95,18 @@ class Rope:
         self.axes, self.rotary = len(self.sections), 2 * sum(self.sections)
         self._sections = (ctypes.c_int * self.axes)(*self.sections)
         self._freq = (ctypes.c_double * len(self.freqs))(*self.freqs)
+        self._made = {}         # params structs by what they depend on
+
+    def _struct(self, *key):
+        """The struct for (B, H, Hk, N, dtype, pos_batch, inverse)."""
+        p = self._made.get(key)
+        if p is None:
+            if len(self._made) >= 64:
+                self._made = {}
+            B, H, Hk, N, dtype, pb, inverse = key
+            p = self._made[key] = SageRopeParams(B, H, Hk, N, self.d, _DTYPES[dtype], self.axes, pb, self.rotary,
+                                                 self.interleaved, inverse, self._sections, self._freq)
+        return ctypes.byref(p)
 
 
 def make_rope(d: int, sections, *, base: float = 10000.0, interleaved: bool = False, freqs=None) -> Rope:
@@ -146,9 +158,7 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
         _need(Qo, "out[0]", dtype, shape, dev)
         if K is not None:
             _need(Ko, "out[1]", dtype, K.shape, dev)
-    p = SageRopeParams(B, H, Hk, N, d, _DTYPES[dtype], rope.axes, pb, rope.rotary, rope.interleaved, bool(inverse),
-                       rope._sections, rope._freq)
-    st = lib().sage_rope(ctypes.byref(p), Q.data_ptr(), None if K is None else K.data_ptr(), positions.data_ptr(),
+    st = lib().sage_rope(rope._struct(B, H, Hk, N, dtype, pb, bool(inverse)), Q.data_ptr(), None if K is None else K.data_ptr(), positions.data_ptr(),
                          Qo.data_ptr(), None if K is None else Ko.data_ptr(), _current(dev))
     _check("sage_rope", st)
     return Qo, Ko

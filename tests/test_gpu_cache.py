@@ -468,3 +468,36 @@ def test_serving_loop(kind):
                     assert cache.pos[b, h, :n[b]].tolist() == pos[b][h]
                     assert cache.score[b, h, :n[b]].tolist() == score[b][h]
     assert status(sg) == 0
+
+
+def test_evict_long_rows_over_a_cluster():
+    """Rows that a cluster shares, with ties across its parts, and rows too long for shared memory."""
+    import bit_trainable_attention_sage_gb300 as sg
+    for n, page, budget, levels in ((20000, 64, 7000, 0), (70000, 16, 60000, 40), (400000, 256, 1000, 0)):
+        cap = -(-n // page) * page
+        g = torch.Generator().manual_seed(n)
+        pages = cap // page
+        K = torch.randn(pages, 1, page, 64, generator=g).half().cuda()
+        V = torch.randn(pages, 1, page, 64, generator=g).half().cuda()
+        score = torch.rand(1, 1, cap, generator=g)
+        if levels:
+            score = (score * levels).floor()
+        pos = torch.randperm(cap, generator=g).int().view(1, 1, cap)
+        table = torch.randperm(pages, generator=g).int().view(1, pages)
+        cache = sg.KvCache(K.clone(), V.clone(), table.cuda(), score=score.cuda(), pos=pos.cuda())
+        recent = budget // 10
+        new = sg.sage_kv_evict(cache, ints([n]), ints([cap]), budget=budget, recent=recent)
+        assert status(sg) == 0 and new.tolist() == [budget]
+        key = torch.where(pos[0, 0, :n] >= cap - recent, torch.tensor(float("inf")), score[0, 0, :n])
+        stay = (-key).sort(stable=True).indices[:budget].sort().values
+        src = stay[stay >= budget]
+        gone = torch.ones(budget, dtype=torch.bool)
+        gone[stay[stay < budget]] = False
+        dst = gone.nonzero().flatten()
+        score[0, 0, dst], pos[0, 0, dst] = score[0, 0, src], pos[0, 0, src]
+        assert torch.equal(cache.score.cpu(), score) and torch.equal(cache.pos.cpu(), pos)
+        t = table[0].long()
+        for x, was in ((cache.K, K), (cache.V, V)):
+            want = was.clone()
+            want[t[dst // page].cuda(), 0, (dst % page).cuda()] = was[t[src // page].cuda(), 0, (src % page).cuda()]
+            assert torch.equal(x, want)

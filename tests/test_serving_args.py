@@ -141,14 +141,14 @@ def test_cache_calls_refuse(sg):
 
 def test_cache_workspaces(sg):
     """Decode: two places a CTA for sums, maxima and sums of exponentials, and with scores a logit a
-    slot and head; evict: a count a row and at most min(budget, capacity - budget) pairs."""
+    slot and head; evict: at most min(budget, capacity - budget) pairs a row."""
     L = sg.lib()
     c = _kv(sg, B=1, H=1, max_pages=4)
     plain, scored = (L.sage_decode_workspace_bytes(ctypes.byref(c), 4, s) for s in (0, 1))
     assert plain >= 2 * 8 * 66 * 4 and scored >= plain + 4 * 64 * 4
     assert L.sage_decode_workspace_bytes(ctypes.byref(c), 0, 0) == 0 and L.sage_decode_workspace_bytes(None, 4, 0) == 0
     c = _kv(sg, B=2, H=3, max_pages=4)
-    assert L.sage_evict_workspace_bytes(ctypes.byref(c), 8) >= 6 * (1 + 2 * 8) * 4
+    assert L.sage_evict_workspace_bytes(ctypes.byref(c), 8) >= 6 * 2 * 8 * 4
     assert L.sage_evict_workspace_bytes(ctypes.byref(c), 0) == 0
     # big caches do not overflow the sizes
     c = _kv(sg, B=1024, H=8, page=64, max_pages=1 << 14)
