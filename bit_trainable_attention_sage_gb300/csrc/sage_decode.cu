@@ -55,8 +55,8 @@ struct DecodeShape {
     static constexpr int TILE = GRAN * kDecWarps;
     static constexpr int SCALES = KIND < 2 ? 0 : 2 * GRAN * 4;
     static constexpr int STAGE = 2 * GRAN * ROW + SCALES;
-    static constexpr int STAGES = ROW == 64 ? 4 : 3;
-    static constexpr int CTAS = ROW == 64 ? 3 : 2;           // resident CTAs an SM
+    static constexpr int STAGES = ROW == 64 ? 4 : ROW == 128 ? 2 : 3;
+    static constexpr int CTAS = ROW == 256 ? 2 : 3;          // resident CTAs an SM
     static constexpr int ALIGN = 512;                        // of the ring, so that its addresses can be XORed
     static constexpr int SMEM = kDecWarps * STAGES * STAGE + ALIGN;
 };
@@ -842,7 +842,7 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     const int row = c.d * (c.kind == SAGE_KV_16 ? 2 : 1);
     // one resident wave; never more CTAs than there can be tiles
     p.tile = decode_tile(row);
-    long long n = kSMs * (row == 64 ? 3 : 2);
+    long long n = kSMs * (row == 256 ? 2 : 3);
     const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + p.tile - 1) / p.tile);
     if (n > tiles) n = tiles;
     p.ctas = static_cast<int>(n);
