@@ -18,19 +18,21 @@
 // each keeps its own ring of cp.async stages in shared memory, its own running maximum, sum and
 // output accumulators, and the four are joined once at the end of a pair.
 //
-// Products.  m16n8k16 tensor-core products with the query heads as the 16 rows.  The kernel
-// needs a fraction of their rate, and both operands come from registers, where 8-bit rows can be
+// Products.  m16n8k16 tensor-core products with the tokens (q K^T) and the channels (P V) as the 16
+// rows and the query heads as the 8 columns, so a group of up to 8 heads wastes nothing but the
+// columns it lacks, and the output takes d / 16 registers a lane and column.  The kernel needs a
+// fraction of the products' rate, and both operands come from registers, where 8-bit rows can be
 // widened on the way; tcgen05 would want the widened rows back in shared memory.
 //   - 16-bit pool: K by ldmatrix, V by its transposing form.
 //   - 8-bit pool: codes are exact in fp16.  The products run over channels (or tokens) in any
 //     order as long as both operands agree, so a lane takes 16 consecutive bytes of a row with
 //     one load and assigns them to the products' positions itself; no transposition is needed.
-//     q is scaled by a power of two a row to stay in fp16's range: exact to 2^-39 of its largest
+//     q is scaled by a power of two a head to stay in fp16's range: exact to 2^-39 of its largest
 //     value.  sK multiplies the logit; sV the probability, over a running power of two `vref` that
 //     keeps the product in fp16's range.
 //   - The probabilities enter as hi + lo of two 16-bit values, at least 16 bits: one rounding to
-//     bf16 would show in the output.  With at most 8 query heads a group, hi takes rows 0-7 and
-//     lo rows 8-15 of one product, which the padding to 16 rows would waste otherwise.
+//     bf16 would show in the output.  They change from the first product's layout to the second's
+//     operand by movmatrix (8 x 8 transposition in registers).
 #include <utility>
 
 #include "sage_kv.cuh"
@@ -157,6 +159,14 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     }
 }
 
+// 8 x 8 transposition of 16-bit values over a warp: lane (g, q) gives row g, columns 2q and 2q + 1
+// and gets those of column g.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
 // (x0, x1) as hi + lo pairs of the product's 16-bit type
 template <bool BF16>
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
@@ -254,9 +264,9 @@ template <int D, int KIND, int MR>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND>;
     constexpr bool BF16 = KIND == 1;                 // type of the products
-    constexpr int KS = D / 16, NT = D / 8;           // 16-channel steps of q K^T, 8-channel columns of P V
-    constexpr int GT = S::GRAN / 8, HALVES = S::GRAN / 16;
-    constexpr int R = MR == 16 ? 2 : 1;              // rows of a lane that are heads
+    constexpr int KS = D / 16;                       // 16-channel steps of K q, row tiles of V^T P
+    constexpr int HALVES = S::GRAN / 16;             // row tiles of K q, 16-token steps of V^T P
+    constexpr int NH = MR / 8;                       // column tiles: 8 heads each
     constexpr int HALF = 16 * S::ROW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & (S::ALIGN - 1));
@@ -344,9 +354,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             cp_commit();
         }
 
-        // q: rows g and g + 8 of the products' first operand
-        uint32_t qa[KS][4];
-        float qs[2] = {a.sl2, a.sl2};
+        // q: column g of the products' second operand
+        uint32_t qb[NH][KS][2];
+        float qs[NH][2];                                         // log2 units' factor of heads 2q, 2q + 1
         {
             const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
             auto word = [&](int ks, int half) {                  // channels of k = 2q (+ 8 half), in pairs
@@ -354,16 +364,17 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                 else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
             };
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    qa[ks][2 * half] = g < heads ? __ldg(Q + g * (D / 2) + word(ks, half)) : 0u;
-                    qa[ks][2 * half + 1] = MR == 16 && g + 8 < heads ? __ldg(Q + (g + 8) * (D / 2) + word(ks, half)) : 0u;
-                }
-            if constexpr (KIND >= 2) {
-                // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15)
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                    for (int half = 0; half < 2; ++half)
+                        qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+                qs[nh][0] = qs[nh][1] = a.sl2;
+                if constexpr (KIND >= 2) {
+                    // to fp16 under a power of two a head: the largest value lands in [2^14, 2^15)
                     float mx = 0.0f;
                     auto pair_of = [&](uint32_t x) {
                         return a.bf16 ? __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x))
@@ -373,32 +384,39 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const float2 f = pair_of(qa[ks][2 * half + r]);
-                            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            const float2 f = pair_of(qb[nh][ks][half]);
+                            mx = max3f(mx, fabsf(f.x), fabsf(f.y));
                         }
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     // exponent of the largest, held to [-100, 127] so that both factors are normal
                     const int e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
                     const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-                    qs[r] = a.sl2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+                    const float down = a.sl2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const float2 f = pair_of(qa[ks][2 * half + r]);
-                            qa[ks][2 * half + r] = pack_half2(f.x * up, f.y * up);
+                            const float2 f = pair_of(qb[nh][ks][half]);
+                            qb[nh][ks][half] = pack_half2(f.x * up, f.y * up);
                         }
+                    qs[nh][0] = __shfl_sync(0xffffffffu, down, 8 * q);           // lane (g = 2q, 0)
+                    qs[nh][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
                 }
             }
         }
 
-        float acc[NT][4];
+        float acc[KS][NH][4];                                    // channels (rows g, g + 8) x heads (2q, 2q + 1)
+        float m[NH][2], l[NH][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][nh][i] = 0.0f;
+            m[nh][0] = m[nh][1] = -INFINITY;
+            l[nh][0] = l[nh][1] = 0.0f;
+        }
         float vref = 1.1754943508222875e-38f;                    // 2^-126
 
         int stage = 0, ahead = S::STAGES - 1;                    // stages of granules j and j + STAGES - 1
@@ -411,161 +429,179 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             const int tok = tok0 + j * S::TILE;
             const uint32_t holes = (bad >> (stage * 2)) & 3u;
 
-            // S = q K^T: columns (tokens) nt * 8 + 2 q + {0, 1}
-            float s[GT][4];
+            // S = K q: tokens hf * 16 + g (i = 0, 1) and + 8 (2, 3), heads nh * 8 + 2q (0, 2) and + 1 (1, 3)
+            float s[HALVES][NH][4];
 #pragma unroll
-            for (int nt = 0; nt < GT; ++nt)
+            for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[hf][nh][i] = 0.0f;
             if constexpr (KIND < 2) {
-                const uint32_t at = smem_u32(kst) + chunk_at<D, KIND>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+                const uint32_t at = smem_u32(kst) + chunk_at<D, KIND>(lane & 15, lane >> 4);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf) {
-                        uint32_t kb[4];
-                        ldsm4((at ^ (ks * 32)) + hf * HALF, kb);
-                        mma16816<BF16>(s[2 * hf], qa[ks], kb[0], kb[1]);
-                        mma16816<BF16>(s[2 * hf + 1], qa[ks], kb[2], kb[3]);
+                        uint32_t ka[4];
+                        ldsm4((at ^ (ks * 32)) + hf * HALF, ka);
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh) mma16816<BF16>(s[hf][nh], ka, qb[nh][ks][0], qb[nh][ks][1]);
                     }
             } else {
                 const uint32_t at = chunk_at<D, KIND>(g, q);     // rows 8 apart are 8 * ROW apart
 #pragma unroll
                 for (int jj = 0; jj < D / 64; ++jj)
 #pragma unroll
-                    for (int nt = 0; nt < GT; ++nt) {
-                        const uint4 kk = *reinterpret_cast<const uint4 *>(kst + (at ^ (jj * 64)) + nt * 8 * S::ROW);
-                        const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
+                    for (int hf = 0; hf < HALVES; ++hf) {
+                        const uint8_t *from = kst + (at ^ (jj * 64)) + hf * HALF;
+                        const uint4 k0 = *reinterpret_cast<const uint4 *>(from), k1 = *reinterpret_cast<const uint4 *>(from + 8 * S::ROW);
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            uint32_t b0, b1;
-                            widen4<KIND>(kw[i], b0, b1);
-                            mma16816<false>(s[nt], qa[4 * jj + i], b0, b1);
+                            uint32_t ka[4];
+                            widen4<KIND>(w0[i], ka[0], ka[2]);
+                            widen4<KIND>(w1[i], ka[1], ka[3]);
+#pragma unroll
+                            for (int nh = 0; nh < NH; ++nh)
+                                mma16816<false>(s[hf][nh], ka, qb[nh][4 * jj + i][0], qb[nh][4 * jj + i][1]);
                         }
                     }
             }
-            float2 fv[GT];                                       // sV of the lane's tokens
-            if constexpr (KIND >= 2) {
-                const uint8_t *sc = kst + 2 * S::GRAN * S::ROW + q * 8;
-#pragma unroll
-                for (int nt = 0; nt < GT; ++nt) {
-                    const float2 fk = *reinterpret_cast<const float2 *>(sc + nt * 32);
-                    fv[nt] = *reinterpret_cast<const float2 *>(sc + S::GRAN * 4 + nt * 32);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        s[nt][2 * r] *= fk.x;
-                        s[nt][2 * r + 1] *= fk.y;
-                    }
-                }
-            }
             // log2 units; tokens past the end of the sequence, or without a page, do not exist
+            float fv[HALVES][2];                                 // sV of the lane's tokens
 #pragma unroll
-            for (int nt = 0; nt < GT; ++nt)
+            for (int hf = 0; hf < HALVES; ++hf) {
+                float fk[2] = {1.0f, 1.0f};
+                if constexpr (KIND >= 2) {
+                    const float *sc = reinterpret_cast<const float *>(kst + 2 * S::GRAN * S::ROW) + hf * 16 + g;
+                    fk[0] = sc[0];
+                    fk[1] = sc[8];
+                    fv[hf][0] = sc[S::GRAN];
+                    fv[hf][1] = sc[S::GRAN + 8];
+                }
 #pragma unroll
-                for (int i = 0; i < 2 * R; ++i) s[nt][i] *= qs[i >> 1];
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (KIND >= 2) s[hf][nh][i] *= fk[i >> 1];
+                        s[hf][nh][i] *= qs[nh][i & 1];
+                    }
+            }
             if (len - tok < S::GRAN || holes) {
 #pragma unroll
-                for (int nt = 0; nt < GT; ++nt)
+                for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                    for (int i = 0; i < 2 * R; ++i)
-                        if (nt * 8 + 2 * q + (i & 1) >= len - tok || (holes >> (nt / 2)) & 1u) s[nt][i] = -INFINITY;
+                    for (int i = 0; i < 4; ++i)
+                        if (hf * 16 + g + 8 * (i >> 1) >= len - tok || (holes >> hf) & 1u) {
+#pragma unroll
+                            for (int nh = 0; nh < NH; ++nh) s[hf][nh][i] = -INFINITY;
+                        }
             }
             if (a.logits) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (g + 8 * r < heads) {
-                        float *to = a.logits + (static_cast<size_t>(b) * a.Hq + head0 + g + 8 * r) * a.c.cap + tok + 2 * q;
+                for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                        for (int nt = 0; nt < GT; ++nt)
-                            if (nt < 2 || len - tok > 16)        // (slots up to the next multiple of 16 exist)
-                                *reinterpret_cast<float2 *>(to + nt * 8) = make_float2(s[nt][2 * r], s[nt][2 * r + 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int head = nh * 8 + 2 * q + (i & 1);
+                        float *to = a.logits + (static_cast<size_t>(b) * a.Hq + head0 + head) * a.c.cap + tok + g + 8 * (i >> 1);
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            if (head < heads && len - tok > hf * 16) to[hf * 16] = s[hf][nh][i];   // (slots up to the next multiple of 16 exist)
                     }
             }
-            float alpha[2] = {1.0f, 1.0f};
+            float alpha[NH][2];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float mx = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+            for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                for (int nt = 1; nt < GT; ++nt) mx = max3f(mx, s[nt][2 * r], s[nt][2 * r + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[r], mx);
-                const float ref = mn == -INFINITY ? 0.0f : mn;   // nothing seen yet: all terms are 0
-                alpha[r] = ex2_approx(m[r] - ref);
-                m[r] = mn;
-                float sum = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[0][nh][e], s[0][nh][2 + e]);
 #pragma unroll
-                for (int nt = 0; nt < GT; ++nt)
+                    for (int hf = 1; hf < HALVES; ++hf) mx = max3f(mx, s[hf][nh][e], s[hf][nh][2 + e]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float mn = fmaxf(m[nh][e], mx);
+                    const float ref = mn == -INFINITY ? 0.0f : mn;   // nothing seen yet: all terms are 0
+                    alpha[nh][e] = ex2_approx(m[nh][e] - ref);
+                    m[nh][e] = mn;
+                    float sum = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &x = s[nt][2 * r + i];
-                        x = ex2_approx(x - ref);
-                        sum += x;
-                    }
-                l[r] = l[r] * alpha[r] + sum;
-            }
+                    for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &x = s[hf][nh][2 * i + e];
+                            x = ex2_approx(x - ref);
+                            sum += x;
+                        }
+                    l[nh][e] = l[nh][e] * alpha[nh][e] + sum;
+                }
             if constexpr (KIND >= 2) {
                 // the largest sV so far, as a power of two above it
-                float mv = fmaxf(fv[0].x, fv[0].y);
+                float mv = fmaxf(fv[0][0], fv[0][1]);
 #pragma unroll
-                for (int nt = 1; nt < GT; ++nt) mv = max3f(mv, fv[nt].x, fv[nt].y);
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 2));
+                for (int hf = 1; hf < HALVES; ++hf) mv = max3f(mv, fv[hf][0], fv[hf][1]);
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 4));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 8));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 16));
                 if (mv > vref) {
                     const float up = __uint_as_float(min((__float_as_uint(mv) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
                     const float f = vref / up;
                     vref = up;
-                    alpha[0] *= f;
-                    alpha[1] *= f;
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh) {
+                        alpha[nh][0] *= f;
+                        alpha[nh][1] *= f;
+                    }
                 }
                 const float iv = __uint_as_float(0x7F000000u - __float_as_uint(vref));   // 1 / vref
 #pragma unroll
-                for (int nt = 0; nt < GT; ++nt) {
-                    const float x = fv[nt].x * iv, y = fv[nt].y * iv;
+                for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        s[nt][2 * r] *= x;
-                        s[nt][2 * r + 1] *= y;
-                    }
-                }
+                    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[hf][nh][i] *= fv[hf][i >> 1] * iv;
             }
-            if (MR == 8) alpha[1] = alpha[0];                    // rows 8-15 hold the lo terms of 0-7
-            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+            bool moved = false;
 #pragma unroll
-                for (int jn = 0; jn < NT; ++jn) {
-                    acc[jn][0] *= alpha[0]; acc[jn][1] *= alpha[0];
-                    acc[jn][2] *= alpha[1]; acc[jn][3] *= alpha[1];
-                }
+            for (int nh = 0; nh < NH; ++nh) moved = moved || alpha[nh][0] != 1.0f || alpha[nh][1] != 1.0f;
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int jn = 0; jn < KS; ++jn) {
+                        acc[jn][nh][0] *= alpha[nh][0]; acc[jn][nh][1] *= alpha[nh][1];
+                        acc[jn][nh][2] *= alpha[nh][0]; acc[jn][nh][3] *= alpha[nh][1];
+                    }
             }
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
-                float(&s0)[4] = s[2 * hf], (&s1)[4] = s[2 * hf + 1];
-                uint32_t ph[4], pl[4];
-                if constexpr (MR == 8) {
-                    split2<BF16>(s0[0], s0[1], ph[0], ph[1]);
-                    split2<BF16>(s1[0], s1[1], ph[2], ph[3]);
-                } else {
-                    split2<BF16>(s0[0], s0[1], ph[0], pl[0]);
-                    split2<BF16>(s0[2], s0[3], ph[1], pl[1]);
-                    split2<BF16>(s1[0], s1[1], ph[2], pl[2]);
-                    split2<BF16>(s1[2], s1[3], ph[3], pl[3]);
-                }
-                auto pv = [&](int jn, uint32_t b0, uint32_t b1) {
-                    mma16816<BF16>(acc[jn], ph, b0, b1);
-                    if constexpr (MR == 16) mma16816<BF16>(acc[jn], pl, b0, b1);
+                uint32_t ph[NH][2], pl[NH][2];                   // hi, lo: tokens 2q, 2q + 1 (+ 8) of head g
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        split2<BF16>(s[hf][nh][2 * x], s[hf][nh][2 * x + 1], ph[nh][x], pl[nh][x]);
+                        ph[nh][x] = transpose8(ph[nh][x]);
+                        pl[nh][x] = transpose8(pl[nh][x]);
+                    }
+                auto pv = [&](int jn, const uint32_t (&va)[4]) {
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh) mma16816<BF16>(acc[jn][nh], va, ph[nh][0], ph[nh][1]);
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh) mma16816<BF16>(acc[jn][nh], va, pl[nh][0], pl[nh][1]);
                 };
                 if constexpr (KIND < 2) {
-                    const uint32_t at = smem_u32(vst) + hf * HALF + chunk_at<D, KIND>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4);
+                    const uint32_t at = smem_u32(vst) + hf * HALF + chunk_at<D, KIND>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
-                    for (int jj = 0; jj < D / 16; ++jj) {
-                        uint32_t vb[4];
-                        ldsm4t(at ^ (jj * 32), vb);
-                        pv(2 * jj, vb[0], vb[1]);
-                        pv(2 * jj + 1, vb[2], vb[3]);
+                    for (int jn = 0; jn < KS; ++jn) {
+                        uint32_t va[4];
+                        ldsm4t(at ^ (jn * 32), va);
+                        pv(jn, va);
                     }
                 } else {
-                    // tokens 2q, 2q + 1, 2q + 8, 2q + 9; channels NT * g + jn of products jn = 0 .. NT - 1
-                    constexpr int W = NT / 4;
+                    // tokens 2q, 2q + 1, 2q + 8, 2q + 9; row g of tile jn is channel D / 8 g + 2 jn, row g + 8 the next
+                    constexpr int W = D / 32;
                     uint32_t x[4][W];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
@@ -580,13 +616,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     }
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        uint32_t p[4], r[4];
-                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), p[0], p[1]);
-                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), p[2], p[3]);
-                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), r[0], r[1]);
-                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), r[2], r[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) pv(4 * i + e, p[e], r[e]);
+                        uint32_t va[2][4];
+                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), va[0][0], va[0][1]);
+                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), va[0][2], va[0][3]);
+                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), va[1][0], va[1][1]);
+                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), va[1][2], va[1][3]);
+                        pv(2 * i, va[0]);
+                        pv(2 * i + 1, va[1]);
                     }
                 }
             }
@@ -597,33 +633,27 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
 
         // join the four warps, in their order
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        }
-        if (q == 0) {
-            s_m[warp][g] = m[0];
-            s_l[warp][g] = l[0];
-            if constexpr (MR == 16) {
-                s_m[warp][g + 8] = m[1];
-                s_l[warp][g + 8] = l[1];
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nh][e] += __shfl_xor_sync(0xffffffffu, l[nh][e], o);
+                if (g == 0) {
+                    s_m[warp][nh * 8 + 2 * q + e] = m[nh][e];
+                    s_l[warp][nh * 8 + 2 * q + e] = l[nh][e];
+                }
             }
-        }
         __syncthreads();                                         // every warp's stages are idle from here
         float *so = reinterpret_cast<float *>(smem);             // (warps, MR, D)
 #pragma unroll
-        for (int jn = 0; jn < NT; ++jn)
+        for (int jn = 0; jn < KS; ++jn)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int ch_d = KIND < 2 ? jn * 8 + 2 * q + e : NT * (2 * q + e) + jn;
-                const float sc = KIND < 2 ? 1.0f : vref;
-                if constexpr (MR == 8) {
-                    so[(warp * MR + g) * D + ch_d] = (acc[jn][e] + acc[jn][2 + e]) * sc;
-                } else {
-                    so[(warp * MR + g) * D + ch_d] = acc[jn][e] * sc;
-                    so[(warp * MR + g + 8) * D + ch_d] = acc[jn][2 + e] * sc;
+            for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = KIND < 2 ? jn * 16 + g + 8 * (i >> 1) : D / 8 * g + 2 * jn + (i >> 1);
+                    so[(warp * MR + nh * 8 + 2 * q + (i & 1)) * D + c] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
                 }
-            }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == tiles;
         // a run's first pair that began in an earlier run goes to place 0, one that goes on to place 1
