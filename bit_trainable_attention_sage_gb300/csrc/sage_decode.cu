@@ -311,13 +311,27 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
         const int tok0 = t0 * S::TILE + warp * S::GRAN;
         const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
         uint32_t bad = 0;                                        // halves (2 bits a stage) whose page is not one
+        // pages of the granule that is loaded next: read a granule ahead, so that no load waits for them
+        const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+        int next[HALVES];
+        auto look = [&](int j) {
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf) {
+                const int t = tok0 + j * S::TILE + hf * 16;
+                next[hf] = t < len ? __ldg(table + kv_page_of(a.c, t)) : 0;
+            }
+        };
         auto load = [&](int j, int stage) {
             const int tok = tok0 + j * S::TILE;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
                 const int t = tok + hf * 16;
                 const int left = len - t;
-                const int page = left > 0 ? kv_page(a.c, b, t, &g_decode_err) : 0;
+                int page = next[hf];
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
+                    atomicOr(&g_decode_err, 1u);
+                    page = -1;
+                }
                 const int nv = page < 0 ? 0 : max(0, min(16, left));
                 const uint32_t bit = 1u << (stage * 2 + hf);
                 bad = page < 0 ? bad | bit : bad & ~bit;
@@ -347,7 +361,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     cp_async4(at, sc + (r < nv ? r : 0), r < nv);
                 }
             }
+            look(j + 1);
         };
+        look(0);
 #pragma unroll
         for (int j = 0; j < S::STAGES - 1; ++j) {
             if (j < ng) load(j, j);
