@@ -239,9 +239,15 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
 __device__ __forceinline__ int runs_of(const DecodeArgs &a, long long total) {
     return static_cast<int>(min(static_cast<long long>(a.ctas), total));
 }
-__device__ __forceinline__ long long run_start(long long total, int c, int runs) { return total * c / runs; }
+// (64-bit divisions take a good part of a microsecond: 32 bits where the products fit)
+__device__ __forceinline__ long long div_up_to(long long n, long long d) {
+    return n <= 0xFFFFFFFFll ? static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d)) : n / d;
+}
+__device__ __forceinline__ long long run_start(long long total, int c, int runs) { return div_up_to(total * c, runs); }
 __device__ __forceinline__ int run_of(long long total, long long u, int runs) {
-    return static_cast<int>(((u + 1) * runs - 1) / total);
+    const long long n = (u + 1) * runs - 1;
+    if (n <= 0xFFFFFFFFll && total <= 0xFFFFFFFFll) return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
+    return static_cast<int>(n / total);
 }
 
 __device__ __forceinline__ void store_out(const DecodeArgs &a, size_t at, float x, float y) {
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             ++b;
             continue;
         }
-        const int pair = static_cast<int>((u - first) / tiles);
+        const int pair = static_cast<int>(div_up_to(u - first, tiles));
         const int t0 = static_cast<int>((u - first) - static_cast<long long>(pair) * tiles);
         const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + (u1 - u)));
         const int hk = pair / a.chunks, ch = pair - hk * a.chunks;
@@ -311,23 +317,43 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
         const int tok0 = t0 * S::TILE + warp * S::GRAN;
         const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
         uint32_t bad = 0;                                        // halves (2 bits a stage) whose page is not one
-        // pages of the granule that is loaded next: read a granule ahead, so that no load waits for them
+        // q: column g of the products' second operand (asked for first: all of a pair's first reads
+        // are then on their way together)
+        uint32_t qb[NH][KS][2];
+        {
+            const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
+            auto word = [&](int ks, int half) {                  // channels of k = 2q (+ 8 half), in pairs
+                if constexpr (KIND < 2) return ks * 8 + q + half * 4;
+                else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
+            };
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
+        }
+        // pages of the granules that are loaded next: read two granules ahead, so that no load waits for them
         const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
-        int next[HALVES];
-        auto look = [&](int j) {
+        int next[2][HALVES];
+        auto look = [&](int j, int (&to)[HALVES]) {
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
                 const int t = tok0 + j * S::TILE + hf * 16;
-                next[hf] = t < len ? __ldg(table + kv_page_of(a.c, t)) : 0;
+                to[hf] = t < len ? __ldg(table + kv_page_of(a.c, t)) : 0;
             }
         };
+        look(0, next[0]);
+        look(1, next[1]);
         auto load = [&](int j, int stage) {
             const int tok = tok0 + j * S::TILE;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
                 const int t = tok + hf * 16;
                 const int left = len - t;
-                int page = next[hf];
+                int page = next[0][hf];
+                next[0][hf] = next[1][hf];
                 if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
                     atomicOr(&g_decode_err, 1u);
                     page = -1;
@@ -361,31 +387,16 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     cp_async4(at, sc + (r < nv ? r : 0), r < nv);
                 }
             }
-            look(j + 1);
+            look(j + 2, next[1]);
         };
-        look(0);
 #pragma unroll
         for (int j = 0; j < S::STAGES - 1; ++j) {
             if (j < ng) load(j, j);
             cp_commit();
         }
 
-        // q: column g of the products' second operand
-        uint32_t qb[NH][KS][2];
         float qs[NH][2];                                         // log2 units' factor of heads 2q, 2q + 1
         {
-            const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
-            auto word = [&](int ks, int half) {                  // channels of k = 2q (+ 8 half), in pairs
-                if constexpr (KIND < 2) return ks * 8 + q + half * 4;
-                else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
-            };
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh) {
                 qs[nh][0] = qs[nh][1] = a.sl2;
@@ -646,6 +657,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
             ahead = ahead + 1 == S::STAGES ? 0 : ahead + 1;
         }
         cp_wait<0>();
+        __syncwarp();
 
         // join the four warps, in their order
 #pragma unroll
@@ -659,23 +671,27 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     s_l[warp][nh * 8 + 2 * q + e] = l[nh][e];
                 }
             }
-        __syncthreads();                                         // every warp's stages are idle from here
-        float *so = reinterpret_cast<float *>(smem);             // (warps, MR, D)
+        // Each warp's sums, (MR, D) floats, in its own idle ring.  Heads PITCH apart, and in 8 bits the
+        // channels in the order (k, g) of D / 8 g + k, put a store's 32 lanes into 32 banks.
+        constexpr int PITCH = D + 4;
+        static_assert(MR * PITCH * 4 <= S::STAGES * S::STAGE, "the sums do not fit the ring");
+        float *so = reinterpret_cast<float *>(ring);
 #pragma unroll
         for (int jn = 0; jn < KS; ++jn)
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = KIND < 2 ? jn * 16 + g + 8 * (i >> 1) : D / 8 * g + 2 * jn + (i >> 1);
-                    so[(warp * MR + nh * 8 + 2 * q + (i & 1)) * D + c] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
-                }
+                for (int i = 0; i < 4; ++i)
+                    so[(nh * 8 + 2 * q + (i & 1)) * PITCH + jn * 16 + 8 * (i >> 1) + g] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
         __syncthreads();
         const bool whole = t0 == 0 && t1 == tiles;
         // a run's first pair that began in an earlier run goes to place 0, one that goes on to place 1
         const int place = run_first && t0 > 0 ? 0 : 1;
         for (int idx = tid; idx < heads * (D / 2); idx += kDecThreads) {
-            const int r = idx / (D / 2), c = (idx % (D / 2)) * 2;
+            const int r = idx / (D / 2), x2 = idx % (D / 2);
+            // two channels c, c + 1 and their places
+            const int c = KIND < 2 ? 2 * x2 : D / 8 * (x2 & 7) + 2 * (x2 >> 3);
+            const int p0 = r * PITCH + (KIND < 2 ? c : 16 * (x2 >> 3) + (x2 & 7)), p1 = p0 + (KIND < 2 ? 1 : 8);
             float M = -INFINITY;
 #pragma unroll
             for (int x = 0; x < kDecWarps; ++x) M = fmaxf(M, s_m[x][r]);
@@ -684,9 +700,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
 #pragma unroll
             for (int x = 0; x < kDecWarps; ++x) {
                 const float f = ex2_approx(s_m[x][r] - ref);
-                const float2 v = *reinterpret_cast<const float2 *>(so + (x * MR + r) * D + c);
-                o0 += f * v.x;
-                o1 += f * v.y;
+                const float *from = reinterpret_cast<const float *>(smem + x * (S::STAGES * S::STAGE));
+                o0 += f * from[p0];
+                o1 += f * from[p1];
                 sum += f * s_l[x][r];
             }
             const size_t head = static_cast<size_t>(b) * a.Hq + head0 + r;
@@ -789,15 +805,21 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
                     if (M == -INFINITY) M = 0.0f;
                 }
             } else {
-                // part of CTA c: place 1 of the first, place 0 of the others
+                // part of CTA c: place 1 of the first, place 0 of the others; a lane's parts under its own maximum first
                 auto part = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r; };
                 M = -INFINITY;
-                for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[2 * part(c)]);
+                sum = 0.0f;
+                for (int c = c0 + lane; c <= c1; c += 32) {
+                    const float2 ml = reinterpret_cast<const float2 *>(a.part_ml)[part(c)];
+                    const float mn = fmaxf(M, ml.x), to = mn == -INFINITY ? 0.0f : mn;
+                    sum = sum * ex2_approx(M - to) + ml.y * ex2_approx(ml.x - to);
+                    M = mn;
+                }
+                const float mine = M;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
                 const float ref = M == -INFINITY ? 0.0f : M;
-                sum = 0.0f;
-                for (int c = c0 + lane; c <= c1; c += 32) sum += ex2_approx(a.part_ml[2 * part(c)] - ref) * a.part_ml[2 * part(c) + 1];
+                sum *= ex2_approx(mine - ref);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (lane == 0 && h % gridDim.y == blockIdx.y) a.L[head0 + h] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
@@ -818,7 +840,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
             const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
             if (c0 == c1) continue;
             float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
             for (int c = c0 + grp; c <= c1; c += GROUPS) {
                 const size_t at = (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r;
                 const float f = ex2_approx(a.part_ml[2 * at] - s_M[i]);
