@@ -46,7 +46,7 @@ constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kSMs = 152;
 
 // pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3
-template <int D, int KIND>
+template <int D, int KIND, int MR = 8>
 struct DecodeShape {
     static constexpr int ES = KIND < 2 ? 2 : 1;
     static constexpr int ROW = D * ES;                       // bytes
@@ -57,12 +57,20 @@ struct DecodeShape {
     static constexpr int TILE = GRAN * kDecWarps;
     static constexpr int SCALES = KIND < 2 ? 0 : 2 * GRAN * 4;
     static constexpr int STAGE = 2 * GRAN * ROW + SCALES;
-    static constexpr int STAGES = ROW == 64 ? 4 : ROW == 128 ? 2 : 3;
-    static constexpr int CTAS = ROW == 256 ? 2 : 3;          // resident CTAs an SM
+    // Resident CTAs an SM: three where 168 registers and a third of the shared memory do.  (131072
+    // tokens in E4M3, 8 kv heads, d = 128: with 4 heads a group 58 us at two, 56 at three; with 16
+    // a group 73 at two and 80 at three, which spill.)
+    static constexpr int CTAS = ROW == 256 || (MR == 16 && D == 128) ? 2 : 3;
+    static constexpr int STAGES = ROW == 64 ? 4 : CTAS == 3 ? 2 : 3;
     static constexpr int ALIGN = 512;                        // of the ring, so that its addresses can be XORed
-    static constexpr int SMEM = kDecWarps * STAGES * STAGE + ALIGN;
+    // a warp's ring; its last stage also holds the sums of 16 heads, D + 4 floats each
+    static constexpr int RING = STAGES * STAGE + (ROW == 256 ? 256 : 0);
+    static constexpr int SMEM = kDecWarps * RING + ALIGN;
 };
 constexpr int decode_tile(int row_bytes) { return (row_bytes == 256 ? 16 : 32) * kDecWarps; }
+constexpr int decode_ctas(int row_bytes, int d, int mr) { return row_bytes == 256 || (mr == 16 && d == 128) ? 2 : 3; }
+static_assert(decode_ctas(128, 128, 16) == DecodeShape<128, 2, 16>::CTAS && decode_ctas(128, 64, 16) == DecodeShape<64, 0, 16>::CTAS &&
+              decode_ctas(64, 64, 16) == DecodeShape<64, 3, 16>::CTAS && decode_ctas(256, 128, 8) == DecodeShape<128, 1, 8>::CTAS, "");
 
 struct DecodeArgs {
     KvView c;
@@ -267,8 +275,8 @@ __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)
 
 // ---- main kernel ------------------------------------------------------------------------------
 template <int D, int KIND, int MR>
-__global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    using S = DecodeShape<D, KIND>;
+__global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using S = DecodeShape<D, KIND, MR>;
     constexpr bool BF16 = KIND == 1;                 // type of the products
     constexpr int KS = D / 16;                       // 16-channel steps of K q, row tiles of V^T P
     constexpr int HALVES = S::GRAN / 16;             // row tiles of K q, 16-token steps of V^T P
@@ -284,6 +292,14 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
     const int cta = blockIdx.x;
     // the join may take its place on the GPU; it waits for this grid's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The lengths say where this CTA's pages stand, the pages where its rows: three reads one after
+    // the other.  The table and q are brought into L2 meanwhile, a share by each CTA.
+    {
+        const size_t at = (static_cast<size_t>(cta) * 64 + (tid & 63)) * 128;
+        const size_t bytes = tid < 64 ? static_cast<size_t>(a.c.B) * a.c.max_pages * 4 : static_cast<size_t>(a.c.B) * a.Hq * D * 2;
+        const char *from = tid < 64 ? reinterpret_cast<const char *>(a.c.table) : static_cast<const char *>(a.Q);
+        if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + at));
+    }
     const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
         const int n = runs_of(a, total);
         return cta < n ? run_start(total, cta, n) : total;
@@ -292,109 +308,113 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
     if (cta >= runs) return;
     const long long u1 = run_start(w.total, cta + 1, runs);
     // a warp's ring: stages of K rows, V rows, then (8 bits) K scales, V scales
-    uint8_t *ring = smem + warp * (S::STAGES * S::STAGE);
+    uint8_t *ring = smem + warp * S::RING;
     const uint32_t load_lane = smem_u32(ring) + chunk_at<D, KIND>(lane / S::CPR, lane % S::CPR);
 
+    // the run's pairs, one after the other
     long long u = w.u, first = w.first;
-    int b = w.b;
-    bool run_first = true;
-    while (u < u1) {
-        const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-        const int tiles = (len + S::TILE - 1) / S::TILE;
-        if (u - first >= static_cast<long long>(tiles) * pairs) {
+    int b = w.b, len, tiles, t0, t1, hk, head0, heads, tok0, ng;
+    auto find = [&]() {                              // the pair that unit u lies in
+        for (;;) {
+            len = kv_len(a.c, a.lens, b, &g_decode_err);
+            tiles = (len + S::TILE - 1) / S::TILE;
+            if (u - first < static_cast<long long>(tiles) * pairs) break;
             first += static_cast<long long>(tiles) * pairs;
             ++b;
-            continue;
         }
         const int pair = static_cast<int>(div_up_to(u - first, tiles));
-        const int t0 = static_cast<int>((u - first) - static_cast<long long>(pair) * tiles);
-        const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + (u1 - u)));
-        const int hk = pair / a.chunks, ch = pair - hk * a.chunks;
-        const int head0 = hk * a.G + ch * MR;                    // first query head of the group
-        const int heads = min(MR, a.G - ch * MR);
-
+        t0 = static_cast<int>((u - first) - static_cast<long long>(pair) * tiles);
+        t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + (u1 - u)));
+        hk = pair / a.chunks;
+        const int ch = pair - hk * a.chunks;
+        head0 = hk * a.G + ch * MR;                  // first query head of the group
+        heads = min(MR, a.G - ch * MR);
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
-        const int tok0 = t0 * S::TILE + warp * S::GRAN;
-        const int ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
-        uint32_t bad = 0;                                        // halves (2 bits a stage) whose page is not one
-        // q: column g of the products' second operand (asked for first: all of a pair's first reads
-        // are then on their way together)
-        uint32_t qb[NH][KS][2];
-        {
-            const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
-            auto word = [&](int ks, int half) {                  // channels of k = 2q (+ 8 half), in pairs
-                if constexpr (KIND < 2) return ks * 8 + q + half * 4;
-                else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
-            };
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
-        }
-        // pages of the granules that are loaded next: read two granules ahead, so that no load waits for them
+        tok0 = t0 * S::TILE + warp * S::GRAN;
+        ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
+    };
+    uint32_t bad;                                    // halves (2 bits a stage) whose page is not one
+    uint32_t qb[NH][KS][2];                          // q: column g of the products' second operand
+    int next[2][HALVES];                             // pages of the granules that are loaded next
+    auto look = [&](int j, int (&to)[HALVES]) {
         const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
-        int next[2][HALVES];
-        auto look = [&](int j, int (&to)[HALVES]) {
 #pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf) {
-                const int t = tok0 + j * S::TILE + hf * 16;
-                to[hf] = t < len ? __ldg(table + kv_page_of(a.c, t)) : 0;
+        for (int hf = 0; hf < HALVES; ++hf) {
+            const int t = tok0 + j * S::TILE + hf * 16;
+            to[hf] = t < len ? __ldg(table + kv_page_of(a.c, t)) : 0;
+        }
+    };
+    auto load = [&](int j, int stage) {
+        const int tok = tok0 + j * S::TILE;
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+            const int t = tok + hf * 16;
+            const int left = len - t;
+            int page = next[0][hf];
+            next[0][hf] = next[1][hf];
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
+                atomicOr(&g_decode_err, 1u);
+                page = -1;
             }
+            const int nv = page < 0 ? 0 : max(0, min(16, left));
+            const uint32_t bit = 1u << (stage * 2 + hf);
+            bad = page < 0 ? bad | bit : bad & ~bit;
+            const size_t row = nv == 0 ? 0 : kv_row(a.c, page, hk, t);
+            const uint8_t *k = static_cast<const uint8_t *>(a.c.K) + row * S::ROW + lane * 16;
+            const uint8_t *v = static_cast<const uint8_t *>(a.c.V) + row * S::ROW + lane * 16;
+            const uint32_t dst = load_lane + stage * S::STAGE + hf * HALF;
+            if (nv == 16) {
+                load_half<D, KIND>(dst, dst + S::GRAN * S::ROW, k, v, std::make_integer_sequence<int, HALF / 512>());
+            } else {
+                // rows past the end are zeros: what the pool holds there is never looked at
+                const uint32_t k0 = smem_u32(ring) + stage * S::STAGE + hf * HALF;
+#pragma unroll
+                for (int i = 0; i < HALF / 512; ++i) {
+                    const int r = i * (32 / S::CPR) + lane / S::CPR;
+                    const uint32_t at = k0 + chunk_at<D, KIND>(r, lane % S::CPR);
+                    const uint8_t *ks = r < nv ? k + i * 512 : static_cast<const uint8_t *>(a.c.K);
+                    const uint8_t *vs = r < nv ? v + i * 512 : static_cast<const uint8_t *>(a.c.V);
+                    cp_async16(at, ks, r < nv);
+                    cp_async16(at + S::GRAN * S::ROW, vs, r < nv);
+                }
+            }
+            if constexpr (KIND >= 2) {
+                const int r = lane & 15;
+                const float *sc = (lane < 16 ? a.c.sK : a.c.sV) + row;
+                const uint32_t at = smem_u32(ring) + stage * S::STAGE + 2 * S::GRAN * S::ROW + ((lane >> 4) * S::GRAN + hf * 16 + r) * 4;
+                cp_async4(at, sc + (r < nv ? r : 0), r < nv);
+            }
+        }
+        look(j + 2, next[1]);
+    };
+    // A pair's first reads, all on their way together: q, the pages of two granules, the ring's rows.
+    // The ring has to be idle.
+    auto begin = [&]() {
+        const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
+        auto word = [&](int ks, int half) {          // channels of k = 2q (+ 8 half), in pairs
+            if constexpr (KIND < 2) return ks * 8 + q + half * 4;
+            else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
         };
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
+        bad = 0;
         look(0, next[0]);
         look(1, next[1]);
-        auto load = [&](int j, int stage) {
-            const int tok = tok0 + j * S::TILE;
-#pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf) {
-                const int t = tok + hf * 16;
-                const int left = len - t;
-                int page = next[0][hf];
-                next[0][hf] = next[1][hf];
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
-                    atomicOr(&g_decode_err, 1u);
-                    page = -1;
-                }
-                const int nv = page < 0 ? 0 : max(0, min(16, left));
-                const uint32_t bit = 1u << (stage * 2 + hf);
-                bad = page < 0 ? bad | bit : bad & ~bit;
-                const size_t row = nv == 0 ? 0 : kv_row(a.c, page, hk, t);
-                const uint8_t *k = static_cast<const uint8_t *>(a.c.K) + row * S::ROW + lane * 16;
-                const uint8_t *v = static_cast<const uint8_t *>(a.c.V) + row * S::ROW + lane * 16;
-                const uint32_t dst = load_lane + stage * S::STAGE + hf * HALF;
-                if (nv == 16) {
-                    load_half<D, KIND>(dst, dst + S::GRAN * S::ROW, k, v, std::make_integer_sequence<int, HALF / 512>());
-                } else {
-                    // rows past the end are zeros: what the pool holds there is never looked at
-                    const uint32_t k0 = smem_u32(ring) + stage * S::STAGE + hf * HALF;
-#pragma unroll
-                    for (int i = 0; i < HALF / 512; ++i) {
-                        const int r = i * (32 / S::CPR) + lane / S::CPR;
-                        const uint32_t at = k0 + chunk_at<D, KIND>(r, lane % S::CPR);
-                        const uint8_t *ks = r < nv ? k + i * 512 : static_cast<const uint8_t *>(a.c.K);
-                        const uint8_t *vs = r < nv ? v + i * 512 : static_cast<const uint8_t *>(a.c.V);
-                        cp_async16(at, ks, r < nv);
-                        cp_async16(at + S::GRAN * S::ROW, vs, r < nv);
-                    }
-                }
-                if constexpr (KIND >= 2) {
-                    const int r = lane & 15;
-                    const float *sc = (lane < 16 ? a.c.sK : a.c.sV) + row;
-                    const uint32_t at = smem_u32(ring) + stage * S::STAGE + 2 * S::GRAN * S::ROW + ((lane >> 4) * S::GRAN + hf * 16 + r) * 4;
-                    cp_async4(at, sc + (r < nv ? r : 0), r < nv);
-                }
-            }
-            look(j + 2, next[1]);
-        };
 #pragma unroll
         for (int j = 0; j < S::STAGES - 1; ++j) {
             if (j < ng) load(j, j);
             cp_commit();
         }
+    };
 
+    find();
+    begin();
+    for (bool run_first = true;; run_first = false) {
         float qs[NH][2];                                         // log2 units' factor of heads 2q, 2q + 1
         {
 #pragma unroll
@@ -659,6 +679,19 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
         cp_wait<0>();
         __syncwarp();
 
+        // what the end of this pair needs, and the next pair's first reads on their way meanwhile
+        const bool whole = t0 == 0 && t1 == tiles;
+        // a run's first pair that began in an earlier run goes to place 0, one that goes on to place 1
+        const int place = run_first && t0 > 0 ? 0 : 1;
+        const size_t out0 = static_cast<size_t>(b) * a.Hq + head0;
+        const int outs = heads;
+        u += t1 - t0;
+        const bool more = u < u1;
+        if (more) {
+            find();
+            begin();
+        }
+
         // join the four warps, in their order
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
@@ -671,11 +704,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                     s_l[warp][nh * 8 + 2 * q + e] = l[nh][e];
                 }
             }
-        // Each warp's sums, (MR, D) floats, in its own idle ring.  Heads PITCH apart, and in 8 bits the
+        // Each warp's sums, (MR, D) floats, in the last stage of its own ring.  Heads PITCH apart, and in 8 bits the
         // channels in the order (k, g) of D / 8 g + k, put a store's 32 lanes into 32 banks.
         constexpr int PITCH = D + 4;
-        static_assert(MR * PITCH * 4 <= S::STAGES * S::STAGE, "the sums do not fit the ring");
-        float *so = reinterpret_cast<float *>(ring);
+        constexpr int SUMS = (S::STAGES - 1) * S::STAGE;
+        static_assert(SUMS + MR * PITCH * 4 <= S::RING, "the sums do not fit the last stage");
+        float *so = reinterpret_cast<float *>(ring + SUMS);
 #pragma unroll
         for (int jn = 0; jn < KS; ++jn)
 #pragma unroll
@@ -684,10 +718,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                 for (int i = 0; i < 4; ++i)
                     so[(nh * 8 + 2 * q + (i & 1)) * PITCH + jn * 16 + 8 * (i >> 1) + g] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == tiles;
-        // a run's first pair that began in an earlier run goes to place 0, one that goes on to place 1
-        const int place = run_first && t0 > 0 ? 0 : 1;
-        for (int idx = tid; idx < heads * (D / 2); idx += kDecThreads) {
+        for (int idx = tid; idx < outs * (D / 2); idx += kDecThreads) {
             const int r = idx / (D / 2), x2 = idx % (D / 2);
             // two channels c, c + 1 and their places
             const int c = KIND < 2 ? 2 * x2 : D / 8 * (x2 & 7) + 2 * (x2 >> 3);
@@ -700,12 +731,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
 #pragma unroll
             for (int x = 0; x < kDecWarps; ++x) {
                 const float f = ex2_approx(s_m[x][r] - ref);
-                const float *from = reinterpret_cast<const float *>(smem + x * (S::STAGES * S::STAGE));
+                const float *from = reinterpret_cast<const float *>(smem + x * S::RING + SUMS);
                 o0 += f * from[p0];
                 o1 += f * from[p1];
                 sum += f * s_l[x][r];
             }
-            const size_t head = static_cast<size_t>(b) * a.Hq + head0 + r;
+            const size_t head = out0 + r;
             if (whole) {
                 const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
                 store_out(a, head * D + c, o0 * inv, o1 * inv);
@@ -725,9 +756,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND>::CTAS) decod
                 }
             }
         }
-        __syncthreads();                                         // before the stages are filled again
-        u += t1 - t0;
-        run_first = false;
+        if (!more) break;
+        __syncthreads();                                         // before the last stage is filled again
     }
 }
 
@@ -910,7 +940,7 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     const int row = c.d * (c.kind == SAGE_KV_16 ? 2 : 1);
     // one resident wave; never more CTAs than there can be tiles
     p.tile = decode_tile(row);
-    long long n = kSMs * (row == 256 ? 2 : 3);
+    long long n = kSMs * decode_ctas(row, c.d, p.mr);
     const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + p.tile - 1) / p.tile);
     if (n > tiles) n = tiles;
     p.ctas = static_cast<int>(n);
@@ -934,7 +964,7 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
 
 template <int D, int KIND, int MR>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
-    using S = DecodeShape<D, KIND>;
+    using S = DecodeShape<D, KIND, MR>;
     static bool raised[16] = {false};
     cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR>), S::SMEM, raised);
     if (e != cudaSuccess) return e;
