@@ -27,7 +27,7 @@ struct AppendArgs {
 };
 
 template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[8]) {
+__device__ __forceinline__ void unpack16(const uint4 u, f2 (&v)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -36,50 +36,54 @@ __device__ __forceinline__ void unpack16(const uint4 u, float (&v)[8]) {
             f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         else
             f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[i] = f2{f.x, f.y};
     }
 }
 
-// fl32(x / delta) for two values, r = fl32(1 / delta): Markstein's correction of a quotient
-// ("Computation of elementary functions on the IBM RISC System/6000 processor", 1990), twice.  With
-// significands x, delta in [1, 2) and u = 2^-24, r is off by at most delta u / 2 of itself and
-// q0 = fl(x r) by at most 1.5 units in the last place (ulp); the residual x - q delta is exact, so each
-// correction leaves the quotient times its error times r's, and a rounding.  After the first the
-// error is below 0.5 ulp (1 + 3 u); the second then rounds a value that is within
-// 0.5 (1 + 3 u) delta u / 2 ulp of x / delta, and x / delta is no nearer than u 2^24 / delta * u ulp to a
-// value half way between two floats (25 bits times delta's 24 never make x's 24): less for every
-// delta < 2, so it rounds as x / delta does.  Scales where a residual could underflow take the
-// division.
-__device__ __forceinline__ f2 quotient2(f2 x, float delta, float r) {
-    const f2 d{-delta, -delta}, rr{r, r};
-    f2 q = mul2(x, rr);
-    q = fma2(fma2(q, d, x), rr, q);
-    return fma2(fma2(q, d, x), rr, q);
+// fl32(x / d) for two values, r = fl32(1 / d): Markstein's correction of a quotient ("Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  The residual x - q d is
+// exact, so a correction leaves the quotient's error times r's, and one rounding.
+//   ONCE: for x of at most 11 significant bits (a 16-bit value), one correction of q0 = fl(x r) gives
+//   fl32(x / d) for every pair of significands (all 2^10 x 2^23 checked).
+//   Otherwise two.  With significands x, d in [1, 2) and u = 2^-24: r is off by at most d u / 2 of itself,
+//   q0 by at most 1.5 units in the last place (ulp), and the first correction by less than
+//   0.5 + 3 u ulp; the second then rounds a value within (0.5 + 3 u) d u / 2 ulp of x / d, and
+//   x / d is at least u / d ulp from any value half way between two floats (25 bits times d's 24
+//   never make x's 24).  (0.5 + 3 u) d / 2 < 1 / d for every d < 2: it rounds as x / d does.
+// d and r are pairs (of a value twice, or of two rows' scales).
+template <bool ONCE>
+__device__ __forceinline__ f2 quotient2(f2 x, f2 d, f2 r) {
+    const f2 nd{-d.x, -d.y};
+    f2 q = mul2(x, r);
+    if constexpr (!ONCE) q = fma2(fma2(q, nd, x), r, q);
+    return fma2(fma2(q, nd, x), r, q);
 }
 
-// One row's 8 values of a lane, and the largest of the row -> 8 codes and the row's scale.
+// m / M of two rows, M = 127 or 448.  (Out of the range where the residuals are normal: divisions.)
 template <int KIND>
-__device__ __forceinline__ uint2 kv_codes(const float (&x)[8], float m, float *delta_out) {
-    const float delta = __fdiv_rn(m, KIND == SAGE_KV_INT8 ? 127.0f : 448.0f);
-    *delta_out = delta;
+__device__ __forceinline__ f2 scales_of(f2 m) {
+    constexpr float M = KIND == SAGE_KV_INT8 ? 127.0f : 448.0f, r = 1.0f / M;
+    if (fminf(m.x, m.y) >= 0x1p-80f && fmaxf(m.x, m.y) <= 0x1p96f) return quotient2<false>(m, f2{M, M}, f2{r, r});
+    return f2{__fdiv_rn(m.x, M), __fdiv_rn(m.y, M)};
+}
+
+// One row's 8 values of a lane, and the row's scale -> 8 codes.
+template <int KIND, bool ONCE>
+__device__ __forceinline__ uint2 kv_codes(const f2 (&x)[4], float delta) {
     f2 y[4];
     if (delta >= 0x1p-90f && delta <= 0x1p90f) {
         const float r = __frcp_rn(delta);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = quotient2(f2{x[2 * i], x[2 * i + 1]}, delta, r);
+        for (int i = 0; i < 4; ++i) y[i] = quotient2<ONCE>(x[i], f2{delta, delta}, f2{r, r});
     } else if (delta == 0.0f) {
         return make_uint2(0u, 0u);
     } else {
         // a subnormal delta can be rounded so far down that the quotient exceeds 127 (E4M3 saturates)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[i].x = fminf(fmaxf(__fdiv_rn(x[2 * i], delta), -448.0f), 448.0f);
-            y[i].y = fminf(fmaxf(__fdiv_rn(x[2 * i + 1], delta), -448.0f), 448.0f);
-            if (KIND == SAGE_KV_INT8) {
-                y[i].x = fminf(fmaxf(y[i].x, -127.0f), 127.0f);
-                y[i].y = fminf(fmaxf(y[i].y, -127.0f), 127.0f);
-            }
+            constexpr float top = KIND == SAGE_KV_INT8 ? 127.0f : 448.0f;
+            y[i].x = fminf(fmaxf(__fdiv_rn(x[i].x, delta), -top), top);
+            y[i].y = fminf(fmaxf(__fdiv_rn(x[i].y, delta), -top), top);
         }
     }
     uint32_t w[2];
@@ -99,15 +103,26 @@ __device__ __forceinline__ uint2 kv_codes(const float (&x)[8], float m, float *d
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ float largest8(const float (&x)[8]) {
-    return fmaxf(max3f(max3f(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]), fabsf(x[4])),
-                 max3f(fabsf(x[5]), fabsf(x[6]), fabsf(x[7])));
+// max(|a|, |b|), under some sign
+__device__ __forceinline__ float larger(float a, float b) {
+    float d;
+    asm("max.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// The largest magnitude of a row that LANES lanes hold.  (Shuffles: a reduction instruction under
+// half-warp masks runs once a half, 83 against 76 us for 8192-token prompts.)
+template <int LANES>
+__device__ __forceinline__ float largest(const f2 (&x)[4]) {
+    float m = larger(larger(larger(x[0].x, x[0].y), larger(x[1].x, x[1].y)), larger(larger(x[2].x, x[2].y), larger(x[3].x, x[3].y)));
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return fabsf(m);
 }
 
 // grid: (row groups of a head, B * H).  ROWS rows of each lane group are loaded before any is
 // written.
-template <typename T, int KIND, int D, int ROWS>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+template <typename T, int KIND, int D, int ROWS, bool SMOOTH>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a) {
     constexpr int LANES = D / 8, GROUPS = kAppendThreads / LANES;
     const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -158,28 +173,25 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
                 reinterpret_cast<uint4 *>(a.c.V)[row[r] * LANES + lane] = v[r];
             }
     } else {
-        float mu[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (a.mu) {
+        f2 mu[4];
+        if constexpr (SMOOTH) {
             const float4 *m = reinterpret_cast<const float4 *>(a.mu + static_cast<size_t>(bh) * D + lane * 8);
             const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
-            mu[0] = m0.x; mu[1] = m0.y; mu[2] = m0.z; mu[3] = m0.w;
-            mu[4] = m1.x; mu[5] = m1.y; mu[6] = m1.z; mu[7] = m1.w;
+            mu[0] = f2{m0.x, m0.y}; mu[1] = f2{m0.z, m0.w}; mu[2] = f2{m1.x, m1.y}; mu[3] = f2{m1.z, m1.w};
         }
         // every lane of a warp takes part in the shuffles, rows or none
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            float x[8], y[8], dk, dv;
+            f2 x[4], y[4];
             unpack16<T>(k[r], x);
             unpack16<T>(v[r], y);
+            if constexpr (SMOOTH) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], mu[i]);
-            float mk = largest8(x), mv = largest8(y);
-#pragma unroll
-            for (int o = 1; o < LANES; o <<= 1) {
-                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+                for (int i = 0; i < 4; ++i) x[i] = sub2(x[i], mu[i]);
             }
-            const uint2 ck = kv_codes<KIND>(x, mk, &dk), cv = kv_codes<KIND>(y, mv, &dv);
+            const f2 delta = scales_of<KIND>(f2{largest<LANES>(x), largest<LANES>(y)});
+            const float dk = delta.x, dv = delta.y;
+            const uint2 ck = kv_codes<KIND, !SMOOTH>(x, dk), cv = kv_codes<KIND, true>(y, dv);
             if (row[r] >= 0) {
                 reinterpret_cast<uint2 *>(a.c.K)[row[r] * LANES + lane] = ck;
                 reinterpret_cast<uint2 *>(a.c.V)[row[r] * LANES + lane] = cv;
@@ -192,22 +204,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     }
 }
 
-template <typename T, int KIND, int D>
+template <typename T, int KIND, int D, bool SMOOTH>
 static void launch_append_k(const AppendArgs &a, cudaStream_t st) {
     constexpr int GROUPS = kAppendThreads / (D / 8);
     const unsigned bh = static_cast<unsigned>(a.c.B) * a.c.H;
     if (a.T <= GROUPS) {
-        kv_append_kernel<T, KIND, D, 1><<<dim3(1, bh), kAppendThreads, 0, st>>>(a);
+        kv_append_kernel<T, KIND, D, 1, SMOOTH><<<dim3(1, bh), kAppendThreads, 0, st>>>(a);
     } else {
         const unsigned x = (a.T + GROUPS * 4 - 1) / (GROUPS * 4);
-        kv_append_kernel<T, KIND, D, 4><<<dim3(x, bh), kAppendThreads, 0, st>>>(a);
+        kv_append_kernel<T, KIND, D, 4, SMOOTH><<<dim3(x, bh), kAppendThreads, 0, st>>>(a);
     }
 }
 
 template <typename T, int KIND>
 static void launch_append_d(const AppendArgs &a, int d, cudaStream_t st) {
-    if (d == 64) launch_append_k<T, KIND, 64>(a, st);
-    else launch_append_k<T, KIND, 128>(a, st);
+    if constexpr (KIND != SAGE_KV_16) {
+        if (a.mu) {
+            if (d == 64) launch_append_k<T, KIND, 64, true>(a, st);
+            else launch_append_k<T, KIND, 128, true>(a, st);
+            return;
+        }
+    }
+    if (d == 64) launch_append_k<T, KIND, 64, false>(a, st);
+    else launch_append_k<T, KIND, 128, false>(a, st);
 }
 
 static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st) {
