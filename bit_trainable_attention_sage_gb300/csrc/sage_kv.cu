@@ -249,15 +249,15 @@ static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st
 //
 // One cluster of C CTAs a (sequence, kv head), each with a contiguous C-th of the slots: scores and
 // positions are read once, the keys stay in shared memory (CACHED; rows of more than
-// 8 * 48 K slots read them again each pass), histograms and counts are added up over the cluster
+// 8 * 20 K slots read them again each pass), histograms and counts are added up over the cluster
 // through distributed shared memory, and the same CTAs then move the rows.  One launch, and with
 // C up to 8 a few long rows still use many SMs.
 // ---------------------------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelMaxKeys = 48 * 1024;       // of a CTA in shared memory
+constexpr int kSelMaxKeys = 20 * 1024;       // of a CTA in shared memory; two CTAs an SM
 
 struct EvictArgs {
     KvView c;
@@ -289,61 +289,79 @@ __device__ __forceinline__ int cluster_word(const int *p, int rank) {
     return v;
 }
 
-// One row moved by ROW_BYTES / 16 lanes.
+// and the four (16-byte aligned)
+__device__ __forceinline__ int4 cluster_words(const int *p, int rank) {
+    uint32_t at;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Moves first, first + step, ... of a row, kSelThreads at a time: a thread looks up one move's rows and
+// moves what is a word (scales, score, position), then ROW_BYTES / 16 lanes copy a row's K and V, whose
+// addresses all wait in shared memory.
 template <int ROW_BYTES>
-__device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, int h, int first, int step, int m, int lane) {
-    constexpr int CHUNKS = ROW_BYTES / 16, UNROLL = 2;
+__device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, int h, int begin, int end, size_t (*rows)[kSelThreads]) {
+    constexpr int CHUNKS = ROW_BYTES / 16, GROUPS = kSelThreads / CHUNKS, UNROLL = 4;
     const size_t list = static_cast<size_t>(bh) * a.max_moves, base = static_cast<size_t>(bh) * a.c.cap;
-    uint4 *K = static_cast<uint4 *>(a.c.K), *V = static_cast<uint4 *>(a.c.V);
-    for (int i0 = first; i0 < m; i0 += step * UNROLL) {
-        size_t rd[UNROLL], rs[UNROLL];
-        int d[UNROLL], s[UNROLL];
-        bool ok[UNROLL];
-        uint4 k[UNROLL], v[UNROLL];
-#pragma unroll
-        for (int x = 0; x < UNROLL; ++x) {
-            const int i = i0 + x * step;
-            ok[x] = i < m;
-            d[x] = ok[x] ? a.dst[list + i] : 0;
-            s[x] = ok[x] ? a.src[list + i] : 0;
-        }
-#pragma unroll
-        for (int x = 0; x < UNROLL; ++x) {
-            const int pd = ok[x] ? kv_page(a.c, b, d[x], &g_kv_err) : -1, ps = ok[x] ? kv_page(a.c, b, s[x], &g_kv_err) : -1;
-            ok[x] = pd >= 0 && ps >= 0;
-            rd[x] = ok[x] ? kv_row(a.c, pd, h, d[x]) : 0;
-            rs[x] = ok[x] ? kv_row(a.c, ps, h, s[x]) : 0;
-        }
-#pragma unroll
-        for (int x = 0; x < UNROLL; ++x)
-            if (ok[x]) {
-                k[x] = K[rs[x] * CHUNKS + lane];
-                v[x] = V[rs[x] * CHUNKS + lane];
+    const int tid = threadIdx.x, lane = tid % CHUNKS, group = tid / CHUNKS;
+    uint4 *K = static_cast<uint4 *>(a.c.K) + lane, *V = static_cast<uint4 *>(a.c.V) + lane;
+    constexpr size_t kNone = ~static_cast<size_t>(0);
+    for (int i0 = begin; i0 < end; i0 += kSelThreads) {
+        const int n = min(kSelThreads, end - i0);
+        if (tid < n) {
+            const int d = a.dst[list + i0 + tid], s = a.src[list + i0 + tid];
+            const int pd = kv_page(a.c, b, d, &g_kv_err), ps = kv_page(a.c, b, s, &g_kv_err);
+            size_t rd = kNone, rs = 0;
+            if (pd >= 0 && ps >= 0) {
+                rd = kv_row(a.c, pd, h, d);
+                rs = kv_row(a.c, ps, h, s);
+                const float score = a.c.score[base + s];
+                const int pos = a.c.pos[base + s];
+                if (a.c.sK) {
+                    const float sk = a.c.sK[rs], sv = a.c.sV[rs];
+                    a.c.sK[rd] = sk;
+                    a.c.sV[rd] = sv;
+                }
+                a.c.score[base + d] = score;
+                a.c.pos[base + d] = pos;
             }
+            rows[0][tid] = rd;
+            rows[1][tid] = rs;
+        }
+        __syncthreads();
+        for (int i = group; i < n; i += GROUPS * UNROLL) {
+            uint4 k[UNROLL], v[UNROLL];
+            size_t rd[UNROLL];
 #pragma unroll
-        for (int x = 0; x < UNROLL; ++x)
-            if (ok[x]) {
-                K[rd[x] * CHUNKS + lane] = k[x];
-                V[rd[x] * CHUNKS + lane] = v[x];
-                if (lane == 0) {
-                    a.c.score[base + d[x]] = a.c.score[base + s[x]];
-                    a.c.pos[base + d[x]] = a.c.pos[base + s[x]];
-                    if (a.c.sK) {
-                        a.c.sK[rd[x]] = a.c.sK[rs[x]];
-                        a.c.sV[rd[x]] = a.c.sV[rs[x]];
-                    }
+            for (int x = 0; x < UNROLL; ++x) {
+                const int j = i + x * GROUPS;
+                rd[x] = j < n ? rows[0][j] : kNone;
+                if (rd[x] != kNone) {
+                    const size_t rs = rows[1][j] * CHUNKS;
+                    k[x] = K[rs];
+                    v[x] = V[rs];
                 }
             }
+#pragma unroll
+            for (int x = 0; x < UNROLL; ++x)
+                if (rd[x] != kNone) {
+                    K[rd[x] * CHUNKS] = k[x];
+                    V[rd[x] * CHUNKS] = v[x];
+                }
+        }
+        __syncthreads();
     }
 }
 
 // grid: (cluster, B * H)
 template <bool CACHED, int ROW_BYTES>
-__global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ uint32_t s_key[];
-    __shared__ int hist[3][kSelBins];
+    __shared__ __align__(16) int hist[3][kSelBins];
     __shared__ int s_warp[2][kSelWarps];
-    __shared__ int s_count[4];                   // of this CTA, read by the others: equal keys; freed, movers
+    __shared__ __align__(16) int s_count[4];                   // of this CTA, read by the others: equal keys; freed, movers
     __shared__ int s_digit, s_above, s_here;
     const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H, rank = blockIdx.x;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -365,17 +383,27 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_cons
         else return evict_key(a.c.score[base + lo + s], a.c.pos[base + lo + s] >= newest);
     };
     // first digit: 11 bits.  Recent tokens share one key: counted by the warp.
-    for (int i = 0; i < its; ++i) {
-        const int s = mine + i * 32;
-        uint32_t k = 0;
-        const bool in = s < len;
-        if (in) {
-            k = evict_key(a.c.score[base + lo + s], a.c.pos[base + lo + s] >= newest);
-            if constexpr (CACHED) s_key[s] = k;
+    constexpr int BATCH = 8;                     // reads in flight together
+    for (int i0 = 0; i0 < its; i0 += BATCH) {
+        float score[BATCH];
+        int pos[BATCH];
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) {
+            const int s = mine + (i0 + x) * 32;
+            const bool in = i0 + x < its && s < len;
+            score[x] = in ? a.c.score[base + lo + s] : 0.0f;
+            pos[x] = in ? a.c.pos[base + lo + s] : 0;
         }
-        const uint32_t top = __ballot_sync(0xffffffffu, in && k == 0xFFFFFFFFu);
-        if (in && k != 0xFFFFFFFFu) atomicAdd(&hist[0][k >> 21], 1);
-        if (lane == 0 && top) atomicAdd(&hist[0][kSelBins - 1], __popc(top));
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) {
+            const int s = mine + (i0 + x) * 32;
+            const bool in = i0 + x < its && s < len;
+            const uint32_t k = evict_key(score[x], pos[x] >= newest);
+            if (CACHED && in) s_key[s] = k;
+            const uint32_t top = __ballot_sync(0xffffffffu, in && k == 0xFFFFFFFFu);
+            if (in && k != 0xFFFFFFFFu) atomicAdd(&hist[0][k >> 21], 1);
+            if (lane == 0 && top) atomicAdd(&hist[0][kSelBins - 1], __popc(top));
+        }
     }
     // the budget-th largest key: `T` its leading digits, `need` its rank among the keys that share them
     uint32_t T = 0;
@@ -400,16 +428,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_cons
         }
         if (a.cluster > 1) cluster_sync();
         else __syncthreads();
-        // thread t holds digits bins - 1 - 2t and bins - 2 - 2t, in descending order
-        int c[2] = {0, 0};
-        const int d0 = bins - 1 - 2 * tid;
+        // thread t holds the DIG digits from bins - 1 - DIG t down
+        constexpr int DIG = kSelBins / kSelThreads;
+        static_assert(DIG == 4, "a thread reads its digits as one vector");
+        int c[DIG] = {};
+        const int d0 = bins - 1 - DIG * tid;
         if (d0 > 0) {
-            for (int r = 0; r < a.cluster; ++r) {
-                c[0] += a.cluster > 1 ? cluster_word(&hist[pass][d0], r) : hist[pass][d0];
-                c[1] += a.cluster > 1 ? cluster_word(&hist[pass][d0 - 1], r) : hist[pass][d0 - 1];
-            }
+            int4 v[kSelMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kSelMaxCluster; ++r)
+                if (r < a.cluster) v[r] = cluster_words(&hist[pass][d0 - 3], r);
+#pragma unroll
+            for (int r = 0; r < kSelMaxCluster; ++r)
+                if (r < a.cluster) {
+                    c[0] += v[r].w; c[1] += v[r].z; c[2] += v[r].y; c[3] += v[r].x;
+                }
         }
-        int incl = c[0] + c[1];
+        const int sum = c[0] + c[1] + c[2] + c[3];
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -417,10 +453,11 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_cons
         }
         if (lane == 31) s_warp[0][warp] = incl;
         __syncthreads();
-        int above = incl - c[0] - c[1];
-        for (int w = 0; w < warp; ++w) above += s_warp[0][w];
+        int above = incl - sum;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int w = 0; w < kSelWarps; ++w) above += w < warp ? s_warp[0][w] : 0;
+#pragma unroll
+        for (int i = 0; i < DIG; ++i) {
             if (above < need && need <= above + c[i]) {
                 s_digit = d0 - i;
                 s_above = above;
@@ -433,6 +470,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_cons
         need -= s_above;
         equal = s_here;
         __syncthreads();
+        if (equal == need) break;                // all that share these digits stay: T is their lower bound
     }
     // Of the `equal` keys equal to T, the first `need` in slot order stay.  How many lie before this
     // warp's slots matters only when not all of them do.
@@ -482,32 +520,34 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_kernel(const __grid_cons
                 s_warp[1][warp] = moved;
             }
             __syncthreads();
-            if (tid < 2) {
-                int sum = 0;
-                for (int w = 0; w < kSelWarps; ++w) sum += s_warp[tid][w];
-                s_count[2 + tid] = sum;
+            if (warp < 2) {
+                const int sum = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? s_warp[warp][lane] : 0);
+                if (lane == 0) s_count[2 + warp] = sum;
             }
             if (a.cluster > 1) cluster_sync();
             else __syncthreads();
             for (int r = 0; r < a.cluster; ++r) {
-                const int f = cluster_word(&s_count[2], r), m = cluster_word(&s_count[3], r);
+                const int4 n4 = cluster_words(s_count, r);
+                const int f = n4.z, m = n4.w;
                 if (r < rank) {
                     at[0] += f;
                     at[1] += m;
                 }
                 moves += m;
             }
-            for (int w = 0; w < warp; ++w) {
-                at[0] += s_warp[0][w];
-                at[1] += s_warp[1][w];
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w) {
+                at[0] += w < warp ? s_warp[0][w] : 0;
+                at[1] += w < warp ? s_warp[1][w] : 0;
             }
         }
     }
     // every CTA's part of the lists is written, every read of another's shared memory done
     if (a.cluster > 1) cluster_sync();
     else __syncthreads();
-    constexpr int CHUNKS = ROW_BYTES / 16, GROUPS = kSelThreads / CHUNKS;
-    evict_moves<ROW_BYTES>(a, bh, b, h, rank * GROUPS + tid / CHUNKS, a.cluster * GROUPS, moves, tid % CHUNKS);
+    const int share = (moves + a.cluster - 1) / a.cluster;
+    static_assert(2 * kSelThreads * sizeof(size_t) <= sizeof(hist), "the rows' places do not fit the histograms");
+    evict_moves<ROW_BYTES>(a, bh, b, h, rank * share, min(moves, (rank + 1) * share), reinterpret_cast<size_t(*)[kSelThreads]>(&hist[0][0]));
 }
 
 static int evict_max_moves(const sage_kv &c, int budget) {
@@ -516,7 +556,7 @@ static int evict_max_moves(const sage_kv &c, int budget) {
     return m < 0 ? 0 : (m + 3) & ~3;
 }
 
-// Clusters as large as 8192 slots a CTA ask for, but no more than give every SM a CTA.
+// Clusters as large as 4096 slots a CTA ask for, but no more than give every SM two CTAs.
 template <bool CACHED, int ROW_BYTES>
 static cudaError_t launch_evict_c(const EvictArgs &a, int rows, size_t smem, cudaStream_t st) {
     if (CACHED) {
@@ -543,8 +583,8 @@ static cudaError_t launch_evict_c(const EvictArgs &a, int rows, size_t smem, cud
 template <int ROW_BYTES>
 static cudaError_t launch_evict(EvictArgs a, int rows, cudaStream_t st) {
     int c = 1;
-    while (c < kSelMaxCluster && c * 8192 < a.c.cap) c *= 2;
-    while (c > 1 && static_cast<long long>(rows) * c > 152 && c / 2 * kSelMaxKeys >= a.c.cap) c /= 2;
+    while (c < kSelMaxCluster && c * 4096 < a.c.cap) c *= 2;
+    while (c > 1 && static_cast<long long>(rows) * c > 304 && c / 2 * kSelMaxKeys >= a.c.cap) c /= 2;
     a.cluster = c;
     // keys of a CTA, rounded as the kernel rounds its share of the longest row
     const size_t keys = ((static_cast<size_t>(a.c.cap) + c - 1) / c + kSelThreads - 1) / kSelThreads * kSelThreads;
