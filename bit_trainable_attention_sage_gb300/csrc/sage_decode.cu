@@ -13,6 +13,8 @@
 // in one CTA's run is finished there; the others leave their unnormalised sums, maxima and sums
 // of exponentials in the workspace (two places a CTA: a run's first and last pair), and a second
 // kernel joins them in order, so results do not depend on the order in which CTAs run.
+// Short caches (ONE) take a cluster of up to 8 CTAs a pair instead, joined through distributed
+// shared memory: one launch, no workspace for sums, and no length but its own to read.
 //
 // Inside a CTA four warps each take a quarter of a tile (a granule) and never wait for one another:
 // each keeps its own ring of cp.async stages in shared memory, its own running maximum, sum and
@@ -44,6 +46,7 @@ __device__ unsigned int g_decode_err = 0;   // 1: a page or length was out of ra
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kSMs = 152;
+constexpr int kDecCluster = 8;               // CTAs of a cluster at most
 
 // pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3
 template <int D, int KIND, int MR = 8>
@@ -80,6 +83,7 @@ struct DecodeArgs {
     const int *lens;
     int Hq, G, chunks;       // query heads, heads a kv head, groups of at most MR heads a kv head
     int ctas;                // CTAs that share the work (gridDim.x)
+    int cluster;             // ONE: CTAs a pair
     int tile, tile_shift;    // tokens a unit of work, 64 or 128, and their log2
     int bf16;                // type of q and O
     float sl2;               // log2(e) / sqrt(d)
@@ -194,6 +198,15 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
 }
 
 // ---- the cut of the work ---------------------------------------------------------------------
+// A pair of `tiles` tiles counts kPairUnits + tiles units, the first kPairUnits for what a pair
+// costs besides its tiles (its first reads and its end take about as long as a tile): a run over
+// many short sequences then holds fewer tiles.
+constexpr int kPairUnits = 1;
+__device__ __forceinline__ int pair_units(const DecodeArgs &a, int b) {
+    const int tiles = (kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift;
+    return tiles > 0 ? tiles + kPairUnits : 0;
+}
+
 // The number of units; where unit u lies: its sequence and that sequence's first unit.  Called by
 // a whole CTA of NT threads; `find` gives u from the total (a u outside [0, total) is not looked
 // for).
@@ -211,7 +224,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     const int b0 = min(tid * per, a.c.B), b1 = min(b0 + per, a.c.B);
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
+        mine += static_cast<long long>(pair_units(a, b)) * pairs;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -231,7 +244,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     if (u >= at && u < at + mine) {
         int b = b0;
         for (;; ++b) {
-            const long long k = static_cast<long long>((kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
+            const long long k = static_cast<long long>(pair_units(a, b)) * pairs;
             if (u < at + k) break;
             at += k;
         }
@@ -274,7 +287,7 @@ __device__ __forceinline__ void store_out(const DecodeArgs &a, size_t at, float 
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
 // ---- main kernel ------------------------------------------------------------------------------
-template <int D, int KIND, int MR>
+template <int D, int KIND, int MR, bool ONE>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND, MR>;
     constexpr bool BF16 = KIND == 1;                 // type of the products
@@ -285,46 +298,99 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & (S::ALIGN - 1));
     __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
+    __shared__ float s_part[2][MR], s_f[kDecCluster][MR];        // ONE: a CTA's M and l; factors of the cluster's
+    (void)s_part; (void)s_f;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int pairs = a.c.H * a.chunks;
     const int cta = blockIdx.x;
-    // the join may take its place on the GPU; it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // The lengths say where this CTA's pages stand, the pages where its rows: three reads one after
     // the other.  The table and q are brought into L2 meanwhile, a share by each CTA.
-    {
-        const size_t at = (static_cast<size_t>(cta) * 64 + (tid & 63)) * 128;
-        const size_t bytes = tid < 64 ? static_cast<size_t>(a.c.B) * a.c.max_pages * 4 : static_cast<size_t>(a.c.B) * a.Hq * D * 2;
-        const char *from = tid < 64 ? reinterpret_cast<const char *>(a.c.table) : static_cast<const char *>(a.Q);
-        if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + at));
+    auto fetch = [&](size_t share, const void *table, size_t table_bytes, const void *Q, size_t q_bytes) {
+        const size_t at = (share * 64 + (tid & 63)) * 128;
+        const char *from = static_cast<const char *>(tid < 64 ? table : Q);
+        if (at < (tid < 64 ? table_bytes : q_bytes)) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + at));
+    };
+    // the run [u, u1) of units (ONE: a share of one pair's tiles)
+    long long u = 0, u1 = 0, first = 0;
+    int b, rank = 0;
+    if constexpr (ONE) {
+        const int pr = cta / a.cluster;
+        rank = cta - pr * a.cluster;
+        b = pr / pairs;
+        const int pair = pr - b * pairs, hk = pair / a.chunks, h0 = hk * a.G + (pair - hk * a.chunks) * MR;
+        fetch(rank, a.c.table + static_cast<size_t>(b) * a.c.max_pages, static_cast<size_t>(a.c.max_pages) * 4,
+              static_cast<const char *>(a.Q) + (static_cast<size_t>(b) * a.Hq + h0) * D * 2, rank == 0 ? MR * D * 2 : 0);
+        if (kv_len(a.c, a.lens, b, &g_decode_err) == 0) {                               // the whole cluster alike
+            const int outs = min(MR, a.G - (h0 - hk * a.G));
+            const size_t head = static_cast<size_t>(b) * a.Hq + h0;
+            for (int i = (rank * kDecThreads + tid) * 2; i < outs * D; i += a.cluster * kDecThreads * 2) {
+                store_out(a, head * D + i, 0.0f, 0.0f);
+                if (i % D == 0) a.L[head + i / D] = -INFINITY;
+            }
+            return;
+        }
+    } else {
+        // the join may take its place on the GPU; it waits for this grid's end before it reads
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        fetch(cta, a.c.table, static_cast<size_t>(a.c.B) * a.c.max_pages * 4, a.Q, static_cast<size_t>(a.c.B) * a.Hq * D * 2);
+        // sequences without a token
+        for (int e = cta; e < a.c.B; e += gridDim.x)
+            if (kv_len(a.c, a.lens, e, &g_decode_err) == 0) {
+                const size_t head = static_cast<size_t>(e) * a.Hq;
+                for (int i = tid * 2; i < a.Hq * D; i += kDecThreads * 2) {
+                    store_out(a, head * D + i, 0.0f, 0.0f);
+                    if (i % D == 0) a.L[head + i / D] = -INFINITY;
+                }
+            }
+        const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
+            const int n = runs_of(a, total);
+            return cta < n ? run_start(total, cta, n) : total;
+        });
+        const int runs = runs_of(a, w.total);
+        if (cta >= runs) return;
+        u = w.u;
+        u1 = run_start(w.total, cta + 1, runs);
+        first = w.first;
+        b = w.b;
     }
-    const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
-        const int n = runs_of(a, total);
-        return cta < n ? run_start(total, cta, n) : total;
-    });
-    const int runs = runs_of(a, w.total);
-    if (cta >= runs) return;
-    const long long u1 = run_start(w.total, cta + 1, runs);
     // a warp's ring: stages of K rows, V rows, then (8 bits) K scales, V scales
     uint8_t *ring = smem + warp * S::RING;
     const uint32_t load_lane = smem_u32(ring) + chunk_at<D, KIND>(lane / S::CPR, lane % S::CPR);
 
     // the run's pairs, one after the other
-    long long u = w.u, first = w.first;
-    int b = w.b, len, tiles, t0, t1, hk, head0, heads, tok0, ng;
-    auto find = [&]() {                              // the pair that unit u lies in
-        for (;;) {
+    int len, tiles, t0, t1, hk, head0, heads, tok0, ng;
+    // The next pair of the run with a tile to do, from unit u on; u moves past its units.  False at
+    // the run's end.
+    auto find = [&]() {
+        int pair;
+        if constexpr (ONE) {
             len = kv_len(a.c, a.lens, b, &g_decode_err);
             tiles = (len + S::TILE - 1) / S::TILE;
-            if (u - first < static_cast<long long>(tiles) * pairs) break;
-            first += static_cast<long long>(tiles) * pairs;
-            ++b;
+            pair = cta / a.cluster - b * pairs;
+            t0 = tiles * rank / a.cluster;           // tiles < 2^24
+            t1 = tiles * (rank + 1) / a.cluster;
+        } else {
+            for (;;) {
+                if (u >= u1) return false;
+                len = kv_len(a.c, a.lens, b, &g_decode_err);
+                tiles = (len + S::TILE - 1) / S::TILE;
+                const int units = tiles > 0 ? tiles + kPairUnits : 0;
+                if (u - first >= static_cast<long long>(units) * pairs) {
+                    first += static_cast<long long>(units) * pairs;
+                    ++b;
+                    continue;
+                }
+                pair = static_cast<int>(div_up_to(u - first, units));
+                const int v0 = static_cast<int>((u - first) - static_cast<long long>(pair) * units);
+                const int v1 = static_cast<int>(min(static_cast<long long>(units), v0 + (u1 - u)));
+                u += v1 - v0;
+                t0 = max(0, v0 - kPairUnits);
+                t1 = max(0, v1 - kPairUnits);
+                if (t1 > t0) break;
+            }
         }
-        const int pair = static_cast<int>(div_up_to(u - first, tiles));
-        t0 = static_cast<int>((u - first) - static_cast<long long>(pair) * tiles);
-        t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + (u1 - u)));
         hk = pair / a.chunks;
         const int ch = pair - hk * a.chunks;
         head0 = hk * a.G + ch * MR;                  // first query head of the group
@@ -332,6 +398,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
         tok0 = t0 * S::TILE + warp * S::GRAN;
         ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
+        return true;
     };
     uint32_t bad;                                    // halves (2 bits a stage) whose page is not one
     uint32_t qb[NH][KS][2];                          // q: column g of the products' second operand
@@ -412,7 +479,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         }
     };
 
-    find();
+    if (!find()) return;
     begin();
     for (bool run_first = true;; run_first = false) {
         float qs[NH][2];                                         // log2 units' factor of heads 2q, 2q + 1
@@ -685,11 +752,10 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int place = run_first && t0 > 0 ? 0 : 1;
         const size_t out0 = static_cast<size_t>(b) * a.Hq + head0;
         const int outs = heads;
-        u += t1 - t0;
-        const bool more = u < u1;
-        if (more) {
-            find();
-            begin();
+        bool more = false;
+        if constexpr (!ONE) {
+            more = find();
+            if (more) begin();
         }
 
         // join the four warps, in their order
@@ -718,6 +784,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 for (int i = 0; i < 4; ++i)
                     so[(nh * 8 + 2 * q + (i & 1)) * PITCH + jn * 16 + 8 * (i >> 1) + g] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
         __syncthreads();
+        // ONE: the CTA's sums, (MR, D) floats, in the first stage of the first ring
+        float *sums = reinterpret_cast<float *>(smem);
+        static_assert(MR * D * 4 <= S::STAGE && S::STAGES > 1, "the sums do not fit a stage");
         for (int idx = tid; idx < outs * (D / 2); idx += kDecThreads) {
             const int r = idx / (D / 2), x2 = idx % (D / 2);
             // two channels c, c + 1 and their places
@@ -735,6 +804,14 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 o0 += f * from[p0];
                 o1 += f * from[p1];
                 sum += f * s_l[x][r];
+            }
+            if constexpr (ONE) {
+                *reinterpret_cast<float2 *>(sums + r * D + c) = make_float2(o0, o1);
+                if (c == 0) {
+                    s_part[0][r] = M;
+                    s_part[1][r] = sum;
+                }
+                continue;
             }
             const size_t head = out0 + r;
             if (whole) {
@@ -756,144 +833,223 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 }
             }
         }
+        if constexpr (ONE) {
+            // the cluster's sums: each head's M and 1 / l, then a share of the outputs for each CTA
+            cluster_sync();
+            float M = -INFINITY, sum = 0.0f;
+            if (tid < outs) {
+                float ml[kDecCluster][2];
+#pragma unroll
+                for (int k = 0; k < kDecCluster; ++k)
+                    if (k < a.cluster) {
+                        ml[k][0] = cluster_float(&s_part[0][tid], k);
+                        ml[k][1] = cluster_float(&s_part[1][tid], k);
+                        M = fmaxf(M, ml[k][0]);
+                    }
+                const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+                for (int k = 0; k < kDecCluster; ++k)
+                    if (k < a.cluster) {
+                        const float f = ex2_approx(ml[k][0] - ref);
+                        s_f[k][tid] = f;
+                        sum += f * ml[k][1];
+                    }
+                s_m[0][tid] = ref;
+                s_l[0][tid] = sum > 0.0f ? 1.0f / sum : 0.0f;
+                if (rank == 0) a.L[out0 + tid] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+            }
+            __syncthreads();
+            for (int i = (rank * kDecThreads + tid) * 4; i < outs * D; i += a.cluster * kDecThreads * 4) {
+                const int r = i / D;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < kDecCluster; ++k)
+                    if (k < a.cluster) {
+                        const int4 w4 = cluster_words(reinterpret_cast<const int *>(sums + i), k);
+                        const float f = s_f[k][r];
+                        o.x += f * __int_as_float(w4.x); o.y += f * __int_as_float(w4.y);
+                        o.z += f * __int_as_float(w4.z); o.w += f * __int_as_float(w4.w);
+                    }
+                const float inv = s_l[0][r];
+                store_out(a, out0 * D + i, o.x * inv, o.y * inv);
+                store_out(a, out0 * D + i + 2, o.z * inv, o.w * inv);
+            }
+            if (a.logits) {
+                // scores of this CTA's own tokens (one group of heads a kv head), heads in order
+                float *score = a.c.score + (static_cast<size_t>(b) * a.c.H + hk) * a.c.cap;
+                const int end = min(len, t1 * S::TILE);
+                for (int t = t0 * S::TILE + tid; t < end; t += kDecThreads) {
+                    float w = 0.0f;
+                    for (int r = 0; r < outs; ++r) w += ex2_approx(a.logits[(out0 + r) * a.c.cap + t] - s_m[0][r]) * s_l[0][r];
+                    score[t] += w;
+                }
+            }
+            cluster_sync();                                      // no CTA leaves while its sums are read
+            return;
+        }
         if (!more) break;
         __syncthreads();                                         // before the last stage is filled again
     }
 }
 
-// ---- join and scores ----------------------------------------------------------------------------
-// grid: (sequences * kv heads, blocks a row).  A pair that several runs share is the sum of their
-// parts, each under 2^(m_part - M), in their order; sequences without a token get O = 0, L = -inf.
-// Then score[b][hk][t] += sum over the group's heads of 2^(logit - M) / l, from the logits that the
-// main kernel kept: four tokens a thread, heads in order.  Launched while the main kernel still
-// runs (programmatic dependent launch): the lengths are added up before the wait for its end.
+// ---- join ---------------------------------------------------------------------------------------
+// A pair that several runs share is the sum of their parts, each under 2^(m_part - M), in their
+// order.  Launched while the main kernel still runs (programmatic dependent launch): the lengths
+// are added up before the wait for its end, which every block does, work or none: what is launched
+// after this kernel then comes after the main kernel too.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinHeads = 64;               // heads whose M and 1 / l are held at a time
 
-template <int D, int MR>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC, WARPS = kJoinThreads / 32;
-    __shared__ float4 s_o[GROUPS][VEC];
-    __shared__ float s_M[kJoinHeads], s_inv[kJoinHeads];
-    __shared__ long long s_n[2][WARPS];
-    const int bh = blockIdx.x, b = bh / a.c.H, hk = bh - b * a.c.H;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int pairs = a.c.H * a.chunks;
-    const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
-    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-    const int tiles = (len + a.tile - 1) >> a.tile_shift;
-    // this sequence's first unit, and the total
-    long long lo = 0, total = 0;
-    for (int i = tid; i < a.c.B; i += kJoinThreads) {
-        const long long k = static_cast<long long>((kv_len(a.c, a.lens, i, &g_decode_err) + a.tile - 1) >> a.tile_shift) * pairs;
-        total += k;
-        if (i < b) lo += k;
+// The runs c0 .. c1 that hold tiles of the pair whose first unit is p0; part c is in place 1 of the
+// first, place 0 of the others.
+__device__ __forceinline__ void runs_of_pair(long long total, int runs, long long p0, int tiles, int &c0, int &c1) {
+    c0 = run_of(total, p0 + kPairUnits, runs);
+    c1 = run_of(total, p0 + kPairUnits + tiles - 1, runs);
+}
+__device__ __forceinline__ size_t part_of(int c, int c0, int mr, int r) {
+    return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * mr + r;
+}
+
+// M and the sum over parts c0 .. c1 of row r, by a warp
+__device__ __forceinline__ float2 join_ml(const DecodeArgs &a, int c0, int c1, int mr, int r, int lane) {
+    float M = -INFINITY, sum = 0.0f;                 // a lane's parts under its own maximum first
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const float2 ml = reinterpret_cast<const float2 *>(a.part_ml)[part_of(c, c0, mr, r)];
+        const float mn = fmaxf(M, ml.x), to = mn == -INFINITY ? 0.0f : mn;
+        sum = sum * ex2_approx(M - to) + ml.y * ex2_approx(ml.x - to);
+        M = mn;
     }
+    const float mine = M;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    sum *= ex2_approx(mine - (M == -INFINITY ? 0.0f : M));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return make_float2(M, sum);
+}
+
+// grid: (pairs, heads of a group) with at most as many pairs as runs, one head a block, its threads
+// over the parts; or (runs, 1), where the block of run c joins the pair that starts in run c and
+// goes on, if there is one: few parts, its threads over the heads.
+template <int D, int MR, bool PAIRS>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
+    __shared__ float4 s_o[GROUPS][VEC];
+    __shared__ float s_M[MR], s_inv[MR];
+    __shared__ long long s_lo[kJoinThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int v = tid % VEC, grp = tid / VEC;
+    const int pairs = a.c.H * a.chunks;
+    int b = 0, pair = 0, c0 = 0, c1 = 0;             // c0 == c1: nothing to join
+    if constexpr (PAIRS) {
+        b = blockIdx.x / pairs;
+        pair = blockIdx.x - b * pairs;
+        long long lo = 0;                            // units of the sequences before
+        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units(a, i)) * pairs;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        if (lane == 0) s_lo[warp] = lo;
+        const WorkAt w = locate<kJoinThreads>(a, pairs, [](long long total) { return total; });
+        lo = 0;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x) lo += s_lo[x];
+        const int units = pair_units(a, b);
+        if (units > 0)
+            runs_of_pair(w.total, runs_of(a, w.total), lo + static_cast<long long>(pair) * units, units - kPairUnits, c0, c1);
+    } else {
+        const int c = blockIdx.x;
+        const WorkAt w = locate<kJoinThreads>(a, pairs, [&](long long total) {
+            const int n = runs_of(a, total);
+            return c + 1 < n ? run_start(total, c + 1, n) - 1 : total;
+        });
+        if (w.u < w.total) {
+            b = w.b;
+            const int units = pair_units(a, b);
+            pair = static_cast<int>(div_up_to(w.u - w.first, units));
+            runs_of_pair(w.total, runs_of(a, w.total), w.first + static_cast<long long>(pair) * units, units - kPairUnits, c0, c1);
+            if (c0 != c) c0 = c1;                    // another block's
+        }
     }
-    if (lane == 0) {
-        s_n[0][warp] = total;
-        s_n[1][warp] = lo;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c0 == c1) return;
+    const int hk = pair / a.chunks, ch = pair - hk * a.chunks;
+    const int heads = min(MR, a.G - ch * MR);
+    const size_t head0 = static_cast<size_t>(b) * a.Hq + hk * a.G + ch * MR;
+    if (PAIRS && static_cast<int>(blockIdx.y) >= heads) return;
+    for (int r = PAIRS ? blockIdx.y + warp * MR : warp; r < heads; r += PAIRS ? MR * kJoinThreads : kJoinThreads / 32) {
+        const float2 ml = join_ml(a, c0, c1, MR, r, lane);
+        if (lane == 0) {
+            s_M[r] = ml.x == -INFINITY ? 0.0f : ml.x;
+            s_inv[r] = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+            a.L[head0 + r] = ml.y > 0.0f ? lse_of(ml.x, ml.y) : -INFINITY;
+            if (a.row_ml) {
+                a.row_ml[2 * (head0 + r)] = s_M[r];
+                a.row_ml[2 * (head0 + r) + 1] = ml.y;
+            }
+        }
     }
     __syncthreads();
-    total = lo = 0;
-#pragma unroll
-    for (int x = 0; x < WARPS; ++x) {
-        total += s_n[0][x];
-        lo += s_n[1][x];
-    }
-    // nothing of this row is this block's (block 0 always goes on to the wait)
-    if (blockIdx.y > 0 && blockIdx.y >= a.G && blockIdx.y * (kJoinThreads * 4) >= len) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (len == 0) {
-        for (int i = blockIdx.y * (kJoinThreads * 2) + tid * 2; i < a.G * D; i += gridDim.y * (kJoinThreads * 2)) {
-            store_out(a, head0 * D + i, 0.0f, 0.0f);
-            if (i % D == 0) a.L[head0 + i / D] = -INFINITY;
+    // a thread's four channels of row r from parts c, c + step, ...
+    auto sums = [&](int r, int c, int step) {
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (; c <= c1; c += step) {
+            const size_t at = part_of(c, c0, MR, r);
+            const float f = ex2_approx(a.part_ml[2 * at] - s_M[r]);
+            const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
+            o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
         }
-        return;
+        return o;
+    };
+    auto store = [&](int r, float4 o) {
+        const float inv = s_inv[r];
+        store_out(a, (head0 + r) * D + v * 4, o.x * inv, o.y * inv);
+        store_out(a, (head0 + r) * D + v * 4 + 2, o.z * inv, o.w * inv);
+    };
+    if constexpr (PAIRS) {
+        const int r = blockIdx.y;
+        s_o[grp][v] = sums(r, c0 + grp, GROUPS);
+        __syncthreads();
+        if (tid < VEC) {
+            float4 o = s_o[0][v];
+#pragma unroll
+            for (int x = 1; x < GROUPS; ++x) {
+                const float4 y = s_o[x][v];
+                o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+            }
+            store(r, o);
+        }
+    } else {
+        for (int r = grp; r < heads; r += GROUPS) store(r, sums(r, c0, 1));
     }
-    const int runs = runs_of(a, total);
-    // the four tokens of this thread
+}
+
+// ---- scores -------------------------------------------------------------------------------------
+// grid: (sequences * kv heads, groups of 1024 slots).  score[b][hk][t] += sum over the group's heads of
+// 2^(logit - M) / l, from the logits that the main kernel kept and the M and l that it or the join left:
+// four slots a thread, heads in order.
+constexpr int kScoreHeads = 128;             // heads whose M and 1 / l are held at a time
+
+__global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid_constant__ DecodeArgs a) {
+    __shared__ float s_M[kScoreHeads], s_inv[kScoreHeads];
+    const int bh = blockIdx.x, b = bh / a.c.H, hk = bh - b * a.c.H;
+    const int tid = threadIdx.x;
+    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // (by every block, as above)
+    if (static_cast<int>(blockIdx.y) * (kJoinThreads * 4) >= len) return;
+    const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
     const int t = (blockIdx.y * kJoinThreads + tid) * 4;
     float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int h0 = 0; h0 < a.G; h0 += kJoinHeads) {
-        const int n = min(kJoinHeads, a.G - h0);
-        // M and l of every head, a warp each
-        for (int i = warp; i < n; i += WARPS) {
-            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
-            const long long p0 = lo + (static_cast<long long>(hk) * a.chunks + ch) * tiles;
-            const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
-            float M, sum;
-            if (c0 == c1) {
-                M = sum = 0.0f;
-                if (a.row_ml) {
-                    M = a.row_ml[2 * (head0 + h)];
-                    sum = a.row_ml[2 * (head0 + h) + 1];
-                    if (M == -INFINITY) M = 0.0f;
-                }
-            } else {
-                // part of CTA c: place 1 of the first, place 0 of the others; a lane's parts under its own maximum first
-                auto part = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r; };
-                M = -INFINITY;
-                sum = 0.0f;
-                for (int c = c0 + lane; c <= c1; c += 32) {
-                    const float2 ml = reinterpret_cast<const float2 *>(a.part_ml)[part(c)];
-                    const float mn = fmaxf(M, ml.x), to = mn == -INFINITY ? 0.0f : mn;
-                    sum = sum * ex2_approx(M - to) + ml.y * ex2_approx(ml.x - to);
-                    M = mn;
-                }
-                const float mine = M;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                const float ref = M == -INFINITY ? 0.0f : M;
-                sum *= ex2_approx(mine - ref);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0 && h % gridDim.y == blockIdx.y) a.L[head0 + h] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
-                M = ref;
-            }
-            if (lane == 0) {
-                s_M[i] = M;
-                s_inv[i] = sum > 0.0f ? 1.0f / sum : 0.0f;
-            }
+    for (int h0 = 0; h0 < a.G; h0 += kScoreHeads) {
+        const int n = min(kScoreHeads, a.G - h0);
+        if (tid < n) {
+            const float M = a.row_ml[2 * (head0 + h0 + tid)], l = a.row_ml[2 * (head0 + h0 + tid) + 1];
+            s_M[tid] = M == -INFINITY ? 0.0f : M;
+            s_inv[tid] = l > 0.0f ? 1.0f / l : 0.0f;
         }
         __syncthreads();
-        // this block's heads of the shared pairs
-        const int v = tid % VEC, grp = tid / VEC;
-        for (int i = 0; i < n; ++i) {
-            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
-            if (h % gridDim.y != blockIdx.y) continue;
-            const long long p0 = lo + (static_cast<long long>(hk) * a.chunks + ch) * tiles;
-            const int c0 = run_of(total, p0, runs), c1 = run_of(total, p0 + tiles - 1, runs);
-            if (c0 == c1) continue;
-            float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int c = c0 + grp; c <= c1; c += GROUPS) {
-                const size_t at = (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * MR + r;
-                const float f = ex2_approx(a.part_ml[2 * at] - s_M[i]);
-                const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
-                o4.x += f * x.x; o4.y += f * x.y; o4.z += f * x.z; o4.w += f * x.w;
-            }
-            s_o[grp][v] = o4;
-            __syncthreads();
-            if (tid < VEC) {
-                o4 = s_o[0][tid];
-#pragma unroll
-                for (int x = 1; x < GROUPS; ++x) {
-                    const float4 y = s_o[x][tid];
-                    o4.x += y.x; o4.y += y.y; o4.z += y.z; o4.w += y.w;
-                }
-                const float inv = s_inv[i];
-                store_out(a, (head0 + h) * D + tid * 4, o4.x * inv, o4.y * inv);
-                store_out(a, (head0 + h) * D + tid * 4 + 2, o4.z * inv, o4.w * inv);
-            }
-            __syncthreads();
-        }
-        if (a.logits && t < len) {
+        if (t < len) {
             const float *x = a.logits + (head0 + h0) * a.c.cap + t;
+#pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const float4 y = *reinterpret_cast<const float4 *>(x + static_cast<size_t>(i) * a.c.cap);
                 const float M = s_M[i], inv = s_inv[i];
@@ -905,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         }
         __syncthreads();
     }
-    if (a.logits && t < len) {
+    if (t < len) {
         float *to = a.c.score + static_cast<size_t>(bh) * a.c.cap + t;
         if (t + 4 <= len) {
             float4 y = *reinterpret_cast<const float4 *>(to);
@@ -927,8 +1083,11 @@ unsigned int take_decode_error() {
 }
 
 // ---- host -------------------------------------------------------------------------------------
+constexpr int kDecOneTiles = 4;              // tiles a CTA of a pair's cluster takes at most
+
 struct DecodePlan {
     int mr, chunks, ctas, tile;
+    int cluster;             // not 0: a cluster a pair
     size_t off_ml, off_rows, off_logits, bytes;
 };
 
@@ -942,14 +1101,22 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     p.tile = decode_tile(row);
     long long n = kSMs * decode_ctas(row, c.d, p.mr);
     const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + p.tile - 1) / p.tile);
+    // A cluster a pair while all pairs are resident together and a CTA takes few tiles: as many CTAs as
+    // there are tiles and room.  (us, cluster / split: 8 pairs of 1000 tokens in INT8, d = 128 5.8 / 8.4, of
+    // 4000 9.4 / 10.1; 64 pairs of up to 4000, 8 tiles a CTA, 16.4 / 14.0; 256 of up to 300 8.7 / 12.3;
+    // 1024 of 64, more than are resident, 16.5 / 14.7.)
+    const long long pairs = static_cast<long long>(c.B) * c.H * p.chunks, most = tiles / pairs;
+    int cl = 1;
+    while (cl < kDecCluster && cl < most && pairs * cl * 2 <= n) cl *= 2;
+    p.cluster = pairs <= n && (most + cl - 1) / cl <= kDecOneTiles && (!add_score || p.chunks == 1) ? cl : 0;
     if (n > tiles) n = tiles;
-    p.ctas = static_cast<int>(n);
+    p.ctas = static_cast<int>(p.cluster ? pairs * cl : n);
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-    const size_t parts = static_cast<size_t>(p.ctas) * 2 * p.mr;
+    const size_t parts = p.cluster ? 0 : static_cast<size_t>(p.ctas) * 2 * p.mr;
     const size_t heads = static_cast<size_t>(c.B) * Hq;
     p.off_ml = up(parts * c.d * sizeof(float));
     p.off_rows = p.off_ml + up(parts * 2 * sizeof(float));
-    p.off_logits = p.off_rows + (add_score ? up(heads * 2 * sizeof(float)) : 0);
+    p.off_logits = p.off_rows + (add_score && !p.cluster ? up(heads * 2 * sizeof(float)) : 0);
     p.bytes = p.off_logits + (add_score ? heads * c.max_pages * c.page * sizeof(float) : 0);
     return p;
 }
@@ -965,15 +1132,30 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
 template <int D, int KIND, int MR>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     using S = DecodeShape<D, KIND, MR>;
-    static bool raised[16] = {false};
-    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR>), S::SMEM, raised);
+    static bool raised[2][16] = {{false}};
+    if (a.cluster) {
+        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, true>), S::SMEM, raised[1]);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.ctas);
+        cfg.blockDim = dim3(kDecThreads);
+        cfg.dynamicSmemBytes = S::SMEM;
+        cfg.stream = st;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = a.cluster;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, MR, true>, a);
+    }
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, false>), S::SMEM, raised[0]);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, KIND, MR><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
+    decode_kernel<D, KIND, MR, false><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int y = a.logits ? (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : a.G < 16 ? a.G : 16;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, y);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -981,7 +1163,17 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR>, a);
+    const long long pairs = static_cast<long long>(a.c.B) * a.c.H * a.chunks;
+    if (pairs <= a.ctas) {
+        cfg.gridDim = dim3(static_cast<unsigned>(pairs), a.G < MR ? a.G : MR);
+        e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, true>, a);
+    } else {
+        cfg.gridDim = dim3(a.ctas);
+        e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, false>, a);
+    }
+    if (e != cudaSuccess || !a.logits) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
+    return cudaLaunchKernelEx(&cfg, decode_score_kernel, a);
 }
 
 template <int D, int KIND>
@@ -1014,18 +1206,18 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
     if (!Q || !lens || !O || !L || (add_score && !c->score)) return SAGE_ERR_ARG;
     if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(L, 16) || misaligned(lens, 4)) return SAGE_ERR_ALIGN;
     const DecodePlan p = decode_plan(*c, Hq, add_score);
-    if (!workspace || workspace_bytes < p.bytes) return SAGE_ERR_WORKSPACE;
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return SAGE_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     DecodeArgs a;
     a.c = kv_view(*c);
     a.Q = Q; a.O = O; a.L = L; a.lens = lens;
-    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas; a.tile = p.tile; a.tile_shift = p.tile == 64 ? 6 : 7;
+    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas; a.cluster = p.cluster; a.tile = p.tile; a.tile_shift = p.tile == 64 ? 6 : 7;
     a.bf16 = c->dtype == SAGE_BF16;
     a.sl2 = scale_log2(c->d);
     a.part_O = reinterpret_cast<float *>(w);
     a.part_ml = reinterpret_cast<float *>(w + p.off_ml);
-    a.row_ml = add_score ? reinterpret_cast<float *>(w + p.off_rows) : nullptr;
+    a.row_ml = add_score && !p.cluster ? reinterpret_cast<float *>(w + p.off_rows) : nullptr;
     a.logits = add_score ? reinterpret_cast<float *>(w + p.off_logits) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;

@@ -277,28 +277,7 @@ __device__ __forceinline__ uint32_t evict_key(float s, bool recent) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);      // at most 0xFF800000 (+inf)
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the word at this address of CTA `rank`'s shared memory
-__device__ __forceinline__ int cluster_word(const int *p, int rank) {
-    uint32_t at;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-
-// and the four (16-byte aligned)
-__device__ __forceinline__ int4 cluster_words(const int *p, int rank) {
-    uint32_t at;
-    int4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
-// Moves first, first + step, ... of a row, kSelThreads at a time: a thread looks up one move's rows and
+// Moves begin .. end - 1 of a row, kSelThreads at a time: a thread looks up one move's rows and
 // moves what is a word (scales, score, position), then ROW_BYTES / 16 lanes copy a row's K and V, whose
 // addresses all wait in shared memory.
 template <int ROW_BYTES>

@@ -8,6 +8,31 @@
 
 namespace sage {
 
+// ---- thread-block clusters ---------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the word at this address of CTA `rank`'s shared memory
+__device__ __forceinline__ int cluster_word(const int *p, int rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float cluster_float(const float *p, int rank) {
+    return __int_as_float(cluster_word(reinterpret_cast<const int *>(p), rank));
+}
+// and the four (16-byte aligned)
+__device__ __forceinline__ int4 cluster_words(const int *p, int rank) {
+    uint32_t at;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 struct KvView {
     void *K, *V;
     float *sK, *sV;

@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from .binding import SAGE_BF16, SAGE_FP16, _check, _ptr, lib
+from .binding import SAGE_BF16, SAGE_FP16, _check, _ptr, _workspace, lib
 
 SAGE_FP32 = 2
 SAGE_KV_16, SAGE_KV_INT8, SAGE_KV_FP8 = 0, 1, 2
@@ -277,8 +277,8 @@ def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, sco
     _workspace_ok(workspace, dev)
     O = torch.empty_like(Q) if out is None else out
     L = torch.empty((cache.B, Hq, 1), dtype=torch.float32, device=dev) if lse is None else lse
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
-    st = lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(), int(score), ws.data_ptr(),
+    ws = _workspace(nbytes, dev) if workspace is None else workspace
+    st = lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(), int(score), _ptr(ws),
                                 nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
     _check("sage_attn_decode", st)
     return O, L
@@ -309,7 +309,7 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
         _need(out, "out", torch.int32, (cache.B,), dev)
     _workspace_ok(workspace, dev)
     new = torch.empty_like(lens) if out is None else out
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    ws = _workspace(nbytes, dev) if workspace is None else workspace
     st = lib().sage_kv_evict(c, lens.data_ptr(), seen.data_ptr(), budget, recent, new.data_ptr(), ws.data_ptr(),
                              nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
     _check("sage_kv_evict", st)

@@ -428,7 +428,8 @@ SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int 
  * add_score = 1: score[b][kv head][t] += the sum over its query heads of softmax(s)_t.
  * Sums and statistics are float32; the probabilities enter the second product as two 16-bit
  * terms (16 or more significant bits).  Results do not depend on the order in which the GPU runs
- * its blocks.  O and L may not overlap the inputs or the cache. */
+ * its blocks.  O and L may not overlap the inputs or the cache.  Short caches need no workspace
+ * without scores: the query then says 0, and workspace may be NULL. */
 SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score);
 SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, void *O,
                               float *L, int add_score, void *workspace, size_t workspace_bytes,

@@ -128,9 +128,11 @@ def test_cache_calls_refuse(sg):
         assert _append(sg, c, **kw) == st, kw
     assert _append(sg, _kv(sg, kind=0, sK=None, sV=None), mu=_fake(9)) == 2      # smoothing a 16-bit cache
     for kw, st in ((dict(Hq=0), 1), (dict(Hq=7), 1), (dict(score=2), 1), (dict(Q=None), 1), (dict(lens=None), 1), (dict(O=None), 1),
-                   (dict(L=None), 1), (dict(Q=_fake(0) + 8), 3), (dict(O=_fake(0) + 2), 3), (dict(ws=None), 6), (dict(n=100), 6),
-                   (dict(ws=_fake(4) + 16), 3), (dict(Hq=3 << 23), 2)):
+                   (dict(L=None), 1), (dict(Q=_fake(0) + 8), 3), (dict(O=_fake(0) + 2), 3), (dict(Hq=3 << 23), 2)):
         assert _decode(sg, c, **kw) == st, kw
+    for kw, st in ((dict(ws=None), 6), (dict(n=100), 6), (dict(ws=_fake(4) + 16), 3)):
+        assert _decode(sg, _kv(sg, max_pages=5000), **kw) == st, kw
+        assert _decode(sg, c, score=1, **kw) == st, kw
     assert _decode(sg, _kv(sg, score=None), score=1) == 1
     for kw, st in ((dict(lens=None), 1), (dict(seen=None), 1), (dict(out=None), 1), (dict(out=_fake(0)), 1), (dict(budget=0), 1),
                    (dict(recent=-1), 1), (dict(recent=9), 1), (dict(ws=None), 6), (dict(n=8), 6), (dict(ws=_fake(3) + 8), 3)):
@@ -140,12 +142,15 @@ def test_cache_calls_refuse(sg):
 
 
 def test_cache_workspaces(sg):
-    """Decode: two places a CTA for sums, maxima and sums of exponentials, and with scores a logit a
-    slot and head; evict: at most min(budget, capacity - budget) pairs a row."""
+    """Decode: two places a CTA for sums, maxima and sums of exponentials (long caches), and with scores
+    a logit a slot and head; evict: at most min(budget, capacity - budget) pairs a row."""
     L = sg.lib()
     c = _kv(sg, B=1, H=1, max_pages=4)
     plain, scored = (L.sage_decode_workspace_bytes(ctypes.byref(c), 4, s) for s in (0, 1))
-    assert plain >= 2 * 8 * 66 * 4 and scored >= plain + 4 * 64 * 4
+    assert plain == 0 and scored >= 4 * 64 * 4
+    c = _kv(sg, B=1, H=1, max_pages=40000)
+    plain, scored = (L.sage_decode_workspace_bytes(ctypes.byref(c), 4, s) for s in (0, 1))
+    assert plain >= 456 * 2 * 8 * 66 * 4 and scored >= plain + 4 * 640000 * 4
     assert L.sage_decode_workspace_bytes(ctypes.byref(c), 0, 0) == 0 and L.sage_decode_workspace_bytes(None, 4, 0) == 0
     c = _kv(sg, B=2, H=3, max_pages=4)
     assert L.sage_evict_workspace_bytes(ctypes.byref(c), 8) >= 6 * 2 * 8 * 4
