@@ -89,7 +89,7 @@ struct DecodeArgs {
     float sl2;               // log2(e) / sqrt(d)
     float *part_O;           // (ctas, 2, MR, d) unnormalised sums
     float *part_ml;          // (ctas, 2, MR, 2) maxima (log2 units) and sums of exponentials
-    float *row_ml;           // (B, Hq, 2) the same of finished rows, with scores only
+    float *row_ml;           // (B, Hq, 2) the same of rows that one run finished, with scores only
     float *logits;           // (B, Hq, cap) log2-unit logits, with scores only
 };
 
@@ -981,10 +981,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
             s_M[r] = ml.x == -INFINITY ? 0.0f : ml.x;
             s_inv[r] = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
             a.L[head0 + r] = ml.y > 0.0f ? lse_of(ml.x, ml.y) : -INFINITY;
-            if (a.row_ml) {
-                a.row_ml[2 * (head0 + r)] = s_M[r];
-                a.row_ml[2 * (head0 + r) + 1] = ml.y;
-            }
         }
     }
     __syncthreads();
@@ -1023,40 +1019,101 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     }
 }
 
-// ---- scores -------------------------------------------------------------------------------------
-// grid: (sequences * kv heads, groups of 1024 slots).  score[b][hk][t] += sum over the group's heads of
-// 2^(logit - M) / l, from the logits that the main kernel kept and the M and l that it or the join left:
+// ---- join and scores ----------------------------------------------------------------------------
+// grid: (sequences * kv heads, groups of 1024 slots), in place of the join.  Every block forms M and l of
+// its kv head's query heads, a warp each, from the parts or (whole pairs) from what the main kernel
+// left; blocks 0, 1, ... take the output rows of the shared pairs in turn; then
+// score[b][hk][t] += sum over the heads of 2^(logit - M) / l, from the logits that the main kernel kept:
 // four slots a thread, heads in order.
-constexpr int kScoreHeads = 128;             // heads whose M and 1 / l are held at a time
+constexpr int kScoreHeads = 64;              // heads whose M and 1 / l are held at a time
 
+template <int D, int MR>
 __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
+    __shared__ float4 s_o[GROUPS][VEC];
     __shared__ float s_M[kScoreHeads], s_inv[kScoreHeads];
-    const int bh = blockIdx.x, b = bh / a.c.H, hk = bh - b * a.c.H;
-    const int tid = threadIdx.x;
+    __shared__ long long s_lo[kJoinThreads / 32];
+    const int bh = blockIdx.x, b = bh / a.c.H, hk = bh - b * a.c.H, y = blockIdx.y, ys = gridDim.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int v = tid % VEC, grp = tid / VEC;
+    const int pairs = a.c.H * a.chunks;
     const int len = kv_len(a.c, a.lens, b, &g_decode_err);
-    asm volatile("griddepcontrol.wait;" ::: "memory");       // (by every block, as above)
-    if (static_cast<int>(blockIdx.y) * (kJoinThreads * 4) >= len) return;
     const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
-    const int t = (blockIdx.y * kJoinThreads + tid) * 4;
+    const int t = (y * kJoinThreads + tid) * 4;
+    const bool idle = len == 0 || (y >= a.G && y * (kJoinThreads * 4) >= len);
+    long long lo = 0;                                // units of the sequences before
+    WorkAt w{};
+    if (!idle) {
+        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units(a, i)) * pairs;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        if (lane == 0) s_lo[warp] = lo;
+        w = locate<kJoinThreads>(a, pairs, [](long long total) { return total; });
+        lo = 0;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x) lo += s_lo[x];
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // by every block, as above
+    if (idle) return;
+    const int units = pair_units(a, b), runs = runs_of(a, w.total);
     float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int h0 = 0; h0 < a.G; h0 += kScoreHeads) {
         const int n = min(kScoreHeads, a.G - h0);
-        if (tid < n) {
-            const float M = a.row_ml[2 * (head0 + h0 + tid)], l = a.row_ml[2 * (head0 + h0 + tid) + 1];
-            s_M[tid] = M == -INFINITY ? 0.0f : M;
-            s_inv[tid] = l > 0.0f ? 1.0f / l : 0.0f;
+        for (int i = warp; i < n; i += kJoinThreads / 32) {
+            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
+            int c0, c1;
+            runs_of_pair(w.total, runs, lo + (static_cast<long long>(hk) * a.chunks + ch) * units, units - kPairUnits, c0, c1);
+            float2 ml;
+            if (c0 == c1) {
+                ml = reinterpret_cast<const float2 *>(a.row_ml)[head0 + h];
+            } else {
+                ml = join_ml(a, c0, c1, MR, r, lane);
+                if (lane == 0 && h % ys == y) a.L[head0 + h] = ml.y > 0.0f ? lse_of(ml.x, ml.y) : -INFINITY;
+            }
+            if (lane == 0) {
+                s_M[i] = ml.x == -INFINITY ? 0.0f : ml.x;
+                s_inv[i] = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+            }
         }
         __syncthreads();
+        for (int i = (y - h0 % ys + ys) % ys; i < n; i += ys) {      // heads h = y, y + ys, ...
+            const int h = h0 + i, ch = h / MR, r = h - ch * MR;
+            int c0, c1;
+            runs_of_pair(w.total, runs, lo + (static_cast<long long>(hk) * a.chunks + ch) * units, units - kPairUnits, c0, c1);
+            if (c0 == c1) continue;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int c = c0 + grp; c <= c1; c += GROUPS) {
+                const size_t at = part_of(c, c0, MR, r);
+                const float f = ex2_approx(a.part_ml[2 * at] - s_M[i]);
+                const float4 x = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
+                o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+            }
+            s_o[grp][v] = o;
+            __syncthreads();
+            if (tid < VEC) {
+                o = s_o[0][v];
+#pragma unroll
+                for (int x = 1; x < GROUPS; ++x) {
+                    const float4 z = s_o[x][v];
+                    o.x += z.x; o.y += z.y; o.z += z.z; o.w += z.w;
+                }
+                const float inv = s_inv[i];
+                store_out(a, (head0 + h) * D + v * 4, o.x * inv, o.y * inv);
+                store_out(a, (head0 + h) * D + v * 4 + 2, o.z * inv, o.w * inv);
+            }
+            __syncthreads();
+        }
         if (t < len) {
             const float *x = a.logits + (head0 + h0) * a.c.cap + t;
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
-                const float4 y = *reinterpret_cast<const float4 *>(x + static_cast<size_t>(i) * a.c.cap);
+                const float4 z = *reinterpret_cast<const float4 *>(x + static_cast<size_t>(i) * a.c.cap);
                 const float M = s_M[i], inv = s_inv[i];
-                add.x += ex2_approx(y.x - M) * inv;
-                add.y += ex2_approx(y.y - M) * inv;
-                add.z += ex2_approx(y.z - M) * inv;
-                add.w += ex2_approx(y.w - M) * inv;
+                add.x += ex2_approx(z.x - M) * inv;
+                add.y += ex2_approx(z.y - M) * inv;
+                add.z += ex2_approx(z.z - M) * inv;
+                add.w += ex2_approx(z.w - M) * inv;
             }
         }
         __syncthreads();
@@ -1064,9 +1121,9 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
     if (t < len) {
         float *to = a.c.score + static_cast<size_t>(bh) * a.c.cap + t;
         if (t + 4 <= len) {
-            float4 y = *reinterpret_cast<const float4 *>(to);
-            y.x += add.x; y.y += add.y; y.z += add.z; y.w += add.w;
-            *reinterpret_cast<float4 *>(to) = y;
+            float4 z = *reinterpret_cast<const float4 *>(to);
+            z.x += add.x; z.y += add.y; z.z += add.z; z.w += add.w;
+            *reinterpret_cast<float4 *>(to) = z;
         } else {                                     // slots past the end keep what they hold
             to[0] += add.x;
             if (t + 1 < len) to[1] += add.y;
@@ -1163,17 +1220,17 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    if (a.logits) {
+        cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
+        return cudaLaunchKernelEx(&cfg, decode_score_kernel<D, MR>, a);
+    }
     const long long pairs = static_cast<long long>(a.c.B) * a.c.H * a.chunks;
     if (pairs <= a.ctas) {
         cfg.gridDim = dim3(static_cast<unsigned>(pairs), a.G < MR ? a.G : MR);
-        e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, true>, a);
-    } else {
-        cfg.gridDim = dim3(a.ctas);
-        e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, false>, a);
+        return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, true>, a);
     }
-    if (e != cudaSuccess || !a.logits) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
-    return cudaLaunchKernelEx(&cfg, decode_score_kernel, a);
+    cfg.gridDim = dim3(a.ctas);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, false>, a);
 }
 
 template <int D, int KIND>

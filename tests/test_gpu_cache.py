@@ -501,3 +501,22 @@ def test_evict_long_rows_over_a_cluster():
             want = was.clone()
             want[t[dst // page].cuda(), 0, (dst % page).cuda()] = was[t[src // page].cuda(), 0, (src % page).cuda()]
             assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("kind,Hq,H,d,page,lens", [
+    ("int8", 4, 1, 64, 16, [9000, 130, 0, 2000]),         # every path of a long cache: shared, whole and empty pairs
+    ("fp16", 40, 2, 128, 64, [5000, 1]),                  # three groups of heads a kv head
+    ("bf16", 70, 1, 64, 128, [12000]),                    # more heads than are held at a time
+    ("fp8", 6, 3, 128, 32, [64 * i for i in range(60, 0, -1)] + [7000]),
+])
+@pytest.mark.parametrize("score", [False, True])
+def test_decode_long_caches(kind, Hq, H, d, page, lens, score):
+    """Caches whose capacity takes the split path, with scores and without."""
+    import bit_trainable_attention_sage_gb300 as sg
+    q_dtype = KINDS[kind] if kind in ("fp16", "bf16") else torch.bfloat16
+    cache, K, V = filled(kind, len(lens), H, d, page, lens, seed=Hq, score=score)
+    Q = torch.randn(len(lens), Hq, 1, d, generator=torch.Generator().manual_seed(1)).to(q_dtype).cuda()
+    was = cache.score.clone() if score else None
+    O, L = sg.sage_attn_decode(Q, cache, ints(lens), score=score)
+    assert status(sg) == 0
+    check_decode(Q, O, L, lens, K, V, H, cache.score, was)
