@@ -242,8 +242,8 @@ static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st
 // eviction
 //
 // Which slots stay is a selection, not a sort: the budget-th largest key of a row of n keys by
-// radix selection (11, 11 and 10 bits), then one pass in slot order that takes what is above it
-// and the first of what is equal.  Only stayers in slots >= budget move, into the freed slots
+// radix selection (8 bits a pass, most often three of the four passes), then one pass in slot order
+// that takes what is above it and the first of what is equal.  Only stayers in slots >= budget move, into the freed slots
 // below: sources and destinations are disjoint, so the moves need no order among them, and a
 // cache that is cut back by a few tokens moves a few rows instead of being compacted.
 //
@@ -251,11 +251,14 @@ static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st
 // positions are read once, the keys stay in shared memory (CACHED; rows of more than
 // 8 * 20 K slots read them again each pass), histograms and counts are added up over the cluster
 // through distributed shared memory, and the same CTAs then move the rows.  One launch, and with
-// C up to 8 a few long rows still use many SMs.
+// C up to 8 a few long rows still use many SMs.  Bound by latency: 32 rows of up to 32768 slots cut
+// to 8192 (E4M3, d = 128) take 36 us, 18 of them for the selection's phases (a barrier of the
+// cluster each) and 10 for 57 MB of moves; 64 rows of 1088 cut to 1024 take 9.  (Digits of 11 bits,
+// whose histograms are 64 KB of remote reads a CTA and pass: 39 and 8.8; clusters half as large: 43.)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;
+constexpr int kSelBins = 256;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelMaxKeys = 20 * 1024;       // of a CTA in shared memory; two CTAs an SM
 
@@ -338,7 +341,8 @@ __device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, i
 template <bool CACHED, int ROW_BYTES>
 __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ uint32_t s_key[];
-    __shared__ __align__(16) int hist[3][kSelBins];
+    __shared__ __align__(16) int hist[4][kSelBins];
+    __shared__ size_t s_rows[2][kSelThreads];
     __shared__ int s_warp[2][kSelWarps];
     __shared__ __align__(16) int s_count[4];                   // of this CTA, read by the others: equal keys; freed, movers
     __shared__ int s_digit, s_above, s_here;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_c
     const int seg = ((n + a.cluster - 1) / a.cluster + kSelThreads - 1) / kSelThreads * kSelThreads;
     const int lo = min(n, rank * seg), len = min(n - lo, seg), its = seg / kSelThreads;
     const int mine = warp * its * 32 + lane;
-    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 4 * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     // score and pos are read with plain loads: the moves below write them (after every read here)
     auto key = [&](int i) -> uint32_t {
@@ -361,7 +365,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_c
         if constexpr (CACHED) return s_key[s];
         else return evict_key(a.c.score[base + lo + s], a.c.pos[base + lo + s] >= newest);
     };
-    // first digit: 11 bits.  Recent tokens share one key: counted by the warp.
+    // equal digits of a warp are added once: keys crowd into few of them
+    auto count = [&](int pass, bool in, uint32_t digit) {
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : 256u);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[pass][digit], __popc(same));
+    };
     constexpr int BATCH = 8;                     // reads in flight together
     for (int i0 = 0; i0 < its; i0 += BATCH) {
         float score[BATCH];
@@ -379,39 +387,28 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_c
             const bool in = i0 + x < its && s < len;
             const uint32_t k = evict_key(score[x], pos[x] >= newest);
             if (CACHED && in) s_key[s] = k;
-            const uint32_t top = __ballot_sync(0xffffffffu, in && k == 0xFFFFFFFFu);
-            if (in && k != 0xFFFFFFFFu) atomicAdd(&hist[0][k >> 21], 1);
-            if (lane == 0 && top) atomicAdd(&hist[0][kSelBins - 1], __popc(top));
+            count(0, in, k >> 24);
         }
     }
     // the budget-th largest key: `T` its leading digits, `need` its rank among the keys that share them
     uint32_t T = 0;
     int need = a.budget, equal = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         if (pass > 0) {
-            const uint32_t mask = 0xFFFFFFFFu << (pass == 1 ? 21 : 10);
             for (int i = 0; i < its; ++i) {
                 const int s = mine + i * 32;
-                const uint32_t k = s < len ? key(i) : ~T;                 // ~T shares no digit
-                const bool in = s < len && (k & mask) == T;
-                // ties: equal keys of a warp are added once
-                const uint32_t same = __ballot_sync(0xffffffffu, in);
-                if (same) {
-                    const uint32_t leader = __shfl_sync(0xffffffffu, k, __ffs(same) - 1);
-                    const uint32_t alike = __ballot_sync(0xffffffffu, in && k == leader);
-                    if (in && k != leader) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1);
-                    if (lane == __ffs(same) - 1) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], __popc(alike));
-                }
+                const uint32_t k = s < len ? key(i) : 0u;
+                const bool in = s < len && ((k ^ T) >> (shift + 8)) == 0u;
+                if (__any_sync(0xffffffffu, in)) count(pass, in, (k >> shift) & 255u);
             }
         }
         if (a.cluster > 1) cluster_sync();
         else __syncthreads();
-        // thread t holds the DIG digits from bins - 1 - DIG t down
-        constexpr int DIG = kSelBins / kSelThreads;
-        static_assert(DIG == 4, "a thread reads its digits as one vector");
+        // thread t holds the DIG digits from 255 - DIG t down
+        constexpr int DIG = 4;
         int c[DIG] = {};
-        const int d0 = bins - 1 - DIG * tid;
+        const int d0 = kSelBins - 1 - DIG * tid;
         if (d0 > 0) {
             int4 v[kSelMaxCluster];
 #pragma unroll
@@ -525,8 +522,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_c
     if (a.cluster > 1) cluster_sync();
     else __syncthreads();
     const int share = (moves + a.cluster - 1) / a.cluster;
-    static_assert(2 * kSelThreads * sizeof(size_t) <= sizeof(hist), "the rows' places do not fit the histograms");
-    evict_moves<ROW_BYTES>(a, bh, b, h, rank * share, min(moves, (rank + 1) * share), reinterpret_cast<size_t(*)[kSelThreads]>(&hist[0][0]));
+    evict_moves<ROW_BYTES>(a, bh, b, h, rank * share, min(moves, (rank + 1) * share), s_rows);
 }
 
 static int evict_max_moves(const sage_kv &c, int budget) {
