@@ -11,12 +11,15 @@ __device__ unsigned int g_kv_err = 0;   // 1: a page, length or slot was out of 
 //
 // delta = fl32(max|x| / M), code = nearest of fl32(x / delta), M = 127 (INT8) or 448 (E4M3), one
 // delta a row of d values, x = fl32(K - mu) or V; a 16-bit pool takes the values as they are.
-// Every element is read once and written once: bound by memory bandwidth (prompts) or by latency
-// (single tokens).  d / 8 lanes hold a row, 16 bytes each, so the maximum is 3 or 4 shuffles, a
-// row's loads and stores are whole sectors, and K and V of a row, and ROWS rows, are in flight
-// together.
+// Every element is read once and written once: bound by memory bandwidth (16-bit pools: 64 us for 64
+// heads of up to 8192 tokens, d = 128, 6.8 TB/s), in 8 bits by issuing the arithmetic (to E4M3 with
+// smoothing 58 us, 5.7 TB/s), or by latency (single tokens).  d / 16 lanes hold a row, two 16-byte
+// chunks each, so what is done once a row (its place, scale and reciprocal) is shared by 16 values
+// (8 values a lane: 70 us), the maximum is 2 or 3 shuffles and loads and stores are whole sectors.
+// One row a lane group and 40 warps an SM keep enough reads in flight (several rows a group: 65 us
+// and more).
 // ---------------------------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 struct AppendArgs {
     KvView c;
@@ -27,10 +30,10 @@ struct AppendArgs {
 };
 
 template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 u, f2 (&v)[4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack16(const uint4 (&u)[2], f2 (&v)[8]) {
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         float2 f;
         if constexpr (std::is_same<T, __half>::value)
             f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
@@ -67,28 +70,29 @@ __device__ __forceinline__ f2 scales_of(f2 m) {
     return f2{__fdiv_rn(m.x, M), __fdiv_rn(m.y, M)};
 }
 
-// One row's 8 values of a lane, and the row's scale -> 8 codes.
+// One row's 16 values of a lane, and the row's scale -> 16 codes.
 template <int KIND, bool ONCE>
-__device__ __forceinline__ uint2 kv_codes(const f2 (&x)[4], float delta) {
-    f2 y[4];
+__device__ __forceinline__ void kv_codes(const f2 (&x)[8], float delta, uint2 (&out)[2]) {
+    f2 y[8];
     if (delta >= 0x1p-90f && delta <= 0x1p90f) {
         const float r = __frcp_rn(delta);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = quotient2<ONCE>(x[i], f2{delta, delta}, f2{r, r});
+        for (int i = 0; i < 8; ++i) y[i] = quotient2<ONCE>(x[i], f2{delta, delta}, f2{r, r});
     } else if (delta == 0.0f) {
-        return make_uint2(0u, 0u);
+        out[0] = out[1] = make_uint2(0u, 0u);
+        return;
     } else {
         // a subnormal delta can be rounded so far down that the quotient exceeds 127 (E4M3 saturates)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             constexpr float top = KIND == SAGE_KV_INT8 ? 127.0f : 448.0f;
             y[i].x = fminf(fmaxf(__fdiv_rn(x[i].x, delta), -top), top);
             y[i].y = fminf(fmaxf(__fdiv_rn(x[i].y, delta), -top), top);
         }
     }
-    uint32_t w[2];
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if constexpr (KIND == SAGE_KV_INT8) {
             // y + 1.5 2^23 holds the nearest integer (ties to even) in its low bits
             const f2 magic{12582912.0f, 12582912.0f};
@@ -100,7 +104,8 @@ __device__ __forceinline__ uint2 kv_codes(const f2 (&x)[4], float delta) {
             w[i] = e4m3x2(y[2 * i].x, y[2 * i].y) | static_cast<uint32_t>(e4m3x2(y[2 * i + 1].x, y[2 * i + 1].y)) << 16;
         }
     }
-    return make_uint2(w[0], w[1]);
+    out[0] = make_uint2(w[0], w[1]);
+    out[1] = make_uint2(w[2], w[3]);
 }
 
 // max(|a|, |b|), under some sign
@@ -112,21 +117,21 @@ __device__ __forceinline__ float larger(float a, float b) {
 // The largest magnitude of a row that LANES lanes hold.  (Shuffles: a reduction instruction under
 // half-warp masks runs once a half, 83 against 76 us for 8192-token prompts.)
 template <int LANES>
-__device__ __forceinline__ float largest(const f2 (&x)[4]) {
-    float m = larger(larger(larger(x[0].x, x[0].y), larger(x[1].x, x[1].y)), larger(larger(x[2].x, x[2].y), larger(x[3].x, x[3].y)));
+__device__ __forceinline__ float largest(const f2 (&x)[8]) {
+    float m = larger(x[0].x, x[0].y);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = larger(m, larger(x[i].x, x[i].y));
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
     return fabsf(m);
 }
 
-// grid: (row groups of a head, B * H).  ROWS rows of each lane group are loaded before any is
-// written.
-template <typename T, int KIND, int D, int ROWS, bool SMOOTH>
-__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a) {
-    constexpr int LANES = D / 8, GROUPS = kAppendThreads / LANES;
+// grid: (row groups of a head, B * H); a row a lane group.
+template <typename T, int KIND, int D, bool SMOOTH>
+__global__ void __launch_bounds__(kAppendThreads, 10) kv_append_kernel(const AppendArgs a) {
+    constexpr int LANES = D / 16, GROUPS = kAppendThreads / LANES;
     const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    const int t0 = blockIdx.x * (GROUPS * ROWS);
     int n = a.T;
     if (a.count) {
         n = __ldg(a.count + b);
@@ -135,85 +140,78 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
             n = n < 0 ? 0 : a.T;
         }
     }
-    if (t0 >= n) return;
-    const int start = __ldg(a.start + b);
-    const uint4 *K = reinterpret_cast<const uint4 *>(a.K) + static_cast<size_t>(bh) * a.T * LANES + lane;
-    const uint4 *V = reinterpret_cast<const uint4 *>(a.V) + static_cast<size_t>(bh) * a.T * LANES + lane;
-    uint4 k[ROWS], v[ROWS];
-    long long row[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int t = t0 + r * GROUPS + group;
-        k[r] = v[r] = make_uint4(0u, 0u, 0u, 0u);
-        row[r] = -1;
-        if (t < n) {
-            k[r] = __ldg(K + static_cast<size_t>(t) * LANES);
-            v[r] = __ldg(V + static_cast<size_t>(t) * LANES);
-            const long long s = static_cast<long long>(start) + t;
-            if (s < 0 || s >= a.c.cap) {
-                atomicOr(&g_kv_err, 1u);
-            } else {
-                const int p = kv_page(a.c, b, static_cast<int>(s), &g_kv_err);
-                if (p >= 0) {
-                    row[r] = static_cast<long long>(kv_row(a.c, p, h, static_cast<int>(s)));
-                    if (lane == 0) {
-                        const size_t at = static_cast<size_t>(bh) * a.c.cap + s;
-                        if (a.c.score) a.c.score[at] = 0.0f;
-                        if (a.c.pos) a.c.pos[at] = a.pos0 ? __ldg(a.pos0 + b) + t : static_cast<int>(s);
-                    }
+    if (static_cast<int>(blockIdx.x) * GROUPS >= n) return;
+    const int t = blockIdx.x * GROUPS + group;
+    uint4 k[2], v[2];                                // 16-byte chunks lane and lane + LANES of the row
+    k[0] = k[1] = v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+    long long row = -1;                              // of the pool; -1: nothing to write
+    if (t < n) {
+        const size_t at = (static_cast<size_t>(bh) * a.T + t) * (2 * LANES) + lane;
+        const uint4 *K = static_cast<const uint4 *>(a.K) + at, *V = static_cast<const uint4 *>(a.V) + at;
+        k[0] = __ldg(K);
+        k[1] = __ldg(K + LANES);
+        v[0] = __ldg(V);
+        v[1] = __ldg(V + LANES);
+        const long long s = static_cast<long long>(__ldg(a.start + b)) + t;
+        if (s < 0 || s >= a.c.cap) {
+            atomicOr(&g_kv_err, 1u);
+        } else {
+            const int p = kv_page(a.c, b, static_cast<int>(s), &g_kv_err);
+            if (p >= 0) {
+                row = static_cast<long long>(kv_row(a.c, p, h, static_cast<int>(s)));
+                if (lane == 0) {
+                    const size_t slot = static_cast<size_t>(bh) * a.c.cap + s;
+                    if (a.c.score) a.c.score[slot] = 0.0f;
+                    if (a.c.pos) a.c.pos[slot] = a.pos0 ? __ldg(a.pos0 + b) + t : static_cast<int>(s);
                 }
             }
         }
     }
     if constexpr (KIND == SAGE_KV_16) {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-            if (row[r] >= 0) {
-                reinterpret_cast<uint4 *>(a.c.K)[row[r] * LANES + lane] = k[r];
-                reinterpret_cast<uint4 *>(a.c.V)[row[r] * LANES + lane] = v[r];
-            }
+        if (row < 0) return;
+        uint4 *K = static_cast<uint4 *>(a.c.K) + row * (2 * LANES) + lane, *V = static_cast<uint4 *>(a.c.V) + row * (2 * LANES) + lane;
+        K[0] = k[0];
+        K[LANES] = k[1];
+        V[0] = v[0];
+        V[LANES] = v[1];
     } else {
-        f2 mu[4];
+        // every lane of a warp takes part in the shuffles, row or none
+        f2 x[8], y[8];
+        unpack16<T>(k, x);
+        unpack16<T>(v, y);
         if constexpr (SMOOTH) {
-            const float4 *m = reinterpret_cast<const float4 *>(a.mu + static_cast<size_t>(bh) * D + lane * 8);
-            const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
-            mu[0] = f2{m0.x, m0.y}; mu[1] = f2{m0.z, m0.w}; mu[2] = f2{m1.x, m1.y}; mu[3] = f2{m1.z, m1.w};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float4 *m = reinterpret_cast<const float4 *>(a.mu + static_cast<size_t>(bh) * D + (lane + c * LANES) * 8);
+                const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
+                x[4 * c] = sub2(x[4 * c], f2{m0.x, m0.y});
+                x[4 * c + 1] = sub2(x[4 * c + 1], f2{m0.z, m0.w});
+                x[4 * c + 2] = sub2(x[4 * c + 2], f2{m1.x, m1.y});
+                x[4 * c + 3] = sub2(x[4 * c + 3], f2{m1.z, m1.w});
+            }
         }
-        // every lane of a warp takes part in the shuffles, rows or none
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            f2 x[4], y[4];
-            unpack16<T>(k[r], x);
-            unpack16<T>(v[r], y);
-            if constexpr (SMOOTH) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = sub2(x[i], mu[i]);
-            }
-            const f2 delta = scales_of<KIND>(f2{largest<LANES>(x), largest<LANES>(y)});
-            const float dk = delta.x, dv = delta.y;
-            const uint2 ck = kv_codes<KIND, !SMOOTH>(x, dk), cv = kv_codes<KIND, true>(y, dv);
-            if (row[r] >= 0) {
-                reinterpret_cast<uint2 *>(a.c.K)[row[r] * LANES + lane] = ck;
-                reinterpret_cast<uint2 *>(a.c.V)[row[r] * LANES + lane] = cv;
-                if (lane == 0) {
-                    a.c.sK[row[r]] = dk;
-                    a.c.sV[row[r]] = dv;
-                }
-            }
+        const f2 delta = scales_of<KIND>(f2{largest<LANES>(x), largest<LANES>(y)});
+        uint2 ck[2], cv[2];
+        kv_codes<KIND, !SMOOTH>(x, delta.x, ck);
+        kv_codes<KIND, true>(y, delta.y, cv);
+        if (row < 0) return;
+        uint2 *K = static_cast<uint2 *>(a.c.K) + row * (2 * LANES) + lane, *V = static_cast<uint2 *>(a.c.V) + row * (2 * LANES) + lane;
+        K[0] = ck[0];
+        K[LANES] = ck[1];
+        V[0] = cv[0];
+        V[LANES] = cv[1];
+        if (lane == 0) {
+            a.c.sK[row] = delta.x;
+            a.c.sV[row] = delta.y;
         }
     }
 }
 
 template <typename T, int KIND, int D, bool SMOOTH>
 static void launch_append_k(const AppendArgs &a, cudaStream_t st) {
-    constexpr int GROUPS = kAppendThreads / (D / 8);
-    const unsigned bh = static_cast<unsigned>(a.c.B) * a.c.H;
-    if (a.T <= GROUPS) {
-        kv_append_kernel<T, KIND, D, 1, SMOOTH><<<dim3(1, bh), kAppendThreads, 0, st>>>(a);
-    } else {
-        const unsigned x = (a.T + GROUPS * 4 - 1) / (GROUPS * 4);
-        kv_append_kernel<T, KIND, D, 4, SMOOTH><<<dim3(x, bh), kAppendThreads, 0, st>>>(a);
-    }
+    constexpr int GROUPS = kAppendThreads / (D / 16);
+    const dim3 grid((a.T + GROUPS - 1) / GROUPS, static_cast<unsigned>(a.c.B) * a.c.H);
+    kv_append_kernel<T, KIND, D, SMOOTH><<<grid, kAppendThreads, 0, st>>>(a);
 }
 
 template <typename T, int KIND>
