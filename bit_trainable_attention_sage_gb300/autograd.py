@@ -139,5 +139,9 @@ class SageRotaryFunction(torch.autograd.Function):
 
 
 def sage_rotary(Q: torch.Tensor, K: torch.Tensor, positions: torch.Tensor, rope):
-    """Differentiable rotary positions of Q (B,H,N,d) and K (B,Hk,N,d); see sage_rope."""
+    """Differentiable rotary positions of Q (B,H,N,d) and K (B,Hk,N,d); see sage_rope.
+
+    As with every PyTorch operation, a backward pass cannot be captured into a CUDA graph while an
+    eager graph of the same leaves is alive: their gradient nodes belong to the eager stream, and the
+    capture ends with an error.  Drop the eager outputs first."""
     return SageRotaryFunction.apply(Q, K, positions, rope)

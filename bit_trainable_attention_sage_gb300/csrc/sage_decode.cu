@@ -1020,7 +1020,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 }
 
 // ---- join and scores ----------------------------------------------------------------------------
-// grid: (sequences * kv heads, groups of 1024 slots), in place of the join.  Every block forms M and l of
+// grid: (sequences * kv heads, blocks of 1024 slots at a time), in place of the join.  Every block forms M and l of
 // its kv head's query heads, a warp each, from the parts or (whole pairs) from what the main kernel
 // left; blocks 0, 1, ... take the output rows of the shared pairs in turn; then
 // score[b][hk][t] += sum over the heads of 2^(logit - M) / l, from the logits that the main kernel kept:
@@ -1039,7 +1039,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
     const int pairs = a.c.H * a.chunks;
     const int len = kv_len(a.c, a.lens, b, &g_decode_err);
     const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
-    const int t = (y * kJoinThreads + tid) * 4;
     const bool idle = len == 0 || (y >= a.G && y * (kJoinThreads * 4) >= len);
     long long lo = 0;                                // units of the sequences before
     WorkAt w{};
@@ -1056,7 +1055,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
     asm volatile("griddepcontrol.wait;" ::: "memory");       // by every block, as above
     if (idle) return;
     const int units = pair_units(a, b), runs = runs_of(a, w.total);
-    float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int h0 = 0; h0 < a.G; h0 += kScoreHeads) {
         const int n = min(kScoreHeads, a.G - h0);
         for (int i = warp; i < n; i += kJoinThreads / 32) {
@@ -1104,8 +1102,9 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
             }
             __syncthreads();
         }
-        if (t < len) {
+        for (int t = (y * kJoinThreads + tid) * 4; t < len; t += ys * kJoinThreads * 4) {
             const float *x = a.logits + (head0 + h0) * a.c.cap + t;
+            float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const float4 z = *reinterpret_cast<const float4 *>(x + static_cast<size_t>(i) * a.c.cap);
@@ -1115,20 +1114,18 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
                 add.z += ex2_approx(z.z - M) * inv;
                 add.w += ex2_approx(z.w - M) * inv;
             }
+            float *to = a.c.score + static_cast<size_t>(bh) * a.c.cap + t;
+            if (t + 4 <= len) {
+                float4 z = *reinterpret_cast<const float4 *>(to);
+                z.x += add.x; z.y += add.y; z.z += add.z; z.w += add.w;
+                *reinterpret_cast<float4 *>(to) = z;
+            } else {                                 // slots past the end keep what they hold
+                to[0] += add.x;
+                if (t + 1 < len) to[1] += add.y;
+                if (t + 2 < len) to[2] += add.z;
+            }
         }
         __syncthreads();
-    }
-    if (t < len) {
-        float *to = a.c.score + static_cast<size_t>(bh) * a.c.cap + t;
-        if (t + 4 <= len) {
-            float4 z = *reinterpret_cast<const float4 *>(to);
-            z.x += add.x; z.y += add.y; z.z += add.z; z.w += add.w;
-            *reinterpret_cast<float4 *>(to) = z;
-        } else {                                     // slots past the end keep what they hold
-            to[0] += add.x;
-            if (t + 1 < len) to[1] += add.y;
-            if (t + 2 < len) to[2] += add.z;
-        }
     }
 }
 
@@ -1221,7 +1218,8 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (a.logits) {
-        cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
+        const int y = (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads);
+        cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, y < 1024 ? y : 1024);
         return cudaLaunchKernelEx(&cfg, decode_score_kernel<D, MR>, a);
     }
     const long long pairs = static_cast<long long>(a.c.B) * a.c.H * a.chunks;
@@ -1260,7 +1258,7 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
     if (st != SAGE_OK) return st;
     st = check_kv(c, true);
     if (st != SAGE_OK) return st;
-    if (!Q || !lens || !O || !L || (add_score && !c->score)) return SAGE_ERR_ARG;
+    if (!Q || !lens || !O || !L || O == Q || (add_score && !c->score)) return SAGE_ERR_ARG;
     if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(L, 16) || misaligned(lens, 4)) return SAGE_ERR_ALIGN;
     const DecodePlan p = decode_plan(*c, Hq, add_score);
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return SAGE_ERR_WORKSPACE;

@@ -388,7 +388,8 @@ SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, 
  * is not in [0, pages), or a length or slot outside [0, max_pages * page], is not followed: such
  * rows are skipped (append, evict) or masked (decode; lengths are held to the range), and
  * sage_device_status() returns SAGE_ERR_INDEX.
- * Calls on one cache are ordered by their stream; none allocates, and all can be captured.
+ * No call allocates, and all can be captured.  Calls that write one cache (append, evict, decode with
+ * scores) and those that read it have to be ordered, by one stream or by events.
  * ------------------------------------------------------------------------------------------ */
 #define SAGE_KV_16 0
 #define SAGE_KV_INT8 1
@@ -440,7 +441,7 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
  * far), then the others by score, NaN last; ties go to the lower slot.  The first `budget` stay.
  * Those of them in slots >= budget move to the freed slots < budget, in slot order, with their
  * scales, score and pos; all other slots keep what they hold.  lens_out[b] = min(lens[b], budget).
- * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not be lens. */
+ * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not be lens or seen. */
 SAGE_API size_t sage_evict_workspace_bytes(const sage_kv *c, int budget);
 SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget, int recent,
                            int *lens_out, void *workspace, size_t workspace_bytes,

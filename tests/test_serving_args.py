@@ -128,13 +128,13 @@ def test_cache_calls_refuse(sg):
         assert _append(sg, c, **kw) == st, kw
     assert _append(sg, _kv(sg, kind=0, sK=None, sV=None), mu=_fake(9)) == 2      # smoothing a 16-bit cache
     for kw, st in ((dict(Hq=0), 1), (dict(Hq=7), 1), (dict(score=2), 1), (dict(Q=None), 1), (dict(lens=None), 1), (dict(O=None), 1),
-                   (dict(L=None), 1), (dict(Q=_fake(0) + 8), 3), (dict(O=_fake(0) + 2), 3), (dict(Hq=3 << 23), 2)):
+                   (dict(L=None), 1), (dict(Q=_fake(0) + 8), 3), (dict(O=_fake(0) + 2), 3), (dict(O=_fake(0)), 1), (dict(Hq=3 << 23), 2)):
         assert _decode(sg, c, **kw) == st, kw
     for kw, st in ((dict(ws=None), 6), (dict(n=100), 6), (dict(ws=_fake(4) + 16), 3)):
         assert _decode(sg, _kv(sg, max_pages=5000), **kw) == st, kw
         assert _decode(sg, c, score=1, **kw) == st, kw
     assert _decode(sg, _kv(sg, score=None), score=1) == 1
-    for kw, st in ((dict(lens=None), 1), (dict(seen=None), 1), (dict(out=None), 1), (dict(out=_fake(0)), 1), (dict(budget=0), 1),
+    for kw, st in ((dict(lens=None), 1), (dict(seen=None), 1), (dict(out=None), 1), (dict(out=_fake(0)), 1), (dict(out=_fake(1)), 1), (dict(budget=0), 1),
                    (dict(recent=-1), 1), (dict(recent=9), 1), (dict(ws=None), 6), (dict(n=8), 6), (dict(ws=_fake(3) + 8), 3)):
         assert _evict(sg, c, **kw) == st, kw
     assert _evict(sg, _kv(sg, score=None)) == 1 and _evict(sg, _kv(sg, pos=None)) == 1
