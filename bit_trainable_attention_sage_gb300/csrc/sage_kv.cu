@@ -251,13 +251,15 @@ static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st
 // through distributed shared memory, and the same CTAs then move the rows.  One launch, and with
 // C up to 8 a few long rows still use many SMs.  Bound by latency: 32 rows of up to 32768 slots cut
 // to 8192 (E4M3, d = 128) take 36 us, 18 of them for the selection's phases (a barrier of the
-// cluster each) and 10 for 57 MB of moves; 64 rows of 1088 cut to 1024 take 9.  (Digits of 11 bits,
-// whose histograms are 64 KB of remote reads a CTA and pass: 39 and 8.8; clusters half as large: 43.)
+// cluster each) and 9 for 57 MB of moves; 64 rows of 1088 cut to 1024 take 9.  (Digits of 11 bits,
+// whose histograms are 64 KB of remote reads a CTA and pass: 39 and 8.8; clusters half as large: 43;
+// four keys a lane and step, a third of the instructions: 36 and 8.7.)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 256;
 constexpr int kSelMaxCluster = 8;
+constexpr int kMoves = 2 * kSelThreads;
 constexpr int kSelMaxKeys = 20 * 1024;       // of a CTA in shared memory; two CTAs an SM
 
 struct EvictArgs {
@@ -278,20 +280,23 @@ __device__ __forceinline__ uint32_t evict_key(float s, bool recent) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);      // at most 0xFF800000 (+inf)
 }
 
-// Moves begin .. end - 1 of a row, kSelThreads at a time: a thread looks up one move's rows and
+// Moves begin .. end - 1 of a row, kMoves at a time: a thread looks up two moves' rows and
 // moves what is a word (scales, score, position), then ROW_BYTES / 16 lanes copy a row's K and V, whose
 // addresses all wait in shared memory.
 template <int ROW_BYTES>
-__device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, int h, int begin, int end, size_t (*rows)[kSelThreads]) {
+__device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, int h, int begin, int end, size_t (*rows)[kMoves]) {
     constexpr int CHUNKS = ROW_BYTES / 16, GROUPS = kSelThreads / CHUNKS, UNROLL = 4;
     const size_t list = static_cast<size_t>(bh) * a.max_moves, base = static_cast<size_t>(bh) * a.c.cap;
     const int tid = threadIdx.x, lane = tid % CHUNKS, group = tid / CHUNKS;
     uint4 *K = static_cast<uint4 *>(a.c.K) + lane, *V = static_cast<uint4 *>(a.c.V) + lane;
     constexpr size_t kNone = ~static_cast<size_t>(0);
-    for (int i0 = begin; i0 < end; i0 += kSelThreads) {
-        const int n = min(kSelThreads, end - i0);
-        if (tid < n) {
-            const int d = a.dst[list + i0 + tid], s = a.src[list + i0 + tid];
+    for (int i0 = begin; i0 < end; i0 += kMoves) {
+        const int n = min(kMoves, end - i0);
+#pragma unroll
+        for (int x = 0; x < kMoves / kSelThreads; ++x) {
+            const int i = x * kSelThreads + tid;
+            if (i >= n) break;
+            const int d = a.dst[list + i0 + i], s = a.src[list + i0 + i];
             const int pd = kv_page(a.c, b, d, &g_kv_err), ps = kv_page(a.c, b, s, &g_kv_err);
             size_t rd = kNone, rs = 0;
             if (pd >= 0 && ps >= 0) {
@@ -307,8 +312,8 @@ __device__ __forceinline__ void evict_moves(const EvictArgs &a, int bh, int b, i
                 a.c.score[base + d] = score;
                 a.c.pos[base + d] = pos;
             }
-            rows[0][tid] = rd;
-            rows[1][tid] = rs;
+            rows[0][i] = rd;
+            rows[1][i] = rs;
         }
         __syncthreads();
         for (int i = group; i < n; i += GROUPS * UNROLL) {
@@ -340,7 +345,7 @@ template <bool CACHED, int ROW_BYTES>
 __global__ void __launch_bounds__(kSelThreads, 2) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ uint32_t s_key[];
     __shared__ __align__(16) int hist[4][kSelBins];
-    __shared__ size_t s_rows[2][kSelThreads];
+    __shared__ size_t s_rows[2][kMoves];
     __shared__ int s_warp[2][kSelWarps];
     __shared__ __align__(16) int s_count[4];                   // of this CTA, read by the others: equal keys; freed, movers
     __shared__ int s_digit, s_above, s_here;
