@@ -25,13 +25,14 @@
  *     which keeps its scratch in a fixed array inside the library.  The other state kept between
  *     calls is the device error word that sage_device_status() reads and clears, and host-side
  *     caches (the SM count per device, the quantise kernels' occupancy, that array's address
- *     per device).
+ *     per device, which decode and eviction kernels' shared-memory limits have been raised).
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default stream).  The
  *     return value reports argument and launch errors only; a device-side timeout of a bounded
- *     wait is reported by sage_device_status().
+ *     wait, and indexes out of range in the cache calls, are reported by sage_device_status().
  *   - Supported: N a multiple of 64 (N >= 64), d in {64, 128}, dtype fp16 or bf16, self-attention
  *     (queries and keys share N).  Inputs must be finite.  All device pointers must be 16-byte
- *     aligned.
+ *     aligned.  (sage_rope and the cache calls state their own sizes; their int32 inputs need
+ *     4-byte alignment.)
  *   - Causal masking is top-left aligned: query n attends to keys m <= n.
  */
 #ifndef SAGE_GB300_H
