@@ -320,11 +320,11 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         rank = cta - pr * a.cluster;
         b = pr / pairs;
         const int pair = pr - b * pairs, hk = pair / a.chunks, h0 = hk * a.G + (pair - hk * a.chunks) * MR;
+        const int outs = min(MR, a.G - (h0 - hk * a.G));
+        const size_t head = static_cast<size_t>(b) * a.Hq + h0;
         fetch(rank, a.c.table + static_cast<size_t>(b) * a.c.max_pages, static_cast<size_t>(a.c.max_pages) * 4,
-              static_cast<const char *>(a.Q) + (static_cast<size_t>(b) * a.Hq + h0) * D * 2, rank == 0 ? MR * D * 2 : 0);
-        if (kv_len(a.c, a.lens, b, &g_decode_err) == 0) {                               // the whole cluster alike
-            const int outs = min(MR, a.G - (h0 - hk * a.G));
-            const size_t head = static_cast<size_t>(b) * a.Hq + h0;
+              static_cast<const char *>(a.Q) + head * D * 2, rank == 0 ? outs * D * 2 : 0);
+        if (kv_len(a.c, a.lens, b, &g_decode_err) == 0) {        // the whole cluster alike
             for (int i = (rank * kDecThreads + tid) * 2; i < outs * D; i += a.cluster * kDecThreads * 2) {
                 store_out(a, head * D + i, 0.0f, 0.0f);
                 if (i % D == 0) a.L[head + i / D] = -INFINITY;
@@ -335,15 +335,19 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         // the join may take its place on the GPU; it waits for this grid's end before it reads
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         fetch(cta, a.c.table, static_cast<size_t>(a.c.B) * a.c.max_pages * 4, a.Q, static_cast<size_t>(a.c.B) * a.Hq * D * 2);
-        // sequences without a token
-        for (int e = cta; e < a.c.B; e += gridDim.x)
-            if (kv_len(a.c, a.lens, e, &g_decode_err) == 0) {
-                const size_t head = static_cast<size_t>(e) * a.Hq;
-                for (int i = tid * 2; i < a.Hq * D; i += kDecThreads * 2) {
+        // sequences cta, cta + gridDim.x, ... without a token: a thread looks, its warp writes
+        const int grid = gridDim.x;
+        for (long long e0 = cta; e0 < a.c.B; e0 += static_cast<long long>(grid) * kDecThreads) {
+            const long long mine = e0 + static_cast<long long>(grid) * tid;
+            uint32_t none = __ballot_sync(0xffffffffu, mine < a.c.B && kv_len(a.c, a.lens, static_cast<int>(min(mine, a.c.B - 1ll)), &g_decode_err) == 0);
+            for (; none; none &= none - 1) {
+                const size_t head = static_cast<size_t>(e0 + static_cast<long long>(grid) * (warp * 32 + __ffs(none) - 1)) * a.Hq;
+                for (int i = lane * 2; i < a.Hq * D; i += 64) {
                     store_out(a, head * D + i, 0.0f, 0.0f);
                     if (i % D == 0) a.L[head + i / D] = -INFINITY;
                 }
             }
+        }
         const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
             const int n = runs_of(a, total);
             return cta < n ? run_start(total, cta, n) : total;

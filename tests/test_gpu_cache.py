@@ -520,3 +520,18 @@ def test_decode_long_caches(kind, Hq, H, d, page, lens, score):
     O, L = sg.sage_attn_decode(Q, cache, ints(lens), score=score)
     assert status(sg) == 0
     check_decode(Q, O, L, lens, K, V, H, cache.score, was)
+
+
+@pytest.mark.parametrize("B,page,n", [(5, 16, 0), (2000, 16, 3), (40, 64, 9000)])
+def test_decode_mostly_empty_batches(B, page, n):
+    """Rows without a token, a few with: a padded batch; O = 0 and L = -inf in all the others."""
+    import bit_trainable_attention_sage_gb300 as sg
+    lens = [0] * B
+    if n:
+        lens[B // 2], lens[B - 1] = n, 1
+    cache, K, V = filled("fp16", B, 1, 64, page, lens, seed=B)
+    Q = torch.randn(B, 3, 1, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
+    O, L = torch.full_like(Q, 7.0), torch.full((B, 3, 1), 7.0, device="cuda")
+    sg.sage_attn_decode(Q, cache, ints(lens), out=O, lse=L)
+    assert status(sg) == 0
+    check_decode(Q, O, L, lens, K, V, 1)
