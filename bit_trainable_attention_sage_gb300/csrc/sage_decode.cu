@@ -461,21 +461,32 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     // A pair's first reads, all on their way together: q, the pages of two granules, the ring's rows.
     // The ring has to be idle.
     auto begin = [&]() {
-        const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
-        auto word = [&](int ks, int half) {          // channels of k = 2q (+ 8 half), in pairs
-            if constexpr (KIND < 2) return ks * 8 + q + half * 4;
-            else return 8 * (q + 4 * (ks >> 2)) + 2 * (ks & 3) + half;
-        };
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    qb[nh][ks][half] = g + 8 * nh < heads ? __ldg(Q + (g + 8 * nh) * (D / 2) + word(ks, half)) : 0u;
-        bad = 0;
         look(0, next[0]);
         look(1, next[1]);
+        // 16 bits: k = 2q (+ 8 half) of step ks are channels ks * 16 + 2q (+ 8 half), as ldmatrix deals K's
+        // rows out; 8 bits: channels 16 (q + 4 jj) + 4 i + 2 half of step 4 jj + i, 32 consecutive bytes a lane
+        const uint32_t *Q = static_cast<const uint32_t *>(a.Q) + (static_cast<size_t>(b) * a.Hq + head0) * (D / 2);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const bool is = g + 8 * nh < heads;
+            const uint32_t *row = Q + (is ? (g + 8 * nh) * (D / 2) : 0);
+            if constexpr (KIND < 2) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) qb[nh][ks][half] = is ? __ldg(row + ks * 8 + q + half * 4) : 0u;
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += 2) {
+                    const uint4 w = is ? __ldg(reinterpret_cast<const uint4 *>(row + 8 * (q + ks / 4 * 4) + 2 * (ks & 3))) : make_uint4(0u, 0u, 0u, 0u);
+                    qb[nh][ks][0] = w.x;
+                    qb[nh][ks][1] = w.y;
+                    qb[nh][ks + 1][0] = w.z;
+                    qb[nh][ks + 1][1] = w.w;
+                }
+            }
+        }
+        bad = 0;
 #pragma unroll
         for (int j = 0; j < S::STAGES - 1; ++j) {
             if (j < ng) load(j, j);
@@ -979,6 +990,19 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     const int heads = min(MR, a.G - ch * MR);
     const size_t head0 = static_cast<size_t>(b) * a.Hq + hk * a.G + ch * MR;
     if (PAIRS && static_cast<int>(blockIdx.y) >= heads) return;
+    // (PAIRS: a thread's first parts are asked for before the maximum is known)
+    constexpr int EARLY = PAIRS ? 8 : 1;
+    float4 part[EARLY];
+    float part_m[EARLY];
+    if constexpr (PAIRS) {
+#pragma unroll
+        for (int x = 0; x < EARLY; ++x) {
+            const int c = c0 + grp + x * GROUPS;
+            const size_t at = part_of(min(c, c1), c0, MR, blockIdx.y);
+            part[x] = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
+            part_m[x] = c <= c1 ? a.part_ml[2 * at] : -INFINITY;
+        }
+    }
     for (int r = PAIRS ? blockIdx.y + warp * MR : warp; r < heads; r += PAIRS ? MR * kJoinThreads : kJoinThreads / 32) {
         const float2 ml = join_ml(a, c0, c1, MR, r, lane);
         if (lane == 0) {
@@ -1007,10 +1031,16 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     };
     if constexpr (PAIRS) {
         const int r = blockIdx.y;
-        s_o[grp][v] = sums(r, c0 + grp, GROUPS);
+        float4 o = sums(r, c0 + grp + EARLY * GROUPS, GROUPS);
+#pragma unroll
+        for (int x = 0; x < EARLY; ++x) {
+            const float f = ex2_approx(part_m[x] - s_M[r]);
+            o.x += f * part[x].x; o.y += f * part[x].y; o.z += f * part[x].z; o.w += f * part[x].w;
+        }
+        s_o[grp][v] = o;
         __syncthreads();
         if (tid < VEC) {
-            float4 o = s_o[0][v];
+            o = s_o[0][v];
 #pragma unroll
             for (int x = 1; x < GROUPS; ++x) {
                 const float4 y = s_o[x][v];
