@@ -38,11 +38,11 @@ class SageRopeParams(ctypes.Structure):
 
 def _need(t: torch.Tensor, what: str, dtype, shape, device):
     """A contiguous tensor of this type and shape on this device."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -60,8 +60,9 @@ def _cuda(device):
 
 
 def _elsewhere(stream, device) -> bool:
-    """Whether the call has to change the current stream or device first (with _on)."""
-    return stream is not None or torch.cuda.current_device() != device.index
+    """Whether the call has to change the current stream or device first (with _on).
+    torch.cuda.current_device() would check that CUDA is initialised; the call's tensors show it."""
+    return stream is not None or torch._C._cuda_getDevice() != device.index
 
 
 @contextlib.contextmanager
@@ -104,9 +105,9 @@ class Rope:
             if len(self._made) >= 64:
                 self._made = {}
             B, H, Hk, N, dtype, pb, inverse = key
-            p = self._made[key] = SageRopeParams(B, H, Hk, N, self.d, _DTYPES[dtype], self.axes, pb, self.rotary,
-                                                 self.interleaved, inverse, self._sections, self._freq)
-        return ctypes.byref(p)
+            p = self._made[key] = ctypes.byref(SageRopeParams(B, H, Hk, N, self.d, _DTYPES[dtype], self.axes, pb, self.rotary,
+                                                              self.interleaved, inverse, self._sections, self._freq))
+        return p
 
 
 def make_rope(d: int, sections, *, base: float = 10000.0, interleaved: bool = False, freqs=None) -> Rope:
@@ -158,8 +159,8 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
         _need(Qo, "out[0]", dtype, shape, dev)
         if K is not None:
             _need(Ko, "out[1]", dtype, K.shape, dev)
-    st = lib().sage_rope(rope._struct(B, H, Hk, N, dtype, pb, bool(inverse)), Q.data_ptr(), None if K is None else K.data_ptr(), positions.data_ptr(),
-                         Qo.data_ptr(), None if K is None else Ko.data_ptr(), _current(dev))
+    st = lib().sage_rope(rope._struct(B, H, Hk, N, dtype, pb, bool(inverse)), Q.data_ptr(), None if K is None else K.data_ptr(),
+                         positions.data_ptr(), Qo.data_ptr(), None if K is None else Ko.data_ptr(), _current(dev))
     _check("sage_rope", st)
     return Qo, Ko
 
@@ -198,17 +199,18 @@ class KvCache:
                 _need(t, name, dt, (B, H, self.capacity), dev)
         self.K, self.V, self.sK, self.sV, self.table, self.score, self.pos = K, V, sK, sV, table, score, pos
         self.B, self.H, self.d, self.page, self.pages, self.device = B, H, d, page, pages, dev
-        self._c = {dt: SageKv(B, H, d, dt, self.kind, page, pages, max_pages, K.data_ptr(), V.data_ptr(), _ptr(sK), _ptr(sV),
-                              table.data_ptr(), _ptr(score), _ptr(pos)) for dt in (SAGE_FP16, SAGE_BF16)}
+        # a struct for each 16-bit type that calls may bring
+        types = (K.dtype,) if self.kind == SAGE_KV_16 else (torch.float16, torch.bfloat16)
+        self._c = {t: ctypes.byref(SageKv(B, H, d, _DTYPES[t], self.kind, page, pages, max_pages, K.data_ptr(), V.data_ptr(),
+                                          _ptr(sK), _ptr(sV), table.data_ptr(), _ptr(score), _ptr(pos))) for t in types}
         self._bytes = {}        # workspace sizes by what they depend on
 
     def _struct(self, t: torch.Tensor, what: str):
         """The struct for a call on 16-bit tensors like ``t``."""
-        if t.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError(f"{what}: SageBwd takes fp16 or bf16 tensors, got {t.dtype}")
-        if self.kind == SAGE_KV_16 and t.dtype != self.K.dtype:
-            raise TypeError(f"{what}: the cache holds {self.K.dtype}, got {t.dtype}")
-        return ctypes.byref(self._c[_DTYPES[t.dtype]])
+        c = self._c.get(t.dtype)
+        if c is None:
+            raise TypeError(f"{what}: the cache takes {', '.join(map(str, self._c))}, got {t.dtype}")
+        return c
 
 
 def make_kv_cache(B: int, H: int, d: int, capacity: int, *, dtype=torch.int8, page: int = 64, score: bool = False,
@@ -298,7 +300,7 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
     recent = min(recent, budget)
     _need(lens, "lens", torch.int32, (cache.B,), dev)
     _need(seen, "seen", torch.int32, (cache.B,), dev)
-    c = ctypes.byref(cache._c[SAGE_BF16 if cache.K.dtype == torch.bfloat16 else SAGE_FP16])
+    c = next(iter(cache._c.values()))
     nbytes = cache._bytes.get(budget)
     if nbytes is None:
         nbytes = cache._bytes[budget] = lib().sage_evict_workspace_bytes(c, budget)
