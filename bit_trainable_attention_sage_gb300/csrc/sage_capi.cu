@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "sage_internal.h"
+#include "sage_kv.cuh"
 
 namespace sage {
 

@@ -145,10 +145,6 @@ cudaError_t launch_bwd_qat(const sage_params &p, const void *Qf, const void *Kf,
                            const void *dO, BwdArgs a, cudaStream_t st);
 unsigned int take_bwd_error();
 
-// sage_kv.cu, sage_decode.cu: nonzero if a page, length or slot was out of range (and clear it)
-unsigned int take_kv_error();
-unsigned int take_decode_error();
-
 // tensor maps (sage_capi.cu)
 // (d, N, B*H) 16-bit tensor maps with 64 x box_rows boxes and the 128-byte swizzle
 bool make_tmap_3d(CUtensorMap *map, const void *ptr, int d, int N, uint64_t bh, uint32_t box_rows = 128);

@@ -8,6 +8,10 @@
 
 namespace sage {
 
+// sage_kv.cu, sage_decode.cu: nonzero if a page, length or slot was out of range (and clear it)
+unsigned int take_kv_error();
+unsigned int take_decode_error();
+
 // ---- thread-block clusters ---------------------------------------------------------------------
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
