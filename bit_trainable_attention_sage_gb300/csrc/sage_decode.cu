@@ -283,7 +283,9 @@ __device__ __forceinline__ void store_out(const DecodeArgs &a, size_t at, float 
     reinterpret_cast<uint32_t *>(a.O)[at / 2] = w;
 }
 
-// m + log2 l in natural units
+// 1 / l, and 0 where nothing was summed; a NaN stays one
+__device__ __forceinline__ float inv_of(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// m + log2 l in natural units; -inf where nothing was summed (m = -inf, l = 0)
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
 // ---- main kernel ------------------------------------------------------------------------------
@@ -830,10 +832,10 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             }
             const size_t head = out0 + r;
             if (whole) {
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                const float inv = inv_of(sum);
                 store_out(a, head * D + c, o0 * inv, o1 * inv);
                 if (c == 0) {
-                    a.L[head] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+                    a.L[head] = lse_of(M, sum);
                     if (a.row_ml) {
                         a.row_ml[2 * head] = M;
                         a.row_ml[2 * head + 1] = sum;
@@ -870,8 +872,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                         sum += f * ml[k][1];
                     }
                 s_m[0][tid] = ref;
-                s_l[0][tid] = sum > 0.0f ? 1.0f / sum : 0.0f;
-                if (rank == 0) a.L[out0 + tid] = sum > 0.0f ? lse_of(M, sum) : -INFINITY;
+                s_l[0][tid] = inv_of(sum);
+                if (rank == 0) a.L[out0 + tid] = lse_of(M, sum);
             }
             __syncthreads();
             for (int i = (rank * kDecThreads + tid) * 4; i < outs * D; i += a.cluster * kDecThreads * 4) {
@@ -998,17 +1000,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < EARLY; ++x) {
             const int c = c0 + grp + x * GROUPS;
-            const size_t at = part_of(min(c, c1), c0, MR, blockIdx.y);
+            part[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            part_m[x] = -INFINITY;
+            if (c > c1) continue;
+            const size_t at = part_of(c, c0, MR, blockIdx.y);
             part[x] = reinterpret_cast<const float4 *>(a.part_O + at * D)[v];
-            part_m[x] = c <= c1 ? a.part_ml[2 * at] : -INFINITY;
+            part_m[x] = a.part_ml[2 * at];
         }
     }
     for (int r = PAIRS ? blockIdx.y + warp * MR : warp; r < heads; r += PAIRS ? MR * kJoinThreads : kJoinThreads / 32) {
         const float2 ml = join_ml(a, c0, c1, MR, r, lane);
         if (lane == 0) {
             s_M[r] = ml.x == -INFINITY ? 0.0f : ml.x;
-            s_inv[r] = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
-            a.L[head0 + r] = ml.y > 0.0f ? lse_of(ml.x, ml.y) : -INFINITY;
+            s_inv[r] = inv_of(ml.y);
+            a.L[head0 + r] = lse_of(ml.x, ml.y);
         }
     }
     __syncthreads();
@@ -1100,11 +1105,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
                 ml = reinterpret_cast<const float2 *>(a.row_ml)[head0 + h];
             } else {
                 ml = join_ml(a, c0, c1, MR, r, lane);
-                if (lane == 0 && h % ys == y) a.L[head0 + h] = ml.y > 0.0f ? lse_of(ml.x, ml.y) : -INFINITY;
+                if (lane == 0 && h % ys == y) a.L[head0 + h] = lse_of(ml.x, ml.y);
             }
             if (lane == 0) {
                 s_M[i] = ml.x == -INFINITY ? 0.0f : ml.x;
-                s_inv[i] = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+                s_inv[i] = inv_of(ml.y);
             }
         }
         __syncthreads();

@@ -205,6 +205,66 @@ def test_decode_scales_far_apart(kind):
         check_decode(Q, O, L, [n], K, V, 1)
 
 
+@pytest.mark.parametrize("score", [False, True])
+@pytest.mark.parametrize("kind,lens", [
+    ("fp16", [40, 100]),                                 # a pair in one cluster
+    ("fp8", [9, 30]),
+    ("bf16", [20000, 33]),                               # few long sequences: joined a head a block
+    ("int8", [20000, 33]),
+    ("int8", [300 + 7 * b for b in range(90)]),          # joined where runs meet, and whole pairs
+    ("bf16", [300 + 7 * b for b in range(90)]),
+])
+def test_decode_keeps_a_nan(kind, lens, score):
+    """A NaN in one head's q makes that head's O and L NaN (not L = -inf, which says: no slots) and
+    leaves every other head's bits as they are; scores of its kv head become NaN, others keep theirs."""
+    import bit_trainable_attention_sage_gb300 as sg
+    B, d = len(lens), 64
+    dtype = KINDS[kind] if kind in ("fp16", "bf16") else torch.float16
+    cache, _, _ = filled(kind, B, 2, d, 64, lens, seed=3, score=True)
+    was = cache.score.clone()
+    Q = torch.randn(B, 6, 1, d, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    O, L = sg.sage_attn_decode(Q, cache, ints(lens), score=score)
+    clean = cache.score.clone()
+    cache.score.copy_(was)
+    Q2 = Q.clone()
+    Q2[0, 1, 0, 5] = float("nan")
+    O2, L2 = sg.sage_attn_decode(Q2, cache, ints(lens), score=score)
+    assert status(sg) == 0
+    assert torch.isnan(O2[0, 1]).all() and torch.isnan(L2[0, 1]).all()
+    O2[0, 1], L2[0, 1] = O[0, 1], L[0, 1]
+    assert torch.equal(bits(O2), bits(O)) and torch.equal(bits(L2), bits(L))
+    if score:
+        assert torch.isnan(cache.score[0, 0, :lens[0]]).all()
+        cache.score[0, 0, :lens[0]] = clean[0, 0, :lens[0]]
+        assert torch.equal(bits(cache.score), bits(clean))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "int8", "fp8"])
+@pytest.mark.parametrize("n", [50, 5000])
+def test_decode_keeps_a_nan_of_the_cache(kind, n):
+    """A NaN in a cached V (8 bits: in its scale) reaches O alone; one in a cached K every head's O and L
+    of its kv head.  The other kv head's bits stay."""
+    import bit_trainable_attention_sage_gb300 as sg
+    dtype = KINDS[kind] if kind in ("fp16", "bf16") else torch.float16
+    Q = torch.randn(1, 4, 1, 64, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    for which in ("V", "K"):
+        cache, _, _ = filled(kind, 1, 2, 64, 16, [n], seed=4)
+        O, L = sg.sage_attn_decode(Q, cache, ints([n]))
+        t = n // 2
+        page = int(cache.table[0, t // 16])
+        if kind in ("int8", "fp8"):
+            getattr(cache, "s" + which)[page, 0, t % 16] = float("nan")
+        else:
+            getattr(cache, which)[page, 0, t % 16, 7] = float("nan")
+        O2, L2 = sg.sage_attn_decode(Q, cache, ints([n]))
+        assert torch.equal(bits(O2[:, 2:]), bits(O[:, 2:])) and torch.equal(bits(L2[:, 2:]), bits(L[:, 2:]))
+        if which == "K":
+            assert torch.isnan(O2[:, :2]).all() and torch.isnan(L2[:, :2]).all()
+        else:
+            where = slice(None) if kind in ("int8", "fp8") else slice(7, 8)
+            assert torch.isnan(O2[:, :2, :, where]).all() and torch.equal(bits(L2), bits(L))
+
+
 def test_decode_shared_prefix_pages():
     """Two sequences read the same pages; scores stay each sequence's own."""
     import bit_trainable_attention_sage_gb300 as sg
