@@ -108,10 +108,11 @@ __device__ __forceinline__ void kv_codes(const f2 (&x)[8], float delta, uint2 (&
     out[1] = make_uint2(w[2], w[3]);
 }
 
-// max(|a|, |b|), under some sign
+// max(|a|, |b|), under some sign; a NaN stays one, so that a row with one gets a scale that says so
+// (INT8 has no code for it)
 __device__ __forceinline__ float larger(float a, float b) {
     float d;
-    asm("max.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 // The largest magnitude of a row that LANES lanes hold.  (Shuffles: a reduction instruction under

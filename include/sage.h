@@ -417,6 +417,7 @@ typedef struct sage_kv {
  * mu (B,H,d) float32, 8-bit kinds only, nullable: K-smoothing, the codes are those of
  * fl32(K - mu); attention over keys that share one mu does not change (L does, by q . mu /
  * sqrt(d)).  sage_quantize_smooth's muK of the prompt is such a mu.
+ * 8-bit kinds: a row with a NaN or an infinity gets a scale that is NaN or infinite.
  * Where the cache has score: score[slot] = 0.  Where it has pos: pos[slot] = pos0[b] + t, with
  * pos0 NULL: the slot itself. */
 SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int T, const int *start,
@@ -427,6 +428,7 @@ SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int 
  * if it has been appended): s_t = q . K_t / sqrt(d), O = sum_t softmax(s)_t V_t,
  * L = log sum_t exp s_t.  Query head h reads kv head h / (Hq / H).  lens[b] = 0: O = 0, L = -inf.
  * In:  Q (B,Hq,1,d).  Out: O (B,Hq,1,d), L (B,Hq,1) float32.
+ * A NaN in q, or in a cached K or its scale, makes the O and L of the heads that read it NaN.
  * add_score = 1: score[b][kv head][t] += the sum over its query heads of softmax(s)_t.
  * Sums and statistics are float32; the probabilities enter the second product as two 16-bit
  * terms (16 or more significant bits).  Results do not depend on the order in which the GPU runs

@@ -94,6 +94,45 @@ def test_append_extreme_rows(kind):
     assert torch.equal(bits(cache.K.cpu()), bits(pools[0])) and torch.equal(bits(cache.V.cpu()), bits(pools[1]))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mu", [False, True])
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_append_keeps_nan_and_infinity(kind, mu, d):
+    """A NaN or infinite value in a row shows in the row's scale (INT8 has no code for it) and so in what is
+    read back; all other rows, of the same warp too, keep their bits."""
+    import bit_trainable_attention_sage_gb300 as sg
+    T = 40
+    g = torch.Generator().manual_seed(d)
+    K, V = (torch.randn(1, 2, T, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    mu_t = torch.randn(1, 2, d, generator=g).cuda() if mu else None
+
+    def stored(K, V):
+        cache = sg.make_kv_cache(1, 2, d, T, dtype=KINDS[kind], page=48)
+        sg.sage_kv_append(cache, K, V, ints([0]), mu=mu_t)
+        assert status(sg) == 0
+        return cache
+
+    clean = stored(K, V)
+    K2, V2 = K.clone(), V.clone()
+    for i, bad in enumerate((float("nan"), float("inf"), float("-inf"))):
+        for c in (0, d // 2 + 3, d - 1):
+            K2[0, 0, 3 * c % 13 + i * 13, c] = bad
+        V2[0, 1, 5 + i, 9] = bad
+    V2[0, 0, 20], V2[0, 0, 20, 1] = 0, float("nan")      # the rest of the row zero
+    got = stored(K2, V2)
+    for x, x2, pool, pool2, scale, scale2 in ((K, K2, clean.K, got.K, clean.sK, got.sK), (V, V2, clean.V, got.V, clean.sV, got.sV)):
+        ok = torch.isfinite(x2).all(-1)[0]
+        assert not ok.all()
+        nan = torch.isnan(x2).any(-1)[0]
+        assert torch.equal(torch.isnan(scale2[0, :, :T]), nan) and torch.equal(torch.isinf(scale2[0, :, :T]), ~ok & ~nan)
+        assert torch.equal(bits(scale2[0, :, :T][ok]), bits(scale[0, :, :T][ok]))
+        assert torch.equal(bits(pool2[0, :, :T][ok]), bits(pool[0, :, :T][ok]))
+    Q = torch.ones(1, 2, 1, d, dtype=torch.bfloat16, device="cuda")
+    O, L = sg.sage_attn_decode(Q, got, ints([T]))
+    assert torch.isnan(L[0, 0]).all() and torch.isnan(O[0, 0]).all()
+    assert torch.isfinite(L[0, 1]).all() and not torch.isfinite(O[0, 1]).any()
+
+
 def test_append_long_prompt_default_count_and_positions():
     import bit_trainable_attention_sage_gb300 as sg
     T = 1000
