@@ -123,19 +123,19 @@ def sage_attention_qat(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, *, cau
 
 
 class SageRotaryFunction(torch.autograd.Function):
-    """(Q, K) turned by rotary positions; the gradients are turned back."""
+    """(Q, K) turned by rotary positions; the gradients are turned back, and theirs forward again."""
 
     @staticmethod
-    def forward(ctx, Q, K, positions, rope):
-        ctx.rope = rope
+    def forward(ctx, Q, K, positions, rope, inverse=False):
+        ctx.rope, ctx.inverse = rope, inverse
         ctx.save_for_backward(positions)
-        return sage_rope(Q.contiguous(), K.contiguous(), positions, rope)
+        return sage_rope(Q.contiguous(), K.contiguous(), positions, rope, inverse=inverse)
 
     @staticmethod
     def backward(ctx, dQ, dK):
         (positions,) = ctx.saved_tensors
-        dQ, dK = sage_rope(dQ.contiguous(), dK.contiguous(), positions, ctx.rope, inverse=True)
-        return dQ, dK, None, None
+        dQ, dK = SageRotaryFunction.apply(dQ, dK, positions, ctx.rope, not ctx.inverse)
+        return dQ, dK, None, None, None
 
 
 def sage_rotary(Q: torch.Tensor, K: torch.Tensor, positions: torch.Tensor, rope):

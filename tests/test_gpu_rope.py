@@ -155,6 +155,32 @@ def test_rotary_gradient(dtype):
         assert abs(lhs - rhs) <= bound
 
 
+def test_rotary_second_derivative():
+    """f = sum of x'^4 / 12 over the turned x' = R x: the gradient R^T x'^3 / 3 is itself differentiable, and its
+    product with t is R^T (x'^2 R t).  float32: with ey, et the tolerances of the turned x and t and a rounding each,
+    x'^2 R t is off by 2 |y t| ey + y^2 et (1 + 2^-10 for their products) and its own arithmetic: powers of at most
+    2 units in the last place, and fewer than 12 further roundings, 16 u; the last turn adds both channels' errors,
+    its own tolerance and a rounding."""
+    import bit_trainable_attention_sage_gb300 as sg
+    rope = sg.make_rope(64, [8, 24])
+    g = torch.Generator().manual_seed(0)
+    Q, K, tq, tk = (torch.randn(2, h, 33, 64, generator=g) for h in (3, 2, 3, 2))
+    pos = torch.randint(0, 5000, (2, 1, 33), generator=g, dtype=torch.int32)
+    Qc, Kc = Q.cuda().requires_grad_(), K.cuda().requires_grad_()
+    Qo, Ko = sg.sage_rotary(Qc, Kc, pos.cuda(), rope)
+    dQ, dK = torch.autograd.grad((Qo ** 4).sum() / 12 + (Ko ** 4).sum() / 12, (Qc, Kc), create_graph=True)
+    hQ, hK = torch.autograd.grad((dQ * tq.cuda()).sum() + (dK * tk.cuda()).sum(), (Qc, Kc))
+    p = pos.numpy().astype(np.int64)
+    for x, t, got in ((Q, tq, hQ), (K, tk, hK)):
+        (y, ey), (ty, et) = reference(x.numpy(), p, rope), reference(t.numpy(), p, rope)
+        ey, et = ey + U * np.abs(y), et + U * np.abs(ty)
+        e = (2 * np.abs(y * ty) * ey + y * y * et) * (1 + 2.0 ** -10) + 16 * U * np.abs(y * y * ty)
+        half = rope.rotary // 2
+        e = np.concatenate([e[..., :half] + e[..., half:]] * 2, -1)
+        want, tol = reference(y * y * ty, p, rope, inverse=True)
+        check(got, want, (e + tol) * (1 + 2.0 ** -10))
+
+
 @pytest.mark.parametrize("causal,dtype,norm", [(False, "fp16", False), (True, "bf16", True)])
 def test_attention_with_rope_equals_its_calls(causal, dtype, norm):
     """sage_attention(rope=...) is turn -> quantise -> forward, and backward -> turn back in float32."""
