@@ -30,11 +30,17 @@
 //     order as long as both operands agree, so a lane takes 16 consecutive bytes of a row with
 //     one load and assigns them to the products' positions itself; no transposition is needed.
 //     q is scaled by a power of two a head to stay in fp16's range: exact to 2^-39 of its largest
-//     value.  sK multiplies the logit; sV the probability, over a running power of two `vref` that
-//     keeps the product in fp16's range.
-//   - The probabilities enter as hi + lo of two 16-bit values, at least 16 bits: one rounding to
-//     bf16 would show in the output.  They change from the first product's layout to the second's
-//     operand by movmatrix (8 x 8 transposition in registers).
+//     value.  sK multiplies the logit, sV the probability.
+//   - The probabilities enter as hi + lo of two values with float32's exponents, 16 bits or more of
+//     each: one rounding to bf16 would show in the output, and fp16's exponents would end 2^-24 below
+//     the largest, where the small weights beside a key that takes nearly all of it still make up the
+//     output if that key's value is small.  bf16 and 8-bit pools: bf16 (8 + 8 bits), which holds the
+//     codes too.  fp16 pools: the 11-bit type of m16n8k8, which holds fp16's 11 bits.  Two fp16 terms,
+//     which lose the small weights, would save 1 % in fp16 pools (32 x 8191 tokens of 16 heads, d = 128:
+//     312 against 317 us) and 1 to 7 % in 8 bits (262144 tokens of 8 heads: 89.9 against 90.9 in E4M3,
+//     88.3 against 92.8 in INT8).  bf16 pools in the 11-bit type: 319 against 313.
+//   - They change from the first product's layout to the second's operand by movmatrix (8 x 8
+//     transposition in registers).
 #include <utility>
 
 #include "sage_kv.cuh"
@@ -130,6 +136,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// the same over 8 rows of the second dimension, 32-bit values of 11 bits
+__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Place of 16-byte chunk c of row r in half a granule (16 rows; the other half follows).  Rows of 128 and 256 bytes in 16 bits: the 8
 // rows an ldmatrix reads at one chunk fall into the 8 different 16-byte bank groups.  In 8 bits
 // a quarter-warp reads chunks 0-3 of rows (2i, 2i + 1), or chunks (2i, 2i + 1) of rows 0, 2, 4, 6
@@ -171,6 +184,23 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     }
 }
 
+// The same as bf16 pairs.  INT8: the low seven bits under 0x43 are 128 + them in bf16, the sign under 0x43
+// 128 or 256; their difference is the code.  E4M3 through float32.  All exact.
+template <int KIND>
+__device__ __forceinline__ void widen4_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (KIND == 2) {
+        const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
+    } else {
+        widen4<KIND>(w, lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
+    }
+}
+
 // 8 x 8 transposition of 16-bit values over a warp: lane (g, q) gives row g, columns 2q and 2q + 1
 // and gets those of column g.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -178,23 +208,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+// The same of 32-bit values, by their halves: (row g, column 2q), (row g, column 2q + 1) in, (row 2q, column g),
+// (row 2q + 1, column g) out.
+__device__ __forceinline__ void transpose8(float &x0, float &x1) {
+    const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
+    const uint32_t lo = transpose8(prmt(a, b, 0x5410)), hi = transpose8(prmt(a, b, 0x7632));
+    x0 = __uint_as_float(prmt(lo, hi, 0x5410));
+    x1 = __uint_as_float(prmt(lo, hi, 0x7632));
+}
 
-// (x0, x1) as hi + lo pairs of the product's 16-bit type
-template <bool BF16>
+// (x0, x1) as hi + lo pairs of bf16
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(x0, x1);
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// x as hi + lo of 11 bits each under float32's exponents (cut: 21 bits together)
+__device__ __forceinline__ void split11(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
 }
 
 // ---- the cut of the work ---------------------------------------------------------------------
@@ -292,7 +326,8 @@ __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)
 template <int D, int KIND, int MR, bool ONE>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND, MR>;
-    constexpr bool BF16 = KIND == 1;                 // type of the products
+    constexpr bool BF16 = KIND == 1;                 // type of the product K q
+    constexpr bool TF32 = KIND == 0;                 // type of the product V^T P: 11 bits under float32's exponents, or bf16
     constexpr int KS = D / 16;                       // 16-channel steps of K q, row tiles of V^T P
     constexpr int HALVES = S::GRAN / 16;             // row tiles of K q, 16-token steps of V^T P
     constexpr int NH = MR / 8;                       // column tiles: 8 heads each
@@ -548,7 +583,6 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             m[nh][0] = m[nh][1] = -INFINITY;
             l[nh][0] = l[nh][1] = 0.0f;
         }
-        float vref = 1.1754943508222875e-38f;                    // 2^-126
 
         int stage = 0, ahead = S::STAGES - 1;                    // stages of granules j and j + STAGES - 1
         for (int j = 0; j < ng; ++j) {
@@ -668,30 +702,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                     l[nh][e] = l[nh][e] * alpha[nh][e] + sum;
                 }
             if constexpr (KIND >= 2) {
-                // the largest sV so far, as a power of two above it
-                float mv = fmaxf(fv[0][0], fv[0][1]);
-#pragma unroll
-                for (int hf = 1; hf < HALVES; ++hf) mv = max3f(mv, fv[hf][0], fv[hf][1]);
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 4));
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 8));
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 16));
-                if (mv > vref) {
-                    const float up = __uint_as_float(min((__float_as_uint(mv) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
-                    const float f = vref / up;
-                    vref = up;
-#pragma unroll
-                    for (int nh = 0; nh < NH; ++nh) {
-                        alpha[nh][0] *= f;
-                        alpha[nh][1] *= f;
-                    }
-                }
-                const float iv = __uint_as_float(0x7F000000u - __float_as_uint(vref));   // 1 / vref
 #pragma unroll
                 for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
                     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[hf][nh][i] *= fv[hf][i >> 1] * iv;
+                        for (int i = 0; i < 4; ++i) s[hf][nh][i] *= fv[hf][i >> 1];
             }
             bool moved = false;
 #pragma unroll
@@ -707,53 +723,82 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             }
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
-                uint32_t ph[NH][2], pl[NH][2];                   // hi, lo: tokens 2q, 2q + 1 (+ 8) of head g
+                if constexpr (TF32) {
+                    uint32_t ph[NH][4], pl[NH][4];               // hi, lo: tokens 2q, 2q + 1, 2q + 8, 2q + 9 of head g
 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh)
+                    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        split2<BF16>(s[hf][nh][2 * x], s[hf][nh][2 * x + 1], ph[nh][x], pl[nh][x]);
-                        ph[nh][x] = transpose8(ph[nh][x]);
-                        pl[nh][x] = transpose8(pl[nh][x]);
-                    }
-                auto pv = [&](int jn, const uint32_t (&va)[4]) {
-#pragma unroll
-                    for (int nh = 0; nh < NH; ++nh) mma16816<BF16>(acc[jn][nh], va, ph[nh][0], ph[nh][1]);
-#pragma unroll
-                    for (int nh = 0; nh < NH; ++nh) mma16816<BF16>(acc[jn][nh], va, pl[nh][0], pl[nh][1]);
-                };
-                if constexpr (KIND < 2) {
+                        for (int x = 0; x < 4; x += 2) {
+                            transpose8(s[hf][nh][x], s[hf][nh][x + 1]);
+                            split11(s[hf][nh][x], ph[nh][x], pl[nh][x]);
+                            split11(s[hf][nh][x + 1], ph[nh][x + 1], pl[nh][x + 1]);
+                        }
                     const uint32_t at = smem_u32(vst) + hf * HALF + chunk_at<D, KIND>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
                     for (int jn = 0; jn < KS; ++jn) {
                         uint32_t va[4];
                         ldsm4t(at ^ (jn * 32), va);
-                        pv(jn, va);
-                    }
-                } else {
-                    // tokens 2q, 2q + 1, 2q + 8, 2q + 9; row g of tile jn is channel D / 8 g + 2 jn, row g + 8 the next
-                    constexpr int W = D / 32;
-                    uint32_t x[4][W];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint8_t *at = vst + hf * HALF + (t >> 1) * 8 * S::ROW;
-                        if constexpr (D == 128) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g));
-                            x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g >> 1) + (g & 1) * 8);
-                            x[t][0] = v.x; x[t][1] = v.y;
+                        for (int x = 0; x < 4; x += 2) {
+                            // rows g, g + 8; the products' rows q and q + 4 of the second dimension are tokens 2q and 2q + 1
+                            const float2 v0 = __half22float2(*reinterpret_cast<const __half2 *>(&va[x]));
+                            const float2 v1 = __half22float2(*reinterpret_cast<const __half2 *>(&va[x + 1]));
+                            const uint32_t a0 = __float_as_uint(v0.x), a1 = __float_as_uint(v1.x), a2 = __float_as_uint(v0.y), a3 = __float_as_uint(v1.y);
+#pragma unroll
+                            for (int nh = 0; nh < NH; ++nh) mma1688(acc[jn][nh], a0, a1, a2, a3, ph[nh][x], ph[nh][x + 1]);
+#pragma unroll
+                            for (int nh = 0; nh < NH; ++nh) mma1688(acc[jn][nh], a0, a1, a2, a3, pl[nh][x], pl[nh][x + 1]);
                         }
                     }
+                } else {
+                    uint32_t ph[NH][2], pl[NH][2];                   // hi, lo: tokens 2q, 2q + 1 (+ 8) of head g
 #pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        uint32_t va[2][4];
-                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x5140), va[0][0], va[0][1]);
-                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x5140), va[0][2], va[0][3]);
-                        widen4<KIND>(prmt(x[0][i], x[1][i], 0x7362), va[1][0], va[1][1]);
-                        widen4<KIND>(prmt(x[2][i], x[3][i], 0x7362), va[1][2], va[1][3]);
-                        pv(2 * i, va[0]);
-                        pv(2 * i + 1, va[1]);
+                    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            split2(s[hf][nh][2 * x], s[hf][nh][2 * x + 1], ph[nh][x], pl[nh][x]);
+                            ph[nh][x] = transpose8(ph[nh][x]);
+                            pl[nh][x] = transpose8(pl[nh][x]);
+                        }
+                    auto pv = [&](int jn, const uint32_t (&va)[4]) {
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh) mma16816<true>(acc[jn][nh], va, ph[nh][0], ph[nh][1]);
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh) mma16816<true>(acc[jn][nh], va, pl[nh][0], pl[nh][1]);
+                    };
+                    if constexpr (KIND < 2) {
+                        const uint32_t at = smem_u32(vst) + hf * HALF + chunk_at<D, KIND>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+#pragma unroll
+                        for (int jn = 0; jn < KS; ++jn) {
+                            uint32_t va[4];
+                            ldsm4t(at ^ (jn * 32), va);
+                            pv(jn, va);
+                        }
+                    } else {
+                        // tokens 2q, 2q + 1, 2q + 8, 2q + 9; row g of tile jn is channel D / 8 g + 2 jn, row g + 8 the next
+                        constexpr int W = D / 32;
+                        uint32_t x[4][W];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint8_t *at = vst + hf * HALF + (t >> 1) * 8 * S::ROW;
+                            if constexpr (D == 128) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g));
+                                x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2 *>(at + chunk_at<D, KIND>(2 * q + (t & 1), g >> 1) + (g & 1) * 8);
+                                x[t][0] = v.x; x[t][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            uint32_t va[2][4];
+                            widen4_bf16<KIND>(prmt(x[0][i], x[1][i], 0x5140), va[0][0], va[0][1]);
+                            widen4_bf16<KIND>(prmt(x[2][i], x[3][i], 0x5140), va[0][2], va[0][3]);
+                            widen4_bf16<KIND>(prmt(x[0][i], x[1][i], 0x7362), va[1][0], va[1][1]);
+                            widen4_bf16<KIND>(prmt(x[2][i], x[3][i], 0x7362), va[1][2], va[1][3]);
+                            pv(2 * i, va[0]);
+                            pv(2 * i + 1, va[1]);
+                        }
                     }
                 }
             }
@@ -799,7 +844,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    so[(nh * 8 + 2 * q + (i & 1)) * PITCH + jn * 16 + 8 * (i >> 1) + g] = acc[jn][nh][i] * (KIND < 2 ? 1.0f : vref);
+                    so[(nh * 8 + 2 * q + (i & 1)) * PITCH + jn * 16 + 8 * (i >> 1) + g] = acc[jn][nh][i];
         __syncthreads();
         // ONE: the CTA's sums, (MR, D) floats, in the first stage of the first ring
         float *sums = reinterpret_cast<float *>(smem);

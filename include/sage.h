@@ -430,8 +430,9 @@ SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int 
  * In:  Q (B,Hq,1,d).  Out: O (B,Hq,1,d), L (B,Hq,1) float32.
  * A NaN in q, or in a cached K or its scale, makes the O and L of the heads that read it NaN.
  * add_score = 1: score[b][kv head][t] += the sum over its query heads of softmax(s)_t.
- * Sums and statistics are float32; the probabilities enter the second product as two 16-bit
- * terms (16 or more significant bits).  Results do not depend on the order in which the GPU runs
+ * Sums and statistics are float32; the probabilities (8-bit kinds: times their row's sV) enter the
+ * second product as two terms that keep 16 or more significant bits of each down to 2^-110, however
+ * small it is beside the largest.  Results do not depend on the order in which the GPU runs
  * its blocks.  O and L may not overlap the inputs or the cache.  Short caches need no workspace
  * without scores: the query then says 0, and workspace may be NULL. */
 SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score);
