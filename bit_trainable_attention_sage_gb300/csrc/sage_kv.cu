@@ -13,7 +13,7 @@ __device__ unsigned int g_kv_err = 0;   // 1: a page, length or slot was out of 
 // delta a row of d values, x = fl32(K - mu) or V; a 16-bit pool takes the values as they are.
 // Every element is read once and written once: bound by memory bandwidth (16-bit pools: 64 us for 64
 // heads of up to 8192 tokens, d = 128, 6.8 TB/s), in 8 bits by issuing the arithmetic (to E4M3 with
-// smoothing 58 us, 5.7 TB/s), or by latency (single tokens).  d / 16 lanes hold a row, two 16-byte
+// smoothing 59 us, 5.6 TB/s), or by latency (single tokens).  d / 16 lanes hold a row, two 16-byte
 // chunks each, so what is done once a row (its place, scale and reciprocal) is shared by 16 values
 // (8 values a lane: 70 us), the maximum is 2 or 3 shuffles and loads and stores are whole sectors.
 // One row a lane group and 40 warps an SM keep enough reads in flight (several rows a group: 65 us
@@ -43,7 +43,7 @@ __device__ __forceinline__ void unpack16(const uint4 (&u)[2], f2 (&v)[8]) {
     }
 }
 
-// fl32(x / d) for two values, r = fl32(1 / d): Markstein's correction of a quotient ("Computation of
+// -fl32(x / d) for two values, nr = -fl32(1 / d): Markstein's correction of a quotient ("Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990).  The residual x - q d is
 // exact, so a correction leaves the quotient's error times r's, and one rounding.
 //   ONCE: for x of at most 11 significant bits (a 16-bit value), one correction of q0 = fl(x r) gives
@@ -53,31 +53,32 @@ __device__ __forceinline__ void unpack16(const uint4 (&u)[2], f2 (&v)[8]) {
 //   0.5 + 3 u ulp; the second then rounds a value within (0.5 + 3 u) d u / 2 ulp of x / d, and
 //   x / d is at least u / d ulp from any value half way between two floats (25 bits times d's 24
 //   never make x's 24).  (0.5 + 3 u) d / 2 < 1 / d for every d < 2: it rounds as x / d does.
-// d and r are pairs (of a value twice, or of two rows' scales).
+// The negated quotient is what is corrected, because its zeros keep their sign: the residual of either
+// zero is +0, and +0 * nr is the -0 that leaves both alone (+0 * r would make +0 of a -0).
+// d and nr are pairs (of a value twice, or of two rows' scales).
 template <bool ONCE>
-__device__ __forceinline__ f2 quotient2(f2 x, f2 d, f2 r) {
-    const f2 nd{-d.x, -d.y};
-    f2 q = mul2(x, r);
-    if constexpr (!ONCE) q = fma2(fma2(q, nd, x), r, q);
-    return fma2(fma2(q, nd, x), r, q);
+__device__ __forceinline__ f2 neg_quotient2(f2 x, f2 d, f2 nr) {
+    f2 n = mul2(x, nr);
+    if constexpr (!ONCE) n = fma2(fma2(n, d, x), nr, n);
+    return fma2(fma2(n, d, x), nr, n);
 }
 
 // m / M of two rows, M = 127 or 448.  (Out of the range where the residuals are normal: divisions.)
 template <int KIND>
 __device__ __forceinline__ f2 scales_of(f2 m) {
     constexpr float M = KIND == SAGE_KV_INT8 ? 127.0f : 448.0f, r = 1.0f / M;
-    if (fminf(m.x, m.y) >= 0x1p-80f && fmaxf(m.x, m.y) <= 0x1p96f) return quotient2<false>(m, f2{M, M}, f2{r, r});
+    if (fminf(m.x, m.y) >= 0x1p-80f && fmaxf(m.x, m.y) <= 0x1p96f) return neg_quotient2<false>(f2{-m.x, -m.y}, f2{M, M}, f2{-r, -r});
     return f2{__fdiv_rn(m.x, M), __fdiv_rn(m.y, M)};
 }
 
-// One row's 16 values of a lane, and the row's scale -> 16 codes.
+// One row's 16 values of a lane, and the row's scale -> 16 codes.  n: the negated quotients.
 template <int KIND, bool ONCE>
 __device__ __forceinline__ void kv_codes(const f2 (&x)[8], float delta, uint2 (&out)[2]) {
-    f2 y[8];
+    f2 n[8];
     if (delta >= 0x1p-90f && delta <= 0x1p90f) {
-        const float r = __frcp_rn(delta);
+        const float nr = -__frcp_rn(delta);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = quotient2<ONCE>(x[i], f2{delta, delta}, f2{r, r});
+        for (int i = 0; i < 8; ++i) n[i] = neg_quotient2<ONCE>(x[i], f2{delta, delta}, f2{nr, nr});
     } else if (delta == 0.0f) {
         out[0] = out[1] = make_uint2(0u, 0u);
         return;
@@ -86,22 +87,22 @@ __device__ __forceinline__ void kv_codes(const f2 (&x)[8], float delta, uint2 (&
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             constexpr float top = KIND == SAGE_KV_INT8 ? 127.0f : 448.0f;
-            y[i].x = fminf(fmaxf(__fdiv_rn(x[i].x, delta), -top), top);
-            y[i].y = fminf(fmaxf(__fdiv_rn(x[i].y, delta), -top), top);
+            n[i].x = -fminf(fmaxf(__fdiv_rn(x[i].x, delta), -top), top);
+            n[i].y = -fminf(fmaxf(__fdiv_rn(x[i].y, delta), -top), top);
         }
     }
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (KIND == SAGE_KV_INT8) {
-            // y + 1.5 2^23 holds the nearest integer (ties to even) in its low bits
+            // 1.5 2^23 - n holds the nearest integer (ties to even) in its low bits
             const f2 magic{12582912.0f, 12582912.0f};
-            const f2 a = add2(y[2 * i], magic), b = add2(y[2 * i + 1], magic);
+            const f2 a = sub2(magic, n[2 * i]), b = sub2(magic, n[2 * i + 1]);
             const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
             const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
             w[i] = __byte_perm(lo, hi, 0x5410);
         } else {
-            w[i] = e4m3x2(y[2 * i].x, y[2 * i].y) | static_cast<uint32_t>(e4m3x2(y[2 * i + 1].x, y[2 * i + 1].y)) << 16;
+            w[i] = (e4m3x2(n[2 * i].x, n[2 * i].y) | static_cast<uint32_t>(e4m3x2(n[2 * i + 1].x, n[2 * i + 1].y)) << 16) ^ 0x80808080u;
         }
     }
     out[0] = make_uint2(w[0], w[1]);
