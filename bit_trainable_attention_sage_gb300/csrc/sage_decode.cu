@@ -1345,8 +1345,10 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
     if (!Q || !lens || !O || !L || O == Q || (add_score && !c->score)) return SAGE_ERR_ARG;
     if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(L, 16) || misaligned(lens, 4)) return SAGE_ERR_ALIGN;
     const DecodePlan p = decode_plan(*c, Hq, add_score);
-    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return SAGE_ERR_WORKSPACE;
-    if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
+    if (p.bytes) {                               // else it is not looked at
+        if (!workspace || workspace_bytes < p.bytes) return SAGE_ERR_WORKSPACE;
+        if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
+    }
     uint8_t *w = static_cast<uint8_t *>(workspace);
     DecodeArgs a;
     a.c = kv_view(*c);

@@ -257,7 +257,8 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
 def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, score: bool = False, out=None, lse=None,
                      workspace=None, stream=None):
     """Attention of one new token a sequence, Q (B,Hq,1,d), over its lens[b] cached slots; Hq is a
-    multiple of the cache's heads.  ``score`` adds the attention weights to cache.score.
+    multiple of the cache's heads.  ``score`` adds the attention weights to cache.score.  A ``workspace``
+    of the caller's begins at a multiple of 256 bytes, as PyTorch's allocations do.
     Returns (O (B,Hq,1,d) in Q's type, L (B,Hq,1) float32); a sequence of no slots gives 0 and -inf."""
     shape, dtype, dev = Q.shape, Q.dtype, cache.device
     c = cache._struct(Q, "Q")

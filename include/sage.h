@@ -49,7 +49,7 @@ extern "C" {
 #define SAGE_OK 0
 #define SAGE_ERR_ARG 1          /* null pointer, non-positive size, bad flag value            */
 #define SAGE_ERR_UNSUPPORTED 2  /* d not in {64,128}, N % 64 != 0, unknown dtype              */
-#define SAGE_ERR_ALIGN 3        /* a device pointer is not 16-byte aligned                     */
+#define SAGE_ERR_ALIGN 3         /* a device pointer is not aligned as the call wants (16 bytes)  */
 #define SAGE_ERR_CUDA 4         /* a kernel launch or CUDA runtime call failed                 */
 #define SAGE_ERR_TIMEOUT 5      /* a bounded device-side wait expired (see sage_device_status) */
 #define SAGE_ERR_WORKSPACE 6    /* workspace missing or smaller than the query says            */
@@ -433,8 +433,9 @@ SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int 
  * Sums and statistics are float32; the probabilities (8-bit kinds: times their row's sV) enter the
  * second product as two terms that keep 16 or more significant bits of each down to 2^-110, however
  * small it is beside the largest.  Results do not depend on the order in which the GPU runs
- * its blocks.  O and L may not overlap the inputs or the cache.  Short caches need no workspace
- * without scores: the query then says 0, and workspace may be NULL. */
+ * its blocks.  O and L may not overlap the inputs or the cache.  The workspace must be 256-byte
+ * aligned.  Short caches need none without scores: the query then says 0, and workspace may be
+ * anything. */
 SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score);
 SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, void *O,
                               float *L, int add_score, void *workspace, size_t workspace_bytes,
