@@ -168,11 +168,25 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
 # ---- paged key-value cache ------------------------------------------------------------------
 
 
+def _kv_sizes(B: int, H: int, d: int, page: int, pages: int, max_pages: int):
+    """The sizes that struct sage_kv takes."""
+    if min(B, H, page, pages, max_pages) < 1:
+        raise ValueError(f"a cache of {B} sequences, {H} heads, {pages} pages of {page} tokens, {max_pages} a sequence: none may be 0")
+    if d not in (64, 128):
+        raise ValueError(f"d must be 64 or 128, got {d}")
+    if page % 16:
+        raise ValueError(f"page must be a multiple of 16 tokens, got {page}")
+    if max_pages * page >= 1 << 30:
+        raise ValueError(f"{max_pages} pages of {page} tokens a sequence: fewer than 2^30 slots are wanted")
+    if B * H > 65535:
+        raise ValueError(f"{B} sequences of {H} heads: at most 65535 rows are taken")
+
+
 class KvCache:
     """A paged key-value cache over tensors of the caller (struct sage_kv).
 
     K, V (pages,H,page,d): fp16 or bf16 values, or int8 / float8_e4m3fn codes with sK, sV
-    (pages,H,page) float32, one scale a row.  table (B,max_pages) int32: the pages of each
+    (pages,H,page) float32, one scale a row; page a multiple of 16, B * H at most 65535.  table (B,max_pages) int32: the pages of each
     sequence; entries behind its last page are not read.  score (B,H,max_pages*page) float32 and
     pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict.  The tensors
     are fixed for the life of the object; their contents are the caller's and the calls'."""
@@ -183,6 +197,7 @@ class KvCache:
         pages, H, page, d = K.shape
         B, max_pages = table.shape
         dev = K.device
+        _kv_sizes(B, H, d, page, pages, max_pages)
         _cuda(dev)
         _need(K, "K", K.dtype, K.shape, dev)
         _need(V, "V", K.dtype, K.shape, dev)
@@ -220,7 +235,8 @@ def make_kv_cache(B: int, H: int, d: int, capacity: int, *, dtype=torch.int8, pa
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    m = max(1, -(-capacity // page))
+    m = max(1, -(-capacity // max(page, 1)))
+    _kv_sizes(B, H, d, page, B * m, m)
     table = torch.arange(B * m, dtype=torch.int32, device=device).view(B, m)
     shape = (B * m, H, page, d)
     K, V = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
