@@ -559,7 +559,8 @@ int sage_device_status(sage_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SAGE_ERR_CUDA;
     const unsigned int e = take_fwd_error() | take_bwd_error() | take_quant_error();
-    const unsigned int index = take_kv_error() | take_decode_error();
+    // beside a timeout the index error stays for the next call
+    const unsigned int index = e ? 0u : take_kv_error() | take_decode_error();
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
     return e ? SAGE_ERR_TIMEOUT : index ? SAGE_ERR_INDEX : SAGE_OK;
 }

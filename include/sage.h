@@ -457,7 +457,8 @@ SAGE_API size_t sage_dump_bytes(const sage_params *p, int which);
 
 /* Waits for `stream`, then reads and clears the device-side error word of the current device:
  * SAGE_OK, SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call, or else
- * SAGE_ERR_INDEX if a cache call met a page, length or slot out of range. */
+ * SAGE_ERR_INDEX if a cache call met a page, length or slot out of range (beside a timeout this one
+ * is kept and returned by the next call). */
 SAGE_API int sage_device_status(sage_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
