@@ -610,7 +610,9 @@ int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget
                   void *workspace, size_t workspace_bytes, sage_stream_t stream) {
     const int st = check_kv(c, true);
     if (st != SAGE_OK) return st;
-    if (!lens || !seen || !lens_out || lens_out == lens || lens_out == seen || !c->score || !c->pos) return SAGE_ERR_ARG;
+    if (!lens || !seen || !lens_out || !c->score || !c->pos) return SAGE_ERR_ARG;
+    const size_t nl = static_cast<size_t>(c->B) * sizeof(int);       // one sequence's length may be read after another's is written
+    if (overlap(lens_out, nl, lens, nl) || overlap(lens_out, nl, seen, nl)) return SAGE_ERR_ARG;
     if (budget <= 0 || recent < 0 || recent > budget) return SAGE_ERR_ARG;
     if (misaligned(lens, 4) || misaligned(seen, 4) || misaligned(lens_out, 4)) return SAGE_ERR_ALIGN;
     if (!workspace || workspace_bytes < sage_evict_workspace_bytes(c, budget)) return SAGE_ERR_WORKSPACE;

@@ -94,6 +94,11 @@ inline cudaError_t raise_smem(const void *kernel, size_t bytes, bool (&raised)[1
     return e;
 }
 
+// Whether two ranges of bytes share one.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 inline bool misaligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 // The rules of struct sage_kv (`pointers` false: sizes only, for the workspace queries).

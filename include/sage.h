@@ -446,7 +446,8 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
  * far), then the others by score, NaN last; ties go to the lower slot.  The first `budget` stay.
  * Those of them in slots >= budget move to the freed slots < budget, in slot order, with their
  * scales, score and pos; all other slots keep what they hold.  lens_out[b] = min(lens[b], budget).
- * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not be lens or seen. */
+ * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not overlap lens
+ * or seen. */
 SAGE_API size_t sage_evict_workspace_bytes(const sage_kv *c, int budget);
 SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget, int recent,
                            int *lens_out, void *workspace, size_t workspace_bytes,
