@@ -98,6 +98,9 @@ class Rope:
         self._freq = (ctypes.c_double * len(self.freqs))(*self.freqs)
         self._made = {}         # params structs by what they depend on
 
+    def __reduce__(self):
+        return Rope, (self.d, self.sections, self.freqs, self.interleaved)   # structs and arrays are made again
+
     def _struct(self, *key):
         """The struct for (B, H, Hk, N, dtype, pos_batch, inverse)."""
         p = self._made.get(key)

@@ -36,3 +36,15 @@ def test_make_kv_cache_checks_before_it_allocates(sg, kw, what):
     v.update(kw)
     with pytest.raises(ValueError, match=what):
         sg.make_kv_cache(**v, device="cpu")
+
+
+def test_rope_can_be_copied_and_pickled(sg):
+    """A Rope held by a module is copied with it, after calls too."""
+    import copy
+    import pickle
+    r = sg.make_rope(128, (16, 24, 24), interleaved=True)
+    for _ in range(2):
+        for c in (copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r)), copy.deepcopy({"rope": r})["rope"]):
+            assert (c.d, c.sections, c.freqs, c.interleaved, c.axes, c.rotary) == (r.d, r.sections, r.freqs, True, 3, 128)
+            assert list(c._freq) == list(r.freqs) and c._sections is not r._sections and c._made is not r._made
+        r._struct(2, 4, 2, 3, torch.float16, 1, False)     # what a call leaves behind
