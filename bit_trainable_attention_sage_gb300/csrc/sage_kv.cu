@@ -45,11 +45,12 @@ __device__ __forceinline__ void unpack16(const uint4 (&u)[2], f2 (&v)[8]) {
 
 // -fl32(x / d) for two values, nr = -fl32(1 / d): Markstein's correction of a quotient ("Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990).  The residual x - q d is
-// exact, so a correction leaves the quotient's error times r's, and one rounding.
+// exact where q is off by a unit in the last place (ulp) or less, and rounded once where it is off by more:
+// a correction leaves the quotient's error times r's and that rounding's, and one rounding.
 //   ONCE: for x of at most 11 significant bits (a 16-bit value), one correction of q0 = fl(x r) gives
-//   fl32(x / d) for every pair of significands (all 2^10 x 2^23 checked).
+//   fl32(x / d) for every pair of significands (tests/test_gpu_quotients.py tries all 2^10 x 2^23).
 //   Otherwise two.  With significands x, d in [1, 2) and u = 2^-24: r is off by at most d u / 2 of itself,
-//   q0 by at most 1.5 units in the last place (ulp), and the first correction by less than
+//   q0 by at most 1.5 ulp, and the first correction by less than
 //   0.5 + 3 u ulp; the second then rounds a value within (0.5 + 3 u) d u / 2 ulp of x / d, and
 //   x / d is at least u / d ulp from any value half way between two floats (25 bits times d's 24
 //   never make x's 24).  (0.5 + 3 u) d / 2 < 1 / d for every d < 2: it rounds as x / d does.
