@@ -67,8 +67,8 @@ struct DecodeShape {
     static constexpr int SCALES = KIND < 2 ? 0 : 2 * GRAN * 4;
     static constexpr int STAGE = 2 * GRAN * ROW + SCALES;
     // Resident CTAs an SM: three where 168 registers and a third of the shared memory do.  (131072
-    // tokens in E4M3, 8 kv heads, d = 128: with 4 heads a group 58 us at two, 56 at three; with 16
-    // a group 73 at two and 80 at three, which spill.)
+    // tokens in E4M3, 8 kv heads, d = 128: with 4 heads a group 51 us at two, 48 at three; with 16
+    // a group 63 at two and 67 at three, which spill.)
     static constexpr int CTAS = ROW == 256 || (MR == 16 && D == 128) ? 2 : 3;
     static constexpr int STAGES = ROW == 64 ? 4 : CTAS == 3 ? 2 : 3;
     static constexpr int ALIGN = 512;                        // of the ring, so that its addresses can be XORed
@@ -1240,9 +1240,9 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     long long n = kSMs * decode_ctas(row, c.d, p.mr);
     const long long tiles = static_cast<long long>(c.B) * c.H * p.chunks * ((static_cast<long long>(c.max_pages) * c.page + p.tile - 1) / p.tile);
     // A cluster a pair while all pairs are resident together and a CTA takes few tiles: as many CTAs as
-    // there are tiles and room.  (us, cluster / split: 8 pairs of 1000 tokens in INT8, d = 128 5.8 / 8.4, of
-    // 4000 9.4 / 10.1; 64 pairs of up to 4000, 8 tiles a CTA, 16.4 / 14.0; 256 of up to 300 8.7 / 12.3;
-    // 1024 of 64, more than are resident, 16.5 / 14.7.)
+    // there are tiles and room.  (Device us in a graph, cluster / split: 8 pairs of 1000 tokens in INT8, d = 128
+    // 5.9 / 8.0, of 4000, 4 tiles a CTA, 9.6 / 9.0, where the second launch costs the host 3; 64 pairs of up to
+    // 4000, 8 tiles a CTA, 16.9 / 14.8; 256 of up to 300 8.4 / 14.0; 1024 of 64, more than are resident, 15.5 / 13.8.)
     const long long pairs = static_cast<long long>(c.B) * c.H * p.chunks, most = tiles / pairs;
     int cl = 1;
     while (cl < kDecCluster && cl < most && pairs * cl * 2 <= n) cl *= 2;

@@ -253,7 +253,9 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
                    pos=None, stream=None) -> None:
     """Writes tokens 0 .. count[b] - 1 (None: all T) of K, V (B,H,T,d) to slots start[b] + t of the
     cache, in its form.  ``mu`` (B,H,d) float32 (8-bit caches): K-smoothing, codes of K - mu.
-    ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot)."""
+    ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot).
+    Scores of the new slots are 0: decoding adds to them, weights of a prompt's own queries are the
+    caller's to write to cache.score."""
     shape, dev = K.shape, cache.device
     B, H, T, d = shape
     c = cache._struct(K, "K")
@@ -310,7 +312,9 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
                   workspace=None, stream=None) -> torch.Tensor:
     """Cuts every sequence of more than ``budget`` slots to the ``budget`` slots of the largest
     accumulated weight (cache.score), those at positions >= seen[b] - recent first; each head for
-    itself, rows moved into the freed slots.  Returns the new lengths (B) int32."""
+    itself, rows moved into the freed slots, ties to the lower slot (right after a prompt, whose scores
+    are 0 unless the caller wrote them, its later part goes).  Returns the new lengths (B) int32, in
+    ``out`` if given, which may not overlap ``lens`` or ``seen``."""
     dev = cache.device
     if cache.score is None or cache.pos is None:
         raise ValueError("eviction needs a cache with score and pos")

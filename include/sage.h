@@ -398,7 +398,7 @@ SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, 
 
 typedef struct sage_kv {
     int B;              /* sequences (rows of the table)                                         */
-    int H;              /* kv heads                                                              */
+    int H;              /* kv heads; B * H <= 65535                                              */
     int d;              /* 64 or 128                                                             */
     int dtype;          /* SAGE_FP16 or SAGE_BF16: K, V, q, O of the calls (and a 16-bit pool)   */
     int kind;           /* SAGE_KV_*                                                             */
@@ -413,12 +413,14 @@ typedef struct sage_kv {
 } sage_kv;
 
 /* sage_kv_append -- tokens 0 .. count[b] - 1 of K, V (B,H,T,d) go to slots start[b] + t.
- * count NULL: T for every sequence; count[b] < T: the rest of a padded row is not written.
+ * 1 <= T < 2^30.  count NULL: T for every sequence; count[b] < T: the rest of a padded row is not
+ * written.  K and V may not lie in rows that the call writes.
  * mu (B,H,d) float32, 8-bit kinds only, nullable: K-smoothing, the codes are those of
  * fl32(K - mu); attention over keys that share one mu does not change (L does, by q . mu /
  * sqrt(d)).  sage_quantize_smooth's muK of the prompt is such a mu.
  * 8-bit kinds: a row with a NaN or an infinity gets a scale that is NaN or infinite.
- * Where the cache has score: score[slot] = 0.  Where it has pos: pos[slot] = pos0[b] + t, with
+ * Where the cache has score: score[slot] = 0 (only sage_attn_decode adds to it: weights of a prompt's
+ * own queries are the caller's to write there).  Where it has pos: pos[slot] = pos0[b] + t, with
  * pos0 NULL: the slot itself. */
 SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int T, const int *start,
                             const int *count, const float *mu, const int *pos0,
@@ -427,13 +429,15 @@ SAGE_API int sage_kv_append(const sage_kv *c, const void *K, const void *V, int 
 /* sage_attn_decode -- one new token a sequence over its `lens[b]` cached slots (its own included,
  * if it has been appended): s_t = q . K_t / sqrt(d), O = sum_t softmax(s)_t V_t,
  * L = log sum_t exp s_t.  Query head h reads kv head h / (Hq / H).  lens[b] = 0: O = 0, L = -inf.
- * In:  Q (B,Hq,1,d).  Out: O (B,Hq,1,d), L (B,Hq,1) float32.
- * A NaN in q, or in a cached K or its scale, makes the O and L of the heads that read it NaN.
+ * In:  Q (B,Hq,1,d), Hq a multiple of H, B * Hq <= 2^24.  Out: O (B,Hq,1,d), L (B,Hq,1) float32.
+ * A NaN in q, or in a cached K or its scale, makes the O and L of the heads that read it NaN.  An
+ * infinity in a cached V or its scale makes the channels of O that it reaches infinite or NaN.
  * add_score = 1: score[b][kv head][t] += the sum over its query heads of softmax(s)_t.
  * Sums and statistics are float32; the probabilities (8-bit kinds: times their row's sV) enter the
  * second product as two terms that keep 16 or more significant bits of each down to 2^-110, however
- * small it is beside the largest.  Results do not depend on the order in which the GPU runs
- * its blocks.  O and L may not overlap the inputs or the cache.  The workspace must be 256-byte
+ * small it is beside the largest.  Results do not depend on the order in which the GPU runs its
+ * blocks; their last bits do on the capacity and on the other sequences' lengths, by which the work
+ * is cut.  O and L may not overlap the inputs or the cache.  The workspace must be 256-byte
  * aligned.  Short caches need none without scores: the query then says 0, and workspace may be
  * anything. */
 SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_score);
@@ -443,7 +447,9 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
 
 /* sage_kv_evict -- cuts every sequence with lens[b] > budget to `budget` slots, each kv head for
  * itself.  First rank the slots with pos >= seen[b] - recent (seen[b]: the tokens of the text so
- * far), then the others by score, NaN last; ties go to the lower slot.  The first `budget` stay.
+ * far), then the others by score, NaN last; ties go to the lower slot (right after
+ * a prompt, whose scores are 0 unless the caller wrote them, its later part goes).  The first `budget`
+ * stay.
  * Those of them in slots >= budget move to the freed slots < budget, in slot order, with their
  * scales, score and pos; all other slots keep what they hold.  lens_out[b] = min(lens[b], budget).
  * 0 <= recent <= budget, budget >= 1; needs score and pos.  lens_out may not overlap lens
