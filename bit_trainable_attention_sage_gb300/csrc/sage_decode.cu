@@ -54,7 +54,7 @@ constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kSMs = 152;
 constexpr int kDecCluster = 8;               // CTAs of a cluster at most
 
-// pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3
+// pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3; BLOCK: one scale for 16 or more rows (8 bits)
 template <int D, int KIND, int MR = 8>
 struct DecodeShape {
     static constexpr int ES = KIND < 2 ? 2 : 1;
@@ -323,7 +323,7 @@ __device__ __forceinline__ float inv_of(float l) { return l == 0.0f ? 0.0f : 1.0
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
 // ---- main kernel ------------------------------------------------------------------------------
-template <int D, int KIND, int MR, bool ONE>
+template <int D, int KIND, int MR, bool ONE, bool BLOCK>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND, MR>;
     constexpr bool BF16 = KIND == 1;                 // type of the product K q
@@ -486,7 +486,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                     cp_async16(at + S::GRAN * S::ROW, vs, r < nv);
                 }
             }
-            if constexpr (KIND >= 2) {
+            if constexpr (BLOCK) {
+                // the 16 rows share a scale: one word each for K and V
+                const float *sc = (lane == 0 ? a.c.sK : a.c.sV) + (row >> a.c.block_shift);
+                const uint32_t at = smem_u32(ring) + stage * S::STAGE + 2 * S::GRAN * S::ROW + (lane * S::GRAN + hf * 16) * 4;
+                if (lane < 2) cp_async4(at, sc, nv > 0);
+            } else if constexpr (KIND >= 2) {
                 const int r = lane & 15;
                 const float *sc = (lane < 16 ? a.c.sK : a.c.sV) + row;
                 const uint32_t at = smem_u32(ring) + stage * S::STAGE + 2 * S::GRAN * S::ROW + ((lane >> 4) * S::GRAN + hf * 16 + r) * 4;
@@ -639,11 +644,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             for (int hf = 0; hf < HALVES; ++hf) {
                 float fk[2] = {1.0f, 1.0f};
                 if constexpr (KIND >= 2) {
-                    const float *sc = reinterpret_cast<const float *>(kst + 2 * S::GRAN * S::ROW) + hf * 16 + g;
+                    const float *sc = reinterpret_cast<const float *>(kst + 2 * S::GRAN * S::ROW) + hf * 16 + (BLOCK ? 0 : g);
+                    constexpr int next_row = BLOCK ? 0 : 8;
                     fk[0] = sc[0];
-                    fk[1] = sc[8];
+                    fk[1] = sc[next_row];
                     fv[hf][0] = sc[S::GRAN];
-                    fv[hf][1] = sc[S::GRAN + 8];
+                    fv[hf][1] = sc[S::GRAN + next_row];
                 }
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh)
@@ -1234,7 +1240,7 @@ static DecodePlan decode_plan(const sage_kv &c, int Hq, int add_score) {
     const int G = Hq / c.H;
     p.mr = G <= 8 ? 8 : 16;
     p.chunks = (G + p.mr - 1) / p.mr;
-    const int row = c.d * (c.kind == SAGE_KV_16 ? 2 : 1);
+    const int row = c.d * (kv_format(c) == SAGE_KV_16 ? 2 : 1);
     // one resident wave; never more CTAs than there can be tiles
     p.tile = decode_tile(row);
     long long n = kSMs * decode_ctas(row, c.d, p.mr);
@@ -1267,12 +1273,12 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
     return SAGE_OK;
 }
 
-template <int D, int KIND, int MR>
+template <int D, int KIND, int MR, bool BLOCK>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     using S = DecodeShape<D, KIND, MR>;
     static bool raised[2][16] = {{false}};
     if (a.cluster) {
-        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, true>), S::SMEM, raised[1]);
+        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, true, BLOCK>), S::SMEM, raised[1]);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.ctas);
@@ -1286,11 +1292,11 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, MR, true>, a);
+        return cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, MR, true, BLOCK>, a);
     }
-    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, false>), S::SMEM, raised[0]);
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, false, BLOCK>), S::SMEM, raised[0]);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, KIND, MR, false><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
+    decode_kernel<D, KIND, MR, false, BLOCK><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1317,7 +1323,10 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
 
 template <int D, int KIND>
 static cudaError_t launch_decode_m(const DecodeArgs &a, int mr, cudaStream_t st) {
-    return mr == 8 ? launch_decode_k<D, KIND, 8>(a, st) : launch_decode_k<D, KIND, 16>(a, st);
+    if constexpr (KIND >= 2) {
+        if (a.c.block_shift) return mr == 8 ? launch_decode_k<D, KIND, 8, true>(a, st) : launch_decode_k<D, KIND, 16, true>(a, st);
+    }
+    return mr == 8 ? launch_decode_k<D, KIND, 8, false>(a, st) : launch_decode_k<D, KIND, 16, false>(a, st);
 }
 
 template <int KIND>
@@ -1362,8 +1371,8 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
     a.logits = add_score ? reinterpret_cast<float *>(w + p.off_logits) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (c->kind == SAGE_KV_INT8) e = launch_decode_d<2>(a, c->d, p.mr, s);
-    else if (c->kind == SAGE_KV_FP8) e = launch_decode_d<3>(a, c->d, p.mr, s);
+    if (kv_format(*c) == SAGE_KV_INT8) e = launch_decode_d<2>(a, c->d, p.mr, s);
+    else if (kv_format(*c) == SAGE_KV_FP8) e = launch_decode_d<3>(a, c->d, p.mr, s);
     else if (a.bf16) e = launch_decode_d<1>(a, c->d, p.mr, s);
     else e = launch_decode_d<0>(a, c->d, p.mr, s);
     return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;

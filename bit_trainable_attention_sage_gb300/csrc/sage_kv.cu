@@ -230,13 +230,213 @@ static void launch_append_d(const AppendArgs &a, int d, cudaStream_t st) {
     else launch_append_k<T, KIND, 128, false>(a, st);
 }
 
+// ---------------------------------------------------------------------------------------------
+// append to a cache with one scale a block
+//
+// Blocks of R = 16, 32 or 64 slots share s = fl32(max|x| / M).  A block that begins with the call's rows
+// takes its scale from them; one that goes on (rows before `start`) keeps the larger of its scale and theirs,
+// and where that grows its kept rows' codes become the nearest of fl32(code * fl32(s_old / s)).
+// A CTA takes a block of one head: its rows stay in registers between the maximum and the codes, so that
+// every element is read once and written once, and only a block whose scale grows reads codes.
+// ---------------------------------------------------------------------------------------------
+template <int D, int R>
+struct AppendBlock {
+    static constexpr int LANES = D / 16;
+    static constexpr int THREADS = R * LANES < 256 ? R * LANES : 256;
+    static constexpr int GROUPS = THREADS / LANES;               // rows at a time
+    static constexpr int ROWS = R / GROUPS;                      // rows a lane group
+};
+
+// 16 codes times r <= 1, to the nearest code
+template <int KIND>
+__device__ __forceinline__ uint2 kv_rescaled(uint2 codes, float r) {
+    uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (KIND == SAGE_KV_INT8) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float c = static_cast<float>(static_cast<int8_t>(w[i] >> (8 * k)));
+                o |= static_cast<uint32_t>(__float2int_rn(__fmul_rn(c, r)) & 255) << (8 * k);
+            }
+            w[i] = o;
+        } else {
+            const uint32_t lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])), hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            w[i] = e4m3x2(__fmul_rn(a.x, r), __fmul_rn(a.y, r)) | static_cast<uint32_t>(e4m3x2(__fmul_rn(b.x, r), __fmul_rn(b.y, r))) << 16;
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// grid: (blocks of a sequence that T tokens can touch, B * H)
+template <typename T, int KIND, int D, int R, bool SMOOTH>
+__global__ void __launch_bounds__(AppendBlock<D, R>::THREADS) kv_append_block_kernel(const AppendArgs a) {
+    using S = AppendBlock<D, R>;
+    constexpr int LANES = S::LANES, WARPS = S::THREADS / 32;
+    constexpr int SHIFT = R == 16 ? 4 : R == 32 ? 5 : 6;
+    __shared__ float s_max[2][WARPS];
+    const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    int n = a.T;
+    if (a.count) {
+        n = __ldg(a.count + b);
+        if (n < 0 || n > a.T) {
+            if (threadIdx.x == 0) atomicOr(&g_kv_err, 1u);
+            n = n < 0 ? 0 : a.T;
+        }
+    }
+    const long long start = __ldg(a.start + b);
+    const long long s0 = ((start >> SHIFT) + blockIdx.x) << SHIFT;   // the block's first slot
+    if (s0 >= start + n || n == 0) return;
+    if (s0 < 0 || s0 >= a.c.cap) {                   // the capacity is a multiple of the block
+        if (threadIdx.x == 0) atomicOr(&g_kv_err, 1u);
+        return;
+    }
+    // this lane group's rows: slots s0 + group + i * GROUPS
+    uint4 k[S::ROWS][2], v[S::ROWS][2];
+    const long long t0 = s0 - start + group;
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const long long t = t0 + i * S::GROUPS;
+        k[i][0] = k[i][1] = v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (t >= 0 && t < n) {
+            const size_t at = (static_cast<size_t>(bh) * a.T + t) * (2 * LANES) + lane;
+            const uint4 *K = static_cast<const uint4 *>(a.K) + at, *V = static_cast<const uint4 *>(a.V) + at;
+            k[i][0] = __ldg(K);
+            k[i][1] = __ldg(K + LANES);
+            v[i][0] = __ldg(V);
+            v[i][1] = __ldg(V + LANES);
+        }
+    }
+    const int p = kv_page(a.c, b, static_cast<int>(s0), &g_kv_err);
+    if (p < 0) return;                               // the whole CTA alike
+    const size_t row0 = kv_row(a.c, p, h, static_cast<int>(s0)), place = row0 >> SHIFT;
+    const bool goes_on = start > s0;
+    f2 old{0.0f, 0.0f};
+    if (goes_on) old = f2{a.c.sK[place], a.c.sV[place]};
+    f2 mu[8];
+    if constexpr (SMOOTH) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float4 *m = reinterpret_cast<const float4 *>(a.mu + static_cast<size_t>(bh) * D + (lane + c * LANES) * 8);
+            const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
+            mu[4 * c] = f2{m0.x, m0.y};
+            mu[4 * c + 1] = f2{m0.z, m0.w};
+            mu[4 * c + 2] = f2{m1.x, m1.y};
+            mu[4 * c + 3] = f2{m1.z, m1.w};
+        }
+    }
+    auto values = [&](const uint4 (&u)[2], bool key, f2 (&x)[8]) {
+        unpack16<T>(u, x);
+        if constexpr (SMOOTH) {
+            if (key) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = sub2(x[j], mu[j]);
+            }
+        }
+    };
+    float mk = 0.0f, mv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const long long t = t0 + i * S::GROUPS;
+        if (t >= 0 && t < n) {                       // (other rows' zeros less mu are no values)
+            f2 x[8];
+            values(k[i], true, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mk = larger(mk, larger(x[j].x, x[j].y));
+            values(v[i], false, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mv = larger(mv, larger(x[j].x, x[j].y));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        mk = larger(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+        mv = larger(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    if (threadIdx.x % 32 == 0) {
+        s_max[0][threadIdx.x / 32] = mk;
+        s_max[1][threadIdx.x / 32] = mv;
+    }
+    __syncthreads();                                 // and every thread has the old scales
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        mk = larger(mk, s_max[0][w]);
+        mv = larger(mv, s_max[1][w]);
+    }
+    f2 s = scales_of<KIND>(f2{fabsf(mk), fabsf(mv)});
+    if (goes_on) s = f2{fabsf(larger(s.x, old.x)), fabsf(larger(s.y, old.y))};
+    if (threadIdx.x == 0) {
+        a.c.sK[place] = s.x;
+        a.c.sV[place] = s.y;
+    }
+    const bool more_k = goes_on && s.x > old.x, more_v = goes_on && s.y > old.y;
+    const float rk = more_k ? __fdiv_rn(old.x, s.x) : 1.0f, rv = more_v ? __fdiv_rn(old.y, s.y) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const long long t = t0 + i * S::GROUPS;
+        const size_t at = (row0 + group + i * S::GROUPS) * (2 * LANES) + lane;
+        uint2 *K = static_cast<uint2 *>(a.c.K) + at, *V = static_cast<uint2 *>(a.c.V) + at;
+        if (t >= 0 && t < n) {
+            f2 x[8];
+            uint2 c[2];
+            values(k[i], true, x);
+            kv_codes<KIND, !SMOOTH>(x, s.x, c);
+            K[0] = c[0];
+            K[LANES] = c[1];
+            values(v[i], false, x);
+            kv_codes<KIND, true>(x, s.y, c);
+            V[0] = c[0];
+            V[LANES] = c[1];
+        } else if (t < 0) {                          // a kept row
+            if (more_k) {
+                K[0] = kv_rescaled<KIND>(K[0], rk);
+                K[LANES] = kv_rescaled<KIND>(K[LANES], rk);
+            }
+            if (more_v) {
+                V[0] = kv_rescaled<KIND>(V[0], rv);
+                V[LANES] = kv_rescaled<KIND>(V[LANES], rv);
+            }
+        }
+    }
+}
+
+template <typename T, int KIND, int D, int R>
+static void launch_append_block_r(const AppendArgs &a, cudaStream_t st) {
+    const dim3 grid((a.T + R - 2) / R + 1, static_cast<unsigned>(a.c.B) * a.c.H);
+    if (a.mu) kv_append_block_kernel<T, KIND, D, R, true><<<grid, AppendBlock<D, R>::THREADS, 0, st>>>(a);
+    else kv_append_block_kernel<T, KIND, D, R, false><<<grid, AppendBlock<D, R>::THREADS, 0, st>>>(a);
+}
+
+template <typename T, int KIND>
+static void launch_append_block(const AppendArgs &a, int d, int block, cudaStream_t st) {
+    if (d == 64) {
+        if (block == 16) launch_append_block_r<T, KIND, 64, 16>(a, st);
+        else if (block == 32) launch_append_block_r<T, KIND, 64, 32>(a, st);
+        else launch_append_block_r<T, KIND, 64, 64>(a, st);
+    } else {
+        if (block == 16) launch_append_block_r<T, KIND, 128, 16>(a, st);
+        else if (block == 32) launch_append_block_r<T, KIND, 128, 32>(a, st);
+        else launch_append_block_r<T, KIND, 128, 64>(a, st);
+    }
+}
+
+template <typename T, int KIND>
+static void launch_append_8(const AppendArgs &a, const sage_kv &c, cudaStream_t st) {
+    if (kv_block(c)) launch_append_block<T, KIND>(a, c.d, kv_block(c), st);
+    else launch_append_d<T, KIND>(a, c.d, st);
+}
+
 static void launch_append(const sage_kv &c, const AppendArgs &a, cudaStream_t st) {
+    const int format = kv_format(c);
     // a 16-bit pool is copied: one instance serves both 16-bit types
-    if (c.kind == SAGE_KV_16) launch_append_d<__half, SAGE_KV_16>(a, c.d, st);
-    else if (c.kind == SAGE_KV_INT8 && c.dtype == SAGE_FP16) launch_append_d<__half, SAGE_KV_INT8>(a, c.d, st);
-    else if (c.kind == SAGE_KV_INT8) launch_append_d<__nv_bfloat16, SAGE_KV_INT8>(a, c.d, st);
-    else if (c.dtype == SAGE_FP16) launch_append_d<__half, SAGE_KV_FP8>(a, c.d, st);
-    else launch_append_d<__nv_bfloat16, SAGE_KV_FP8>(a, c.d, st);
+    if (format == SAGE_KV_16) launch_append_d<__half, SAGE_KV_16>(a, c.d, st);
+    else if (format == SAGE_KV_INT8 && c.dtype == SAGE_FP16) launch_append_8<__half, SAGE_KV_INT8>(a, c, st);
+    else if (format == SAGE_KV_INT8) launch_append_8<__nv_bfloat16, SAGE_KV_INT8>(a, c, st);
+    else if (c.dtype == SAGE_FP16) launch_append_8<__half, SAGE_KV_FP8>(a, c, st);
+    else launch_append_8<__nv_bfloat16, SAGE_KV_FP8>(a, c, st);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -592,7 +792,7 @@ int sage_kv_append(const sage_kv *c, const void *K, const void *V, int T, const 
     if (st != SAGE_OK) return st;
     if (T <= 0 || !K || !V || !start) return SAGE_ERR_ARG;
     if (T >= (1 << 30)) return SAGE_ERR_UNSUPPORTED;
-    if (mu && c->kind == SAGE_KV_16) return SAGE_ERR_UNSUPPORTED;
+    if (mu && kv_format(*c) == SAGE_KV_16) return SAGE_ERR_UNSUPPORTED;
     if (misaligned(K, 16) || misaligned(V, 16) || misaligned(mu, 16) || misaligned(start, 4) ||
         misaligned(count, 4) || misaligned(pos0, 4))
         return SAGE_ERR_ALIGN;
@@ -611,6 +811,7 @@ int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget
                   void *workspace, size_t workspace_bytes, sage_stream_t stream) {
     const int st = check_kv(c, true);
     if (st != SAGE_OK) return st;
+    if (kv_block(*c)) return SAGE_ERR_UNSUPPORTED;                   // rows that share a scale do not move alone
     if (!lens || !seen || !lens_out || !c->score || !c->pos) return SAGE_ERR_ARG;
     const size_t nl = static_cast<size_t>(c->B) * sizeof(int);       // one sequence's length may be read after another's is written
     if (overlap(lens_out, nl, lens, nl) || overlap(lens_out, nl, seen, nl)) return SAGE_ERR_ARG;
@@ -627,7 +828,7 @@ int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, int budget
     a.max_moves = evict_max_moves(*c, budget);
     a.dst = static_cast<int *>(workspace);
     a.src = a.dst + static_cast<size_t>(rows) * a.max_moves;
-    const int row_bytes = c->d * (c->kind == SAGE_KV_16 ? 2 : 1);
+    const int row_bytes = c->d * (kv_format(*c) == SAGE_KV_16 ? 2 : 1);
     cudaError_t e;
     if (row_bytes == 64) e = launch_evict<64>(a, rows, s);
     else if (row_bytes == 128) e = launch_evict<128>(a, rows, s);

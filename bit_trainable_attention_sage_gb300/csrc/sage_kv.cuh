@@ -45,7 +45,12 @@ struct KvView {
     int *pos;
     int B, H, page, pages, max_pages, cap;   // cap = max_pages * page
     uint32_t page_mul, page_shift;           // s / page = s * page_mul >> page_shift for s < 2^30
+    int block_shift;                         // row >> block_shift: its scale's place (0: a scale a row)
 };
+
+// struct sage_kv's kind: the rows' format, and the tokens that share a scale (0: each row has its own)
+inline int kv_format(const sage_kv &c) { return c.kind & 255; }
+inline int kv_block(const sage_kv &c) { return c.kind >> 8; }
 
 // s / page without a division: page_mul = ceil(2^(30 + k) / page) with 2^k >= page exceeds the
 // quotient by less than 2^k / page / 2^(30 + k) of s, so by less than 1 / page for s < 2^30: the
@@ -80,8 +85,10 @@ inline KvView kv_view(const sage_kv &c) {
     uint32_t k = 0;
     while ((1ull << k) < static_cast<uint64_t>(c.page)) ++k;
     const uint64_t mul = ((1ull << (30 + k)) + c.page - 1) / c.page;     // at most 2^31
+    int shift = 0;
+    while ((1 << shift) < kv_block(c)) ++shift;
     return KvView{c.K, c.V, c.sK, c.sV, c.table, c.score, c.pos, c.B, c.H, c.page, c.pages,
-                  c.max_pages, c.max_pages * c.page, static_cast<uint32_t>(mul), 30 + k};
+                  c.max_pages, c.max_pages * c.page, static_cast<uint32_t>(mul), 30 + k, shift};
 }
 
 // A kernel's dynamic shared-memory limit, raised once a device (`raised`; again is harmless).
@@ -106,7 +113,11 @@ inline int check_kv(const sage_kv *c, bool pointers) {
     if (!c) return SAGE_ERR_ARG;
     if (c->B <= 0 || c->H <= 0 || c->d <= 0 || c->page <= 0 || c->pages <= 0 || c->max_pages <= 0) return SAGE_ERR_ARG;
     if (c->dtype != SAGE_FP16 && c->dtype != SAGE_BF16) return SAGE_ERR_UNSUPPORTED;
-    if (c->kind != SAGE_KV_16 && c->kind != SAGE_KV_INT8 && c->kind != SAGE_KV_FP8) return SAGE_ERR_UNSUPPORTED;
+    const int format = kv_format(*c), block = kv_block(*c);
+    if (c->kind < 0 || (format != SAGE_KV_16 && format != SAGE_KV_INT8 && format != SAGE_KV_FP8)) return SAGE_ERR_UNSUPPORTED;
+    // blocks of 16, 32 or 64 rows that divide the page, in 8 bits, and not with what eviction needs: it moves single rows
+    if (block && (format == SAGE_KV_16 || (block != 16 && block != 32 && block != 64) || c->page % block != 0 || c->score || c->pos))
+        return SAGE_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128) return SAGE_ERR_UNSUPPORTED;
     if (c->page % 16 != 0) return SAGE_ERR_UNSUPPORTED;
     if (static_cast<long long>(c->max_pages) * c->page >= (1ll << 30)) return SAGE_ERR_UNSUPPORTED;
@@ -114,7 +125,7 @@ inline int check_kv(const sage_kv *c, bool pointers) {
     if (!pointers) return SAGE_OK;
     if (!c->K || !c->V || !c->table) return SAGE_ERR_ARG;
     if (misaligned(c->K, 16) || misaligned(c->V, 16) || misaligned(c->table, 4)) return SAGE_ERR_ALIGN;
-    if (c->kind == SAGE_KV_16 ? (c->sK || c->sV) : (!c->sK || !c->sV)) return SAGE_ERR_ARG;
+    if (format == SAGE_KV_16 ? (c->sK || c->sV) : (!c->sK || !c->sV)) return SAGE_ERR_ARG;
     if (misaligned(c->sK, 16) || misaligned(c->sV, 16) || misaligned(c->score, 16) || misaligned(c->pos, 16))
         return SAGE_ERR_ALIGN;
     return SAGE_OK;

@@ -18,6 +18,7 @@ from .binding import SAGE_BF16, SAGE_FP16, _check, _ptr, _workspace, lib
 
 SAGE_FP32 = 2
 SAGE_KV_16, SAGE_KV_INT8, SAGE_KV_FP8 = 0, 1, 2
+KV_BLOCKS = (16, 32, 64)            # rows that may share a scale
 _KINDS = {torch.float16: SAGE_KV_16, torch.bfloat16: SAGE_KV_16, torch.int8: SAGE_KV_INT8,
           torch.float8_e4m3fn: SAGE_KV_FP8}
 _DTYPES = {torch.float16: SAGE_FP16, torch.bfloat16: SAGE_BF16, torch.float32: SAGE_FP32}
@@ -171,7 +172,7 @@ def sage_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, 
 # ---- paged key-value cache ------------------------------------------------------------------
 
 
-def _kv_sizes(B: int, H: int, d: int, page: int, pages: int, max_pages: int):
+def _kv_sizes(B: int, H: int, d: int, page: int, pages: int, max_pages: int, block: int = 0):
     """The sizes that struct sage_kv takes."""
     if min(B, H, page, pages, max_pages) < 1:
         raise ValueError(f"a cache of {B} sequences, {H} heads, {pages} pages of {page} tokens, {max_pages} a sequence: none may be 0")
@@ -183,16 +184,20 @@ def _kv_sizes(B: int, H: int, d: int, page: int, pages: int, max_pages: int):
         raise ValueError(f"{max_pages} pages of {page} tokens a sequence: fewer than 2^30 slots are wanted")
     if B * H > 65535:
         raise ValueError(f"{B} sequences of {H} heads: at most 65535 rows are taken")
+    if block and (block not in KV_BLOCKS or page % block):
+        raise ValueError(f"block must be 16, 32 or 64 rows and divide the page of {page}, got {block}")
 
 
 class KvCache:
     """A paged key-value cache over tensors of the caller (struct sage_kv).
 
     K, V (pages,H,page,d): fp16 or bf16 values, or int8 / float8_e4m3fn codes with sK, sV
-    (pages,H,page) float32, one scale a row; page a multiple of 16, B * H at most 65535.  table (B,max_pages) int32: the pages of each
+    (pages,H,page) float32, one scale a row, or (pages,H,page/R), one for each block of R = 16, 32 or 64
+    rows; page a multiple of 16, B * H at most 65535.  table (B,max_pages) int32: the pages of each
     sequence; entries behind its last page are not read.  score (B,H,max_pages*page) float32 and
-    pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict.  The tensors
-    are fixed for the life of the object; their contents are the caller's and the calls'."""
+    pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict (not with scales of
+    blocks).  The tensors are fixed for the life of the object; their contents are the caller's and
+    the calls'."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None):
         if K.dtype not in _KINDS or K.dim() != 4 or table.dim() != 2:
@@ -200,7 +205,8 @@ class KvCache:
         pages, H, page, d = K.shape
         B, max_pages = table.shape
         dev = K.device
-        _kv_sizes(B, H, d, page, pages, max_pages)
+        block = page // sK.shape[2] if isinstance(sK, torch.Tensor) and sK.dim() == 3 and 0 < sK.shape[2] < page else 0
+        _kv_sizes(B, H, d, page, pages, max_pages, block)
         _cuda(dev)
         _need(K, "K", K.dtype, K.shape, dev)
         _need(V, "V", K.dtype, K.shape, dev)
@@ -210,7 +216,10 @@ class KvCache:
             raise ValueError("sK and sV belong to int8 and float8_e4m3fn pools, and only to them")
         for name, t in (("sK", sK), ("sV", sV)):
             if t is not None:
-                _need(t, name, torch.float32, (pages, H, page), dev)
+                _need(t, name, torch.float32, (pages, H, page // (block or 1)), dev)
+        if block and (score is not None or pos is not None):
+            raise ValueError("a cache with scales of blocks has no score and no pos: rows are not evicted from it")
+        self.block = block
         self.capacity = max_pages * page
         for name, t, dt in (("score", score, torch.float32), ("pos", pos, torch.int32)):
             if t is not None:
@@ -219,7 +228,7 @@ class KvCache:
         self.B, self.H, self.d, self.page, self.pages, self.device = B, H, d, page, pages, dev
         # a struct for each 16-bit type that calls may bring
         types = (K.dtype,) if self.kind == SAGE_KV_16 else (torch.float16, torch.bfloat16)
-        self._c = {t: ctypes.byref(SageKv(B, H, d, _DTYPES[t], self.kind, page, pages, max_pages, K.data_ptr(), V.data_ptr(),
+        self._c = {t: ctypes.byref(SageKv(B, H, d, _DTYPES[t], self.kind | block << 8, page, pages, max_pages, K.data_ptr(), V.data_ptr(),
                                           _ptr(sK), _ptr(sV), table.data_ptr(), _ptr(score), _ptr(pos))) for t in types}
         self._bytes = {}        # workspace sizes by what they depend on
 
@@ -232,19 +241,22 @@ class KvCache:
 
 
 def make_kv_cache(B: int, H: int, d: int, capacity: int, *, dtype=torch.int8, page: int = 64, score: bool = False,
-                  device="cuda") -> KvCache:
+                  block: int = 0, device="cuda") -> KvCache:
     """A cache for B sequences of up to ``capacity`` tokens, each with pages of its own; ``score``
-    adds what eviction needs.  dtype: fp16, bf16, int8 or float8_e4m3fn."""
+    adds what eviction needs.  dtype: fp16, bf16, int8 or float8_e4m3fn.  ``block`` (8-bit types): one
+    scale for each block of 16, 32 or 64 rows instead of one a row."""
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     m = max(1, -(-capacity // max(page, 1)))
-    _kv_sizes(B, H, d, page, B * m, m)
+    _kv_sizes(B, H, d, page, B * m, m, block)
+    eight = dtype in (torch.int8, torch.float8_e4m3fn)
+    if block and (score or not eight):
+        raise ValueError("block belongs to int8 and float8_e4m3fn caches without score")
     table = torch.arange(B * m, dtype=torch.int32, device=device).view(B, m)
     shape = (B * m, H, page, d)
     K, V = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
-    eight = dtype in (torch.int8, torch.float8_e4m3fn)
-    sK, sV = (torch.zeros(shape[:3], device=device) if eight else None for _ in range(2))
+    sK, sV = (torch.zeros((B * m, H, page // (block or 1)), device=device) if eight else None for _ in range(2))
     extra = [torch.zeros((B, H, m * page), dtype=t, device=device) if score else None for t in (torch.float32, torch.int32)]
     return KvCache(K, V, table, sK=sK, sV=sV, score=extra[0], pos=extra[1])
 
@@ -254,6 +266,8 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
     """Writes tokens 0 .. count[b] - 1 (None: all T) of K, V (B,H,T,d) to slots start[b] + t of the
     cache, in its form.  ``mu`` (B,H,d) float32 (8-bit caches): K-smoothing, codes of K - mu.
     ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot).
+    With scales of blocks a block's scale grows with its rows (the codes before start[b] follow), and
+    what it holds behind the last new token is lost.
     Scores of the new slots are 0: decoding adds to them, weights of a prompt's own queries are the
     caller's to write to cache.score."""
     shape, dev = K.shape, cache.device
@@ -317,7 +331,7 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
     ``out`` if given, which may not overlap ``lens`` or ``seen``."""
     dev = cache.device
     if cache.score is None or cache.pos is None:
-        raise ValueError("eviction needs a cache with score and pos")
+        raise ValueError("eviction needs a cache with score and pos")      # (which one with scales of blocks cannot have)
     if not 0 <= recent <= budget or budget < 1:
         raise ValueError(f"budget {budget}, recent {recent}: 0 <= recent <= budget and budget >= 1 are wanted")
     budget = min(budget, cache.capacity)     # no length exceeds it

@@ -385,6 +385,10 @@ SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, 
  *   SAGE_KV_INT8  INT8 codes with one scale a row: delta = fl32(max|x| / 127), codes round half
  *                 to even of fl32(x / delta), all zero where delta = 0.
  *   SAGE_KV_FP8   the same with 448 and the nearest E4M3 code.
+ *   either | SAGE_KV_BLOCK(R)  the same with one scale for each block of R = 16, 32 or 64 rows of a
+ *                 page and head, R a divisor of the page: the scales are (pages,H,page/R).  (The
+ *                 blocks that sage_quantize_smooth codes by are R = 64.)  Such a cache has no
+ *                 score and no pos, and rows are not evicted from it.
  * Lengths, starts, counts, positions and tables are device int32 (4-byte alignment).  A page that
  * is not in [0, pages), or a length or slot outside [0, max_pages * page], is not followed: such
  * rows are skipped (append, evict) or masked (decode; lengths are held to the range), and
@@ -395,18 +399,19 @@ SAGE_API int sage_rope(const sage_rope_params *r, const void *Q, const void *K, 
 #define SAGE_KV_16 0
 #define SAGE_KV_INT8 1
 #define SAGE_KV_FP8 2
+#define SAGE_KV_BLOCK(rows) ((rows) << 8)
 
 typedef struct sage_kv {
     int B;              /* sequences (rows of the table)                                         */
     int H;              /* kv heads; B * H <= 65535                                              */
     int d;              /* 64 or 128                                                             */
     int dtype;          /* SAGE_FP16 or SAGE_BF16: K, V, q, O of the calls (and a 16-bit pool)   */
-    int kind;           /* SAGE_KV_*                                                             */
+    int kind;           /* SAGE_KV_*, 8-bit kinds with SAGE_KV_BLOCK(R) or without               */
     int page;           /* tokens a page, a multiple of 16                                       */
     int pages;          /* pages in the pool                                                     */
     int max_pages;      /* table entries a sequence; capacity = max_pages * page < 2^30          */
     void *K, *V;        /* (pages,H,page,d)                                                      */
-    float *sK, *sV;     /* (pages,H,page), 8-bit kinds only, else NULL                           */
+    float *sK, *sV;     /* (pages,H,page) or (pages,H,page/R), 8-bit kinds only, else NULL       */
     const int *table;   /* (B,max_pages)                                                         */
     float *score;       /* (B,H,capacity) accumulated weight of each slot, or NULL               */
     int *pos;           /* (B,H,capacity) position of each slot's token in the text, or NULL     */
@@ -419,6 +424,12 @@ typedef struct sage_kv {
  * fl32(K - mu); attention over keys that share one mu does not change (L does, by q . mu /
  * sqrt(d)).  sage_quantize_smooth's muK of the prompt is such a mu.
  * 8-bit kinds: a row with a NaN or an infinity gets a scale that is NaN or infinite.
+ * Scales of blocks: a block that begins with the call's rows takes its scale from them, delta =
+ * fl32(max|x| / 127 or 448) over all its new rows.  A block that goes on (it has slots before
+ * start[b]) takes the larger of its scale and theirs; where that grows, the codes of its rows before
+ * start[b] become the nearest (ties to even) of fl32(code * fl32(delta_old / delta)).  What the
+ * block holds behind the call's last row is lost.  A NaN or an infinity makes the scale of its whole
+ * block NaN or infinite.
  * Where the cache has score: score[slot] = 0 (only sage_attn_decode adds to it: weights of a prompt's
  * own queries are the caller's to write there).  Where it has pos: pos[slot] = pos0[b] + t, with
  * pos0 NULL: the slot itself. */
