@@ -29,6 +29,7 @@ EXPORTED = (
     "sage_device_status", "sage_status_string", "sage_version", "sage_quantize_smooth_qknorm",
     "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4", "sage_rope", "sage_kv_append",
     "sage_decode_workspace_bytes", "sage_attn_decode", "sage_evict_workspace_bytes", "sage_kv_evict",
+    "sage_extend_workspace_bytes", "sage_attn_extend",
 )
 
 
@@ -121,6 +122,10 @@ def lib() -> ctypes.CDLL:
     L.sage_evict_workspace_bytes.restype = sz
     L.sage_kv_evict.argtypes = [vp] * 3 + [ci, ci] + [vp] * 2 + [sz, vp]
     L.sage_kv_evict.restype = ci
+    L.sage_extend_workspace_bytes.argtypes = [vp, ci, ci]
+    L.sage_extend_workspace_bytes.restype = sz
+    L.sage_attn_extend.argtypes = [vp, ci, ci] + [vp] * 6 + [sz, vp]
+    L.sage_attn_extend.restype = ci
     _lib = L
     return L
 

@@ -7,6 +7,7 @@
 
 #include "sage_internal.h"
 #include "sage_kv.cuh"
+#include "sage_decode.h"
 
 namespace sage {
 
@@ -558,9 +559,9 @@ size_t sage_dump_bytes(const sage_params *p, int which) {
 int sage_device_status(sage_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SAGE_ERR_CUDA;
-    const unsigned int e = take_fwd_error() | take_bwd_error() | take_quant_error();
+    const unsigned int e = take_fwd_error() | take_bwd_error() | take_quant_error() | take_extend_error();
     // beside a timeout the index error stays for the next call
-    const unsigned int index = e ? 0u : take_kv_error() | take_decode_error();
+    const unsigned int index = e ? 0u : take_kv_error() | take_decode_error() | take_extend_index();
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
     return e ? SAGE_ERR_TIMEOUT : index ? SAGE_ERR_INDEX : SAGE_OK;
 }

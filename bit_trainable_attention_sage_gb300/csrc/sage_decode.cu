@@ -44,6 +44,7 @@
 #include <utility>
 
 #include "sage_kv.cuh"
+#include "sage_decode.h"
 
 namespace sage {
 
@@ -51,7 +52,6 @@ __device__ unsigned int g_decode_err = 0;   // 1: a page or length was out of ra
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kSMs = 152;
 constexpr int kDecCluster = 8;               // CTAs of a cluster at most
 
 // pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3; BLOCK: one scale for 16 or more rows (8 bits)
@@ -93,6 +93,11 @@ struct DecodeArgs {
     int tile, tile_shift;    // tokens a unit of work, 64 or 128, and their log2
     int bf16;                // type of q and O
     float sl2;               // log2(e) / sqrt(d)
+    // Several new tokens a sequence (sage_attn_extend): T of them, lens[b] the slots before the first, count[b]
+    // (NULL: T) those that are there.  The rows of a kv head are its heads' tokens: Hq and G count them,
+    // row r's token is r mod T.  0: one token, lens[b] its slots.
+    int T;
+    const int *count;
     float *part_O;           // (ctas, 2, MR, d) unnormalised sums
     float *part_ml;          // (ctas, 2, MR, 2) maxima (log2 units) and sums of exponentials
     float *row_ml;           // (B, Hq, 2) the same of rows that one run finished, with scores only
@@ -201,6 +206,24 @@ __device__ __forceinline__ void widen4_bf16(uint32_t w, uint32_t &lo, uint32_t &
     }
 }
 
+// Which 16-bit values (E4M3 codes) of a word are not finite, as a mask of their bits.
+template <int KIND>
+__device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
+    if constexpr (KIND == 3) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    else if constexpr (KIND == 1) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+    else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
+}
+// A pool's values i and i + 1 (E4M3: codes).
+template <int KIND>
+__device__ __forceinline__ float2 value_pair(const void *pool, size_t i) {
+    if constexpr (KIND == 0) return __half22float2(*reinterpret_cast<const __half2 *>(static_cast<const __half *>(pool) + i));
+    else if constexpr (KIND == 1) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(static_cast<const __nv_bfloat16 *>(pool) + i));
+    else {
+        const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(pool) + i));
+        return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    }
+}
+
 // 8 x 8 transposition of 16-bit values over a warp: lane (g, q) gives row g, columns 2q and 2q + 1
 // and gets those of column g.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -231,13 +254,40 @@ __device__ __forceinline__ void split11(float x, uint32_t &hi, uint32_t &lo) {
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
 }
 
+// ---- the slots of a sequence and of a row -----------------------------------------------------
+__device__ __forceinline__ int new_tokens(const DecodeArgs &a, int b) {
+    if (!a.count) return a.T;
+    const int n = __ldg(a.count + b);
+    if (n >= 0 && n <= a.T) return n;
+    atomicOr(&g_decode_err, 1u);
+    return n < 0 ? 0 : a.T;
+}
+__device__ __forceinline__ int seq_len(const DecodeArgs &a, int b) {
+    int n = kv_len(a.c, a.lens, b, &g_decode_err);
+    if (a.T) {
+        const int k = new_tokens(a, b);
+        if (k == 0) return 0;
+        n += k;
+        if (n > a.c.cap) {
+            atomicOr(&g_decode_err, 1u);
+            n = a.c.cap;
+        }
+    }
+    return n;
+}
+// the slots that row r of a kv head sees (several tokens only)
+__device__ __forceinline__ int row_limit(const DecodeArgs &a, int b, int r, int len) {
+    const int t = r % a.T;
+    return t < new_tokens(a, b) ? min(kv_len(a.c, a.lens, b, &g_decode_err) + t + 1, len) : 0;
+}
+
 // ---- the cut of the work ---------------------------------------------------------------------
 // A pair of `tiles` tiles counts kPairUnits + tiles units, the first kPairUnits for what a pair
 // costs besides its tiles (its first reads and its end take about as long as a tile): a run over
 // many short sequences then holds fewer tiles.
 constexpr int kPairUnits = 1;
 __device__ __forceinline__ int pair_units(const DecodeArgs &a, int b) {
-    const int tiles = (kv_len(a.c, a.lens, b, &g_decode_err) + a.tile - 1) >> a.tile_shift;
+    const int tiles = (seq_len(a, b) + a.tile - 1) >> a.tile_shift;
     return tiles > 0 ? tiles + kPairUnits : 0;
 }
 
@@ -336,12 +386,17 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & (S::ALIGN - 1));
     __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
     __shared__ float s_part[2][MR], s_f[kDecCluster][MR];        // ONE: a CTA's M and l; factors of the cluster's
+    __shared__ int s_not_finite;                                 // several tokens: a V was taken out of the products
     (void)s_part; (void)s_f;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int pairs = a.c.H * a.chunks;
     const int cta = blockIdx.x;
+    if (a.T) {
+        if (tid == 0) s_not_finite = 0;
+        __syncthreads();
+    }
     // The lengths say where this CTA's pages stand, the pages where its rows: three reads one after
     // the other.  The table and q are brought into L2 meanwhile, a share by each CTA.
     auto fetch = [&](size_t share, const void *table, size_t table_bytes, const void *Q, size_t q_bytes) {
@@ -361,7 +416,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const size_t head = static_cast<size_t>(b) * a.Hq + h0;
         fetch(rank, a.c.table + static_cast<size_t>(b) * a.c.max_pages, static_cast<size_t>(a.c.max_pages) * 4,
               static_cast<const char *>(a.Q) + head * D * 2, rank == 0 ? outs * D * 2 : 0);
-        if (kv_len(a.c, a.lens, b, &g_decode_err) == 0) {        // the whole cluster alike
+        if (seq_len(a, b) == 0) {                                // the whole cluster alike
             for (int i = (rank * kDecThreads + tid) * 2; i < outs * D; i += a.cluster * kDecThreads * 2) {
                 store_out(a, head * D + i, 0.0f, 0.0f);
                 if (i % D == 0) a.L[head + i / D] = -INFINITY;
@@ -376,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int grid = gridDim.x;
         for (long long e0 = cta; e0 < a.c.B; e0 += static_cast<long long>(grid) * kDecThreads) {
             const long long mine = e0 + static_cast<long long>(grid) * tid;
-            uint32_t none = __ballot_sync(0xffffffffu, mine < a.c.B && kv_len(a.c, a.lens, static_cast<int>(min(mine, a.c.B - 1ll)), &g_decode_err) == 0);
+            uint32_t none = __ballot_sync(0xffffffffu, mine < a.c.B && seq_len(a, static_cast<int>(min(mine, a.c.B - 1ll))) == 0);
             for (; none; none &= none - 1) {
                 const size_t head = static_cast<size_t>(e0 + static_cast<long long>(grid) * (warp * 32 + __ffs(none) - 1)) * a.Hq;
                 for (int i = lane * 2; i < a.Hq * D; i += 64) {
@@ -401,13 +456,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     const uint32_t load_lane = smem_u32(ring) + chunk_at<D, KIND>(lane / S::CPR, lane % S::CPR);
 
     // the run's pairs, one after the other
-    int len, tiles, t0, t1, hk, head0, heads, tok0, ng;
+    int len, tiles, t0, t1, hk, head0, heads, tok0, ng, edge;
     // The next pair of the run with a tile to do, from unit u on; u moves past its units.  False at
     // the run's end.
     auto find = [&]() {
         int pair;
         if constexpr (ONE) {
-            len = kv_len(a.c, a.lens, b, &g_decode_err);
+            len = seq_len(a, b);
             tiles = (len + S::TILE - 1) / S::TILE;
             pair = cta / a.cluster - b * pairs;
             t0 = tiles * rank / a.cluster;           // tiles < 2^24
@@ -415,7 +470,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         } else {
             for (;;) {
                 if (u >= u1) return false;
-                len = kv_len(a.c, a.lens, b, &g_decode_err);
+                len = seq_len(a, b);
                 tiles = (len + S::TILE - 1) / S::TILE;
                 const int units = tiles > 0 ? tiles + kPairUnits : 0;
                 if (u - first >= static_cast<long long>(units) * pairs) {
@@ -436,6 +491,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int ch = pair - hk * a.chunks;
         head0 = hk * a.G + ch * MR;                  // first query head of the group
         heads = min(MR, a.G - ch * MR);
+        // the last granules, where a slot may be hidden from a row: those with fewer than `edge` slots to the end
+        edge = S::GRAN;
+        if (a.T) edge = new_tokens(a, b) < a.T ? 0x7FFFFFFF : S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
         tok0 = t0 * S::TILE + warp * S::GRAN;
         ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
@@ -659,7 +717,37 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                         s[hf][nh][i] *= qs[nh][i & 1];
                     }
             }
-            if (len - tok < S::GRAN || holes) {
+            const bool hidden = a.T && len - tok < edge;
+            if (hidden) {
+                // several tokens: each row ends at a slot of its own
+                int limit[NH][2];
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) limit[nh][e] = row_limit(a, b, head0 - hk * a.G + nh * 8 + 2 * q + e, len) - tok;
+#pragma unroll
+                for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (hf * 16 + g + 8 * (i >> 1) >= limit[nh][i & 1] || (holes >> hf) & 1u) s[hf][nh][i] = -INFINITY;
+                // 0 times a V that is not finite would reach the rows that do not see it: it is taken out, and
+                // added at the end to those that do (INT8 codes are finite)
+                if constexpr (KIND != 2) {
+                    uint32_t bad = 0;
+                    for (int i = lane; i < S::GRAN * S::ROW / 16; i += 32) {
+                        uint4 *at = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(vst)) + i;
+                        const uint4 w = *at;
+                        const uint32_t m0 = not_finite_mask<KIND>(w.x), m1 = not_finite_mask<KIND>(w.y);
+                        const uint32_t m2 = not_finite_mask<KIND>(w.z), m3 = not_finite_mask<KIND>(w.w);
+                        if (m0 | m1 | m2 | m3) *at = make_uint4(w.x & ~m0, w.y & ~m1, w.z & ~m2, w.w & ~m3);
+                        bad |= m0 | m1 | m2 | m3;
+                    }
+                    if (bad) s_not_finite = 1;
+                    __syncwarp();
+                }
+            } else if (len - tok < S::GRAN || holes) {
 #pragma unroll
                 for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
@@ -713,7 +801,10 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 #pragma unroll
                     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[hf][nh][i] *= fv[hf][i >> 1];
+                        for (int i = 0; i < 4; ++i) {
+                            // (a hidden slot's scale may be anything)
+                            if (!hidden || s[hf][nh][i] != 0.0f) s[hf][nh][i] *= fv[hf][i >> 1];
+                        }
             }
             bool moved = false;
 #pragma unroll
@@ -820,6 +911,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int place = run_first && t0 > 0 ? 0 : 1;
         const size_t out0 = static_cast<size_t>(b) * a.Hq + head0;
         const int outs = heads;
+        // (of this pair, for values that are not finite: its sequence, kv head, first row, and the slots of its tiles)
+        const int pb = b, pk = hk, prow = head0 - hk * a.G, plen = len, pfrom = max(t0 * S::TILE, edge >= len ? 0 : len - edge), pto = t1 * S::TILE;
         bool more = false;
         if constexpr (!ONE) {
             more = find();
@@ -872,6 +965,18 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 o0 += f * from[p0];
                 o1 += f * from[p1];
                 sum += f * s_l[x][r];
+            }
+            if constexpr (KIND != 2) {
+                if (a.T && s_not_finite) {
+                    const int to = min(row_limit(a, pb, prow + r, plen), pto);
+                    for (int t = pfrom; t < to; ++t) {
+                        const int p = kv_page(a.c, pb, t, &g_decode_err);
+                        if (p < 0) continue;
+                        const float2 v = value_pair<KIND>(a.c.V, kv_row(a.c, p, pk, t) * D + c);
+                        if (!(fabsf(v.x) < INFINITY)) o0 += v.x;
+                        if (!(fabsf(v.y) < INFINITY)) o1 += v.y;
+                    }
+                }
             }
             if constexpr (ONE) {
                 *reinterpret_cast<float2 *>(sums + r * D + c) = make_float2(o0, o1);
@@ -1127,7 +1232,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int v = tid % VEC, grp = tid / VEC;
     const int pairs = a.c.H * a.chunks;
-    const int len = kv_len(a.c, a.lens, b, &g_decode_err);
+    const int len = seq_len(a, b);
     const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
     const bool idle = len == 0 || (y >= a.G && y * (kJoinThreads * 4) >= len);
     long long lo = 0;                                // units of the sequences before
@@ -1334,6 +1439,35 @@ static cudaError_t launch_decode_d(const DecodeArgs &a, int d, int mr, cudaStrea
     return d == 64 ? launch_decode_m<64, KIND>(a, mr, st) : launch_decode_m<128, KIND>(a, mr, st);
 }
 
+static cudaError_t run_decode(const sage_kv &c, const DecodePlan &p, int Hq, const void *Q, const int *lens, void *O, float *L, int add_score,
+                              int T, const int *count, void *workspace, cudaStream_t st) {
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    DecodeArgs a;
+    a.c = kv_view(c);
+    a.Q = Q; a.O = O; a.L = L; a.lens = lens;
+    a.Hq = Hq; a.G = Hq / c.H; a.chunks = p.chunks; a.ctas = p.ctas; a.cluster = p.cluster; a.tile = p.tile; a.tile_shift = p.tile == 64 ? 6 : 7;
+    a.T = T; a.count = count;
+    a.bf16 = c.dtype == SAGE_BF16;
+    a.sl2 = scale_log2(c.d);
+    a.part_O = reinterpret_cast<float *>(w);
+    a.part_ml = reinterpret_cast<float *>(w + p.off_ml);
+    a.row_ml = add_score && !p.cluster ? reinterpret_cast<float *>(w + p.off_rows) : nullptr;
+    a.logits = add_score ? reinterpret_cast<float *>(w + p.off_logits) : nullptr;
+    cudaError_t e;
+    if (kv_format(c) == SAGE_KV_INT8) e = launch_decode_d<2>(a, c.d, p.mr, st);
+    else if (kv_format(c) == SAGE_KV_FP8) e = launch_decode_d<3>(a, c.d, p.mr, st);
+    else if (a.bf16) e = launch_decode_d<1>(a, c.d, p.mr, st);
+    else e = launch_decode_d<0>(a, c.d, p.mr, st);
+    return e;
+}
+
+size_t decode_rows_bytes(const sage_kv &c, int Hq, int T) { return decode_plan(c, Hq * T, 0).bytes; }
+
+cudaError_t decode_rows(const sage_kv &c, int Hq, int T, const void *Q, const int *start, const int *count, void *O, float *L, void *workspace,
+                        cudaStream_t st) {
+    return run_decode(c, decode_plan(c, Hq * T, 0), Hq * T, Q, start, O, L, 0, T, count, workspace, st);
+}
+
 }  // namespace sage
 
 using namespace sage;
@@ -1358,23 +1492,7 @@ int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, v
         if (!workspace || workspace_bytes < p.bytes) return SAGE_ERR_WORKSPACE;
         if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
     }
-    uint8_t *w = static_cast<uint8_t *>(workspace);
-    DecodeArgs a;
-    a.c = kv_view(*c);
-    a.Q = Q; a.O = O; a.L = L; a.lens = lens;
-    a.Hq = Hq; a.G = Hq / c->H; a.chunks = p.chunks; a.ctas = p.ctas; a.cluster = p.cluster; a.tile = p.tile; a.tile_shift = p.tile == 64 ? 6 : 7;
-    a.bf16 = c->dtype == SAGE_BF16;
-    a.sl2 = scale_log2(c->d);
-    a.part_O = reinterpret_cast<float *>(w);
-    a.part_ml = reinterpret_cast<float *>(w + p.off_ml);
-    a.row_ml = add_score && !p.cluster ? reinterpret_cast<float *>(w + p.off_rows) : nullptr;
-    a.logits = add_score ? reinterpret_cast<float *>(w + p.off_logits) : nullptr;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (kv_format(*c) == SAGE_KV_INT8) e = launch_decode_d<2>(a, c->d, p.mr, s);
-    else if (kv_format(*c) == SAGE_KV_FP8) e = launch_decode_d<3>(a, c->d, p.mr, s);
-    else if (a.bf16) e = launch_decode_d<1>(a, c->d, p.mr, s);
-    else e = launch_decode_d<0>(a, c->d, p.mr, s);
+    const cudaError_t e = run_decode(*c, p, Hq, Q, lens, O, L, add_score, 0, nullptr, workspace, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
 }
 

@@ -1,0 +1,888 @@
+// sage_extend.cu -- attention of several new tokens a sequence over the paged key-value cache: a prompt's
+// chunk, a conversation's next turn, drafted tokens.
+//
+//   s_tk = q_t . K_k / sqrt(d),  O_t = sum_k softmax(s_t)_k V_k,  L_t = log sum_k exp s_tk,
+//   over the slots k <= start[b] + t  (token t's own slot is start[b] + t),  t < count[b].
+//
+// Work.  4 d multiply-adds a query head, new token and visible slot against a cache that is read once a
+// tile of rows: bound by the tensor cores from a few hundred rows a kv head on.  The rows of a kv head, its G query
+// heads times T tokens, are consecutive in Q (B,Hq,T,d): a tile is 128 consecutive ones, whatever heads
+// they belong to, so that grouped heads fill tiles when T is small, and row r's token is r mod T.
+// (Few rows, up to kExtendFewRows a kv head, go to the one-token kernel's warps instead: sage_decode.cu.)
+//
+// One CTA takes two tiles (256 rows) of one kv head and walks the slots in steps of 128:
+//   warps 8-11  load K and V rows by page, widen codes to the 16-bit type of Q, and store both as
+//               swizzled operands, two stages each.  8-bit rows come through registers, one step
+//               ahead; 16-bit rows by cp.async.
+//   warp 12     issues every MMA: S_t = Q_t K^T and O_t += P_t V, M = 128, N = 128 and d
+//   warps 0-3   softmax of tile 0, warps 4-7 of tile 1: a thread a row.  P goes back to TMEM over S,
+//               as the A operand of the second product; O stays in TMEM over the whole walk and is rescaled
+//               only when a row's maximum has grown by more than kSlack (a power of two) since the last time.
+// TMEM: columns 256 t + [0, 128) S_t and P_t, 256 t + 128 + [0, d) O_t.
+//
+// Scales.  Codes are exact in fp16 and bf16, so a logit is acc * (sK log2(e) / sqrt(d)); with one scale a
+// block that is one factor for 16 or more columns, and the maximum of a group's products is scaled once.  V's
+// scale goes into the exponent: p' = 2^(x + log2 sV - m), m the running maximum of x + log2 sV, feeds the
+// second product and keeps its largest value near 1 whatever the scales are; l sums p' / sV.
+// Roundings: p' is rounded to Q's type, bf16 (8 bits) or fp16 (11 bits, under 2^11 of the running maximum's, so that
+// they are all there down to 2^-25 of it and gone below 2^-36): half a step of the output's own type each,
+// and they average over the slots.  Sums, statistics and O are float32.
+//
+// Few CTAs are given more to do by cutting the slots into up to kExtMaxSplits ranges; a second kernel joins
+// their O, m and l in order, so results do not depend on the order in which CTAs run.
+//
+// What a row does not see never reaches it.  Logits of hidden slots are replaced (not added to); hidden
+// V rows are multiplied by 0, so a V that is not finite in the steps that only some rows see is set
+// to 0 in the operand, and added at the end to the rows that do see it.
+#include "sage_kv.cuh"
+#include "sage_decode.h"
+
+namespace sage {
+
+__device__ unsigned int g_ext_err = 0;      // bounded waits that gave up
+__device__ unsigned int g_ext_index = 0;    // 1: a page, start or count was out of range
+
+namespace ext {
+
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8;                // 8 .. 11
+constexpr int kMmaWarp = 12;
+// Launched at 128 registers a thread (512 x 128 = 65536): 2 x 128 x 184 + 128 x 104 + 128 x 40 = 65536.
+constexpr uint32_t kRegsSoftmax = 184, kRegsLoad = 104, kRegsControl = 40;
+constexpr int kRows = 256;                  // of a CTA
+constexpr int kStep = 128;                  // slots a step
+constexpr int kExtMaxSplits = 16;
+
+struct Args {
+    KvView c;
+    const void *Q;
+    void *O;
+    float *L;
+    const int *start, *count;
+    int T, rows;                            // new tokens; rows of a kv head (heads a kv head times T)
+    int tiles, splits;                      // CTAs a kv head's rows and slots are cut into
+    int order_heads, order_tiles;           // T a multiple of 256: heads a kv head, tiles a head; else 0
+    float sl2;                              // log2(e) / sqrt(d)
+    float *part_O, *part_ml;                // splits > 1: (items, splits, 256, d), (items, splits, 256, 2)
+};
+
+template <int D>
+struct Smem {
+    alignas(1024) uint8_t q[2][D / 64][128 * 128];   // [tile][64 channels][row][128 bytes], 128-byte swizzle
+    alignas(1024) uint8_t k[2][D / 64][128 * 128];   // two stages: step j's rows in stage j & 1
+    alignas(1024) uint8_t v[2][D / 64][128 * 128];
+    // of step j in place j & 3 (a place is written again when the step before the last has been read):
+    // factor of the products, log2 of V's scale and its reciprocal, a slot or a group of 16 slots each
+    alignas(16) float kc[4][128], lv[4][128], rv[4][128];
+    uint32_t holes[4];                               // groups of 16 slots whose page is none
+    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint32_t tmem_base;
+    int abort_flag, not_finite;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Four codes as two pairs of the operand type: INT8 by the difference of two integers under one exponent,
+// E4M3 by the conversion instruction.  All exact.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FP8) {
+        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+        if constexpr (BF16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+            lo = *reinterpret_cast<const uint32_t *>(&x);
+            hi = *reinterpret_cast<const uint32_t *>(&y);
+        }
+    } else if constexpr (BF16) {
+        // the low seven bits under 0x43 are 128 + them in bf16, the sign under 0x43 128 or 256
+        const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
+    } else {
+        // byte ^ 0x80 under 0x64 is 1024 + 128 + code in fp16
+        const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, 0x64646464u, 0x4140)), "r"(k));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, 0x64646464u, 0x4342)), "r"(k));
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        return pack_half2(lo, hi);
+    }
+}
+
+// Which 16-bit values (E4M3 codes) of a word are not finite, as a mask of their bits.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
+    if constexpr (FP8) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    else if constexpr (BF16) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+    else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
+}
+
+// Place of 16-byte chunk c of row r in an operand of 64-channel parts.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128u(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// What a sequence brings: its first new slot, its new tokens and its slots in all, held to what exists.
+struct Seq {
+    int start, count, len;
+};
+__device__ __forceinline__ Seq sequence(const Args &a, int b) {
+    Seq s;
+    s.start = kv_len(a.c, a.start, b, &g_ext_index);
+    s.count = a.T;
+    if (a.count) {
+        s.count = __ldg(a.count + b);
+        if (s.count < 0 || s.count > a.T) {
+            atomicOr(&g_ext_index, 1u);
+            s.count = s.count < 0 ? 0 : a.T;
+        }
+    }
+    s.len = s.count > 0 ? s.start + s.count : 0;
+    if (s.len > a.c.cap) {
+        atomicOr(&g_ext_index, 1u);
+        s.len = a.c.cap;
+    }
+    return s;
+}
+// the slots that row r sees
+__device__ __forceinline__ int row_limit(const Args &a, const Seq &s, int r) {
+    const int t = r % a.T;
+    return r < a.rows && t < s.count ? min(s.start + t + 1, s.len) : 0;
+}
+// the first and the last token of rows [r0, r1) of a kv head that exist
+__device__ __forceinline__ int first_token(const Args &a, int r0, int r1) {
+    const int t0 = r0 % a.T;
+    return t0 + (r1 - r0) > a.T ? 0 : t0;
+}
+__device__ __forceinline__ int last_token(const Args &a, int r0, int r1) {
+    const int t0 = r0 % a.T;
+    return t0 + (r1 - r0) > a.T ? a.T - 1 : t0 + (r1 - r0) - 1;
+}
+// slots that any row of [r0, r0 + n) sees
+__device__ __forceinline__ int tile_end(const Args &a, const Seq &s, int r0, int n) {
+    const int r1 = min(r0 + n, a.rows);
+    if (r0 >= r1 || s.len == 0) return 0;
+    const int t = min(last_token(a, r0, r1), s.count - 1);
+    // (a range of one head's tokens that all lie behind the count)
+    if (first_token(a, r0, r1) >= s.count) return 0;
+    return min(s.start + t + 1, s.len);
+}
+
+// SC: 0 a 16-bit pool, 1 a scale a row, 2 a scale a block
+template <int D, bool BF16, int SC, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem<D> &s = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // Results are referred to 2^kShift of the running maximum, which lags by up to 2^kSlack.
+    constexpr float kSlack = BF16 ? 8.0f : 4.0f, kShift = BF16 ? 0.0f : 11.0f;
+    const int warp = threadIdx.x >> 5;
+    const int BH = a.c.B * a.c.H;
+    // item: tiles with many slots first, all heads of a rank after one another
+    int x = blockIdx.x;
+    const int split = x % a.splits;
+    x /= a.splits;
+    const int bh = x % BH, rank = x / BH, b = bh / a.c.H, hk = bh - b * a.c.H;
+    const int tile = a.order_heads ? (rank % a.order_heads) * a.order_tiles + a.order_tiles - 1 - rank / a.order_heads : a.tiles - 1 - rank;
+    const int r0 = tile * kRows;
+    const Seq seq = sequence(a, b);
+    int end[2];                                       // slots a tile's rows see
+    end[0] = tile_end(a, seq, r0, 128);
+    end[1] = tile_end(a, seq, r0 + 128, 128);
+    const int all = (max(end[0], end[1]) + kStep - 1) / kStep;
+    const int j0 = static_cast<int>(static_cast<long long>(all) * split / a.splits), j1 = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits);
+    const int kv_end = max(end[0], end[1]);
+    int n_t[2];                                       // a tile's steps: j0 .. n_t - 1
+    n_t[0] = min(j1, (end[0] + kStep - 1) / kStep);
+    n_t[1] = min(j1, (end[1] + kStep - 1) / kStep);
+    const size_t item = (static_cast<size_t>(bh) * a.tiles + tile) * a.splits + split;
+    const size_t out0 = static_cast<size_t>(bh) * a.rows;            // first row of the kv head in O and L
+    // steps from here on hold slots that not every row sees
+    const int mixed = seq.len == 0 ? 0 : (seq.start + first_token(a, r0, min(r0 + kRows, a.rows)) + 1) / kStep;
+
+    if (j0 >= j1) {                                   // nothing to see: the whole CTA alike
+        const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
+        if (r0 + row >= a.rows) return;
+        if (a.splits > 1) {
+            if (half == 0) reinterpret_cast<float2 *>(a.part_ml)[item * kRows + row] = make_float2(-INFINITY, 0.0f);
+        } else {
+            uint4 *O = static_cast<uint4 *>(a.O) + (out0 + r0 + row) * (D / 8) + half * (D / 16);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) O[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (half == 0) a.L[out0 + r0 + row] = -INFINITY;
+        }
+        return;
+    }
+
+    if (warp == kMmaWarp) {
+        tmem_alloc(&s.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        s.abort_flag = 0;
+        s.not_finite = 0;
+        mbar_init(&s.q_full, 4);
+        for (int st = 0; st < 2; ++st) {
+            mbar_init(&s.k_full[st], 4);
+            mbar_init(&s.k_free[st], 1);
+            mbar_init(&s.v_full[st], 4);
+            mbar_init(&s.v_free[st], 1);
+        }
+        mbar_init(&s.mma_done, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s.s_full[t], 1);
+            mbar_init(&s.p_full[t], 4);
+            mbar_init(&s.o_full[t], 1);
+        }
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    volatile int *abort_flag = &s.abort_flag;
+    // step j is the (j - j0)th: stage (j - j0) & 1, its barriers' phase ((j - j0) >> 1) & 1
+
+    if (warp >= kMmaWarp) {
+        regs_dec<kRegsControl>();
+        if (warp == kMmaWarp && elect_one()) {
+            // ------------------------------------------------------------------ MMA issuer
+            constexpr uint32_t idS = idesc_f16(128, 128, BF16, false, false);
+            constexpr uint32_t idPV = idesc_f16(128, D, BF16, false, true);
+            auto issue_s = [&](const int t, int st) {
+                const uint32_t q_addr = smem_u32(s.q[t][0]), k_addr = smem_u32(s.k[st][0]);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+                    umma_ss(tmem + 256 * t, sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0);
+                }
+                umma_commit(&s.s_full[t]);
+            };
+            bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&s.k_full[0], 0, abort_flag, &g_ext_err, 2);
+            if (ok) {
+                tc_fence_after();
+                if (j0 < n_t[0]) issue_s(0, 0);
+                if (j0 < n_t[1]) issue_s(1, 0);
+                umma_commit(&s.k_free[0]);
+            }
+            // As in the forward kernel a tile's next S follows its PV in issue order and overwrites the P that the
+            // PV reads: the tensor pipe runs MMAs in that order.
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int i = j - j0, st = i & 1, nst = st ^ 1;
+                if (!(ok = mbar_wait(&s.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
+                const uint32_t v_addr = smem_u32(s.v[st][0]);
+                bool k_next = false;
+                auto tile_step = [&](const int t) -> bool {
+                    if (j >= n_t[t]) return true;
+                    if (!mbar_wait(&s.p_full[t], i & 1, abort_flag, &g_ext_err, 4)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (i > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(&s.o_full[t]);
+                    if (j + 1 < n_t[t]) {
+                        if (!k_next) {
+                            if (!mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
+                            tc_fence_after();
+                            k_next = true;
+                        }
+                        issue_s(t, nst);
+                    }
+                    return true;
+                };
+                ok = tile_step(0) && tile_step(1);
+                if (!ok) break;
+                if (j + 1 < j1) umma_commit(&s.k_free[nst]);
+                umma_commit(&s.v_free[st]);
+            }
+            // every MMA must have finished before the tensor memory is released
+            umma_commit(&s.mma_done);
+            mbar_wait_drain(&s.mma_done, 0, &g_ext_err, 5);
+        }
+    } else if (warp >= kLoadWarp) {
+        regs_dec<kRegsLoad>();
+        // ------------------------------------------------------------------ K, V and Q rows
+        const int tid = threadIdx.x - kLoadWarp * 32, lane = tid & 31;
+        constexpr int ROW = SC ? D : 2 * D;                          // bytes of a row
+        constexpr int CPR = ROW / 16, RPI = 128 / CPR, ITS = 128 / RPI;   // 16-byte chunks a row, rows at a time
+        const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
+        const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+        // the pool's row of a slot, -1 where it has no page
+        auto row_of = [&](int slot) -> long long {
+            const int p = __ldg(table + kv_page_of(a.c, slot));
+            if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.c.pages)) {
+                atomicOr(&g_ext_index, 1u);
+                return -1;
+            }
+            return static_cast<long long>(kv_row(a.c, p, hk, slot));
+        };
+        auto done = [&](uint64_t *bar) {                             // this warp's part is stored
+            fence_view_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        // ---- scales, one step ahead
+        float sk = 0.0f, sv = 0.0f;
+        bool hole = false;
+        auto load_scales = [&](int j) {
+            // a thread a slot (SC = 1), or threads 0 .. 7 a group of 16 each; of a 16-bit pool the holes alone
+            const int slot = j * kStep + (SC == 1 ? tid : tid * 16);
+            sk = sv = 0.0f;
+            hole = false;
+            if ((SC == 1 || tid < 8) && slot < kv_end) {
+                const long long r = row_of(slot);
+                hole = r < 0;
+                if (SC && r >= 0) {
+                    sk = __ldg(a.c.sK + (r >> a.c.block_shift));
+                    sv = __ldg(a.c.sV + (r >> a.c.block_shift));
+                }
+            }
+        };
+        auto store_scales = [&](int i) {
+            const int at = i & 3;
+            if (SC == 1 || (SC == 2 && tid < 8)) {
+                s.kc[at][tid] = sk * a.sl2;
+                // no value is lost with a scale of 0 (its codes are): a NaN stays one
+                s.lv[at][tid] = sv == 0.0f ? 0.0f : log2f(sv);
+                s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;
+            }
+            if constexpr (SC == 1) {
+                // slots 32 w .. of warp w: two groups
+                const uint32_t h = __ballot_sync(0xffffffffu, hole);
+                if (lane == 0) {
+                    const uint32_t two = (h & 0xFFFFu ? 1u : 0u) | (h >> 16 ? 2u : 0u);
+                    reinterpret_cast<uint8_t *>(&s.holes[at])[warp - kLoadWarp] = static_cast<uint8_t>(two);
+                }
+            } else if (warp == kLoadWarp) {
+                const uint32_t h = __ballot_sync(0xffffffffu, hole);
+                // groups 2 w and 2 w + 1 in byte w, as above
+                if (lane == 0) s.holes[at] = (h & 3u) | ((h >> 2) & 3u) << 8 | ((h >> 4) & 3u) << 16 | ((h >> 6) & 3u) << 24;
+            }
+        };
+        // ---- Q: both tiles' rows, zeros behind the last
+        auto load_q = [&]() {
+            const uint4 *Q = static_cast<const uint4 *>(a.Q) + out0 * (D / 8);
+            constexpr int QC = D / 8, QR = 128 / QC;
+            for (int t = 0; t < 2; ++t) {
+                if (j0 >= n_t[t]) continue;
+#pragma unroll 8
+                for (int r = tid / QC; r < 128; r += QR) {
+                    const int row = r0 + 128 * t + r;
+                    const uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
+                    sts128(smem_u32(s.q[t][0]) + chunk_at(r, tid % QC), w);
+                }
+            }
+            done(&s.q_full);
+        };
+        auto free_of = [&](uint64_t *bar, int i) {                   // the stage of step j0 + i has been read
+            return i < 2 || mbar_wait_warp(&bar[i & 1], ((i >> 1) - 1) & 1, abort_flag, &g_ext_err, 6);
+        };
+        if constexpr (SC != 0) {
+            uint4 kr[ITS], vr[ITS];
+            auto load = [&](const void *pool, int j, uint4 (&to)[ITS]) {
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    const int slot = j * kStep + rr + i * RPI;
+                    to[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (slot < kv_end) {
+                        const long long r = row_of(slot);
+                        if (r >= 0) to[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) + r * ROW) + cc);
+                    }
+                }
+            };
+            // 16 codes become chunks 2 cc and 2 cc + 1; lanes of the second 64 channels store theirs the
+            // other way round, so that a row's eight stores meet eight different 16-byte bank groups
+            auto store = [&](uint32_t to, const uint4 (&from)[ITS]) {
+                const int flip = cc >> 2 & 1;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    const int r = rr + i * RPI;
+                    uint4 lo, hi;
+                    widen4<BF16, FP8>(from[i].x, lo.x, lo.y);
+                    widen4<BF16, FP8>(from[i].y, lo.z, lo.w);
+                    widen4<BF16, FP8>(from[i].z, hi.x, hi.y);
+                    widen4<BF16, FP8>(from[i].w, hi.z, hi.w);
+                    sts128(to + chunk_at(r, 2 * cc + flip), flip ? hi : lo);
+                    sts128(to + chunk_at(r, 2 * cc + 1 - flip), flip ? lo : hi);
+                }
+            };
+            load_scales(j0);
+            load(a.c.K, j0, kr);
+            load(a.c.V, j0, vr);
+            load_q();
+            for (int j = j0; j < j1; ++j) {
+                const int i = j - j0, st = i & 1;
+                if (!free_of(s.k_free, i)) break;
+                store(smem_u32(s.k[st][0]), kr);
+                store_scales(i);
+                done(&s.k_full[st]);
+                if (j + 1 < j1) {
+                    load_scales(j + 1);
+                    load(a.c.K, j + 1, kr);
+                }
+                if (!free_of(s.v_free, i)) break;
+                if constexpr (FP8) {
+                    if (j >= mixed) {
+#pragma unroll
+                        for (int x = 0; x < ITS; ++x) {
+                            uint32_t *w = &vr[x].x;
+                            uint32_t bad = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t m = not_finite_mask<BF16, true>(w[e]);
+                                w[e] &= ~m;
+                                bad |= m;
+                            }
+                            if (bad) s.not_finite = 1;
+                        }
+                    }
+                }
+                store(smem_u32(s.v[st][0]), vr);
+                done(&s.v_full[st]);
+                if (j + 1 < j1) load(a.c.V, j + 1, vr);
+            }
+        } else {
+            auto load = [&](const void *pool, uint32_t to, int j) {
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    const int r = rr + i * RPI, slot = j * kStep + r;
+                    long long row = -1;
+                    if (slot < kv_end) row = row_of(slot);
+                    const uint8_t *from = static_cast<const uint8_t *>(pool) + (row < 0 ? 0 : row * ROW + cc * 16);
+                    cp_async16(to + chunk_at(r, cc), from, row >= 0);
+                }
+                cp_commit();
+            };
+            load(a.c.K, smem_u32(s.k[0][0]), j0);
+            load(a.c.V, smem_u32(s.v[0][0]), j0);
+            load_scales(j0);
+            load_q();
+            for (int j = j0; j < j1; ++j) {
+                const int i = j - j0, st = i & 1;
+                store_scales(i);
+                if (j + 1 < j1) {
+                    if (!free_of(s.k_free, i + 1)) break;
+                    load(a.c.K, smem_u32(s.k[st ^ 1][0]), j + 1);
+                    load_scales(j + 1);
+                    cp_wait<2>();
+                } else {
+                    cp_wait<1>();
+                }
+                done(&s.k_full[st]);
+                if (j + 1 < j1) {
+                    if (!free_of(s.v_free, i + 1)) break;
+                    load(a.c.V, smem_u32(s.v[st ^ 1][0]), j + 1);
+                    cp_wait<2>();
+                } else {
+                    cp_wait<0>();
+                }
+                if (j >= mixed) {                                    // the chunks this thread has copied itself
+#pragma unroll 4
+                    for (int x = 0; x < ITS; ++x) {
+                        const uint32_t at = smem_u32(s.v[st][0]) + chunk_at(rr + x * RPI, cc);
+                        uint4 w = lds128u(at);
+                        const uint32_t m0 = not_finite_mask<BF16, false>(w.x), m1 = not_finite_mask<BF16, false>(w.y);
+                        const uint32_t m2 = not_finite_mask<BF16, false>(w.z), m3 = not_finite_mask<BF16, false>(w.w);
+                        if (m0 | m1 | m2 | m3) {
+                            sts128(at, make_uint4(w.x & ~m0, w.y & ~m1, w.z & ~m2, w.w & ~m3));
+                            s.not_finite = 1;
+                        }
+                    }
+                }
+                done(&s.v_full[st]);
+            }
+            cp_wait<0>();                                            // no copy outlives the CTA's shared memory
+        }
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // ------------------------------------------------------------------ softmax
+        const int t = warp >> 2, quarter = warp & 3, lane = static_cast<int>(lane_id());
+        const int row = 128 * t + 32 * quarter + lane;
+        const int limit = row_limit(a, seq, r0 + row);               // slots this row sees
+        const int steps = t ? n_t[1] : n_t[0];
+        const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 256 * t);
+        float m = -INFINITY, l = 0.0f;                               // reference of O and l; l
+        bool ok = true;
+        for (int j = j0; j < steps; ++j) {
+            const int i = j - j0, at = i & 3;
+            if (!(ok = mbar_wait_warp(&s.s_full[t], i & 1, abort_flag, &g_ext_err, 7))) break;
+            tc_fence_after();
+            uint32_t raw[128];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) tmem_ld16(lane_base + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&raw[16 * q]));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&raw[16 * q]));
+            const uint32_t holes = s.holes[at];
+            const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
+            const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
+            // ---- the step's largest x = acc kc + lv.  `scaled`: raw holds x itself afterwards
+            const bool scaled = SC == 1 || !whole;
+            float mx = -INFINITY;
+            if (SC != 1 && whole) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    float gm = fmaxf(__uint_as_float(raw[16 * g]), __uint_as_float(raw[16 * g + 1]));
+#pragma unroll
+                    for (int k = 2; k < 16; k += 2) gm = max3f(gm, __uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1]));
+                    mx = fmaxf(mx, SC == 2 ? __fmaf_rn(gm, s.kc[at][g], s.lv[at][g]) : gm * a.sl2);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 128; k += 4) {
+                    float4 kc = make_float4(a.sl2, a.sl2, a.sl2, a.sl2), lv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if constexpr (SC == 1) {
+                        kc = lds128(smem_u32(&s.kc[at][k]));
+                        lv = lds128(smem_u32(&s.lv[at][k]));
+                    } else if constexpr (SC == 2) {
+                        kc.x = kc.y = kc.z = kc.w = s.kc[at][k / 16];
+                        lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
+                    }
+                    const f2 lo = fma2(f2{__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])}, f2{kc.x, kc.y}, f2{lv.x, lv.y});
+                    const f2 hi = fma2(f2{__uint_as_float(raw[k + 2]), __uint_as_float(raw[k + 3])}, f2{kc.z, kc.w}, f2{lv.z, lv.w});
+                    float v[4] = {lo.x, lo.y, hi.x, hi.y};
+                    if (!whole) {
+                        const bool none = (holes >> (k / 32 * 8 + (k / 16 & 1))) & 1u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (none || k + e >= seen) v[e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) raw[k + e] = __float_as_uint(v[e]);
+                    mx = max3f(mx, v[0], v[1]);
+                    mx = max3f(mx, v[2], v[3]);
+                }
+            }
+            // ---- the reference follows the maximum when it lags too far
+            const bool moves = mx > m + kSlack;
+            if (__any_sync(0xffffffffu, moves)) {
+                const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
+                m = to;
+                l *= alpha;
+                if (i > 0) {
+                    if (!(ok = mbar_wait_warp(&s.o_full[t], (i - 1) & 1, abort_flag, &g_ext_err, 8))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(lane_base + 128 + c, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st16(lane_base + 128 + c, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
+            // ---- p' = 2^(x - ref), to TMEM over S, and l
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                uint32_t pk[8];
+                f2 sum{0.0f, 0.0f};
+                f2 f{1.0f, 1.0f}, off{-ref, -ref};
+                if (SC == 0 && !scaled) f = f2{a.sl2, a.sl2};
+                if (SC == 2 && !scaled) {
+                    f.x = f.y = s.kc[at][g];
+                    off.x = off.y = s.lv[at][g] - ref;
+                }
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    const f2 r2{__uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1])};
+                    const f2 x2 = scaled ? add2(r2, off) : fma2(r2, f, off);
+                    const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
+                    if constexpr (SC == 1) {
+                        const f2 rv{s.rv[at][16 * g + k], s.rv[at][16 * g + k + 1]};
+                        // (a hidden slot's reciprocal may be anything)
+                        sum.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
+                        sum.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
+                    } else {
+                        sum = add2(sum, p);
+                    }
+                    pk[k / 2] = pack2<BF16>(p.x, p.y);
+                }
+                const float add = sum.x + sum.y;
+                if constexpr (SC == 2) l += add == 0.0f ? 0.0f : add * s.rv[at][g];
+                else l += add;
+                tmem_st8(lane_base + 8 * g, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_full[t]);
+        }
+        if (ok && steps > j0) ok = mbar_wait_warp(&s.o_full[t], (steps - 1 - j0) & 1, abort_flag, &g_ext_err, 9);
+        tc_fence_after();
+        const bool there = r0 + row < a.rows;
+        const bool empty = limit == 0 || l == 0.0f;                  // saw nothing (a NaN is no 0)
+        const bool part = a.splits > 1;
+        if (ok && !*abort_flag) {
+            const float inv = empty ? 0.0f : 1.0f / l;
+            if (there) {
+                const float ref = m - kShift;
+                if (part) reinterpret_cast<float2 *>(a.part_ml)[item * kRows + row] = empty ? make_float2(-INFINITY, 0.0f) : make_float2(ref, l);
+                else a.L[out0 + r0 + row] = empty ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+            }
+            // V values that are not finite and were taken out of the products: added for the rows that see them
+            const bool fix = s.not_finite != 0;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = 0u;
+                if (steps > j0) {
+                    tmem_ld16(lane_base + 128 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+                    tmem_ld16(lane_base + 128 + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                    tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+                    tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                }
+                float v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = empty ? 0.0f : __uint_as_float(o[k]) * (part ? 1.0f : inv);
+                if (fix) {
+                    const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+                    for (int slot = max(j0, mixed) * kStep; slot < min(limit, j1 * kStep); ++slot) {
+                        const int p = __ldg(table + kv_page_of(a.c, slot));
+                        if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.c.pages)) continue;
+                        const size_t from = kv_row(a.c, p, hk, slot) * D + c;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float z = 0.0f;
+                            if constexpr (SC != 0) {
+                                if (FP8 && (static_cast<const uint8_t *>(a.c.V)[from + k] & 0x7Fu) == 0x7Fu) z = __int_as_float(0x7FC00000);
+                            } else if constexpr (BF16) {
+                                z = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.c.V)[from + k]);
+                            } else {
+                                z = __half2float(static_cast<const __half *>(a.c.V)[from + k]);
+                            }
+                            if (!(fabsf(z) < INFINITY)) v[k] += z;
+                        }
+                    }
+                }
+                if (!there) continue;
+                if (part) {
+                    if (empty) continue;                             // not read
+                    float4 *to = reinterpret_cast<float4 *>(a.part_O + (item * kRows + row) * D + c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                } else {
+                    uint4 *to = static_cast<uint4 *>(a.O) + ((out0 + r0 + row) * D + c) / 8;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        to[k] = make_uint4(pack2<BF16>(v[8 * k], v[8 * k + 1]), pack2<BF16>(v[8 * k + 2], v[8 * k + 3]),
+                                           pack2<BF16>(v[8 * k + 4], v[8 * k + 5]), pack2<BF16>(v[8 * k + 6], v[8 * k + 7]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// A row's parts under their common reference, in their order.  A warp a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) extend_join_kernel(const __grid_constant__ Args a) {
+    const int lane = threadIdx.x & 31;
+    const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);     // of all kv heads
+    const size_t total = static_cast<size_t>(a.c.B) * a.c.H * a.rows;
+    if (row >= total) return;
+    const size_t bh = row / a.rows;
+    const int r = static_cast<int>(row - bh * a.rows), tile = r / kRows;
+    const size_t first = ((bh * a.tiles + tile) * a.splits) * kRows + (r - tile * kRows);   // part k: + k * kRows
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < a.splits) ml = reinterpret_cast<const float2 *>(a.part_ml)[first + static_cast<size_t>(lane) * kRows];
+    float M = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mine = ml.y == 0.0f ? 0.0f : ex2_approx(ml.x - M);
+    float l = mine * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    constexpr int V = D / 32;                                        // channels a lane: 2 or 4
+    float o[V] = {};
+    for (int k = 0; k < a.splits; ++k) {
+        const float f = __shfl_sync(0xffffffffu, mine, k), lk = __shfl_sync(0xffffffffu, ml.y, k);
+        if (lk == 0.0f) continue;                                    // saw nothing: not written
+        const float *from = a.part_O + (first + static_cast<size_t>(k) * kRows) * D + lane * V;
+        if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(from);
+            o[0] += f * x.x; o[1] += f * x.y; o[2] += f * x.z; o[3] += f * x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(from);
+            o[0] += f * x.x; o[1] += f * x.y;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t *to = static_cast<uint32_t *>(a.O) + (row * D + lane * V) / 2;
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) to[k] = pack2<BF16>(o[2 * k] * inv, o[2 * k + 1] * inv);
+    if (lane == 0) a.L[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+// ---- host -------------------------------------------------------------------------------------
+struct Plan {
+    int tiles, splits;
+    size_t off_ml, bytes;
+};
+
+static Plan plan(const sage_kv &c, int Hq, int T) {
+    Plan p;
+    const long long rows = static_cast<long long>(Hq / c.H) * T;
+    p.tiles = static_cast<int>((rows + kRows - 1) / kRows);
+    const long long items = static_cast<long long>(c.B) * c.H * p.tiles;
+    // The slots are cut where CTAs are fewer than SMs: into as many ranges as make the last wave fullest, at
+    // least four steps of the capacity each.
+    const long long steps = (static_cast<long long>(c.max_pages) * c.page + kStep - 1) / kStep;
+    p.splits = 1;
+    if (items < kSMs) {
+        double best = 1.0;
+        for (int k = 2; k <= kExtMaxSplits && steps / k >= 4; ++k) {
+            const double cost = static_cast<double>((items * k + kSMs - 1) / kSMs) / k;
+            if (cost < best * 0.97) {
+                best = cost;
+                p.splits = k;
+            }
+        }
+    }
+    const size_t parts = p.splits > 1 ? static_cast<size_t>(items) * p.splits * kRows : 0;
+    p.off_ml = parts * c.d * sizeof(float);
+    p.bytes = p.off_ml + parts * 2 * sizeof(float);
+    return p;
+}
+
+template <int D, bool BF16, int SC, bool FP8>
+static cudaError_t launch_k(const Args &a, cudaStream_t st) {
+    auto kernel = extend_kernel<D, BF16, SC, FP8>;
+    const size_t smem = sizeof(Smem<D>) + 1024;
+    static bool raised[16] = {false};
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), smem, raised);
+    if (e != cudaSuccess) return e;
+    // the register split must fit in what the block is launched with, or an increase could never be granted
+    static int regs = 0;
+    if (regs == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        regs = fa.numRegs;
+    }
+    if (regs * kThreads < 2 * 128 * static_cast<int>(kRegsSoftmax) + 128 * static_cast<int>(kRegsLoad + kRegsControl)) return cudaErrorInvalidConfiguration;
+    const long long grid = static_cast<long long>(a.c.B) * a.c.H * a.tiles * a.splits;
+    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const size_t rows = static_cast<size_t>(a.c.B) * a.c.H * a.rows;
+    extend_join_kernel<D, BF16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+static cudaError_t launch(const sage_kv &c, const Args &a, cudaStream_t st) {
+    const bool fp8 = kv_format(c) == SAGE_KV_FP8;
+    if (kv_format(c) == SAGE_KV_16) return launch_k<D, BF16, 0, false>(a, st);
+    if (kv_block(c)) return fp8 ? launch_k<D, BF16, 2, true>(a, st) : launch_k<D, BF16, 2, false>(a, st);
+    return fp8 ? launch_k<D, BF16, 1, true>(a, st) : launch_k<D, BF16, 1, false>(a, st);
+}
+
+}  // namespace ext
+
+unsigned int take_extend_error() {
+    unsigned int v = 0;
+    const unsigned int zero = 0;
+    cudaMemcpyFromSymbol(&v, g_ext_err, sizeof(v));
+    if (v) cudaMemcpyToSymbol(g_ext_err, &zero, sizeof(zero));
+    return v;
+}
+unsigned int take_extend_index() {
+    unsigned int v = 0;
+    const unsigned int zero = 0;
+    cudaMemcpyFromSymbol(&v, g_ext_index, sizeof(v));
+    if (v) cudaMemcpyToSymbol(g_ext_index, &zero, sizeof(zero));
+    return v;
+}
+
+}  // namespace sage
+
+using namespace sage;
+
+// Rows a kv head up to which the one-token kernel takes the call.
+constexpr int kExtendFewRows = 32;
+
+static int check_extend(const sage_kv *c, int Hq, int T) {
+    const int st = check_kv(c, false);
+    if (st != SAGE_OK) return st;
+    if (Hq <= 0 || Hq % c->H != 0 || T <= 0) return SAGE_ERR_ARG;
+    if (static_cast<long long>(c->B) * Hq > (1 << 24) || static_cast<long long>(c->B) * Hq * T > (1 << 28)) return SAGE_ERR_UNSUPPORTED;
+    return SAGE_OK;
+}
+
+extern "C" {
+
+size_t sage_extend_workspace_bytes(const sage_kv *c, int Hq, int T) {
+    if (check_extend(c, Hq, T) != SAGE_OK) return 0;
+    return static_cast<long long>(Hq / c->H) * T <= kExtendFewRows ? decode_rows_bytes(*c, Hq, T) : ext::plan(*c, Hq, T).bytes;
+}
+
+int sage_attn_extend(const sage_kv *c, int Hq, int T, const void *Q, const int *start, const int *count, void *O, float *L,
+                     void *workspace, size_t workspace_bytes, sage_stream_t stream) {
+    int st = check_extend(c, Hq, T);
+    if (st != SAGE_OK) return st;
+    st = check_kv(c, true);
+    if (st != SAGE_OK) return st;
+    if (!Q || !start || !O || !L || O == Q) return SAGE_ERR_ARG;
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(L, 16) || misaligned(start, 4) || misaligned(count, 4)) return SAGE_ERR_ALIGN;
+    const size_t bytes = sage_extend_workspace_bytes(c, Hq, T);
+    if (bytes) {                                 // else it is not looked at
+        if (!workspace || workspace_bytes < bytes) return SAGE_ERR_WORKSPACE;
+        if (misaligned(workspace, 256)) return SAGE_ERR_ALIGN;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int G = Hq / c->H;
+    cudaError_t e;
+    if (static_cast<long long>(G) * T <= kExtendFewRows) {
+        e = decode_rows(*c, Hq, T, Q, start, count, O, L, workspace, s);
+    } else {
+        const ext::Plan p = ext::plan(*c, Hq, T);
+        ext::Args a;
+        a.c = kv_view(*c);
+        a.Q = Q; a.O = O; a.L = L; a.start = start; a.count = count;
+        a.T = T; a.rows = G * T; a.tiles = p.tiles; a.splits = p.splits;
+        const bool whole = T % ext::kRows == 0;
+        a.order_heads = whole ? G : 0;
+        a.order_tiles = whole ? T / ext::kRows : 0;
+        a.sl2 = scale_log2(c->d);
+        a.part_O = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + p.off_ml);
+        const bool bf16 = c->dtype == SAGE_BF16;
+        if (c->d == 64) e = bf16 ? ext::launch<64, true>(*c, a, s) : ext::launch<64, false>(*c, a, s);
+        else e = bf16 ? ext::launch<128, true>(*c, a, s) : ext::launch<128, false>(*c, a, s);
+    }
+    return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+}
+
+}  // extern "C"

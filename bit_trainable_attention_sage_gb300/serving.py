@@ -1,5 +1,5 @@
 """Thin ctypes binding of the position and cache calls of libsage_gb300.so (include/sage.h):
-rotary positions, the paged key-value cache, attention of one new token over it, eviction.
+rotary positions, the paged key-value cache, attention of one or several new tokens over it, eviction.
 
 As in binding.py, every function has the name of the C entry point it wraps, checks and marshals
 its arguments, and takes outputs and workspaces from PyTorch; nothing is computed here.  Calls run
@@ -319,6 +319,41 @@ def sage_attn_decode(Q: torch.Tensor, cache: KvCache, lens: torch.Tensor, *, sco
     st = lib().sage_attn_decode(c, Hq, Q.data_ptr(), lens.data_ptr(), O.data_ptr(), L.data_ptr(), int(score), _ptr(ws),
                                 nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
     _check("sage_attn_decode", st)
+    return O, L
+
+
+def sage_attn_extend(Q: torch.Tensor, cache: KvCache, start: torch.Tensor, *, count=None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """Attention of T new tokens a sequence, Q (B,Hq,T,d), whose K and V sage_kv_append has written to slots
+    start[b] + t: token t sees the slots up to its own.  count[b] of them are there (None: all T); the
+    others' O is 0 and L -inf.  Hq is a multiple of the cache's heads, the cache of any kind.  A ``workspace``
+    of the caller's begins at a multiple of 256 bytes.  Returns (O (B,Hq,T,d) in Q's type, L (B,Hq,T) float32)."""
+    shape, dtype, dev = Q.shape, Q.dtype, cache.device
+    c = cache._struct(Q, "Q")
+    B, Hq, T, d = shape
+    _need(Q, "Q", dtype, (cache.B, Hq, T, cache.d), dev)
+    _need(start, "start", torch.int32, (cache.B,), dev)
+    if count is not None:
+        _need(count, "count", torch.int32, (cache.B,), dev)
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return sage_attn_extend(Q, cache, start, count=count, out=out, lse=lse, workspace=workspace)
+    nbytes = cache._bytes.get(("extend", Hq, T))
+    if nbytes is None:
+        if len(cache._bytes) >= 4096:
+            cache._bytes.clear()
+        nbytes = cache._bytes["extend", Hq, T] = lib().sage_extend_workspace_bytes(c, Hq, T)
+    if out is not None:
+        _need(out, "out", dtype, shape, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, Hq, T), dev)
+    _workspace_ok(workspace, dev)
+    O = torch.empty_like(Q) if out is None else out
+    L = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    ws = _workspace(nbytes, dev) if workspace is None else workspace
+    st = lib().sage_attn_extend(c, Hq, T, Q.data_ptr(), start.data_ptr(), _ptr(count), O.data_ptr(), L.data_ptr(), _ptr(ws),
+                                nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
+    _check("sage_attn_extend", st)
     return O, L
 
 

@@ -14,6 +14,7 @@
  *   sage_rope             rotary positions with several axes, and their gradient
  *   sage_kv_append        new tokens' K and V into a paged cache (16-bit, INT8 or E4M3)
  *   sage_attn_decode      attention of one new token a sequence over that cache
+ *   sage_attn_extend      the same of several new tokens a sequence: a prompt's chunk, a turn, drafts
  *   sage_kv_evict         eviction from the cache by accumulated attention weight
  *
  * Conventions shared by every entry point
@@ -455,6 +456,27 @@ SAGE_API size_t sage_decode_workspace_bytes(const sage_kv *c, int Hq, int add_sc
 SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int *lens, void *O,
                               float *L, int add_score, void *workspace, size_t workspace_bytes,
                               sage_stream_t stream);
+
+/* sage_attn_extend -- T new tokens a sequence over the cache, after sage_kv_append has written their
+ * K and V to slots start[b] + t: token t sees the slots k <= start[b] + t (what stands there, in
+ * whatever order), s_tk = q_t . K_k / sqrt(d), O_t = sum_k softmax(s_t)_k V_k, L_t = log sum_k exp
+ * s_tk.  count NULL: T tokens in every sequence; t >= count[b]: O = 0, L = -inf (Q may hold anything).
+ * In:  Q (B,Hq,T,d), Hq a multiple of H, B * Hq <= 2^24, B * Hq * T <= 2^28.
+ * Out: O (B,Hq,T,d), L (B,Hq,T) float32.
+ * What a token does not see does not reach it, whatever it holds.  A NaN in a visible K or its scale
+ * makes O and L NaN, an infinity or a NaN in a visible V the channels of O that it reaches infinite
+ * or NaN; in V's scale all of them.
+ * Sums and statistics are float32.  Up to 32 rows a kv head (Hq / H * T) the probabilities keep 16
+ * bits or more, as in sage_attn_decode.  Above that p sV enters the second product rounded to Q's
+ * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and
+ * nothing below 2^-36 of it; scales sV outside [2^-100, 2^100] (and not 0) lose bits there.
+ * Results do not depend on the order in which the GPU runs its blocks; their last bits do on the
+ * capacity, and up to 32 rows on the other sequences' lengths.  O and L may not overlap the inputs
+ * or the cache.  The workspace must be 256-byte aligned; where the query says 0 it may be anything. */
+SAGE_API size_t sage_extend_workspace_bytes(const sage_kv *c, int Hq, int T);
+SAGE_API int sage_attn_extend(const sage_kv *c, int Hq, int T, const void *Q, const int *start,
+                              const int *count, void *O, float *L, void *workspace,
+                              size_t workspace_bytes, sage_stream_t stream);
 
 /* sage_kv_evict -- cuts every sequence with lens[b] > budget to `budget` slots, each kv head for
  * itself.  First rank the slots with pos >= seen[b] - recent (seen[b]: the tokens of the text so
