@@ -54,7 +54,8 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecCluster = 8;               // CTAs of a cluster at most
 
-// pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3; BLOCK: one scale for 16 or more rows (8 bits)
+// pools: KIND 0 fp16, 1 bf16, 2 INT8, 3 E4M3; BLOCK: one scale for 16 or more rows (8 bits); ROWS: several new
+// tokens a sequence (instances of their own: what they need cost one token 1 to 2 %)
 template <int D, int KIND, int MR = 8>
 struct DecodeShape {
     static constexpr int ES = KIND < 2 ? 2 : 1;
@@ -262,9 +263,10 @@ __device__ __forceinline__ int new_tokens(const DecodeArgs &a, int b) {
     atomicOr(&g_decode_err, 1u);
     return n < 0 ? 0 : a.T;
 }
+template <bool ROWS>
 __device__ __forceinline__ int seq_len(const DecodeArgs &a, int b) {
     int n = kv_len(a.c, a.lens, b, &g_decode_err);
-    if (a.T) {
+    if constexpr (ROWS) {
         const int k = new_tokens(a, b);
         if (k == 0) return 0;
         n += k;
@@ -286,8 +288,9 @@ __device__ __forceinline__ int row_limit(const DecodeArgs &a, int b, int r, int 
 // costs besides its tiles (its first reads and its end take about as long as a tile): a run over
 // many short sequences then holds fewer tiles.
 constexpr int kPairUnits = 1;
+template <bool ROWS>
 __device__ __forceinline__ int pair_units(const DecodeArgs &a, int b) {
-    const int tiles = (seq_len(a, b) + a.tile - 1) >> a.tile_shift;
+    const int tiles = (seq_len<ROWS>(a, b) + a.tile - 1) >> a.tile_shift;
     return tiles > 0 ? tiles + kPairUnits : 0;
 }
 
@@ -298,7 +301,7 @@ struct WorkAt {
     long long total, u, first;
     int b;
 };
-template <int NT, typename F>
+template <int NT, bool ROWS, typename F>
 __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find) {
     __shared__ long long s_sum[NT / 32];
     __shared__ long long s_first;
@@ -308,7 +311,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     const int b0 = min(tid * per, a.c.B), b1 = min(b0 + per, a.c.B);
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += static_cast<long long>(pair_units(a, b)) * pairs;
+        mine += static_cast<long long>(pair_units<ROWS>(a, b)) * pairs;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -328,7 +331,7 @@ __device__ __forceinline__ WorkAt locate(const DecodeArgs &a, int pairs, F find)
     if (u >= at && u < at + mine) {
         int b = b0;
         for (;; ++b) {
-            const long long k = static_cast<long long>(pair_units(a, b)) * pairs;
+            const long long k = static_cast<long long>(pair_units<ROWS>(a, b)) * pairs;
             if (u < at + k) break;
             at += k;
         }
@@ -373,7 +376,7 @@ __device__ __forceinline__ float inv_of(float l) { return l == 0.0f ? 0.0f : 1.0
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
 // ---- main kernel ------------------------------------------------------------------------------
-template <int D, int KIND, int MR, bool ONE, bool BLOCK>
+template <int D, int KIND, int MR, bool ONE, bool BLOCK, bool ROWS>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = DecodeShape<D, KIND, MR>;
     constexpr bool BF16 = KIND == 1;                 // type of the product K q
@@ -387,13 +390,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
     __shared__ float s_part[2][MR], s_f[kDecCluster][MR];        // ONE: a CTA's M and l; factors of the cluster's
     __shared__ int s_not_finite;                                 // several tokens: a V was taken out of the products
-    (void)s_part; (void)s_f;
+    (void)s_part; (void)s_f; (void)s_not_finite;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int pairs = a.c.H * a.chunks;
     const int cta = blockIdx.x;
-    if (a.T) {
+    if constexpr (ROWS) {
         if (tid == 0) s_not_finite = 0;
         __syncthreads();
     }
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const size_t head = static_cast<size_t>(b) * a.Hq + h0;
         fetch(rank, a.c.table + static_cast<size_t>(b) * a.c.max_pages, static_cast<size_t>(a.c.max_pages) * 4,
               static_cast<const char *>(a.Q) + head * D * 2, rank == 0 ? outs * D * 2 : 0);
-        if (seq_len(a, b) == 0) {                                // the whole cluster alike
+        if (seq_len<ROWS>(a, b) == 0) {                                // the whole cluster alike
             for (int i = (rank * kDecThreads + tid) * 2; i < outs * D; i += a.cluster * kDecThreads * 2) {
                 store_out(a, head * D + i, 0.0f, 0.0f);
                 if (i % D == 0) a.L[head + i / D] = -INFINITY;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int grid = gridDim.x;
         for (long long e0 = cta; e0 < a.c.B; e0 += static_cast<long long>(grid) * kDecThreads) {
             const long long mine = e0 + static_cast<long long>(grid) * tid;
-            uint32_t none = __ballot_sync(0xffffffffu, mine < a.c.B && seq_len(a, static_cast<int>(min(mine, a.c.B - 1ll))) == 0);
+            uint32_t none = __ballot_sync(0xffffffffu, mine < a.c.B && seq_len<ROWS>(a, static_cast<int>(min(mine, a.c.B - 1ll))) == 0);
             for (; none; none &= none - 1) {
                 const size_t head = static_cast<size_t>(e0 + static_cast<long long>(grid) * (warp * 32 + __ffs(none) - 1)) * a.Hq;
                 for (int i = lane * 2; i < a.Hq * D; i += 64) {
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 }
             }
         }
-        const WorkAt w = locate<kDecThreads>(a, pairs, [&](long long total) {
+        const WorkAt w = locate<kDecThreads, ROWS>(a, pairs, [&](long long total) {
             const int n = runs_of(a, total);
             return cta < n ? run_start(total, cta, n) : total;
         });
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     auto find = [&]() {
         int pair;
         if constexpr (ONE) {
-            len = seq_len(a, b);
+            len = seq_len<ROWS>(a, b);
             tiles = (len + S::TILE - 1) / S::TILE;
             pair = cta / a.cluster - b * pairs;
             t0 = tiles * rank / a.cluster;           // tiles < 2^24
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         } else {
             for (;;) {
                 if (u >= u1) return false;
-                len = seq_len(a, b);
+                len = seq_len<ROWS>(a, b);
                 tiles = (len + S::TILE - 1) / S::TILE;
                 const int units = tiles > 0 ? tiles + kPairUnits : 0;
                 if (u - first >= static_cast<long long>(units) * pairs) {
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         heads = min(MR, a.G - ch * MR);
         // the last granules, where a slot may be hidden from a row: those with fewer than `edge` slots to the end
         edge = S::GRAN;
-        if (a.T) edge = new_tokens(a, b) < a.T ? 0x7FFFFFFF : S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
+        if constexpr (ROWS) edge = new_tokens(a, b) < a.T ? 0x7FFFFFFF : S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
         tok0 = t0 * S::TILE + warp * S::GRAN;
         ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
@@ -717,8 +720,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                         s[hf][nh][i] *= qs[nh][i & 1];
                     }
             }
-            const bool hidden = a.T && len - tok < edge;
-            if (hidden) {
+            const bool hidden = ROWS && len - tok < edge;
+            if (ROWS && hidden) {
                 // several tokens: each row ends at a slot of its own
                 int limit[NH][2];
 #pragma unroll
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             // (a hidden slot's scale may be anything)
-                            if (!hidden || s[hf][nh][i] != 0.0f) s[hf][nh][i] *= fv[hf][i >> 1];
+                            if (!ROWS || !hidden || s[hf][nh][i] != 0.0f) s[hf][nh][i] *= fv[hf][i >> 1];
                         }
             }
             bool moved = false;
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const size_t out0 = static_cast<size_t>(b) * a.Hq + head0;
         const int outs = heads;
         // (of this pair, for values that are not finite: its sequence, kv head, first row, and the slots of its tiles)
-        const int pb = b, pk = hk, prow = head0 - hk * a.G, plen = len, pfrom = max(t0 * S::TILE, edge >= len ? 0 : len - edge), pto = t1 * S::TILE;
+        [[maybe_unused]] const int pb = b, pk = hk, prow = head0 - hk * a.G, plen = len, pfrom = max(t0 * S::TILE, edge >= len ? 0 : len - edge), pto = t1 * S::TILE;
         bool more = false;
         if constexpr (!ONE) {
             more = find();
@@ -966,8 +969,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 o1 += f * from[p1];
                 sum += f * s_l[x][r];
             }
-            if constexpr (KIND != 2) {
-                if (a.T && s_not_finite) {
+            if constexpr (ROWS && KIND != 2) {
+                if (s_not_finite) {
                     const int to = min(row_limit(a, pb, prow + r, plen), pto);
                     for (int t = pfrom; t < to; ++t) {
                         const int p = kv_page(a.c, pb, t, &g_decode_err);
@@ -1103,7 +1106,7 @@ __device__ __forceinline__ float2 join_ml(const DecodeArgs &a, int c0, int c1, i
 // grid: (pairs, heads of a group) with at most as many pairs as runs, one head a block, its threads
 // over the parts; or (runs, 1), where the block of run c joins the pair that starts in run c and
 // goes on, if there is one: few parts, its threads over the heads.
-template <int D, int MR, bool PAIRS>
+template <int D, int MR, bool PAIRS, bool ROWS>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
     __shared__ float4 s_o[GROUPS][VEC];
@@ -1117,26 +1120,26 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         b = blockIdx.x / pairs;
         pair = blockIdx.x - b * pairs;
         long long lo = 0;                            // units of the sequences before
-        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units(a, i)) * pairs;
+        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units<ROWS>(a, i)) * pairs;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
         if (lane == 0) s_lo[warp] = lo;
-        const WorkAt w = locate<kJoinThreads>(a, pairs, [](long long total) { return total; });
+        const WorkAt w = locate<kJoinThreads, ROWS>(a, pairs, [](long long total) { return total; });
         lo = 0;
 #pragma unroll
         for (int x = 0; x < kJoinThreads / 32; ++x) lo += s_lo[x];
-        const int units = pair_units(a, b);
+        const int units = pair_units<ROWS>(a, b);
         if (units > 0)
             runs_of_pair(w.total, runs_of(a, w.total), lo + static_cast<long long>(pair) * units, units - kPairUnits, c0, c1);
     } else {
         const int c = blockIdx.x;
-        const WorkAt w = locate<kJoinThreads>(a, pairs, [&](long long total) {
+        const WorkAt w = locate<kJoinThreads, ROWS>(a, pairs, [&](long long total) {
             const int n = runs_of(a, total);
             return c + 1 < n ? run_start(total, c + 1, n) - 1 : total;
         });
         if (w.u < w.total) {
             b = w.b;
-            const int units = pair_units(a, b);
+            const int units = pair_units<ROWS>(a, b);
             pair = static_cast<int>(div_up_to(w.u - w.first, units));
             runs_of_pair(w.total, runs_of(a, w.total), w.first + static_cast<long long>(pair) * units, units - kPairUnits, c0, c1);
             if (c0 != c) c0 = c1;                    // another block's
@@ -1224,6 +1227,7 @@ constexpr int kScoreHeads = 64;              // heads whose M and 1 / l are held
 
 template <int D, int MR>
 __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr bool ROWS = false;
     constexpr int VEC = D / 4, GROUPS = kJoinThreads / VEC;
     __shared__ float4 s_o[GROUPS][VEC];
     __shared__ float s_M[kScoreHeads], s_inv[kScoreHeads];
@@ -1232,24 +1236,24 @@ __global__ void __launch_bounds__(kJoinThreads) decode_score_kernel(const __grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int v = tid % VEC, grp = tid / VEC;
     const int pairs = a.c.H * a.chunks;
-    const int len = seq_len(a, b);
+    const int len = seq_len<ROWS>(a, b);
     const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hk) * a.G;
     const bool idle = len == 0 || (y >= a.G && y * (kJoinThreads * 4) >= len);
     long long lo = 0;                                // units of the sequences before
     WorkAt w{};
     if (!idle) {
-        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units(a, i)) * pairs;
+        for (int i = tid; i < b; i += kJoinThreads) lo += static_cast<long long>(pair_units<ROWS>(a, i)) * pairs;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
         if (lane == 0) s_lo[warp] = lo;
-        w = locate<kJoinThreads>(a, pairs, [](long long total) { return total; });
+        w = locate<kJoinThreads, ROWS>(a, pairs, [](long long total) { return total; });
         lo = 0;
 #pragma unroll
         for (int x = 0; x < kJoinThreads / 32; ++x) lo += s_lo[x];
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");       // by every block, as above
     if (idle) return;
-    const int units = pair_units(a, b), runs = runs_of(a, w.total);
+    const int units = pair_units<ROWS>(a, b), runs = runs_of(a, w.total);
     for (int h0 = 0; h0 < a.G; h0 += kScoreHeads) {
         const int n = min(kScoreHeads, a.G - h0);
         for (int i = warp; i < n; i += kJoinThreads / 32) {
@@ -1378,12 +1382,12 @@ static int check_decode(const sage_kv *c, int Hq, int add_score) {
     return SAGE_OK;
 }
 
-template <int D, int KIND, int MR, bool BLOCK>
+template <int D, int KIND, int MR, bool BLOCK, bool ROWS>
 static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     using S = DecodeShape<D, KIND, MR>;
     static bool raised[2][16] = {{false}};
     if (a.cluster) {
-        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, true, BLOCK>), S::SMEM, raised[1]);
+        const cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, true, BLOCK, ROWS>), S::SMEM, raised[1]);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.ctas);
@@ -1397,11 +1401,11 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, MR, true, BLOCK>, a);
+        return cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, MR, true, BLOCK, ROWS>, a);
     }
-    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, false, BLOCK>), S::SMEM, raised[0]);
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(decode_kernel<D, KIND, MR, false, BLOCK, ROWS>), S::SMEM, raised[0]);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, KIND, MR, false, BLOCK><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
+    decode_kernel<D, KIND, MR, false, BLOCK, ROWS><<<a.ctas, kDecThreads, S::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1412,7 +1416,7 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (a.logits) {
+    if (!ROWS && a.logits) {
         const int y = (a.c.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads);
         cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.H, y < 1024 ? y : 1024);
         return cudaLaunchKernelEx(&cfg, decode_score_kernel<D, MR>, a);
@@ -1420,18 +1424,23 @@ static cudaError_t launch_decode_k(const DecodeArgs &a, cudaStream_t st) {
     const long long pairs = static_cast<long long>(a.c.B) * a.c.H * a.chunks;
     if (pairs <= a.ctas) {
         cfg.gridDim = dim3(static_cast<unsigned>(pairs), a.G < MR ? a.G : MR);
-        return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, true>, a);
+        return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, true, ROWS>, a);
     }
     cfg.gridDim = dim3(a.ctas);
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, false>, a);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, MR, false, ROWS>, a);
+}
+
+template <int D, int KIND, int MR, bool BLOCK>
+static cudaError_t launch_decode_t(const DecodeArgs &a, cudaStream_t st) {
+    return a.T ? launch_decode_k<D, KIND, MR, BLOCK, true>(a, st) : launch_decode_k<D, KIND, MR, BLOCK, false>(a, st);
 }
 
 template <int D, int KIND>
 static cudaError_t launch_decode_m(const DecodeArgs &a, int mr, cudaStream_t st) {
     if constexpr (KIND >= 2) {
-        if (a.c.block_shift) return mr == 8 ? launch_decode_k<D, KIND, 8, true>(a, st) : launch_decode_k<D, KIND, 16, true>(a, st);
+        if (a.c.block_shift) return mr == 8 ? launch_decode_t<D, KIND, 8, true>(a, st) : launch_decode_t<D, KIND, 16, true>(a, st);
     }
-    return mr == 8 ? launch_decode_k<D, KIND, 8, false>(a, st) : launch_decode_k<D, KIND, 16, false>(a, st);
+    return mr == 8 ? launch_decode_t<D, KIND, 8, false>(a, st) : launch_decode_t<D, KIND, 16, false>(a, st);
 }
 
 template <int KIND>

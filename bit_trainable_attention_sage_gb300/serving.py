@@ -199,7 +199,8 @@ class KvCache:
     blocks).  The tensors are fixed for the life of the object; their contents are the caller's and
     the calls'."""
 
-    def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None):
+    def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None, refs=None,
+                 held=None):
         if K.dtype not in _KINDS or K.dim() != 4 or table.dim() != 2:
             raise ValueError("K must be (pages,H,page,d) in fp16, bf16, int8 or float8_e4m3fn, table (B,max_pages)")
         pages, H, page, d = K.shape
@@ -224,7 +225,13 @@ class KvCache:
         for name, t, dt in (("score", score, torch.float32), ("pos", pos, torch.int32)):
             if t is not None:
                 _need(t, name, dt, (B, H, self.capacity), dev)
+        if (refs is None) != (held is None):
+            raise ValueError("refs and held belong together")
+        if refs is not None:
+            _need(refs, "refs", torch.int32, (pages,), dev)
+            _need(held, "held", torch.int32, (B,), dev)
         self.K, self.V, self.sK, self.sV, self.table, self.score, self.pos = K, V, sK, sV, table, score, pos
+        self.refs, self.held = refs, held
         self.B, self.H, self.d, self.page, self.pages, self.device = B, H, d, page, pages, dev
         # a struct for each 16-bit type that calls may bring
         types = (K.dtype,) if self.kind == SAGE_KV_16 else (torch.float16, torch.bfloat16)
