@@ -29,7 +29,8 @@ EXPORTED = (
     "sage_device_status", "sage_status_string", "sage_version", "sage_quantize_smooth_qknorm",
     "sage_qknorm_bwd", "sage_quantize_fp4", "sage_attn_fwd_fp4", "sage_rope", "sage_kv_append",
     "sage_decode_workspace_bytes", "sage_attn_decode", "sage_evict_workspace_bytes", "sage_kv_evict",
-    "sage_extend_workspace_bytes", "sage_attn_extend",
+    "sage_extend_workspace_bytes", "sage_attn_extend", "sage_pages_workspace_bytes", "sage_kv_resize",
+    "sage_kv_fork", "sage_kv_compact",
 )
 
 
@@ -126,6 +127,14 @@ def lib() -> ctypes.CDLL:
     L.sage_extend_workspace_bytes.restype = sz
     L.sage_attn_extend.argtypes = [vp, ci, ci] + [vp] * 6 + [sz, vp]
     L.sage_attn_extend.restype = ci
+    L.sage_pages_workspace_bytes.argtypes = [vp]
+    L.sage_pages_workspace_bytes.restype = sz
+    L.sage_kv_resize.argtypes = [vp] * 6 + [sz, vp]
+    L.sage_kv_resize.restype = ci
+    L.sage_kv_fork.argtypes = [vp] * 7 + [sz, vp]
+    L.sage_kv_fork.restype = ci
+    L.sage_kv_compact.argtypes = [vp] * 5 + [sz, vp]
+    L.sage_kv_compact.restype = ci
     _lib = L
     return L
 
@@ -464,7 +473,8 @@ def sage_dump_bytes(B, H, N, d, which: int) -> int:
 
 
 def sage_device_status(stream=None) -> int:
-    """Waits for the stream; SAGE_OK or SAGE_ERR_TIMEOUT (a bounded device wait expired)."""
+    """Waits for the stream; SAGE_OK, SAGE_ERR_TIMEOUT (a bounded device wait expired), SAGE_ERR_INDEX (a cache call
+    met a page, length or slot out of range) or SAGE_ERR_PAGES (a pool had no free page left)."""
     return lib().sage_device_status(_stream(stream))
 
 

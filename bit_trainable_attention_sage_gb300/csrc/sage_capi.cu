@@ -8,6 +8,7 @@
 #include "sage_internal.h"
 #include "sage_kv.cuh"
 #include "sage_decode.h"
+#include "sage_pages.h"
 
 namespace sage {
 
@@ -560,10 +561,11 @@ int sage_device_status(sage_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SAGE_ERR_CUDA;
     const unsigned int e = take_fwd_error() | take_bwd_error() | take_quant_error() | take_extend_error();
-    // beside a timeout the index error stays for the next call
-    const unsigned int index = e ? 0u : take_kv_error() | take_decode_error() | take_extend_index();
+    // beside a timeout the index error stays for the next call, beside either the pool without a free page
+    const unsigned int index = e ? 0u : take_kv_error() | take_decode_error() | take_extend_index() | take_pages_error(1u);
+    const unsigned int full = e || index ? 0u : take_pages_error(2u);
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
-    return e ? SAGE_ERR_TIMEOUT : index ? SAGE_ERR_INDEX : SAGE_OK;
+    return e ? SAGE_ERR_TIMEOUT : index ? SAGE_ERR_INDEX : full ? SAGE_ERR_PAGES : SAGE_OK;
 }
 
 const char *sage_status_string(int status) {
@@ -576,6 +578,7 @@ const char *sage_status_string(int status) {
         case SAGE_ERR_TIMEOUT: return "device-side bounded wait expired";
         case SAGE_ERR_WORKSPACE: return "workspace missing or too small";
         case SAGE_ERR_INDEX: return "cache page, length or slot out of range";
+        case SAGE_ERR_PAGES: return "the cache's pool has no free page left";
         default: return "unknown status";
     }
 }

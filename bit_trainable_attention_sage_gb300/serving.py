@@ -1,5 +1,6 @@
 """Thin ctypes binding of the position and cache calls of libsage_gb300.so (include/sage.h):
-rotary positions, the paged key-value cache, attention of one or several new tokens over it, eviction.
+rotary positions, the paged key-value cache, attention of one or several new tokens over it, eviction,
+and the pages of a pool that sequences share.
 
 As in binding.py, every function has the name of the C entry point it wraps, checks and marshals
 its arguments, and takes outputs and workspaces from PyTorch; nothing is computed here.  Calls run
@@ -196,7 +197,9 @@ class KvCache:
     rows; page a multiple of 16, B * H at most 65535.  table (B,max_pages) int32: the pages of each
     sequence; entries behind its last page are not read.  score (B,H,max_pages*page) float32 and
     pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict (not with scales of
-    blocks).  The tensors are fixed for the life of the object; their contents are the caller's and
+    blocks).  refs (pages) and held (B) int32, both or none, are there for a pool that sequences share
+    (sage_kv_resize, sage_kv_fork, sage_kv_compact): how many table entries name each page, and how many of each
+    row's entries are its pages; these calls write them and table.  The tensors are fixed for the life of the object; their contents are the caller's and
     the calls'."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None, refs=None,
@@ -248,24 +251,29 @@ class KvCache:
 
 
 def make_kv_cache(B: int, H: int, d: int, capacity: int, *, dtype=torch.int8, page: int = 64, score: bool = False,
-                  block: int = 0, device="cuda") -> KvCache:
+                  block: int = 0, pages: int | None = None, device="cuda") -> KvCache:
     """A cache for B sequences of up to ``capacity`` tokens, each with pages of its own; ``score``
     adds what eviction needs.  dtype: fp16, bf16, int8 or float8_e4m3fn.  ``block`` (8-bit types): one
-    scale for each block of 16, 32 or 64 rows instead of one a row."""
+    scale for each block of 16, 32 or 64 rows instead of one a row.  ``pages``: a pool of so many pages that the
+    sequences share, all free; sage_kv_resize gives them out."""
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     m = max(1, -(-capacity // max(page, 1)))
-    _kv_sizes(B, H, d, page, B * m, m, block)
+    shared = pages is not None
+    pages = B * m if pages is None else pages
+    _kv_sizes(B, H, d, page, pages, m, block)
     eight = dtype in (torch.int8, torch.float8_e4m3fn)
     if block and (score or not eight):
         raise ValueError("block belongs to int8 and float8_e4m3fn caches without score")
-    table = torch.arange(B * m, dtype=torch.int32, device=device).view(B, m)
-    shape = (B * m, H, page, d)
+    ints = lambda n, v: torch.full((n,), v, dtype=torch.int32, device=device)  # noqa: E731
+    table = ints(B * m, -1).view(B, m) if shared else torch.arange(B * m, dtype=torch.int32, device=device).view(B, m)
+    shape = (pages, H, page, d)
     K, V = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
-    sK, sV = (torch.zeros((B * m, H, page // (block or 1)), device=device) if eight else None for _ in range(2))
+    sK, sV = (torch.zeros((pages, H, page // (block or 1)), device=device) if eight else None for _ in range(2))
     extra = [torch.zeros((B, H, m * page), dtype=t, device=device) if score else None for t in (torch.float32, torch.int32)]
-    return KvCache(K, V, table, sK=sK, sV=sV, score=extra[0], pos=extra[1])
+    return KvCache(K, V, table, sK=sK, sV=sV, score=extra[0], pos=extra[1], refs=ints(pages, 0) if shared else None,
+                   held=ints(B, 0) if shared else None)
 
 
 def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor, *, count=None, mu=None,
@@ -396,3 +404,54 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
                              nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
     _check("sage_kv_evict", st)
     return new
+
+
+# ---- pages of a pool that sequences share ---------------------------------------------------
+
+
+def _pages_call(name, cache: KvCache, ins, out, size, workspace, stream):
+    """sage_kv_resize, sage_kv_fork or sage_kv_compact: int32 inputs by name, an int32 output of ``size``."""
+    dev = cache.device
+    if cache.refs is None:
+        raise ValueError(f"{name} needs a cache with refs and held (make_kv_cache(..., pages=))")
+    for what, t in ins:
+        _need(t, what, torch.int32, (cache.B,), dev)
+    if out is not None:
+        _need(out, "out", torch.int32, (size,), dev)
+    _workspace_ok(workspace, dev)
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return _pages_call(name, cache, ins, out, size, workspace, None)
+    c = next(iter(cache._c.values()))
+    nbytes = cache._bytes.get("pages")
+    if nbytes is None:
+        nbytes = cache._bytes["pages"] = lib().sage_pages_workspace_bytes(c)
+    new = torch.empty(size, dtype=torch.int32, device=dev) if out is None else out
+    ws = _workspace(nbytes, dev) if workspace is None else workspace
+    st = getattr(lib(), name)(c, cache.refs.data_ptr(), cache.held.data_ptr(), *[t.data_ptr() for _, t in ins], new.data_ptr(), ws.data_ptr(),
+                              nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
+    _check(name, st)
+    return new
+
+
+def sage_kv_resize(cache: KvCache, want: torch.Tensor, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Gives each sequence pages for ``want`` (B) int32 slots, or takes back those behind them (0: the sequence
+    ends); pages are free again when no row names them.  Returns the slots that each now holds (B) int32, fewer than
+    wanted where the pool has no free page left (sage_device_status() then says SAGE_ERR_PAGES)."""
+    return _pages_call("sage_kv_resize", cache, (("want", want),), out, cache.B, workspace, stream)
+
+
+def sage_kv_fork(cache: KvCache, parent: torch.Tensor, lens: torch.Tensor, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Sequence b goes on as a copy of sequence ``parent[b]``, as all were before, of lens[parent[b]] slots (-1: it
+    ends).  Full pages are shared, the rows of the page in use copied to a page of its own; pages of no
+    sequence are free again.  Returns the new lengths (B) int32.  Sequences that then grow need
+    sage_kv_resize first.  Not for caches with score or pos."""
+    if cache.score is not None or cache.pos is not None:
+        raise ValueError("sage_kv_fork: a cache with score or pos is evicted from, its pages cannot be shared")
+    return _pages_call("sage_kv_fork", cache, (("parent", parent), ("lens", lens)), out, cache.B, workspace, stream)
+
+
+def sage_kv_compact(cache: KvCache, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Moves the pages in use to the pool's front and lets all rows follow.  Returns their number (1) int32: the
+    pool is free from there on."""
+    return _pages_call("sage_kv_compact", cache, (), out, 1, workspace, stream)

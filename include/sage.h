@@ -16,6 +16,8 @@
  *   sage_attn_decode      attention of one new token a sequence over that cache
  *   sage_attn_extend      the same of several new tokens a sequence: a prompt's chunk, a turn, drafts
  *   sage_kv_evict         eviction from the cache by accumulated attention weight
+ *   sage_kv_resize, sage_kv_fork, sage_kv_compact
+ *                         a pool's pages given to and taken from sequences, shared, moved to its front
  *
  * Conventions shared by every entry point
  *   - Tensors are contiguous, row-major (B, H, N, d): token n of head (b, h) starts at element
@@ -56,6 +58,8 @@ extern "C" {
 #define SAGE_ERR_WORKSPACE 6    /* workspace missing or smaller than the query says            */
 #define SAGE_ERR_INDEX 7        /* a page, length or slot read on the device was out of range
                                    (cache calls; see sage_device_status)                       */
+#define SAGE_ERR_PAGES 8        /* a call found no free page left in the cache's pool (see
+                                   sage_device_status)                                         */
 
 /* Element types of the 16-bit tensors (Q, K, V, dO, O). */
 #define SAGE_FP16 0
@@ -492,13 +496,53 @@ SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, i
                            int *lens_out, void *workspace, size_t workspace_bytes,
                            sage_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------ *
+ * The pages of a pool that sequences share.
+ *
+ * refs (pages) int32 counts the table entries that name each page, 0: the page is free.  held (B)
+ * int32: so many entries of a sequence's table row are its pages (entries behind them are -1 once
+ * these calls have written them).  An empty pool is refs = 0, held = 0.  The calls below keep both and WRITE
+ * c->table; a program that gives pages itself counts them in the same way.
+ * Free pages are given in ascending order, to sequences in ascending order: results depend on the
+ * inputs alone.  refs, held and all int32 inputs need 4-byte alignment; out may not overlap an input.
+ * An input out of range is held to it, or a parent out of range read as the sequence itself, and an
+ * entry that is no page left alone: SAGE_ERR_INDEX (from sage_kv_compact where pages move).  A pool without a free page: SAGE_ERR_PAGES.
+ * Workspace: sage_pages_workspace_bytes(c), 16-byte aligned.  No call allocates, and all can be captured.
+ * What writes a page writes it for every sequence that shares it: sage_kv_append goes behind the
+ * shared ones where lengths come from sage_kv_fork, eviction is not for shared pages.
+ *
+ * sage_kv_resize -- every sequence gets or gives back pages at its row's end, until it holds those of
+ *   want[b] slots (0: it ends).  Pages that are given back are free again where nobody else names
+ *   them, and can be given in the same call.  Where the pool has too few, the later sequences get
+ *   fewer.  slots (B): slots that each now holds, pages * page.
+ *
+ * sage_kv_fork -- sequence b goes on as a copy of sequence parent[b] (as all were before the call), of
+ *   lens[parent[b]] slots; -1: it ends, and holds nothing.  Full pages are shared.  Of those that go on from one
+ *   sequence, it itself or else the lowest keeps its other pages (the one in use and any behind);
+ *   each of the rest gets a page of its own for the rows of the one in use, copied with their scales.  Pages of
+ *   nobody are free again, for these copies too.  lens_out (B): the new lengths (without a
+ *   page for its copy a sequence ends at its last full page).  Not with score or pos: SAGE_ERR_UNSUPPORTED.
+ *
+ * sage_kv_compact -- used (1): how many pages have refs > 0.  Those at used and behind it move, in
+ *   ascending order, to the free pages below it, with K, V, scales and counts, and all rows follow: the pool's
+ *   rest is free from page `used` on.  Free pages keep what they hold.
+ * ------------------------------------------------------------------------------------------ */
+SAGE_API size_t sage_pages_workspace_bytes(const sage_kv *c);
+SAGE_API int sage_kv_resize(const sage_kv *c, int *refs, int *held, const int *want, int *slots,
+                            void *workspace, size_t workspace_bytes, sage_stream_t stream);
+SAGE_API int sage_kv_fork(const sage_kv *c, int *refs, int *held, const int *parent, const int *lens,
+                          int *lens_out, void *workspace, size_t workspace_bytes, sage_stream_t stream);
+SAGE_API int sage_kv_compact(const sage_kv *c, int *refs, const int *held, int *used, void *workspace,
+                             size_t workspace_bytes, sage_stream_t stream);
+
 /* Bytes the SAGE_FLAG_DUMP buffer needs for a forward (which = 0) or backward (which = 1). */
 SAGE_API size_t sage_dump_bytes(const sage_params *p, int which);
 
 /* Waits for `stream`, then reads and clears the device-side error word of the current device:
  * SAGE_OK, SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call, or else
  * SAGE_ERR_INDEX if a cache call met a page, length or slot out of range (beside a timeout this one
- * is kept and returned by the next call). */
+ * is kept and returned by the next call), or else SAGE_ERR_PAGES if one found no free page left (kept
+ * beside either). */
 SAGE_API int sage_device_status(sage_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
