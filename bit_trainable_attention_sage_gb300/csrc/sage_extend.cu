@@ -132,6 +132,9 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -332,15 +335,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         constexpr int ROW = SC ? D : 2 * D;                          // bytes of a row
         constexpr int CPR = ROW / 16, RPI = 128 / CPR, ITS = 128 / RPI;   // 16-byte chunks a row, rows at a time
         const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
+        // Pages are asked for two steps ahead, by lane g of every warp (mod 8) for its step's group g of 16 slots,
+        // and become the group's first row of the pool, -1 where it has no page, a step ahead.
         const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
-        // the pool's row of a slot, -1 where it has no page
-        auto row_of = [&](int slot) -> long long {
-            const int p = __ldg(table + kv_page_of(a.c, slot));
-            if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.c.pages)) {
-                atomicOr(&g_ext_index, 1u);
-                return -1;
+        int page = 0;
+        long long base = -1;
+        bool plain = false;
+        auto look = [&](int j) {
+            const int slot = j * kStep + (lane & 7) * 16;
+            page = slot < kv_end ? __ldg(table + kv_page_of(a.c, slot)) : 0;
+        };
+        auto find = [&](int j) {
+            const int slot = j * kStep + (lane & 7) * 16;
+            base = -1;
+            if (slot < kv_end) {
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) base = static_cast<long long>(kv_row(a.c, page, hk, slot));
+                else atomicOr(&g_ext_index, 1u);
             }
-            return static_cast<long long>(kv_row(a.c, p, hk, slot));
+            // every group has its page and all of its slots
+            plain = (j + 1) * kStep <= kv_end && __all_sync(0xffffffffu, base >= 0);
+        };
+        // row r of the step: its row of the pool (whole warps call it)
+        auto row_of = [&](int r) -> long long {
+            const long long first = __shfl_sync(0xffffffffu, base, r >> 4);
+            return first < 0 ? -1 : first + (r & 15);
         };
         auto done = [&](uint64_t *bar) {                             // this warp's part is stored
             fence_view_async_shared();
@@ -352,16 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         bool hole = false;
         auto load_scales = [&](int j) {
             // a thread a slot (SC = 1), or threads 0 .. 7 a group of 16 each; of a 16-bit pool the holes alone
-            const int slot = j * kStep + (SC == 1 ? tid : tid * 16);
+            const int slot = j * kStep + (SC == 1 ? tid : (lane & 7) * 16);
+            const long long r = SC == 1 ? row_of(tid) : base;
             sk = sv = 0.0f;
-            hole = false;
-            if ((SC == 1 || tid < 8) && slot < kv_end) {
-                const long long r = row_of(slot);
-                hole = r < 0;
-                if (SC && r >= 0) {
-                    sk = __ldg(a.c.sK + (r >> a.c.block_shift));
-                    sv = __ldg(a.c.sV + (r >> a.c.block_shift));
-                }
+            hole = slot < kv_end && r < 0 && (SC == 1 || lane < 8);
+            if (SC != 0 && r >= 0 && slot < kv_end && (SC == 1 || tid < 8)) {
+                sk = __ldg(a.c.sK + (r >> a.c.block_shift));
+                sv = __ldg(a.c.sV + (r >> a.c.block_shift));
             }
         };
         auto store_scales = [&](int i) {
@@ -406,13 +421,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         if constexpr (SC != 0) {
             uint4 kr[ITS], vr[ITS];
             auto load = [&](const void *pool, int j, uint4 (&to)[ITS]) {
+                long long row[ITS];
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) {
-                    const int slot = j * kStep + rr + i * RPI;
-                    to[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (slot < kv_end) {
-                        const long long r = row_of(slot);
-                        if (r >= 0) to[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) + r * ROW) + cc);
+                for (int i = 0; i < ITS; ++i) row[i] = row_of(rr + i * RPI);
+                const uint4 *from = static_cast<const uint4 *>(pool) + cc;
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) to[i] = __ldg(from + row[i] * CPR);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        to[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row[i] >= 0 && j * kStep + rr + i * RPI < kv_end) to[i] = __ldg(from + row[i] * CPR);
                     }
                 }
             };
@@ -432,6 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     sts128(to + chunk_at(r, 2 * cc + 1 - flip), flip ? lo : hi);
                 }
             };
+            look(j0);
+            find(j0);
+            look(j0 + 1);
             load_scales(j0);
             load(a.c.K, j0, kr);
             load(a.c.V, j0, vr);
@@ -443,6 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 store_scales(i);
                 done(&s.k_full[st]);
                 if (j + 1 < j1) {
+                    find(j + 1);
+                    look(j + 2);
                     load_scales(j + 1);
                     load(a.c.K, j + 1, kr);
                 }
@@ -469,16 +494,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             }
         } else {
             auto load = [&](const void *pool, uint32_t to, int j) {
+                // this thread has ITS / 8 rows of each of the 8 groups
+                const uint8_t *from[8];
+                bool there[8];
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) {
-                    const int r = rr + i * RPI, slot = j * kStep + r;
-                    long long row = -1;
-                    if (slot < kv_end) row = row_of(slot);
-                    const uint8_t *from = static_cast<const uint8_t *>(pool) + (row < 0 ? 0 : row * ROW + cc * 16);
-                    cp_async16(to + chunk_at(r, cc), from, row >= 0);
+                for (int g = 0; g < 8; ++g) {
+                    const long long row = row_of(16 * g + rr);
+                    there[g] = row >= 0;
+                    from[g] = static_cast<const uint8_t *>(pool) + (row < 0 ? 0 : row * ROW + cc * 16);
+                }
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) cp_async16(to + chunk_at(rr + i * RPI, cc), from[i * RPI / 16] + i * RPI % 16 * ROW);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        const bool is = there[i * RPI / 16] && j * kStep + rr + i * RPI < kv_end;
+                        cp_async16(to + chunk_at(rr + i * RPI, cc), is ? from[i * RPI / 16] + i * RPI % 16 * ROW : static_cast<const uint8_t *>(pool), is);
+                    }
                 }
                 cp_commit();
             };
+            look(j0);
+            find(j0);
+            look(j0 + 1);
             load(a.c.K, smem_u32(s.k[0][0]), j0);
             load(a.c.V, smem_u32(s.v[0][0]), j0);
             load_scales(j0);
@@ -488,6 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 store_scales(i);
                 if (j + 1 < j1) {
                     if (!free_of(s.k_free, i + 1)) break;
+                    find(j + 1);
+                    look(j + 2);
                     load(a.c.K, smem_u32(s.k[st ^ 1][0]), j + 1);
                     load_scales(j + 1);
                     cp_wait<2>();
@@ -541,8 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             const uint32_t holes = s.holes[at];
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
-            // ---- the step's largest x = acc kc + lv.  `scaled`: raw holds x itself afterwards
-            const bool scaled = SC == 1 || !whole;
+            // ---- the step's largest x = acc kc + lv (which raw holds afterwards, where some are hidden or SC = 1)
             float mx = -INFINITY;
             if (SC != 1 && whole) {
 #pragma unroll
@@ -600,37 +640,45 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 }
             }
             const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
-            // ---- p' = 2^(x - ref), to TMEM over S, and l
+            // ---- p' = 2^(x - ref), to TMEM over S, and l.  SCALED: raw holds x; else the products
+            auto probabilities = [&](auto scaled, auto hidden) {
+                constexpr bool SCALED = decltype(scaled)::value;
+                [[maybe_unused]] constexpr bool HIDDEN = decltype(hidden)::value;
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                uint32_t pk[8];
-                f2 sum{0.0f, 0.0f};
-                f2 f{1.0f, 1.0f}, off{-ref, -ref};
-                if (SC == 0 && !scaled) f = f2{a.sl2, a.sl2};
-                if (SC == 2 && !scaled) {
-                    f.x = f.y = s.kc[at][g];
-                    off.x = off.y = s.lv[at][g] - ref;
-                }
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const f2 r2{__uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1])};
-                    const f2 x2 = scaled ? add2(r2, off) : fma2(r2, f, off);
-                    const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
-                    if constexpr (SC == 1) {
-                        const f2 rv{s.rv[at][16 * g + k], s.rv[at][16 * g + k + 1]};
-                        // (a hidden slot's reciprocal may be anything)
-                        sum.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
-                        sum.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
-                    } else {
-                        sum = add2(sum, p);
+                for (int g = 0; g < 8; ++g) {
+                    uint32_t pk[8];
+                    f2 sum{0.0f, 0.0f};
+                    f2 f{a.sl2, a.sl2}, off{-ref, -ref};
+                    if constexpr (SC == 2 && !SCALED) {
+                        f.x = f.y = s.kc[at][g];
+                        off.x = off.y = s.lv[at][g] - ref;
                     }
-                    pk[k / 2] = pack2<BF16>(p.x, p.y);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const f2 r2{__uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1])};
+                        const f2 x2 = SCALED ? add2(r2, off) : fma2(r2, f, off);
+                        const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
+                        if constexpr (SC == 1) {
+                            const f2 rv{s.rv[at][16 * g + k], s.rv[at][16 * g + k + 1]};
+                            if constexpr (HIDDEN) {                  // (a hidden slot's reciprocal may be anything)
+                                sum.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
+                                sum.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
+                            } else {
+                                sum = fma2(p, rv, sum);
+                            }
+                        } else {
+                            sum = add2(sum, p);
+                        }
+                        pk[k / 2] = pack2<BF16>(p.x, p.y);
+                    }
+                    const float add = sum.x + sum.y;
+                    if constexpr (SC == 2) l += HIDDEN && add == 0.0f ? 0.0f : add * s.rv[at][g];
+                    else l += add;
+                    tmem_st8(lane_base + 8 * g, pk);
                 }
-                const float add = sum.x + sum.y;
-                if constexpr (SC == 2) l += add == 0.0f ? 0.0f : add * s.rv[at][g];
-                else l += add;
-                tmem_st8(lane_base + 8 * g, pk);
-            }
+            };
+            if (whole) probabilities(std::integral_constant<bool, SC == 1>(), std::false_type());
+            else probabilities(std::true_type(), std::true_type());
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
