@@ -24,9 +24,11 @@
 // block that is one factor for 16 or more columns, and the maximum of a group's products is scaled once.  V's
 // scale goes into the exponent: p' = 2^(x + log2 sV - m), m the running maximum of x + log2 sV, feeds the
 // second product and keeps its largest value near 1 whatever the scales are; l sums p' / sV.
-// Roundings: p' is rounded to Q's type, bf16 (8 bits) or fp16 (11 bits, under 2^11 of the running maximum's, so that
-// they are all there down to 2^-25 of it and gone below 2^-36): half a step of the output's own type each,
-// and they average over the slots.  Sums, statistics and O are float32.
+// Roundings: p' is rounded to Q's type, bf16 (8 bits) or fp16 (11 bits, the running maximum's at 2^11, so that
+// they are all there down to 2^-25 of it and gone below 2^-36, which shows only in outputs that fp16 cannot hold
+// either): half a step of the output's own type each, and they average over the slots.  K's codes meet Q in fp16
+// (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.  Sums, statistics
+// and O are float32.
 //
 // Few CTAs are given more to do by cutting the slots into up to kExtMaxSplits ranges; a second kernel joins
 // their O, m and l in order, so results do not depend on the order in which CTAs run.
@@ -74,6 +76,7 @@ struct Smem {
     // of step j in place j & 3 (a place is written again when the step before the last has been read):
     // factor of the products, log2 of V's scale and its reciprocal, a slot or a group of 16 slots each
     alignas(16) float kc[4][128], lv[4][128], rv[4][128];
+    float qs[256];                                   // the rows' factors of Q (8-bit pools, Q in bf16)
     uint32_t holes[4];                               // groups of 16 slots whose page is none
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
     uint64_t s_full[2], p_full[2], o_full[2];
@@ -83,8 +86,9 @@ struct Smem {
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
-// Four codes as two pairs of the operand type: INT8 by the difference of two integers under one exponent,
-// E4M3 by the conversion instruction.  All exact.
+// Four codes as two pairs of fp16 (K) or of Q's type (V).  All exact.
+//   fp16: INT8: byte ^ 0x80 under 0x64 is 1024 + 128 + code, less 1152 the code; E4M3 by the conversion instruction.
+//   bf16: INT8: the low seven bits under 0x43 are 128 + them, the sign under 0x43 128 or 256; E4M3 through float32.
 template <bool BF16, bool FP8>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (FP8) {
@@ -97,12 +101,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
             hi = *reinterpret_cast<const uint32_t *>(&y);
         }
     } else if constexpr (BF16) {
-        // the low seven bits under 0x43 are 128 + them in bf16, the sign under 0x43 128 or 256
         const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
     } else {
-        // byte ^ 0x80 under 0x64 is 1024 + 128 + code in fp16
         const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, 0x64646464u, 0x4140)), "r"(k));
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, 0x64646464u, 0x4342)), "r"(k));
@@ -150,6 +152,24 @@ __device__ __forceinline__ uint4 lds128u(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+
+// 16 codes of each of N rows (r, r + STEP, ..), chunk c of 16 of them, to chunks 2 c and 2 c + 1 of the operand;
+// lanes of the second 64 channels store theirs the other way round, so that a row's eight stores meet eight
+// different 16-byte bank groups.
+template <bool BF16, bool FP8, int N, int STEP>
+__device__ __forceinline__ void store_codes(uint32_t to, const uint4 (&from)[N], int r, int c) {
+    const int flip = c >> 2 & 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint4 lo, hi;
+        widen4<BF16, FP8>(from[i].x, lo.x, lo.y);
+        widen4<BF16, FP8>(from[i].y, lo.z, lo.w);
+        widen4<BF16, FP8>(from[i].z, hi.x, hi.y);
+        widen4<BF16, FP8>(from[i].w, hi.z, hi.w);
+        sts128(to + chunk_at(r + i * STEP, 2 * c + flip), flip ? hi : lo);
+        sts128(to + chunk_at(r + i * STEP, 2 * c + 1 - flip), flip ? lo : hi);
+    }
 }
 
 // What a sequence brings: its first new slot, its new tokens and its slots in all, held to what exists.
@@ -276,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         regs_dec<kRegsControl>();
         if (warp == kMmaWarp && elect_one()) {
             // ------------------------------------------------------------------ MMA issuer
-            constexpr uint32_t idS = idesc_f16(128, 128, BF16, false, false);
+            constexpr uint32_t idS = idesc_f16(128, 128, BF16 && SC == 0, false, false);
             constexpr uint32_t idPV = idesc_f16(128, D, BF16, false, true);
             auto issue_s = [&](const int t, int st) {
                 const uint32_t q_addr = smem_u32(s.q[t][0]), k_addr = smem_u32(s.k[st][0]);
@@ -336,10 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         constexpr int CPR = ROW / 16, RPI = 128 / CPR, ITS = 128 / RPI;   // 16-byte chunks a row, rows at a time
         const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
         // Pages are asked for two steps ahead, by lane g of every warp (mod 8) for its step's group g of 16 slots,
-        // and become the group's first row of the pool, -1 where it has no page, a step ahead.
+        // and become the group's first row of the pool, kNone where it has no page, a step ahead.
+        constexpr uint32_t kNone = 0xFFFFFFFFu;
         const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
         int page = 0;
-        long long base = -1;
+        uint32_t base = kNone;                                       // (a pool in memory has fewer than 2^32 - 1 rows)
         bool plain = false;
         auto look = [&](int j) {
             const int slot = j * kStep + (lane & 7) * 16;
@@ -347,18 +368,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         };
         auto find = [&](int j) {
             const int slot = j * kStep + (lane & 7) * 16;
-            base = -1;
+            base = kNone;
             if (slot < kv_end) {
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) base = static_cast<long long>(kv_row(a.c, page, hk, slot));
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) base = static_cast<uint32_t>(kv_row(a.c, page, hk, slot));
                 else atomicOr(&g_ext_index, 1u);
             }
             // every group has its page and all of its slots
-            plain = (j + 1) * kStep <= kv_end && __all_sync(0xffffffffu, base >= 0);
+            plain = (j + 1) * kStep <= kv_end && __all_sync(0xffffffffu, base != kNone);
         };
         // row r of the step: its row of the pool (whole warps call it)
-        auto row_of = [&](int r) -> long long {
-            const long long first = __shfl_sync(0xffffffffu, base, r >> 4);
-            return first < 0 ? -1 : first + (r & 15);
+        auto row_of = [&](int r) -> uint32_t {
+            const uint32_t first = __shfl_sync(0xffffffffu, base, r >> 4);
+            return first == kNone ? kNone : first + (r & 15);
         };
         auto done = [&](uint64_t *bar) {                             // this warp's part is stored
             fence_view_async_shared();
@@ -371,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         auto load_scales = [&](int j) {
             // a thread a slot (SC = 1), or threads 0 .. 7 a group of 16 each; of a 16-bit pool the holes alone
             const int slot = j * kStep + (SC == 1 ? tid : (lane & 7) * 16);
-            const long long r = SC == 1 ? row_of(tid) : base;
+            const uint32_t r = SC == 1 ? row_of(tid) : base;
             sk = sv = 0.0f;
-            hole = slot < kv_end && r < 0 && (SC == 1 || lane < 8);
-            if (SC != 0 && r >= 0 && slot < kv_end && (SC == 1 || tid < 8)) {
+            hole = slot < kv_end && r == kNone && (SC == 1 || lane < 8);
+            if (SC != 0 && r != kNone && slot < kv_end && (SC == 1 || tid < 8)) {
                 sk = __ldg(a.c.sK + (r >> a.c.block_shift));
                 sv = __ldg(a.c.sV + (r >> a.c.block_shift));
             }
@@ -409,7 +430,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll 8
                 for (int r = tid / QC; r < 128; r += QR) {
                     const int row = r0 + 128 * t + r;
-                    const uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
+                    uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (BF16 && SC != 0) {
+                        // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15), and what is
+                        // below 2^-39 of it loses bits
+                        float2 f[4];
+                        float mx = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(&w)[e]);
+                            mx = max3f(mx, fabsf(f[e].x), fabsf(f[e].y));
+                        }
+#pragma unroll
+                        for (int o = 1; o < QC; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        // exponent of the largest, held to [-100, 127] so that both factors are normal
+                        const int e0 = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+                        const float up = __uint_as_float(static_cast<uint32_t>(14 - e0 + 127) << 23);
+                        w = make_uint4(pack_half2(f[0].x * up, f[0].y * up), pack_half2(f[1].x * up, f[1].y * up),
+                                       pack_half2(f[2].x * up, f[2].y * up), pack_half2(f[3].x * up, f[3].y * up));
+                        if (tid % QC == 0) s.qs[128 * t + r] = __uint_as_float(static_cast<uint32_t>(e0 - 14 + 127) << 23);
+                    }
                     sts128(smem_u32(s.q[t][0]) + chunk_at(r, tid % QC), w);
                 }
             }
@@ -420,55 +460,43 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         };
         if constexpr (SC != 0) {
             uint4 kr[ITS], vr[ITS];
-            auto load = [&](const void *pool, int j, uint4 (&to)[ITS]) {
-                long long row[ITS];
+            uint32_t rows[ITS];
+            auto find_rows = [&]() {
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) row[i] = row_of(rr + i * RPI);
+                for (int i = 0; i < ITS; ++i) rows[i] = row_of(rr + i * RPI);
+            };
+            auto load = [&](const void *pool, int j, uint4 (&to)[ITS]) {
                 const uint4 *from = static_cast<const uint4 *>(pool) + cc;
                 if (plain) {
 #pragma unroll
-                    for (int i = 0; i < ITS; ++i) to[i] = __ldg(from + row[i] * CPR);
+                    for (int i = 0; i < ITS; ++i) to[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                 } else {
 #pragma unroll
                     for (int i = 0; i < ITS; ++i) {
                         to[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row[i] >= 0 && j * kStep + rr + i * RPI < kv_end) to[i] = __ldg(from + row[i] * CPR);
+                        if (rows[i] != kNone && j * kStep + rr + i * RPI < kv_end) to[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                     }
-                }
-            };
-            // 16 codes become chunks 2 cc and 2 cc + 1; lanes of the second 64 channels store theirs the
-            // other way round, so that a row's eight stores meet eight different 16-byte bank groups
-            auto store = [&](uint32_t to, const uint4 (&from)[ITS]) {
-                const int flip = cc >> 2 & 1;
-#pragma unroll
-                for (int i = 0; i < ITS; ++i) {
-                    const int r = rr + i * RPI;
-                    uint4 lo, hi;
-                    widen4<BF16, FP8>(from[i].x, lo.x, lo.y);
-                    widen4<BF16, FP8>(from[i].y, lo.z, lo.w);
-                    widen4<BF16, FP8>(from[i].z, hi.x, hi.y);
-                    widen4<BF16, FP8>(from[i].w, hi.z, hi.w);
-                    sts128(to + chunk_at(r, 2 * cc + flip), flip ? hi : lo);
-                    sts128(to + chunk_at(r, 2 * cc + 1 - flip), flip ? lo : hi);
                 }
             };
             look(j0);
             find(j0);
             look(j0 + 1);
             load_scales(j0);
+            find_rows();
             load(a.c.K, j0, kr);
             load(a.c.V, j0, vr);
             load_q();
             for (int j = j0; j < j1; ++j) {
                 const int i = j - j0, st = i & 1;
                 if (!free_of(s.k_free, i)) break;
-                store(smem_u32(s.k[st][0]), kr);
+                store_codes<false, FP8, ITS, RPI>(smem_u32(s.k[st][0]), kr, rr, cc);
                 store_scales(i);
                 done(&s.k_full[st]);
                 if (j + 1 < j1) {
                     find(j + 1);
                     look(j + 2);
                     load_scales(j + 1);
+                    find_rows();
                     load(a.c.K, j + 1, kr);
                 }
                 if (!free_of(s.v_free, i)) break;
@@ -488,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         }
                     }
                 }
-                store(smem_u32(s.v[st][0]), vr);
+                store_codes<BF16, FP8, ITS, RPI>(smem_u32(s.v[st][0]), vr, rr, cc);
                 done(&s.v_full[st]);
                 if (j + 1 < j1) load(a.c.V, j + 1, vr);
             }
@@ -499,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 bool there[8];
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
-                    const long long row = row_of(16 * g + rr);
-                    there[g] = row >= 0;
-                    from[g] = static_cast<const uint8_t *>(pool) + (row < 0 ? 0 : row * ROW + cc * 16);
+                    const uint32_t row = row_of(16 * g + rr);
+                    there[g] = row != kNone;
+                    from[g] = static_cast<const uint8_t *>(pool) + (row == kNone ? 0 : static_cast<size_t>(row) * ROW + cc * 16);
                 }
                 if (plain) {
 #pragma unroll
@@ -580,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
             for (int q = 0; q < 8; ++q) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&raw[16 * q]));
             const uint32_t holes = s.holes[at];
+            const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
             // ---- the step's largest x = acc kc + lv (which raw holds afterwards, where some are hidden or SC = 1)
@@ -590,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     float gm = fmaxf(__uint_as_float(raw[16 * g]), __uint_as_float(raw[16 * g + 1]));
 #pragma unroll
                     for (int k = 2; k < 16; k += 2) gm = max3f(gm, __uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1]));
-                    mx = fmaxf(mx, SC == 2 ? __fmaf_rn(gm, s.kc[at][g], s.lv[at][g]) : gm * a.sl2);
+                    mx = fmaxf(mx, SC == 2 ? __fmaf_rn(gm, s.kc[at][g] * qs, s.lv[at][g]) : gm * a.sl2);
                 }
             } else {
 #pragma unroll
@@ -602,6 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     } else if constexpr (SC == 2) {
                         kc.x = kc.y = kc.z = kc.w = s.kc[at][k / 16];
                         lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
+                    }
+                    if constexpr (BF16 && SC != 0) {
+                        kc.x *= qs; kc.y *= qs; kc.z *= qs; kc.w *= qs;
                     }
                     const f2 lo = fma2(f2{__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])}, f2{kc.x, kc.y}, f2{lv.x, lv.y});
                     const f2 hi = fma2(f2{__uint_as_float(raw[k + 2]), __uint_as_float(raw[k + 3])}, f2{kc.z, kc.w}, f2{lv.z, lv.w});
@@ -650,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     f2 sum{0.0f, 0.0f};
                     f2 f{a.sl2, a.sl2}, off{-ref, -ref};
                     if constexpr (SC == 2 && !SCALED) {
-                        f.x = f.y = s.kc[at][g];
+                        f.x = f.y = s.kc[at][g] * qs;
                         off.x = off.y = s.lv[at][g] - ref;
                     }
 #pragma unroll
