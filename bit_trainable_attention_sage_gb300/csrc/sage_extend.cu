@@ -11,10 +11,10 @@
 // (Few rows, up to kExtendFewRows a kv head, go to the one-token kernel's warps instead: sage_decode.cu.)
 //
 // One CTA takes two tiles (256 rows) of one kv head and walks the slots in steps of 128:
-//   warps 8-11  load K and V rows by page, widen codes to the 16-bit type of Q, and store both as
-//               swizzled operands, two stages each.  8-bit rows come through registers, one step
-//               ahead; 16-bit rows by cp.async.
-//   warp 12     issues every MMA: S_t = Q_t K^T and O_t += P_t V, M = 128, N = 128 and d
+//   warps 8-11  load K's rows by page, widen codes to 16 bits, and store them as swizzled operands, two
+//               stages; warps 12-15 V's.  8-bit rows come through registers, one step ahead; 16-bit
+//               rows by cp.async.
+//   warp 16     issues every MMA: S_t = Q_t K^T and O_t += P_t V, M = 128, N = 128 and d
 //   warps 0-3   softmax of tile 0, warps 4-7 of tile 1: a thread a row.  P goes back to TMEM over S,
 //               as the A operand of the second product; O stays in TMEM over the whole walk and is rescaled
 //               only when a row's maximum has grown by more than kSlack (a power of two) since the last time.
@@ -46,11 +46,11 @@ __device__ unsigned int g_ext_index = 0;    // 1: a page, start or count was out
 
 namespace ext {
 
-constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8;                // 8 .. 11
-constexpr int kMmaWarp = 12;
-// Launched at 128 registers a thread (512 x 128 = 65536): 2 x 128 x 184 + 128 x 104 + 128 x 40 = 65536.
-constexpr uint32_t kRegsSoftmax = 184, kRegsLoad = 104, kRegsControl = 40;
+constexpr int kThreads = 640;
+constexpr int kKeyWarp = 8, kValueWarp = 12;    // 8 .. 11, 12 .. 15
+constexpr int kMmaWarp = 16;                // (17 .. 19 are idle)
+// Launched at 96 registers a thread (640 x 96 = 61440): 256 x 120 + 256 x 88 + 128 x 64 = 61440.
+constexpr uint32_t kRegsSoftmax = 120, kRegsLoad = 88, kRegsControl = 64;
 constexpr int kRows = 256;                  // of a CTA
 constexpr int kStep = 128;                  // slots a step
 constexpr int kExtMaxSplits = 16;
@@ -79,7 +79,7 @@ struct Smem {
     float qs[256];                                   // the rows' factors of Q (8-bit pools, Q in bf16)
     uint32_t holes[4];                               // groups of 16 slots whose page is none
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_done[2];   // p_full[tile][half of the step]; o_full: a half's PV, o_done: a tile's last
     uint32_t tmem_base;
     int abort_flag, not_finite;
 };
@@ -218,13 +218,250 @@ __device__ __forceinline__ int tile_end(const Args &a, const Seq &s, int r0, int
     return min(s.start + t + 1, s.len);
 }
 
+// K's or V's rows, step after step, by 128 threads; first Q's rows of a tile, 0 by K's threads and 1 by V's.
+template <int D, bool BF16, int SC, bool FP8>
+struct Loader {
+    const Args &a;
+    Smem<D> &s;
+    int b, hk, j0, j1, kv_end, mixed, tid, r0, n_q;
+    size_t out0;
+
+    static constexpr int ROW = SC ? D : 2 * D;                       // bytes of a row
+    static constexpr int CPR = ROW / 16, RPI = 128 / CPR, ITS = 128 / RPI;   // 16-byte chunks a row, rows at a time
+    static constexpr uint32_t kNone = 0xFFFFFFFFu;                   // (a pool in memory has fewer rows)
+
+    // this warp's part of an operand is stored
+    __device__ __forceinline__ void done(uint64_t *bar) const {
+        fence_view_async_shared();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(bar);
+    }
+    // the stage of step j0 + i has been read
+    __device__ __forceinline__ bool free_of(uint64_t *bar, int i) const {
+        return i < 2 || mbar_wait_warp(&bar[i & 1], ((i >> 1) - 1) & 1, &s.abort_flag, &g_ext_err, 6);
+    }
+
+    // zeros behind the last row
+    __device__ __forceinline__ void query(int t) const {
+        const uint4 *Q = static_cast<const uint4 *>(a.Q) + out0 * (D / 8);
+        constexpr int QC = D / 8, QR = 128 / QC;
+        if (j0 < n_q) {
+#pragma unroll 8
+            for (int r = tid / QC; r < 128; r += QR) {
+                const int row = r0 + 128 * t + r;
+                uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (BF16 && SC != 0) {
+                    // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15), and what is
+                    // below 2^-39 of it loses bits
+                    float2 f[4];
+                    float mx = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[e] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(&w)[e]);
+                        mx = max3f(mx, fabsf(f[e].x), fabsf(f[e].y));
+                    }
+#pragma unroll
+                    for (int o = 1; o < QC; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // exponent of the largest, held to [-100, 127] so that both factors are normal
+                    const int e0 = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+                    const float up = __uint_as_float(static_cast<uint32_t>(14 - e0 + 127) << 23);
+                    w = make_uint4(pack_half2(f[0].x * up, f[0].y * up), pack_half2(f[1].x * up, f[1].y * up),
+                                   pack_half2(f[2].x * up, f[2].y * up), pack_half2(f[3].x * up, f[3].y * up));
+                    if (tid % QC == 0) s.qs[128 * t + r] = __uint_as_float(static_cast<uint32_t>(e0 - 14 + 127) << 23);
+                }
+                sts128(smem_u32(s.q[t][0]) + chunk_at(r, tid % QC), w);
+            }
+        }
+        done(&s.q_full);
+    }
+
+    template <bool VALUES>
+    __device__ __forceinline__ void run() const {
+        const int lane = tid & 31;
+        const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
+        const void *pool = VALUES ? a.c.V : a.c.K;
+        uint64_t *full = VALUES ? s.v_full : s.k_full, *free = VALUES ? s.v_free : s.k_free;
+        // Pages are asked for two steps ahead, by lane g of every warp (mod 8) for its step's group g of 16 slots,
+        // and become the group's first row of the pool, kNone where it has no page, a step ahead.
+        const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+        int page = 0;
+        uint32_t base = kNone;
+        bool plain = false;                                          // every group has its page and all of its slots
+        auto look = [&](int j) {
+            const int slot = j * kStep + (lane & 7) * 16;
+            page = slot < kv_end ? __ldg(table + kv_page_of(a.c, slot)) : 0;
+        };
+        auto find = [&](int j) {
+            const int slot = j * kStep + (lane & 7) * 16;
+            base = kNone;
+            if (slot < kv_end) {
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) base = static_cast<uint32_t>(kv_row(a.c, page, hk, slot));
+                else atomicOr(&g_ext_index, 1u);
+            }
+            plain = (j + 1) * kStep <= kv_end && __all_sync(0xffffffffu, base != kNone);
+        };
+        // row r of the step: its row of the pool (whole warps call it)
+        auto row_of = [&](int r) -> uint32_t {
+            const uint32_t first = __shfl_sync(0xffffffffu, base, r >> 4);
+            return first == kNone ? kNone : first + (r & 15);
+        };
+        // ---- scales, by K's threads, one step ahead
+        float sk = 0.0f, sv = 0.0f;
+        bool hole = false;
+        auto load_scales = [&](int j) {
+            // a thread a slot (SC = 1), or threads 0 .. 7 a group of 16 each; of a 16-bit pool the holes alone
+            const int slot = j * kStep + (SC == 1 ? tid : (lane & 7) * 16);
+            const uint32_t r = SC == 1 ? row_of(tid) : base;
+            sk = sv = 0.0f;
+            hole = slot < kv_end && r == kNone && (SC == 1 || lane < 8);
+            if (SC != 0 && r != kNone && slot < kv_end && (SC == 1 || tid < 8)) {
+                sk = __ldg(a.c.sK + (r >> a.c.block_shift));
+                sv = __ldg(a.c.sV + (r >> a.c.block_shift));
+            }
+        };
+        auto store_scales = [&](int i) {
+            const int at = i & 3;
+            if (SC == 1 || (SC == 2 && tid < 8)) {
+                s.kc[at][tid] = sk * a.sl2;
+                // no value is lost with a scale of 0 (its codes are): a NaN stays one
+                s.lv[at][tid] = sv == 0.0f ? 0.0f : log2f(sv);
+                s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;
+            }
+            if constexpr (SC == 1) {
+                // slots 32 w .. of warp w: two groups
+                const uint32_t h = __ballot_sync(0xffffffffu, hole);
+                if (lane == 0) {
+                    const uint32_t two = (h & 0xFFFFu ? 1u : 0u) | (h >> 16 ? 2u : 0u);
+                    reinterpret_cast<uint8_t *>(&s.holes[at])[tid >> 5] = static_cast<uint8_t>(two);
+                }
+            } else if (tid < 32) {
+                const uint32_t h = __ballot_sync(0xffffffffu, hole);
+                // groups 2 w and 2 w + 1 in byte w, as above
+                if (lane == 0) s.holes[at] = (h & 3u) | ((h >> 2) & 3u) << 8 | ((h >> 4) & 3u) << 16 | ((h >> 6) & 3u) << 24;
+            }
+        };
+        if constexpr (SC != 0) {
+            uint4 x[ITS];                                            // 8-bit rows, one step ahead
+            auto load = [&](int j) {
+                uint32_t rows[ITS];
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) rows[i] = row_of(rr + i * RPI);
+                const uint4 *from = static_cast<const uint4 *>(pool) + cc;
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        x[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (rows[i] != kNone && j * kStep + rr + i * RPI < kv_end) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                    }
+                }
+            };
+            look(j0);
+            find(j0);
+            look(j0 + 1);
+            if (!VALUES) load_scales(j0);
+            load(j0);
+            query(VALUES);
+            for (int j = j0; j < j1; ++j) {
+                const int i = j - j0, st = i & 1;
+                if (!free_of(free, i)) break;
+                if constexpr (VALUES && FP8) {
+                    if (j >= mixed) {
+#pragma unroll
+                        for (int y = 0; y < ITS; ++y) {
+                            uint32_t *w = &x[y].x;
+                            uint32_t bad = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t m = not_finite_mask<BF16, true>(w[e]);
+                                w[e] &= ~m;
+                                bad |= m;
+                            }
+                            if (bad) s.not_finite = 1;
+                        }
+                    }
+                }
+                if constexpr (VALUES) store_codes<BF16, FP8, ITS, RPI>(smem_u32(s.v[st][0]), x, rr, cc);
+                else store_codes<false, FP8, ITS, RPI>(smem_u32(s.k[st][0]), x, rr, cc);
+                if (!VALUES) store_scales(i);
+                done(&full[st]);
+                if (j + 1 < j1) {
+                    find(j + 1);
+                    look(j + 2);
+                    if (!VALUES) load_scales(j + 1);
+                    load(j + 1);
+                }
+            }
+        } else {
+            auto load = [&](int j) {
+                const uint32_t to = smem_u32(VALUES ? s.v[(j - j0) & 1][0] : s.k[(j - j0) & 1][0]);
+                // this thread has ITS / 8 rows of each of the 8 groups
+                const uint8_t *from[8];
+                bool there[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const uint32_t row = row_of(16 * g + rr);
+                    there[g] = row != kNone;
+                    from[g] = static_cast<const uint8_t *>(pool) + (row == kNone ? 0 : static_cast<size_t>(row) * ROW + cc * 16);
+                }
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) cp_async16(to + chunk_at(rr + i * RPI, cc), from[i * RPI / 16] + i * RPI % 16 * ROW);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        const bool is = there[i * RPI / 16] && j * kStep + rr + i * RPI < kv_end;
+                        cp_async16(to + chunk_at(rr + i * RPI, cc), is ? from[i * RPI / 16] + i * RPI % 16 * ROW : static_cast<const uint8_t *>(pool), is);
+                    }
+                }
+                cp_commit();
+            };
+            look(j0);
+            find(j0);
+            look(j0 + 1);
+            load(j0);
+            if (!VALUES) load_scales(j0);
+            query(VALUES);
+            for (int j = j0; j < j1; ++j) {
+                const int i = j - j0, st = i & 1;
+                if (!VALUES) store_scales(i);
+                cp_wait<0>();
+                if (VALUES && j >= mixed) {                          // the chunks this thread has copied itself
+#pragma unroll 4
+                    for (int y = 0; y < ITS; ++y) {
+                        const uint32_t at = smem_u32(s.v[st][0]) + chunk_at(rr + y * RPI, cc);
+                        uint4 w = lds128u(at);
+                        const uint32_t m0 = not_finite_mask<BF16, false>(w.x), m1 = not_finite_mask<BF16, false>(w.y);
+                        const uint32_t m2 = not_finite_mask<BF16, false>(w.z), m3 = not_finite_mask<BF16, false>(w.w);
+                        if (m0 | m1 | m2 | m3) {
+                            sts128(at, make_uint4(w.x & ~m0, w.y & ~m1, w.z & ~m2, w.w & ~m3));
+                            s.not_finite = 1;
+                        }
+                    }
+                }
+                done(&full[st]);
+                if (j + 1 < j1) {
+                    find(j + 1);
+                    look(j + 2);
+                    if (!free_of(free, i + 1)) break;
+                    load(j + 1);
+                    if (!VALUES) load_scales(j + 1);
+                }
+            }
+            cp_wait<0>();                                            // no copy outlives the CTA's shared memory
+        }
+    }
+};
+
 // SC: 0 a 16-bit pool, 1 a scale a row, 2 a scale a block
 template <int D, bool BF16, int SC, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     Smem<D> &s = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // Results are referred to 2^kShift of the running maximum, which lags by up to 2^kSlack.
-    constexpr float kSlack = BF16 ? 8.0f : 4.0f, kShift = BF16 ? 0.0f : 11.0f;
+    constexpr float kSlack = 4.0f, kShift = BF16 ? 0.0f : 11.0f, kMost = BF16 ? 0x1p15f : 65504.0f;
     const int warp = threadIdx.x >> 5;
     const int BH = a.c.B * a.c.H;
     // item: tiles with many slots first, all heads of a rank after one another
@@ -251,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
     if (j0 >= j1) {                                   // nothing to see: the whole CTA alike
         const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
-        if (r0 + row >= a.rows) return;
+        if (row >= kRows || r0 + row >= a.rows) return;
         if (a.splits > 1) {
             if (half == 0) reinterpret_cast<float2 *>(a.part_ml)[item * kRows + row] = make_float2(-INFINITY, 0.0f);
         } else {
@@ -270,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         s.abort_flag = 0;
         s.not_finite = 0;
-        mbar_init(&s.q_full, 4);
+        mbar_init(&s.q_full, 8);
         for (int st = 0; st < 2; ++st) {
             mbar_init(&s.k_full[st], 4);
             mbar_init(&s.k_free[st], 1);
@@ -280,8 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         mbar_init(&s.mma_done, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s.s_full[t], 1);
-            mbar_init(&s.p_full[t], 4);
+            mbar_init(&s.p_full[t][0], 4);
+            mbar_init(&s.p_full[t][1], 4);
             mbar_init(&s.o_full[t], 1);
+            mbar_init(&s.o_done[t], 1);
         }
         fence_barrier_init();
     }
@@ -319,275 +558,38 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             for (int j = j0; j < j1 && ok; ++j) {
                 const int i = j - j0, st = i & 1, nst = st ^ 1;
                 if (!(ok = mbar_wait(&s.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
+                // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
+                if (j + 1 < j1 && !(ok = mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
                 const uint32_t v_addr = smem_u32(s.v[st][0]);
-                bool k_next = false;
                 auto tile_step = [&](const int t) -> bool {
                     if (j >= n_t[t]) return true;
-                    if (!mbar_wait(&s.p_full[t], i & 1, abort_flag, &g_ext_err, 4)) return false;
-                    tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (i > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&s.o_full[t]);
-                    if (j + 1 < n_t[t]) {
-                        if (!k_next) {
-                            if (!mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
-                            tc_fence_after();
-                            k_next = true;
-                        }
-                        issue_s(t, nst);
+                    for (int h = 0; h < 2; ++h) {
+                        if (!mbar_wait(&s.p_full[t][h], i & 1, abort_flag, &g_ext_err, 4)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (i > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&s.o_full[t]);
                     }
+                    if (j + 1 == n_t[t]) umma_commit(&s.o_done[t]);
+                    if (t == 1 || j >= n_t[1]) umma_commit(&s.v_free[st]);
+                    if (j + 1 < n_t[t]) issue_s(t, nst);
                     return true;
                 };
                 ok = tile_step(0) && tile_step(1);
                 if (!ok) break;
                 if (j + 1 < j1) umma_commit(&s.k_free[nst]);
-                umma_commit(&s.v_free[st]);
             }
             // every MMA must have finished before the tensor memory is released
             umma_commit(&s.mma_done);
             mbar_wait_drain(&s.mma_done, 0, &g_ext_err, 5);
         }
-    } else if (warp >= kLoadWarp) {
+    } else if (warp >= kKeyWarp) {
         regs_dec<kRegsLoad>();
-        // ------------------------------------------------------------------ K, V and Q rows
-        const int tid = threadIdx.x - kLoadWarp * 32, lane = tid & 31;
-        constexpr int ROW = SC ? D : 2 * D;                          // bytes of a row
-        constexpr int CPR = ROW / 16, RPI = 128 / CPR, ITS = 128 / RPI;   // 16-byte chunks a row, rows at a time
-        const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
-        // Pages are asked for two steps ahead, by lane g of every warp (mod 8) for its step's group g of 16 slots,
-        // and become the group's first row of the pool, kNone where it has no page, a step ahead.
-        constexpr uint32_t kNone = 0xFFFFFFFFu;
-        const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
-        int page = 0;
-        uint32_t base = kNone;                                       // (a pool in memory has fewer than 2^32 - 1 rows)
-        bool plain = false;
-        auto look = [&](int j) {
-            const int slot = j * kStep + (lane & 7) * 16;
-            page = slot < kv_end ? __ldg(table + kv_page_of(a.c, slot)) : 0;
-        };
-        auto find = [&](int j) {
-            const int slot = j * kStep + (lane & 7) * 16;
-            base = kNone;
-            if (slot < kv_end) {
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) base = static_cast<uint32_t>(kv_row(a.c, page, hk, slot));
-                else atomicOr(&g_ext_index, 1u);
-            }
-            // every group has its page and all of its slots
-            plain = (j + 1) * kStep <= kv_end && __all_sync(0xffffffffu, base != kNone);
-        };
-        // row r of the step: its row of the pool (whole warps call it)
-        auto row_of = [&](int r) -> uint32_t {
-            const uint32_t first = __shfl_sync(0xffffffffu, base, r >> 4);
-            return first == kNone ? kNone : first + (r & 15);
-        };
-        auto done = [&](uint64_t *bar) {                             // this warp's part is stored
-            fence_view_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-        };
-        // ---- scales, one step ahead
-        float sk = 0.0f, sv = 0.0f;
-        bool hole = false;
-        auto load_scales = [&](int j) {
-            // a thread a slot (SC = 1), or threads 0 .. 7 a group of 16 each; of a 16-bit pool the holes alone
-            const int slot = j * kStep + (SC == 1 ? tid : (lane & 7) * 16);
-            const uint32_t r = SC == 1 ? row_of(tid) : base;
-            sk = sv = 0.0f;
-            hole = slot < kv_end && r == kNone && (SC == 1 || lane < 8);
-            if (SC != 0 && r != kNone && slot < kv_end && (SC == 1 || tid < 8)) {
-                sk = __ldg(a.c.sK + (r >> a.c.block_shift));
-                sv = __ldg(a.c.sV + (r >> a.c.block_shift));
-            }
-        };
-        auto store_scales = [&](int i) {
-            const int at = i & 3;
-            if (SC == 1 || (SC == 2 && tid < 8)) {
-                s.kc[at][tid] = sk * a.sl2;
-                // no value is lost with a scale of 0 (its codes are): a NaN stays one
-                s.lv[at][tid] = sv == 0.0f ? 0.0f : log2f(sv);
-                s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;
-            }
-            if constexpr (SC == 1) {
-                // slots 32 w .. of warp w: two groups
-                const uint32_t h = __ballot_sync(0xffffffffu, hole);
-                if (lane == 0) {
-                    const uint32_t two = (h & 0xFFFFu ? 1u : 0u) | (h >> 16 ? 2u : 0u);
-                    reinterpret_cast<uint8_t *>(&s.holes[at])[warp - kLoadWarp] = static_cast<uint8_t>(two);
-                }
-            } else if (warp == kLoadWarp) {
-                const uint32_t h = __ballot_sync(0xffffffffu, hole);
-                // groups 2 w and 2 w + 1 in byte w, as above
-                if (lane == 0) s.holes[at] = (h & 3u) | ((h >> 2) & 3u) << 8 | ((h >> 4) & 3u) << 16 | ((h >> 6) & 3u) << 24;
-            }
-        };
-        // ---- Q: both tiles' rows, zeros behind the last
-        auto load_q = [&]() {
-            const uint4 *Q = static_cast<const uint4 *>(a.Q) + out0 * (D / 8);
-            constexpr int QC = D / 8, QR = 128 / QC;
-            for (int t = 0; t < 2; ++t) {
-                if (j0 >= n_t[t]) continue;
-#pragma unroll 8
-                for (int r = tid / QC; r < 128; r += QR) {
-                    const int row = r0 + 128 * t + r;
-                    uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
-                    if constexpr (BF16 && SC != 0) {
-                        // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15), and what is
-                        // below 2^-39 of it loses bits
-                        float2 f[4];
-                        float mx = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            f[e] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(&w)[e]);
-                            mx = max3f(mx, fabsf(f[e].x), fabsf(f[e].y));
-                        }
-#pragma unroll
-                        for (int o = 1; o < QC; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        // exponent of the largest, held to [-100, 127] so that both factors are normal
-                        const int e0 = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
-                        const float up = __uint_as_float(static_cast<uint32_t>(14 - e0 + 127) << 23);
-                        w = make_uint4(pack_half2(f[0].x * up, f[0].y * up), pack_half2(f[1].x * up, f[1].y * up),
-                                       pack_half2(f[2].x * up, f[2].y * up), pack_half2(f[3].x * up, f[3].y * up));
-                        if (tid % QC == 0) s.qs[128 * t + r] = __uint_as_float(static_cast<uint32_t>(e0 - 14 + 127) << 23);
-                    }
-                    sts128(smem_u32(s.q[t][0]) + chunk_at(r, tid % QC), w);
-                }
-            }
-            done(&s.q_full);
-        };
-        auto free_of = [&](uint64_t *bar, int i) {                   // the stage of step j0 + i has been read
-            return i < 2 || mbar_wait_warp(&bar[i & 1], ((i >> 1) - 1) & 1, abort_flag, &g_ext_err, 6);
-        };
-        if constexpr (SC != 0) {
-            uint4 kr[ITS], vr[ITS];
-            uint32_t rows[ITS];
-            auto find_rows = [&]() {
-#pragma unroll
-                for (int i = 0; i < ITS; ++i) rows[i] = row_of(rr + i * RPI);
-            };
-            auto load = [&](const void *pool, int j, uint4 (&to)[ITS]) {
-                const uint4 *from = static_cast<const uint4 *>(pool) + cc;
-                if (plain) {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) to[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) {
-                        to[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (rows[i] != kNone && j * kStep + rr + i * RPI < kv_end) to[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
-                    }
-                }
-            };
-            look(j0);
-            find(j0);
-            look(j0 + 1);
-            load_scales(j0);
-            find_rows();
-            load(a.c.K, j0, kr);
-            load(a.c.V, j0, vr);
-            load_q();
-            for (int j = j0; j < j1; ++j) {
-                const int i = j - j0, st = i & 1;
-                if (!free_of(s.k_free, i)) break;
-                store_codes<false, FP8, ITS, RPI>(smem_u32(s.k[st][0]), kr, rr, cc);
-                store_scales(i);
-                done(&s.k_full[st]);
-                if (j + 1 < j1) {
-                    find(j + 1);
-                    look(j + 2);
-                    load_scales(j + 1);
-                    find_rows();
-                    load(a.c.K, j + 1, kr);
-                }
-                if (!free_of(s.v_free, i)) break;
-                if constexpr (FP8) {
-                    if (j >= mixed) {
-#pragma unroll
-                        for (int x = 0; x < ITS; ++x) {
-                            uint32_t *w = &vr[x].x;
-                            uint32_t bad = 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t m = not_finite_mask<BF16, true>(w[e]);
-                                w[e] &= ~m;
-                                bad |= m;
-                            }
-                            if (bad) s.not_finite = 1;
-                        }
-                    }
-                }
-                store_codes<BF16, FP8, ITS, RPI>(smem_u32(s.v[st][0]), vr, rr, cc);
-                done(&s.v_full[st]);
-                if (j + 1 < j1) load(a.c.V, j + 1, vr);
-            }
-        } else {
-            auto load = [&](const void *pool, uint32_t to, int j) {
-                // this thread has ITS / 8 rows of each of the 8 groups
-                const uint8_t *from[8];
-                bool there[8];
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint32_t row = row_of(16 * g + rr);
-                    there[g] = row != kNone;
-                    from[g] = static_cast<const uint8_t *>(pool) + (row == kNone ? 0 : static_cast<size_t>(row) * ROW + cc * 16);
-                }
-                if (plain) {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) cp_async16(to + chunk_at(rr + i * RPI, cc), from[i * RPI / 16] + i * RPI % 16 * ROW);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) {
-                        const bool is = there[i * RPI / 16] && j * kStep + rr + i * RPI < kv_end;
-                        cp_async16(to + chunk_at(rr + i * RPI, cc), is ? from[i * RPI / 16] + i * RPI % 16 * ROW : static_cast<const uint8_t *>(pool), is);
-                    }
-                }
-                cp_commit();
-            };
-            look(j0);
-            find(j0);
-            look(j0 + 1);
-            load(a.c.K, smem_u32(s.k[0][0]), j0);
-            load(a.c.V, smem_u32(s.v[0][0]), j0);
-            load_scales(j0);
-            load_q();
-            for (int j = j0; j < j1; ++j) {
-                const int i = j - j0, st = i & 1;
-                store_scales(i);
-                if (j + 1 < j1) {
-                    if (!free_of(s.k_free, i + 1)) break;
-                    find(j + 1);
-                    look(j + 2);
-                    load(a.c.K, smem_u32(s.k[st ^ 1][0]), j + 1);
-                    load_scales(j + 1);
-                    cp_wait<2>();
-                } else {
-                    cp_wait<1>();
-                }
-                done(&s.k_full[st]);
-                if (j + 1 < j1) {
-                    if (!free_of(s.v_free, i + 1)) break;
-                    load(a.c.V, smem_u32(s.v[st ^ 1][0]), j + 1);
-                    cp_wait<2>();
-                } else {
-                    cp_wait<0>();
-                }
-                if (j >= mixed) {                                    // the chunks this thread has copied itself
-#pragma unroll 4
-                    for (int x = 0; x < ITS; ++x) {
-                        const uint32_t at = smem_u32(s.v[st][0]) + chunk_at(rr + x * RPI, cc);
-                        uint4 w = lds128u(at);
-                        const uint32_t m0 = not_finite_mask<BF16, false>(w.x), m1 = not_finite_mask<BF16, false>(w.y);
-                        const uint32_t m2 = not_finite_mask<BF16, false>(w.z), m3 = not_finite_mask<BF16, false>(w.w);
-                        if (m0 | m1 | m2 | m3) {
-                            sts128(at, make_uint4(w.x & ~m0, w.y & ~m1, w.z & ~m2, w.w & ~m3));
-                            s.not_finite = 1;
-                        }
-                    }
-                }
-                done(&s.v_full[st]);
-            }
-            cp_wait<0>();                                            // no copy outlives the CTA's shared memory
-        }
+        const Loader<D, BF16, SC, FP8> load{a, s, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, n_t[warp >= kValueWarp], out0};
+        if (warp < kValueWarp) load.template run<false>();
+        else load.template run<true>();
     } else {
         regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------------------ softmax
@@ -602,121 +604,171 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             const int i = j - j0, at = i & 3;
             if (!(ok = mbar_wait_warp(&s.s_full[t], i & 1, abort_flag, &g_ext_err, 7))) break;
             tc_fence_after();
-            uint32_t raw[128];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) tmem_ld16(lane_base + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&raw[16 * q]));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&raw[16 * q]));
             const uint32_t holes = s.holes[at];
             const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
-            // ---- the step's largest x = acc kc + lv (which raw holds afterwards, where some are hidden or SC = 1)
-            float mx = -INFINITY;
-            if (SC != 1 && whole) {
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    float gm = fmaxf(__uint_as_float(raw[16 * g]), __uint_as_float(raw[16 * g + 1]));
-#pragma unroll
-                    for (int k = 2; k < 16; k += 2) gm = max3f(gm, __uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1]));
-                    mx = fmaxf(mx, SC == 2 ? __fmaf_rn(gm, s.kc[at][g] * qs, s.lv[at][g]) : gm * a.sl2);
+            uint32_t raw[2][16];                                     // S, 16 slots a group, a group ahead
+            auto load_group = [&](int g) { tmem_ld16(lane_base + 16 * g, raw[g & 1]); };
+            // x of slots k .. k + 3 of the step (hidden ones: -inf)
+            auto four = [&](const uint32_t *r, int k, float (&v)[4]) {
+                float4 kc = make_float4(a.sl2, a.sl2, a.sl2, a.sl2), lv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if constexpr (SC == 1) {
+                    kc = lds128(smem_u32(&s.kc[at][k]));
+                    lv = lds128(smem_u32(&s.lv[at][k]));
+                } else if constexpr (SC == 2) {
+                    kc.x = kc.y = kc.z = kc.w = s.kc[at][k / 16];
+                    lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 128; k += 4) {
-                    float4 kc = make_float4(a.sl2, a.sl2, a.sl2, a.sl2), lv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if constexpr (SC == 1) {
-                        kc = lds128(smem_u32(&s.kc[at][k]));
-                        lv = lds128(smem_u32(&s.lv[at][k]));
-                    } else if constexpr (SC == 2) {
-                        kc.x = kc.y = kc.z = kc.w = s.kc[at][k / 16];
-                        lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
-                    }
-                    if constexpr (BF16 && SC != 0) {
-                        kc.x *= qs; kc.y *= qs; kc.z *= qs; kc.w *= qs;
-                    }
-                    const f2 lo = fma2(f2{__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])}, f2{kc.x, kc.y}, f2{lv.x, lv.y});
-                    const f2 hi = fma2(f2{__uint_as_float(raw[k + 2]), __uint_as_float(raw[k + 3])}, f2{kc.z, kc.w}, f2{lv.z, lv.w});
-                    float v[4] = {lo.x, lo.y, hi.x, hi.y};
-                    if (!whole) {
-                        const bool none = (holes >> (k / 32 * 8 + (k / 16 & 1))) & 1u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (none || k + e >= seen) v[e] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) raw[k + e] = __float_as_uint(v[e]);
-                    mx = max3f(mx, v[0], v[1]);
-                    mx = max3f(mx, v[2], v[3]);
+                if constexpr (BF16 && SC != 0) {
+                    kc.x *= qs; kc.y *= qs; kc.z *= qs; kc.w *= qs;
                 }
+                const f2 lo = fma2(f2{__uint_as_float(r[0]), __uint_as_float(r[1])}, f2{kc.x, kc.y}, f2{lv.x, lv.y});
+                const f2 hi = fma2(f2{__uint_as_float(r[2]), __uint_as_float(r[3])}, f2{kc.z, kc.w}, f2{lv.z, lv.w});
+                v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
+                if (!whole) {
+                    const bool none = (holes >> (k / 32 * 8 + (k / 16 & 1))) & 1u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (none || k + e >= seen) v[e] = -INFINITY;
+                }
+            };
+            // (scales of blocks: read at once and ahead, not a group at a time: shared memory answers slowly beside the
+            // products' operands and the loaders' stores)
+            [[maybe_unused]] float kcs[8], lvs[8];
+            if constexpr (SC == 2) {
+                const float4 k0 = lds128(smem_u32(&s.kc[at][0])), k1 = lds128(smem_u32(&s.kc[at][4]));
+                const float4 l0 = lds128(smem_u32(&s.lv[at][0])), l1 = lds128(smem_u32(&s.lv[at][4]));
+                kcs[0] = k0.x; kcs[1] = k0.y; kcs[2] = k0.z; kcs[3] = k0.w; kcs[4] = k1.x; kcs[5] = k1.y; kcs[6] = k1.z; kcs[7] = k1.w;
+                lvs[0] = l0.x; lvs[1] = l0.y; lvs[2] = l0.z; lvs[3] = l0.w; lvs[4] = l1.x; lvs[5] = l1.y; lvs[6] = l1.z; lvs[7] = l1.w;
             }
-            // ---- the reference follows the maximum when it lags too far
-            const bool moves = mx > m + kSlack;
-            if (__any_sync(0xffffffffu, moves)) {
-                const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
-                m = to;
-                l *= alpha;
-                if (i > 0) {
-                    if (!(ok = mbar_wait_warp(&s.o_full[t], (i - 1) & 1, abort_flag, &g_ext_err, 8))) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(lane_base + 128 + c, o);
-                        tmem_wait_ld_regs(o);
+            // Half h of the step, 64 slots: p' = 2^(x - ref), packed, and their l; the largest sum of 16 of them
+            uint32_t pk[32];
+            float add;
+            auto probabilities = [&](auto half, float ref, auto plain) -> float {
+                constexpr bool PLAIN = decltype(plain)::value;       // no slot is hidden
+                constexpr int G0 = 4 * decltype(half)::value;
+                float most = 0.0f;
+                [[maybe_unused]] float sums[4];
+                add = 0.0f;
+                load_group(G0);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st16(lane_base + 128 + c, o);
-                    }
-                    tmem_wait_st();
-                }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
-            // ---- p' = 2^(x - ref), to TMEM over S, and l.  SCALED: raw holds x; else the products
-            auto probabilities = [&](auto scaled, auto hidden) {
-                constexpr bool SCALED = decltype(scaled)::value;
-                [[maybe_unused]] constexpr bool HIDDEN = decltype(hidden)::value;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    uint32_t pk[8];
+                for (int g = G0; g < G0 + 4; ++g) {
+                    tmem_wait_ld_regs(raw[g & 1]);
+                    if (g < G0 + 3) load_group(g + 1);
+                    uint32_t(&r)[16] = raw[g & 1];
                     f2 sum{0.0f, 0.0f};
+                    [[maybe_unused]] f2 l2{0.0f, 0.0f};
                     f2 f{a.sl2, a.sl2}, off{-ref, -ref};
-                    if constexpr (SC == 2 && !SCALED) {
-                        f.x = f.y = s.kc[at][g] * qs;
-                        off.x = off.y = s.lv[at][g] - ref;
+                    if constexpr (SC == 2 && PLAIN) {
+                        f.x = f.y = kcs[g] * qs;
+                        off.x = off.y = lvs[g] - ref;
+                    }
+                    if constexpr (SC == 1 || !PLAIN) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            float v[4];
+                            four(&r[k], 16 * g + k, v);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[k + e] = __float_as_uint(v[e]);
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
-                        const f2 r2{__uint_as_float(raw[16 * g + k]), __uint_as_float(raw[16 * g + k + 1])};
-                        const f2 x2 = SCALED ? add2(r2, off) : fma2(r2, f, off);
+                        const f2 r2{__uint_as_float(r[k]), __uint_as_float(r[k + 1])};
+                        const f2 x2 = SC == 1 || !PLAIN ? add2(r2, off) : fma2(r2, f, off);
                         const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
+                        sum = add2(sum, p);
                         if constexpr (SC == 1) {
                             const f2 rv{s.rv[at][16 * g + k], s.rv[at][16 * g + k + 1]};
-                            if constexpr (HIDDEN) {                  // (a hidden slot's reciprocal may be anything)
-                                sum.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
-                                sum.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
-                            } else {
-                                sum = fma2(p, rv, sum);
+                            if constexpr (PLAIN) {
+                                l2 = fma2(p, rv, l2);
+                            } else {                                 // (a hidden slot's reciprocal may be anything)
+                                l2.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
+                                l2.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
                             }
-                        } else {
-                            sum = add2(sum, p);
                         }
-                        pk[k / 2] = pack2<BF16>(p.x, p.y);
+                        pk[8 * (g - G0) + k / 2] = pack2<BF16>(p.x, p.y);
                     }
-                    const float add = sum.x + sum.y;
-                    if constexpr (SC == 2) l += HIDDEN && add == 0.0f ? 0.0f : add * s.rv[at][g];
-                    else l += add;
-                    tmem_st8(lane_base + 8 * g, pk);
+                    const float both = sum.x + sum.y;
+                    most = fmaxf(most, both);
+                    if constexpr (SC == 1) add += l2.x + l2.y;
+                    else if constexpr (SC == 2) sums[g - G0] = both;
+                    else add += both;
                 }
+                if constexpr (SC == 2) {
+                    const float4 r0 = lds128(smem_u32(&s.rv[at][G0]));
+                    const float rv[4] = {r0.x, r0.y, r0.z, r0.w};
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) add += !PLAIN && sums[g] == 0.0f ? 0.0f : sums[g] * rv[g];
+                }
+                return most;
             };
-            if (whole) probabilities(std::integral_constant<bool, SC == 1>(), std::false_type());
-            else probabilities(std::true_type(), std::true_type());
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full[t]);
+            // Most halves keep the reference that they find: the row's largest x then lies so little above it that no p'
+            // exceeds kMost, which the sums of 16 show without a maximum.
+            auto half_step = [&](auto half) -> bool {
+                constexpr int h = decltype(half)::value;
+                bool again = !whole || __any_sync(0xffffffffu, m == -INFINITY);
+                float most = 0.0f;
+                if (!again) {
+                    most = probabilities(half, m - kShift, std::true_type());
+                    again = __any_sync(0xffffffffu, most > kMost);
+                }
+                if (again) {
+                    // ---- the half's largest x = acc kc + lv
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                        uint32_t(&r)[16] = raw[0];
+                        tmem_ld16(lane_base + 16 * g, r);
+                        tmem_wait_ld_regs(r);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            float v[4];
+                            four(r + k, 16 * g + k, v);
+                            mx = max3f(mx, v[0], v[1]);
+                            mx = max3f(mx, v[2], v[3]);
+                        }
+                    }
+                    // ---- the reference follows where it lags
+                    const bool moves = mx > m + kSlack || (most > kMost && mx > m);
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
+                        m = to;
+                        l *= alpha;
+                        // The half before has to be in O.  (s_full says that of all halves of the steps before, so the
+                        // barrier is in the phase of the half before or in the next.)
+                        if (i > 0 || h > 0) {
+                            if (!mbar_wait_warp(&s.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(lane_base + 128 + c, o);
+                                tmem_wait_ld_regs(o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                tmem_st16(lane_base + 128 + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
+                    if (whole) probabilities(half, ref, std::true_type());
+                    else probabilities(half, ref, std::false_type());
+                }
+                l += add;
+                // ---- to TMEM over slots of S that have been read: 32 columns a half, behind which half 1 finds its own
+                tmem_st32(lane_base + 32 * h, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[t][h]);
+                return true;
+            };
+            if (!(ok = half_step(std::integral_constant<int, 0>()) && half_step(std::integral_constant<int, 1>()))) break;
         }
-        if (ok && steps > j0) ok = mbar_wait_warp(&s.o_full[t], (steps - 1 - j0) & 1, abort_flag, &g_ext_err, 9);
+        if (ok && steps > j0) ok = mbar_wait_warp(&s.o_done[t], 0, abort_flag, &g_ext_err, 9);
         tc_fence_after();
         const bool there = r0 + row < a.rows;
         const bool empty = limit == 0 || l == 0.0f;                  // saw nothing (a NaN is no 0)
@@ -871,7 +923,7 @@ static cudaError_t launch_k(const Args &a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         regs = fa.numRegs;
     }
-    if (regs * kThreads < 2 * 128 * static_cast<int>(kRegsSoftmax) + 128 * static_cast<int>(kRegsLoad + kRegsControl)) return cudaErrorInvalidConfiguration;
+    if (regs * kThreads < 256 * static_cast<int>(kRegsSoftmax + kRegsLoad) + 128 * static_cast<int>(kRegsControl)) return cudaErrorInvalidConfiguration;
     const long long grid = static_cast<long long>(a.c.B) * a.c.H * a.tiles * a.splits;
     kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
