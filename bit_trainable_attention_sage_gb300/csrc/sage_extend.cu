@@ -49,8 +49,8 @@ namespace ext {
 constexpr int kThreads = 640;
 constexpr int kKeyWarp = 8, kValueWarp = 12;    // 8 .. 11, 12 .. 15
 constexpr int kMmaWarp = 16;                // (17 .. 19 are idle)
-// Launched at 96 registers a thread (640 x 96 = 61440): 256 x 120 + 256 x 88 + 128 x 64 = 61440.
-constexpr uint32_t kRegsSoftmax = 120, kRegsLoad = 88, kRegsControl = 64;
+// Launched at 96 registers a thread (640 x 96 = 61440): 256 x 128 + 256 x 72 + 128 x 80 = 61440.
+constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 72, kRegsControl = 80;
 constexpr int kRows = 256;                  // of a CTA
 constexpr int kStep = 128;                  // slots a step
 constexpr int kExtMaxSplits = 16;
@@ -341,20 +341,23 @@ struct Loader {
             }
         };
         if constexpr (SC != 0) {
-            uint4 x[ITS];                                            // 8-bit rows, one step ahead
-            auto load = [&](int j) {
-                uint32_t rows[ITS];
+            // 8-bit rows, half a step (64 rows) at a time and half a step ahead.  (A whole step at a time is twice the code, and
+            // the instruction cache is shared with the softmax's.)
+            constexpr int HALF = ITS / 2;
+            uint4 x[HALF];
+            auto load = [&](int j, int h) {
+                uint32_t rows[HALF];
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) rows[i] = row_of(rr + i * RPI);
+                for (int i = 0; i < HALF; ++i) rows[i] = row_of(64 * h + rr + i * RPI);
                 const uint4 *from = static_cast<const uint4 *>(pool) + cc;
                 if (plain) {
 #pragma unroll
-                    for (int i = 0; i < ITS; ++i) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                    for (int i = 0; i < HALF; ++i) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < ITS; ++i) {
+                    for (int i = 0; i < HALF; ++i) {
                         x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (rows[i] != kNone && j * kStep + rr + i * RPI < kv_end) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                        if (rows[i] != kNone && j * kStep + 64 * h + rr + i * RPI < kv_end) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                     }
                 }
             };
@@ -362,15 +365,16 @@ struct Loader {
             find(j0);
             look(j0 + 1);
             if (!VALUES) load_scales(j0);
-            load(j0);
+            load(j0, 0);
             query(VALUES);
-            for (int j = j0; j < j1; ++j) {
-                const int i = j - j0, st = i & 1;
-                if (!free_of(free, i)) break;
+#pragma unroll 1
+            for (int u = 0; u < 2 * (j1 - j0); ++u) {
+                const int i = u >> 1, h = u & 1, j = j0 + i, st = i & 1;
+                if (h == 0 && !free_of(free, i)) break;
                 if constexpr (VALUES && FP8) {
                     if (j >= mixed) {
 #pragma unroll
-                        for (int y = 0; y < ITS; ++y) {
+                        for (int y = 0; y < HALF; ++y) {
                             uint32_t *w = &x[y].x;
                             uint32_t bad = 0;
 #pragma unroll
@@ -383,15 +387,18 @@ struct Loader {
                         }
                     }
                 }
-                if constexpr (VALUES) store_codes<BF16, FP8, ITS, RPI>(smem_u32(s.v[st][0]), x, rr, cc);
-                else store_codes<false, FP8, ITS, RPI>(smem_u32(s.k[st][0]), x, rr, cc);
-                if (!VALUES) store_scales(i);
-                done(&full[st]);
-                if (j + 1 < j1) {
-                    find(j + 1);
-                    look(j + 2);
-                    if (!VALUES) load_scales(j + 1);
-                    load(j + 1);
+                store_codes<VALUES && BF16, FP8, HALF, RPI>(smem_u32(VALUES ? s.v[st][0] : s.k[st][0]), x, 64 * h + rr, cc);
+                if (h == 0) {
+                    load(j, 1);
+                    if (!VALUES) store_scales(i);
+                } else {
+                    done(&full[st]);
+                    if (j + 1 < j1) {
+                        find(j + 1);
+                        look(j + 2);
+                        load(j + 1, 0);
+                        if (!VALUES) load_scales(j + 1);
+                    }
                 }
             }
         } else {
@@ -609,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
             uint32_t raw[2][16];                                     // S, 16 slots a group, a group ahead
-            auto load_group = [&](int g) { tmem_ld16(lane_base + 16 * g, raw[g & 1]); };
             // x of slots k .. k + 3 of the step (hidden ones: -inf)
             auto four = [&](const uint32_t *r, int k, float (&v)[4]) {
                 float4 kc = make_float4(a.sl2, a.sl2, a.sl2, a.sl2), lv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -635,40 +641,38 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             };
             // (scales of blocks: read at once and ahead, not a group at a time: shared memory answers slowly beside the
             // products' operands and the loaders' stores)
-            [[maybe_unused]] float kcs[8], lvs[8];
+            [[maybe_unused]] float4 kc4, lv4, kc4n, lv4n;            // of this half and of the next
             if constexpr (SC == 2) {
-                const float4 k0 = lds128(smem_u32(&s.kc[at][0])), k1 = lds128(smem_u32(&s.kc[at][4]));
-                const float4 l0 = lds128(smem_u32(&s.lv[at][0])), l1 = lds128(smem_u32(&s.lv[at][4]));
-                kcs[0] = k0.x; kcs[1] = k0.y; kcs[2] = k0.z; kcs[3] = k0.w; kcs[4] = k1.x; kcs[5] = k1.y; kcs[6] = k1.z; kcs[7] = k1.w;
-                lvs[0] = l0.x; lvs[1] = l0.y; lvs[2] = l0.z; lvs[3] = l0.w; lvs[4] = l1.x; lvs[5] = l1.y; lvs[6] = l1.z; lvs[7] = l1.w;
+                kc4 = lds128(smem_u32(&s.kc[at][0])); kc4n = lds128(smem_u32(&s.kc[at][4]));
+                lv4 = lds128(smem_u32(&s.lv[at][0])); lv4n = lds128(smem_u32(&s.lv[at][4]));
             }
             // Half h of the step, 64 slots: p' = 2^(x - ref), packed, and their l; the largest sum of 16 of them
             uint32_t pk[32];
             float add;
-            auto probabilities = [&](auto half, float ref, auto plain) -> float {
+            auto probabilities = [&](const int h, float ref, auto plain) -> float {
                 constexpr bool PLAIN = decltype(plain)::value;       // no slot is hidden
-                constexpr int G0 = 4 * decltype(half)::value;
+                const uint32_t from = lane_base + 64 * h;
                 float most = 0.0f;
                 [[maybe_unused]] float sums[4];
                 add = 0.0f;
-                load_group(G0);
+                tmem_ld16(from, raw[0]);
 #pragma unroll
-                for (int g = G0; g < G0 + 4; ++g) {
+                for (int g = 0; g < 4; ++g) {
                     tmem_wait_ld_regs(raw[g & 1]);
-                    if (g < G0 + 3) load_group(g + 1);
+                    if (g < 3) tmem_ld16(from + 16 * (g + 1), raw[(g + 1) & 1]);
                     uint32_t(&r)[16] = raw[g & 1];
                     f2 sum{0.0f, 0.0f};
                     [[maybe_unused]] f2 l2{0.0f, 0.0f};
                     f2 f{a.sl2, a.sl2}, off{-ref, -ref};
                     if constexpr (SC == 2 && PLAIN) {
-                        f.x = f.y = kcs[g] * qs;
-                        off.x = off.y = lvs[g] - ref;
+                        f.x = f.y = (g == 0 ? kc4.x : g == 1 ? kc4.y : g == 2 ? kc4.z : kc4.w) * qs;
+                        off.x = off.y = (g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w) - ref;
                     }
                     if constexpr (SC == 1 || !PLAIN) {
 #pragma unroll
                         for (int k = 0; k < 16; k += 4) {
                             float v[4];
-                            four(&r[k], 16 * g + k, v);
+                            four(&r[k], 64 * h + 16 * g + k, v);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) r[k + e] = __float_as_uint(v[e]);
                         }
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
                         sum = add2(sum, p);
                         if constexpr (SC == 1) {
-                            const f2 rv{s.rv[at][16 * g + k], s.rv[at][16 * g + k + 1]};
+                            const f2 rv{s.rv[at][64 * h + 16 * g + k], s.rv[at][64 * h + 16 * g + k + 1]};
                             if constexpr (PLAIN) {
                                 l2 = fma2(p, rv, l2);
                             } else {                                 // (a hidden slot's reciprocal may be anything)
@@ -688,16 +692,16 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                                 l2.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
                             }
                         }
-                        pk[8 * (g - G0) + k / 2] = pack2<BF16>(p.x, p.y);
+                        pk[8 * g + k / 2] = pack2<BF16>(p.x, p.y);
                     }
                     const float both = sum.x + sum.y;
                     most = fmaxf(most, both);
                     if constexpr (SC == 1) add += l2.x + l2.y;
-                    else if constexpr (SC == 2) sums[g - G0] = both;
+                    else if constexpr (SC == 2) sums[g] = both;
                     else add += both;
                 }
                 if constexpr (SC == 2) {
-                    const float4 r0 = lds128(smem_u32(&s.rv[at][G0]));
+                    const float4 r0 = lds128(smem_u32(&s.rv[at][4 * h]));
                     const float rv[4] = {r0.x, r0.y, r0.z, r0.w};
 #pragma unroll
                     for (int g = 0; g < 4; ++g) add += !PLAIN && sums[g] == 0.0f ? 0.0f : sums[g] * rv[g];
@@ -706,12 +710,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             };
             // Most halves keep the reference that they find: the row's largest x then lies so little above it that no p'
             // exceeds kMost, which the sums of 16 show without a maximum.
-            auto half_step = [&](auto half) -> bool {
-                constexpr int h = decltype(half)::value;
+            auto half_step = [&](const int h) __attribute__((always_inline)) -> bool {
                 bool again = !whole || __any_sync(0xffffffffu, m == -INFINITY);
                 float most = 0.0f;
                 if (!again) {
-                    most = probabilities(half, m - kShift, std::true_type());
+                    most = probabilities(h, m - kShift, std::true_type());
                     again = __any_sync(0xffffffffu, most > kMost);
                 }
                 if (again) {
@@ -754,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         }
                     }
                     const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
-                    if (whole) probabilities(half, ref, std::true_type());
-                    else probabilities(half, ref, std::false_type());
+                    if (whole) probabilities(h, ref, std::true_type());
+                    else probabilities(h, ref, std::false_type());
                 }
                 l += add;
                 // ---- to TMEM over slots of S that have been read: 32 columns a half, behind which half 1 finds its own
@@ -764,9 +767,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.p_full[t][h]);
+                if constexpr (SC == 2) {
+                    kc4 = kc4n;
+                    lv4 = lv4n;
+                }
                 return true;
             };
-            if (!(ok = half_step(std::integral_constant<int, 0>()) && half_step(std::integral_constant<int, 1>()))) break;
+            // One copy of the code where the loaders widen codes beside it, whose instruction cache it shares; with a scale a
+            // row, whose vectors are read at constant places, and over 16-bit pools two.
+            if constexpr (SC == 2) {
+#pragma unroll 1
+                for (int h = 0; h < 2 && ok; ++h) ok = half_step(h);
+            } else {
+                ok = half_step(0) && half_step(1);
+            }
+            if (!ok) break;
         }
         if (ok && steps > j0) ok = mbar_wait_warp(&s.o_done[t], 0, abort_flag, &g_ext_err, 9);
         tc_fence_after();
