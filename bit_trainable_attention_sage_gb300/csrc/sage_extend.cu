@@ -172,6 +172,24 @@ __device__ __forceinline__ void store_codes(uint32_t to, const uint4 (&from)[N],
     }
 }
 
+// Bounded wait of a warp until K of a step has been stored.  S of the step says so too: by then K's barrier may have
+// gone on to the phase after the next, whose parity is that of one not yet over.
+__device__ __forceinline__ bool wait_either(uint64_t *k_full, uint32_t k_parity, uint64_t *s_full, uint32_t s_parity, volatile int *abort_flag) {
+    bool ok = true;
+    const unsigned long long t0 = clock64();
+    for (uint32_t it = 1; !mbar_try_wait(k_full, k_parity) && !mbar_try_wait(s_full, s_parity); ++it) {
+        if ((it & 15u) == 0u && (*abort_flag || clock64() - t0 > SAGE_WAIT_CYCLES)) {
+            if (!*abort_flag) {
+                *abort_flag = 1;
+                atomicOr(&g_ext_err, 1u | (10u << 8));
+            }
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // What a sequence brings: its first new slot, its new tokens and its slots in all, held to what exists.
 struct Seq {
     int start, count, len;
@@ -606,13 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         const int steps = t ? n_t[1] : n_t[0];
         const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 256 * t);
         float m = -INFINITY, l = 0.0f;                               // reference of O and l; l
-        bool ok = true;
-        for (int j = j0; j < steps; ++j) {
+        bool ok = steps <= j0 || mbar_wait_warp(&s.q_full, 0, abort_flag, &g_ext_err, 11);
+        const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
+        for (int j = j0; j < steps && ok; ++j) {
             const int i = j - j0, at = i & 3;
-            if (!(ok = mbar_wait_warp(&s.s_full[t], i & 1, abort_flag, &g_ext_err, 7))) break;
-            tc_fence_after();
+            // What the step's scales say is read ahead of its S, not a group at a time: shared memory answers slowly beside
+            // the products' operands and the loaders' stores.
+            if (!(ok = wait_either(&s.k_full[i & 1], (i >> 1) & 1, &s.s_full[t], i & 1, abort_flag))) break;
             const uint32_t holes = s.holes[at];
-            const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
             uint32_t raw[2][16];                                     // S, 16 slots a group, a group ahead
@@ -639,13 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         if (none || k + e >= seen) v[e] = -INFINITY;
                 }
             };
-            // (scales of blocks: read at once and ahead, not a group at a time: shared memory answers slowly beside the
-            // products' operands and the loaders' stores)
-            [[maybe_unused]] float4 kc4, lv4, kc4n, lv4n;            // of this half and of the next
+            [[maybe_unused]] float4 kc4, lv4, rv4, kc4n, lv4n, rv4n; // of this half and of the next
             if constexpr (SC == 2) {
                 kc4 = lds128(smem_u32(&s.kc[at][0])); kc4n = lds128(smem_u32(&s.kc[at][4]));
                 lv4 = lds128(smem_u32(&s.lv[at][0])); lv4n = lds128(smem_u32(&s.lv[at][4]));
+                rv4 = lds128(smem_u32(&s.rv[at][0])); rv4n = lds128(smem_u32(&s.rv[at][4]));
             }
+            if (!(ok = mbar_wait_warp(&s.s_full[t], i & 1, abort_flag, &g_ext_err, 7))) break;
+            tc_fence_after();
             // Half h of the step, 64 slots: p' = 2^(x - ref), packed, and their l; the largest sum of 16 of them
             uint32_t pk[32];
             float add;
@@ -701,64 +721,81 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     else add += both;
                 }
                 if constexpr (SC == 2) {
-                    const float4 r0 = lds128(smem_u32(&s.rv[at][4 * h]));
-                    const float rv[4] = {r0.x, r0.y, r0.z, r0.w};
+                    const float rvs[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) add += !PLAIN && sums[g] == 0.0f ? 0.0f : sums[g] * rv[g];
+                    for (int g = 0; g < 4; ++g) add += !PLAIN && sums[g] == 0.0f ? 0.0f : sums[g] * rvs[g];
                 }
                 return most;
+            };
+            // The reference follows half h's largest x = acc kc + lv where it lags.  False: a wait gave up.
+            auto follow = [&](const int h, float most) __attribute__((always_inline)) -> bool {
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                    uint32_t(&r)[16] = raw[0];
+                    tmem_ld16(lane_base + 16 * g, r);
+                    tmem_wait_ld_regs(r);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        float v[4];
+                        four(r + k, 16 * g + k, v);
+                        mx = max3f(mx, v[0], v[1]);
+                        mx = max3f(mx, v[2], v[3]);
+                    }
+                }
+                const bool moves = mx > m + kSlack || (most > kMost && mx > m);
+                if (!__any_sync(0xffffffffu, moves)) return true;
+                const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
+                m = to;
+                l *= alpha;
+                if (i == 0 && h == 0) return true;
+                // The half before has to be in O.  (s_full says that of all halves of the steps before, so the
+                // barrier is in the phase of the half before or in the next.)
+                if (!mbar_wait_warp(&s.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(lane_base + 128 + c, o);
+                    tmem_wait_ld_regs(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    tmem_st16(lane_base + 128 + c, o);
+                }
+                tmem_wait_st();
+                return true;
             };
             // Most halves keep the reference that they find: the row's largest x then lies so little above it that no p'
             // exceeds kMost, which the sums of 16 show without a maximum.
             auto half_step = [&](const int h) __attribute__((always_inline)) -> bool {
-                bool again = !whole || __any_sync(0xffffffffu, m == -INFINITY);
+                bool known = whole && !__any_sync(0xffffffffu, m == -INFINITY);
                 float most = 0.0f;
-                if (!again) {
-                    most = probabilities(h, m - kShift, std::true_type());
-                    again = __any_sync(0xffffffffu, most > kMost);
-                }
-                if (again) {
-                    // ---- the half's largest x = acc kc + lv
-                    float mx = -INFINITY;
+                if constexpr (SC == 2) {
+                    // (at most twice round)
+                    bool sure = false;
 #pragma unroll 1
-                    for (int g = 4 * h; g < 4 * h + 4; ++g) {
-                        uint32_t(&r)[16] = raw[0];
-                        tmem_ld16(lane_base + 16 * g, r);
-                        tmem_wait_ld_regs(r);
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            float v[4];
-                            four(r + k, 16 * g + k, v);
-                            mx = max3f(mx, v[0], v[1]);
-                            mx = max3f(mx, v[2], v[3]);
+                    for (;;) {
+                        if (known) {
+                            most = probabilities(h, m - kShift, std::true_type());
+                            if (sure || !__any_sync(0xffffffffu, most > kMost)) break;
                         }
+                        if (!follow(h, most)) return false;
+                        known = sure = whole && !__any_sync(0xffffffffu, m == -INFINITY);
+                        if (known) continue;
+                        probabilities(h, m == -INFINITY ? 0.0f : m - kShift, std::false_type());   // (nothing seen yet: all terms are 0)
+                        break;
                     }
-                    // ---- the reference follows where it lags
-                    const bool moves = mx > m + kSlack || (most > kMost && mx > m);
-                    if (__any_sync(0xffffffffu, moves)) {
-                        const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
-                        m = to;
-                        l *= alpha;
-                        // The half before has to be in O.  (s_full says that of all halves of the steps before, so the
-                        // barrier is in the phase of the half before or in the next.)
-                        if (i > 0 || h > 0) {
-                            if (!mbar_wait_warp(&s.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(lane_base + 128 + c, o);
-                                tmem_wait_ld_regs(o);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                                tmem_st16(lane_base + 128 + c, o);
-                            }
-                            tmem_wait_st();
-                        }
+                } else {
+                    if (known) {
+                        most = probabilities(h, m - kShift, std::true_type());
+                        known = !__any_sync(0xffffffffu, most > kMost);
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m - kShift;    // nothing seen yet: all terms are 0
-                    if (whole) probabilities(h, ref, std::true_type());
-                    else probabilities(h, ref, std::false_type());
+                    if (!known) {
+                        if (!follow(h, most)) return false;
+                        const float ref = m == -INFINITY ? 0.0f : m - kShift;
+                        if (whole) probabilities(h, ref, std::true_type());
+                        else probabilities(h, ref, std::false_type());
+                    }
                 }
                 l += add;
                 // ---- to TMEM over slots of S that have been read: 32 columns a half, behind which half 1 finds its own
@@ -770,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 if constexpr (SC == 2) {
                     kc4 = kc4n;
                     lv4 = lv4n;
+                    rv4 = rv4n;
                 }
                 return true;
             };
