@@ -236,13 +236,13 @@ static void launch_append_d(const AppendArgs &a, int d, cudaStream_t st) {
 // Blocks of R = 16, 32 or 64 slots share s = fl32(max|x| / M).  A block that begins with the call's rows
 // takes its scale from them; one that goes on (rows before `start`) keeps the larger of its scale and theirs,
 // and where that grows its kept rows' codes become the nearest of fl32(code * fl32(s_old / s)).
-// A CTA takes a block of one head: its rows stay in registers between the maximum and the codes, so that
+// A CTA takes a block of K or of V of one head (both would hold twice the registers): its rows stay in registers between the maximum and the codes, so that
 // every element is read once and written once, and only a block whose scale grows reads codes.
 // ---------------------------------------------------------------------------------------------
 template <int D, int R>
 struct AppendBlock {
     static constexpr int LANES = D / 16;
-    static constexpr int THREADS = R * LANES < 256 ? R * LANES : 256;
+    static constexpr int THREADS = R * LANES < 128 ? 32 : R * LANES / 4;
     static constexpr int GROUPS = THREADS / LANES;               // rows at a time
     static constexpr int ROWS = R / GROUPS;                      // rows a lane group
 };
@@ -270,15 +270,92 @@ __device__ __forceinline__ uint2 kv_rescaled(uint2 codes, float r) {
     return make_uint2(w[0], w[1]);
 }
 
-// grid: (blocks of a sequence that T tokens can touch, B * H)
+// One block of K or of V: x, its pool and scales.
 template <typename T, int KIND, int D, int R, bool SMOOTH>
-__global__ void __launch_bounds__(AppendBlock<D, R>::THREADS) kv_append_block_kernel(const AppendArgs a) {
+__device__ __forceinline__ void append_block(const AppendArgs &a, const void *x_in, void *pool, float *scales, const float *mu_in, int bh, int n, long long start,
+                                             long long s0, int b, int h) {
     using S = AppendBlock<D, R>;
     constexpr int LANES = S::LANES, WARPS = S::THREADS / 32;
     constexpr int SHIFT = R == 16 ? 4 : R == 32 ? 5 : 6;
-    __shared__ float s_max[2][WARPS];
-    const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
+    __shared__ float s_max[WARPS];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    // this lane group's rows: slots s0 + group + i * GROUPS, tokens t0 + i * GROUPS
+    uint4 in[S::ROWS][2];
+    const int t0 = static_cast<int>(s0 - start) + group;             // (at least -R, below 2^30)
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const int t = t0 + i * S::GROUPS;
+        in[i][0] = in[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (t >= 0 && t < n) {
+            const uint4 *X = static_cast<const uint4 *>(x_in) + (static_cast<size_t>(bh) * a.T + t) * (2 * LANES) + lane;
+            in[i][0] = __ldg(X);
+            in[i][1] = __ldg(X + LANES);
+        }
+    }
+    const int p = kv_page(a.c, b, static_cast<int>(s0), &g_kv_err);
+    if (p < 0) return;                               // the whole CTA alike
+    const size_t row0 = kv_row(a.c, p, h, static_cast<int>(s0)), place = row0 >> SHIFT;
+    const bool goes_on = start > s0;
+    const float old = goes_on ? scales[place] : 0.0f;
+    // (kept as float32: forming the values again for the codes costs more than the registers)
+    f2 x[S::ROWS][8];
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) unpack16<T>(in[i], x[i]);
+    if constexpr (SMOOTH) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float4 *m = reinterpret_cast<const float4 *>(mu_in + static_cast<size_t>(bh) * D + (lane + c * LANES) * 8);
+            const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
+#pragma unroll
+            for (int i = 0; i < S::ROWS; ++i) {
+                x[i][4 * c] = sub2(x[i][4 * c], f2{m0.x, m0.y});
+                x[i][4 * c + 1] = sub2(x[i][4 * c + 1], f2{m0.z, m0.w});
+                x[i][4 * c + 2] = sub2(x[i][4 * c + 2], f2{m1.x, m1.y});
+                x[i][4 * c + 3] = sub2(x[i][4 * c + 3], f2{m1.z, m1.w});
+            }
+        }
+    }
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const int t = t0 + i * S::GROUPS;
+        float m = larger(x[i][0].x, x[i][0].y);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = larger(m, larger(x[i][j].x, x[i][j].y));
+        if (t >= 0 && t < n) most = larger(most, m);                 // (other rows' zeros less mu are no values)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = larger(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = most;
+    __syncthreads();                                 // and every thread has the old scale
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) most = larger(most, s_max[w]);
+    float s = scales_of<KIND>(f2{fabsf(most), fabsf(most)}).x;
+    if (goes_on) s = fabsf(larger(s, old));
+    if (threadIdx.x == 0) scales[place] = s;
+    const bool grew = goes_on && s > old;
+    const float ratio = grew ? __fdiv_rn(old, s) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < S::ROWS; ++i) {
+        const int t = t0 + i * S::GROUPS;
+        uint2 *to = static_cast<uint2 *>(pool) + (row0 + group + i * S::GROUPS) * (2 * LANES) + lane;
+        if (t >= 0 && t < n) {
+            uint2 c[2];
+            kv_codes<KIND, !SMOOTH>(x[i], s, c);
+            to[0] = c[0];
+            to[LANES] = c[1];
+        } else if (t < 0 && grew) {                  // a kept row
+            to[0] = kv_rescaled<KIND>(to[0], ratio);
+            to[LANES] = kv_rescaled<KIND>(to[LANES], ratio);
+        }
+    }
+}
+
+// grid: (blocks of a sequence that T tokens can touch, B * H, K and V)
+template <typename T, int KIND, int D, int R, bool SMOOTH>
+__global__ void __launch_bounds__(AppendBlock<D, R>::THREADS, 896 / AppendBlock<D, R>::THREADS) kv_append_block_kernel(const AppendArgs a) {
+    constexpr int SHIFT = R == 16 ? 4 : R == 32 ? 5 : 6;
+    const int bh = blockIdx.y, b = bh / a.c.H, h = bh - b * a.c.H;
     int n = a.T;
     if (a.count) {
         n = __ldg(a.count + b);
@@ -294,118 +371,13 @@ __global__ void __launch_bounds__(AppendBlock<D, R>::THREADS) kv_append_block_ke
         if (threadIdx.x == 0) atomicOr(&g_kv_err, 1u);
         return;
     }
-    // this lane group's rows: slots s0 + group + i * GROUPS
-    uint4 k[S::ROWS][2], v[S::ROWS][2];
-    const long long t0 = s0 - start + group;
-#pragma unroll
-    for (int i = 0; i < S::ROWS; ++i) {
-        const long long t = t0 + i * S::GROUPS;
-        k[i][0] = k[i][1] = v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (t >= 0 && t < n) {
-            const size_t at = (static_cast<size_t>(bh) * a.T + t) * (2 * LANES) + lane;
-            const uint4 *K = static_cast<const uint4 *>(a.K) + at, *V = static_cast<const uint4 *>(a.V) + at;
-            k[i][0] = __ldg(K);
-            k[i][1] = __ldg(K + LANES);
-            v[i][0] = __ldg(V);
-            v[i][1] = __ldg(V + LANES);
-        }
-    }
-    const int p = kv_page(a.c, b, static_cast<int>(s0), &g_kv_err);
-    if (p < 0) return;                               // the whole CTA alike
-    const size_t row0 = kv_row(a.c, p, h, static_cast<int>(s0)), place = row0 >> SHIFT;
-    const bool goes_on = start > s0;
-    f2 old{0.0f, 0.0f};
-    if (goes_on) old = f2{a.c.sK[place], a.c.sV[place]};
-    f2 mu[8];
-    if constexpr (SMOOTH) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const float4 *m = reinterpret_cast<const float4 *>(a.mu + static_cast<size_t>(bh) * D + (lane + c * LANES) * 8);
-            const float4 m0 = __ldg(m), m1 = __ldg(m + 1);
-            mu[4 * c] = f2{m0.x, m0.y};
-            mu[4 * c + 1] = f2{m0.z, m0.w};
-            mu[4 * c + 2] = f2{m1.x, m1.y};
-            mu[4 * c + 3] = f2{m1.z, m1.w};
-        }
-    }
-    auto values = [&](const uint4 (&u)[2], bool key, f2 (&x)[8]) {
-        unpack16<T>(u, x);
-        if constexpr (SMOOTH) {
-            if (key) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = sub2(x[j], mu[j]);
-            }
-        }
-    };
-    float mk = 0.0f, mv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < S::ROWS; ++i) {
-        const long long t = t0 + i * S::GROUPS;
-        if (t >= 0 && t < n) {                       // (other rows' zeros less mu are no values)
-            f2 x[8];
-            values(k[i], true, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mk = larger(mk, larger(x[j].x, x[j].y));
-            values(v[i], false, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mv = larger(mv, larger(x[j].x, x[j].y));
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        mk = larger(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = larger(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
-    if (threadIdx.x % 32 == 0) {
-        s_max[0][threadIdx.x / 32] = mk;
-        s_max[1][threadIdx.x / 32] = mv;
-    }
-    __syncthreads();                                 // and every thread has the old scales
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        mk = larger(mk, s_max[0][w]);
-        mv = larger(mv, s_max[1][w]);
-    }
-    f2 s = scales_of<KIND>(f2{fabsf(mk), fabsf(mv)});
-    if (goes_on) s = f2{fabsf(larger(s.x, old.x)), fabsf(larger(s.y, old.y))};
-    if (threadIdx.x == 0) {
-        a.c.sK[place] = s.x;
-        a.c.sV[place] = s.y;
-    }
-    const bool more_k = goes_on && s.x > old.x, more_v = goes_on && s.y > old.y;
-    const float rk = more_k ? __fdiv_rn(old.x, s.x) : 1.0f, rv = more_v ? __fdiv_rn(old.y, s.y) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < S::ROWS; ++i) {
-        const long long t = t0 + i * S::GROUPS;
-        const size_t at = (row0 + group + i * S::GROUPS) * (2 * LANES) + lane;
-        uint2 *K = static_cast<uint2 *>(a.c.K) + at, *V = static_cast<uint2 *>(a.c.V) + at;
-        if (t >= 0 && t < n) {
-            f2 x[8];
-            uint2 c[2];
-            values(k[i], true, x);
-            kv_codes<KIND, !SMOOTH>(x, s.x, c);
-            K[0] = c[0];
-            K[LANES] = c[1];
-            values(v[i], false, x);
-            kv_codes<KIND, true>(x, s.y, c);
-            V[0] = c[0];
-            V[LANES] = c[1];
-        } else if (t < 0) {                          // a kept row
-            if (more_k) {
-                K[0] = kv_rescaled<KIND>(K[0], rk);
-                K[LANES] = kv_rescaled<KIND>(K[LANES], rk);
-            }
-            if (more_v) {
-                V[0] = kv_rescaled<KIND>(V[0], rv);
-                V[LANES] = kv_rescaled<KIND>(V[LANES], rv);
-            }
-        }
-    }
+    if (blockIdx.z == 0) append_block<T, KIND, D, R, SMOOTH>(a, a.K, a.c.K, a.c.sK, a.mu, bh, n, start, s0, b, h);
+    else append_block<T, KIND, D, R, false>(a, a.V, a.c.V, a.c.sV, nullptr, bh, n, start, s0, b, h);
 }
 
 template <typename T, int KIND, int D, int R>
 static void launch_append_block_r(const AppendArgs &a, cudaStream_t st) {
-    const dim3 grid((a.T + R - 2) / R + 1, static_cast<unsigned>(a.c.B) * a.c.H);
+    const dim3 grid((a.T + R - 2) / R + 1, static_cast<unsigned>(a.c.B) * a.c.H, 2);
     if (a.mu) kv_append_block_kernel<T, KIND, D, R, true><<<grid, AppendBlock<D, R>::THREADS, 0, st>>>(a);
     else kv_append_block_kernel<T, KIND, D, R, false><<<grid, AppendBlock<D, R>::THREADS, 0, st>>>(a);
 }
