@@ -237,7 +237,10 @@ static void launch_append_d(const AppendArgs &a, int d, cudaStream_t st) {
 // takes its scale from them; one that goes on (rows before `start`) keeps the larger of its scale and theirs,
 // and where that grows its kept rows' codes become the nearest of fl32(code * fl32(s_old / s)).
 // A CTA takes a block of K or of V of one head (both would hold twice the registers): its rows stay in registers between the maximum and the codes, so that
-// every element is read once and written once, and only a block whose scale grows reads codes.
+// every element is read once and written once, and only a block whose scale grows reads codes.  Few threads
+// with four rows each, so that the barrier between the two holds few up: 64 heads of up to 8192 tokens, d = 128, to
+// E4M3 with smoothing 60 us, 5.4 TB/s (256 threads 70, 512 threads 94; K and V in one CTA 80), bound by issuing the
+// arithmetic as above; single tokens by latency (3 us).
 // ---------------------------------------------------------------------------------------------
 template <int D, int R>
 struct AppendBlock {

@@ -24,6 +24,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kAll = kCluster * kThreads;
 constexpr int kCopyThreads = 256;
+constexpr int kSmall = 2048;                 // sequences whose children a CTA counts in its shared memory
 
 struct Args {
     KvView c;
@@ -46,37 +47,43 @@ struct Args {
 
 __device__ __forceinline__ int cluster_rank() { return blockIdx.x; }     // the grid is one cluster
 
-// The sum of `mine` over the cluster's threads before this one, and over all of them.  One call a place `slot`
-// of s_total (a place is read by other CTAs until the next barrier of the cluster).
+// The sums of x and y over the cluster's threads before this one, and over all of them.  (Read by other CTAs until the
+// next barrier of the cluster.)
 struct Prefix {
-    int before, total;
+    int before[2], total[2];
 };
-__device__ __forceinline__ Prefix prefix(int mine, int *s_total, int *s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = mine;
+__device__ __forceinline__ Prefix prefix(int x, int y, int (&s_total)[2], int (&s_warp)[2][kWarps]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine[2] = {x, y};
+    Prefix p{};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+    for (int k = 0; k < 2; ++k) {
+        int incl = mine[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s_warp[k][warp] = incl;
+        p.before[k] = incl - mine[k];
     }
-    if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    Prefix p{incl - mine, 0};
-    int cta = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const int n = s_warp[w];
-        if (w < warp) p.before += n;
-        cta += n;
+    if (warp < 2) {
+        const int sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[warp][lane] : 0);
+        if (lane == 0) s_total[warp] = sum;
     }
-    if (threadIdx.x == 0) *s_total = cta;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) p.before[k] += w < warp ? s_warp[k][w] : 0;
     cluster_sync();
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
-        const int n = cluster_word(s_total, r);
-        if (r < cluster_rank()) p.before += n;
-        p.total += n;
-    }
+    for (int r = 0; r < kCluster; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = cluster_word(&s_total[k], r);
+            if (r < cluster_rank()) p.before[k] += n;
+            p.total[k] += n;
+        }
     return p;
 }
 
@@ -108,21 +115,25 @@ __device__ __forceinline__ bool is_page(const Args &a, int p) {
     return false;
 }
 
-// The first `wanted` free pages in ascending order to a.list, and how many there are in all.
-__device__ __forceinline__ int list_free(const Args &a, int wanted, int *s_total, int *s_warp) {
-    int begin, end, n = 0;
+// This thread's pages that are free.
+__device__ __forceinline__ int free_pages(const Args &a, int &begin, int &end) {
     part_of(a.c.pages, begin, end);
+    int n = 0;
     for (int p = begin; p < end; ++p) n += __ldcg(a.refs + p) == 0;
-    const Prefix f = prefix(n, s_total, s_warp);
-    int at = f.before;
+    return n;
+}
+// They, n of them, to their places in the list, as far as it is wanted.
+__device__ __forceinline__ void list_free(const Args &a, int begin, int end, int n, int at, int wanted) {
     for (int p = begin; p < end && n > 0 && at < wanted; ++p)
-        if (__ldcg(a.refs + p) == 0) a.list[at++] = p;
-    return f.total;
+        if (__ldcg(a.refs + p) == 0) {
+            a.list[at++] = p;
+            --n;
+        }
 }
 
 // ---- resize --------------------------------------------------------------------------------------
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) resize_kernel(const __grid_constant__ Args a) {
-    __shared__ int s_total[2], s_warp[2][kWarps];
+    __shared__ int s_total[2][2], s_warp[2][kWarps];
     const int lane = threadIdx.x & 31, warp = cluster_rank() * kWarps + (threadIdx.x >> 5);
     // pages that are no longer wanted go back, a warp a sequence
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
@@ -134,18 +145,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) res
             *entry = -1;
         }
     }
-    // the places in the list of free pages of those that grow
+    // the places in the list of free pages of those that grow; in most steps of a decoding loop none does
     int begin, end, n = 0;
     part_of(a.c.B, begin, end);
     for (int b = begin; b < end; ++b) n += max(0, pages_of(a, __ldg(a.want + b)) - held_of(a, b));
-    const Prefix grow = prefix(n, &s_total[0], s_warp[0]);           // (a barrier of the cluster: the counts are down)
-    int at = grow.before;
-    for (int b = begin; b < end; ++b) {
-        a.need[b] = at;
-        at += max(0, pages_of(a, __ldg(a.want + b)) - held_of(a, b));
+    const Prefix grow = prefix(n, 0, s_total[0], s_warp);            // (a barrier of the cluster: the counts are down)
+    int free = 0;
+    if (grow.total[0] > 0) {                                         // the whole cluster alike
+        int at = grow.before[0], p0, p1;
+        for (int b = begin; b < end; ++b) {
+            a.need[b] = at;
+            at += max(0, pages_of(a, __ldg(a.want + b)) - held_of(a, b));
+        }
+        const int mine = free_pages(a, p0, p1);
+        __syncthreads();                                             // s_warp has been read
+        const Prefix f = prefix(mine, 0, s_total[1], s_warp);
+        list_free(a, p0, p1, mine, f.before[0], grow.total[0]);
+        free = f.total[0];
     }
-    const int free = grow.total > 0 ? list_free(a, grow.total, &s_total[1], s_warp[1]) : 0;   // (all CTAs alike)
-    cluster_sync();
+    cluster_sync();                                                  // (in either case: no CTA leaves while its sums are read)
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
         const int m = held_of(a, b), k = pages_of(a, __ldg(a.want + b));
         int got = 0;
@@ -166,7 +184,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) res
             a.out[b] = now * a.c.page;
         }
     }
-    cluster_sync();                                                  // no CTA leaves while its shared memory is read
 }
 
 // ---- fork ----------------------------------------------------------------------------------------
@@ -188,25 +205,33 @@ __device__ __forceinline__ int slots_of(const Args &a, int q, int held) {
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ Args a) {
     __shared__ int s_total[2], s_warp[2][kWarps];
+    __shared__ int s_children[kSmall], s_heir[kSmall];
     const int lane = threadIdx.x & 31, warp = cluster_rank() * kWarps + (threadIdx.x >> 5);
-    const int at = cluster_rank() * kThreads + threadIdx.x;
-    for (int b = at; b < a.c.B; b += kAll) {
-        a.children[b] = 0;
-        a.heir[b] = a.c.B;
+    // How many go on from each sequence, and which of them keeps its last pages: itself, or else the first.  Each CTA
+    // finds that for itself where the sequences are few: a barrier of the cluster costs more.
+    const bool small = a.c.B <= kSmall;
+    int *children = small ? s_children : a.children, *heirs = small ? s_heir : a.heir;
+    const int first = small ? threadIdx.x : cluster_rank() * kThreads + threadIdx.x, step = small ? kThreads : kAll;
+    for (int b = first; b < a.c.B; b += step) {
+        children[b] = 0;
+        heirs[b] = a.c.B;
     }
-    cluster_sync();
-    // how many go on from each sequence, and which of them keeps its last pages: itself, or else the first
-    for (int b = at; b < a.c.B; b += kAll) {
+    if (small) __syncthreads();
+    else cluster_sync();
+    for (int b = first; b < a.c.B; b += step) {
         const int p = parent_of(a, b);
         if (p < 0) continue;
-        atomicAdd(a.children + p, 1);
-        atomicMin(a.heir + p, p == b ? -1 : b);
+        atomicAdd(children + p, 1);
+        atomicMin(heirs + p, p == b ? -1 : b);
     }
-    cluster_sync();
+    if (small) __syncthreads();
+    else cluster_sync();
+    auto children_of = [&](int q) { return small ? s_children[q] : __ldcg(a.children + q); };
+    auto heir_of = [&](int q) { return small ? s_heir[q] : __ldcg(a.heir + q); };
     // counts of the pages, and the rows as they were, a warp a sequence
     for (int q = warp; q < a.c.B; q += kCluster * kWarps) {
-        const int h = held_of(a, q), c = __ldcg(a.children + q), full = kv_page_of(a.c, slots_of(a, q, h));
-        const bool stays = c == 1 && __ldcg(a.heir + q) == -1;
+        const int h = held_of(a, q), c = children_of(q), full = kv_page_of(a.c, slots_of(a, q, h));
+        const bool stays = c == 1 && heir_of(q) == -1;
         if (!stays) {
             for (int e = lane; e < h; e += 32) {
                 const size_t i = static_cast<size_t>(q) * a.c.max_pages + e;
@@ -217,20 +242,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
         }
         if (lane == 0) a.held0[q] = h;
     }
-    // places in the list of free pages of those that need a copy of a page in use
+    cluster_sync();                                                  // the counts are as the new rows will have them
+    // places in the list of free pages of those that need a copy of a page in use, and the list
     auto copies = [&](int b) -> bool {
         const int p = parent_of(a, b);
-        if (p < 0 || p == b || __ldcg(a.heir + p) == b) return false;
-        const int n = slots_of(a, p, held_of(a, p));
+        if (p < 0 || p == b || heir_of(p) == b) return false;
+        const int n = slots_of(a, p, __ldcg(a.held0 + p));
         return n > kv_page_of(a.c, n) * a.c.page;
     };
-    int begin, end, n = 0;
+    int begin, end, p0, p1, n = 0;
     part_of(a.c.B, begin, end);
     for (int b = begin; b < end; ++b) n += copies(b);
-    const Prefix grow = prefix(n, &s_total[0], s_warp[0]);           // (a barrier of the cluster)
-    int place = grow.before;
+    const int mine = free_pages(a, p0, p1);
+    const Prefix f = prefix(n, mine, s_total, s_warp);
+    int place = f.before[0];
     for (int b = begin; b < end; ++b) a.need[b] = copies(b) ? place++ : -1;
-    const int free = grow.total > 0 ? list_free(a, grow.total, &s_total[1], s_warp[1]) : 0;
+    list_free(a, p0, p1, mine, f.before[1], f.total[0]);
+    const int free = f.total[1];
     cluster_sync();
     // the new rows
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
@@ -241,7 +269,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
             slots = slots_of(a, p, h);
             const int full = kv_page_of(a.c, slots);
             rows = slots - full * a.c.page;
-            keep = p == b || __ldcg(a.heir + p) == b ? h : full;
+            keep = p == b || heir_of(p) == b ? h : full;
             if (want >= 0) {
                 if (want < free) {
                     src = __ldcg(a.old + static_cast<size_t>(p) * a.c.max_pages + full);
@@ -270,7 +298,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
             a.copy[3 * b + 2] = rows;
         }
     }
-    cluster_sync();
 }
 
 // ROW_BYTES / 16 lanes a row, rows [0, n) of a head from one page to another, K and V together.
@@ -312,15 +339,15 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const __grid_co
 // ---- compact ---------------------------------------------------------------------------------------
 // The i-th of the used pages from place U on (U: how many are used) moves to the i-th free page below U.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ Args a) {
-    __shared__ int s_total, s_warp[kWarps];
+    __shared__ int s_total[2], s_warp[2][kWarps];
     int begin, end, n = 0;
     part_of(a.c.pages, begin, end);
     for (int p = begin; p < end; ++p) n += __ldcg(a.refs + p) != 0;
-    const Prefix used = prefix(n, &s_total, s_warp);
-    const int U = used.total;
+    const Prefix used = prefix(n, 0, s_total, s_warp);
+    const int U = used.total[0];
     // `at` used pages lie before p: a free p below U is free page p - at of them; a used one from U on has
     // place `at` in the order of all, of which the last ones move
-    int at = used.before;
+    int at = used.before[0];
     for (int p = begin; p < end; ++p) {
         const bool there = __ldcg(a.refs + p) != 0;
         if (p == U) a.count[1] = U - at;                             // moves: free pages below U

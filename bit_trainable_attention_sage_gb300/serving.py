@@ -199,7 +199,7 @@ class KvCache:
     pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict (not with scales of
     blocks).  refs (pages) and held (B) int32, both or none, are there for a pool that sequences share
     (sage_kv_resize, sage_kv_fork, sage_kv_compact): how many table entries name each page, and how many of each
-    row's entries are its pages; these calls write them and table.  The tensors are fixed for the life of the object; their contents are the caller's and
+    row's entries are its pages; these calls write them and table, by a workspace that the object holds.  The tensors are fixed for the life of the object; their contents are the caller's and
     the calls'."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None, refs=None,
@@ -241,6 +241,8 @@ class KvCache:
         self._c = {t: ctypes.byref(SageKv(B, H, d, _DTYPES[t], self.kind | block << 8, page, pages, max_pages, K.data_ptr(), V.data_ptr(),
                                           _ptr(sK), _ptr(sV), table.data_ptr(), _ptr(score), _ptr(pos))) for t in types}
         self._bytes = {}        # workspace sizes by what they depend on
+        # the page calls' workspace: they all write table, refs and held, so that no two may run at once anyway
+        self._pages_ws = None if refs is None else _workspace(lib().sage_pages_workspace_bytes(next(iter(self._c.values()))), dev)
 
     def _struct(self, t: torch.Tensor, what: str):
         """The struct for a call on 16-bit tensors like ``t``."""
@@ -409,36 +411,35 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
 # ---- pages of a pool that sequences share ---------------------------------------------------
 
 
-def _pages_call(name, cache: KvCache, ins, out, size, workspace, stream):
+def _pages_call(name: str, cache: KvCache, ins, size: int, out, workspace, stream) -> torch.Tensor:
     """sage_kv_resize, sage_kv_fork or sage_kv_compact: int32 inputs by name, an int32 output of ``size``."""
     dev = cache.device
     if cache.refs is None:
         raise ValueError(f"{name} needs a cache with refs and held (make_kv_cache(..., pages=))")
     for what, t in ins:
-        _need(t, what, torch.int32, (cache.B,), dev)
-    if out is not None:
-        _need(out, "out", torch.int32, (size,), dev)
-    _workspace_ok(workspace, dev)
+        _need(t, what, torch.int32, cache.held.shape, dev)
     if _elsewhere(stream, dev):
         with _on(stream, dev):
-            return _pages_call(name, cache, ins, out, size, workspace, None)
-    c = next(iter(cache._c.values()))
-    nbytes = cache._bytes.get("pages")
-    if nbytes is None:
-        nbytes = cache._bytes["pages"] = lib().sage_pages_workspace_bytes(c)
-    new = torch.empty(size, dtype=torch.int32, device=dev) if out is None else out
-    ws = _workspace(nbytes, dev) if workspace is None else workspace
-    st = getattr(lib(), name)(c, cache.refs.data_ptr(), cache.held.data_ptr(), *[t.data_ptr() for _, t in ins], new.data_ptr(), ws.data_ptr(),
-                              nbytes if workspace is None else ws.numel() * ws.element_size(), _current(dev))
+            return _pages_call(name, cache, ins, size, out, workspace, None)
+    if out is None:
+        out = torch.empty(size, dtype=torch.int32, device=dev)
+    else:
+        _need(out, "out", torch.int32, (size,), dev)
+    if workspace is None:
+        workspace = cache._pages_ws
+    else:
+        _workspace_ok(workspace, dev)
+    st = getattr(lib(), name)(next(iter(cache._c.values())), cache.refs.data_ptr(), cache.held.data_ptr(), *[t.data_ptr() for _, t in ins],
+                              out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current(dev))
     _check(name, st)
-    return new
+    return out
 
 
 def sage_kv_resize(cache: KvCache, want: torch.Tensor, *, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Gives each sequence pages for ``want`` (B) int32 slots, or takes back those behind them (0: the sequence
     ends); pages are free again when no row names them.  Returns the slots that each now holds (B) int32, fewer than
     wanted where the pool has no free page left (sage_device_status() then says SAGE_ERR_PAGES)."""
-    return _pages_call("sage_kv_resize", cache, (("want", want),), out, cache.B, workspace, stream)
+    return _pages_call("sage_kv_resize", cache, (("want", want),), cache.B, out, workspace, stream)
 
 
 def sage_kv_fork(cache: KvCache, parent: torch.Tensor, lens: torch.Tensor, *, out=None, workspace=None, stream=None) -> torch.Tensor:
@@ -448,10 +449,10 @@ def sage_kv_fork(cache: KvCache, parent: torch.Tensor, lens: torch.Tensor, *, ou
     sage_kv_resize first.  Not for caches with score or pos."""
     if cache.score is not None or cache.pos is not None:
         raise ValueError("sage_kv_fork: a cache with score or pos is evicted from, its pages cannot be shared")
-    return _pages_call("sage_kv_fork", cache, (("parent", parent), ("lens", lens)), out, cache.B, workspace, stream)
+    return _pages_call("sage_kv_fork", cache, (("parent", parent), ("lens", lens)), cache.B, out, workspace, stream)
 
 
 def sage_kv_compact(cache: KvCache, *, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Moves the pages in use to the pool's front and lets all rows follow.  Returns their number (1) int32: the
     pool is free from there on."""
-    return _pages_call("sage_kv_compact", cache, (), out, 1, workspace, stream)
+    return _pages_call("sage_kv_compact", cache, (), 1, out, workspace, stream)
