@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         heads = min(MR, a.G - ch * MR);
         // the last granules, where a slot may be hidden from a row: those with fewer than `edge` slots to the end
         edge = S::GRAN;
-        if constexpr (ROWS) edge = new_tokens(a, b) < a.T ? 0x7FFFFFFF : S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
+        if constexpr (ROWS) edge = S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
         tok0 = t0 * S::TILE + warp * S::GRAN;
         ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
@@ -799,15 +799,22 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                     l[nh][e] = l[nh][e] * alpha[nh][e] + sum;
                 }
             if constexpr (KIND >= 2) {
+                if (ROWS && hidden) {                                // (a hidden slot's scale may be anything)
 #pragma unroll
-                for (int hf = 0; hf < HALVES; ++hf)
+                    for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh)
+                        for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // (a hidden slot's scale may be anything)
-                            if (!ROWS || !hidden || s[hf][nh][i] != 0.0f) s[hf][nh][i] *= fv[hf][i >> 1];
-                        }
+                            for (int i = 0; i < 4; ++i)
+                                if (s[hf][nh][i] != 0.0f) s[hf][nh][i] *= fv[hf][i >> 1];
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[hf][nh][i] *= fv[hf][i >> 1];
+                }
             }
             bool moved = false;
 #pragma unroll
@@ -968,6 +975,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                 o0 += f * from[p0];
                 o1 += f * from[p1];
                 sum += f * s_l[x][r];
+            }
+            if constexpr (ROWS) {
+                // a row behind its sequence's last token has seen what it was not hidden from
+                if (row_limit(a, pb, prow + r, plen) == 0) {
+                    o0 = o1 = sum = 0.0f;
+                    M = -INFINITY;
+                }
             }
             if constexpr (ROWS && KIND != 2) {
                 if (s_not_finite) {

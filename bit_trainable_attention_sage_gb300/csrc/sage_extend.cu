@@ -30,6 +30,8 @@
 // (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.  Sums, statistics
 // and O are float32.
 //
+// Up to 128 rows a kv head there is one tile: its steps go to the two softmax groups in turn, so that one's MMAs
+// run beside the other's softmax here too, and the two parts are joined like ranges.
 // Few CTAs are given more to do by cutting the slots into up to kExtMaxSplits ranges; a second kernel joins
 // their O, m and l in order, so results do not depend on the order in which CTAs run.
 //
@@ -49,11 +51,13 @@ namespace ext {
 constexpr int kThreads = 640;
 constexpr int kKeyWarp = 8, kValueWarp = 12;    // 8 .. 11, 12 .. 15
 constexpr int kMmaWarp = 16;                // (17 .. 19 are idle)
-// Launched at 96 registers a thread (640 x 96 = 61440): 256 x 128 + 256 x 72 + 128 x 80 = 61440.
-constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 72, kRegsControl = 80;
+// Launched at 96 registers a thread (640 x 96 = 61440): 256 x 128 + 256 x 80 + 128 x 64 = 61440.
+constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsControl = 64;
 constexpr int kRows = 256;                  // of a CTA
 constexpr int kStep = 128;                  // slots a step
 constexpr int kExtMaxSplits = 16;
+constexpr int kMinSteps = 8;                // of a range of slots
+constexpr int kCtaSteps = 4;                // what a CTA costs besides its steps, in steps
 
 struct Args {
     KvView c;
@@ -65,7 +69,7 @@ struct Args {
     int tiles, splits;                      // CTAs a kv head's rows and slots are cut into
     int order_heads, order_tiles;           // T a multiple of 256: heads a kv head, tiles a head; else 0
     float sl2;                              // log2(e) / sqrt(d)
-    float *part_O, *part_ml;                // splits > 1: (items, splits, 256, d), (items, splits, 256, 2)
+    float *part_O, *part_ml;                // splits > 1 or one tile: (items, splits, 256, d), (items, splits, 256, 2)
 };
 
 template <int D>
@@ -359,41 +363,32 @@ struct Loader {
             }
         };
         if constexpr (SC != 0) {
-            // 8-bit rows, half a step (64 rows) at a time and half a step ahead.  (A whole step at a time is twice the code, and
-            // the instruction cache is shared with the softmax's.)
+            // 8-bit rows, half a step (64 rows) at a time, a step ahead
             constexpr int HALF = ITS / 2;
-            uint4 x[HALF];
-            auto load = [&](int j, int h) {
+            uint4 x[2][HALF];
+            auto load = [&](int j, const int h) {
                 uint32_t rows[HALF];
 #pragma unroll
                 for (int i = 0; i < HALF; ++i) rows[i] = row_of(64 * h + rr + i * RPI);
                 const uint4 *from = static_cast<const uint4 *>(pool) + cc;
                 if (plain) {
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                    for (int i = 0; i < HALF; ++i) x[h][i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                 } else {
 #pragma unroll
                     for (int i = 0; i < HALF; ++i) {
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (rows[i] != kNone && j * kStep + 64 * h + rr + i * RPI < kv_end) x[i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
+                        x[h][i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (rows[i] != kNone && j * kStep + 64 * h + rr + i * RPI < kv_end) x[h][i] = __ldg(from + static_cast<size_t>(rows[i]) * CPR);
                     }
                 }
             };
-            look(j0);
-            find(j0);
-            look(j0 + 1);
-            if (!VALUES) load_scales(j0);
-            load(j0, 0);
-            query(VALUES);
-#pragma unroll 1
-            for (int u = 0; u < 2 * (j1 - j0); ++u) {
-                const int i = u >> 1, h = u & 1, j = j0 + i, st = i & 1;
-                if (h == 0 && !free_of(free, i)) break;
+            auto store = [&](int j, const int h) {
+                const int st = (j - j0) & 1;
                 if constexpr (VALUES && FP8) {
                     if (j >= mixed) {
 #pragma unroll
                         for (int y = 0; y < HALF; ++y) {
-                            uint32_t *w = &x[y].x;
+                            uint32_t *w = &x[h][y].x;
                             uint32_t bad = 0;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -405,19 +400,30 @@ struct Loader {
                         }
                     }
                 }
-                store_codes<VALUES && BF16, FP8, HALF, RPI>(smem_u32(VALUES ? s.v[st][0] : s.k[st][0]), x, 64 * h + rr, cc);
-                if (h == 0) {
-                    load(j, 1);
-                    if (!VALUES) store_scales(i);
-                } else {
-                    done(&full[st]);
-                    if (j + 1 < j1) {
-                        find(j + 1);
-                        look(j + 2);
-                        load(j + 1, 0);
-                        if (!VALUES) load_scales(j + 1);
-                    }
+                store_codes<VALUES && BF16, FP8, HALF, RPI>(smem_u32(VALUES ? s.v[st][0] : s.k[st][0]), x[h], 64 * h + rr, cc);
+            };
+            look(j0);
+            find(j0);
+            look(j0 + 1);
+            if (!VALUES) load_scales(j0);
+            load(j0, 0);
+            load(j0, 1);
+            query(VALUES);
+#pragma unroll 1
+            for (int j = j0; j < j1; ++j) {
+                const int i = j - j0;
+                if (!free_of(free, i)) break;
+                store(j, 0);
+                if (!VALUES) store_scales(i);
+                if (j + 1 < j1) {
+                    find(j + 1);
+                    look(j + 2);
+                    if (!VALUES) load_scales(j + 1);
+                    load(j + 1, 0);
                 }
+                store(j, 1);
+                done(&full[i & 1]);
+                if (j + 1 < j1) load(j + 1, 1);
             }
         } else {
             auto load = [&](int j) {
@@ -493,15 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     int x = blockIdx.x;
     const int split = x % a.splits;
     x /= a.splits;
+    // One tile of rows: its steps are dealt out to the two softmax groups in turn, as two parts of the slots.
+    const bool dealt = a.rows <= 128;
     const int bh = x % BH, rank = x / BH, b = bh / a.c.H, hk = bh - b * a.c.H;
     const int tile = a.order_heads ? (rank % a.order_heads) * a.order_tiles + a.order_tiles - 1 - rank / a.order_heads : a.tiles - 1 - rank;
     const int r0 = tile * kRows;
     const Seq seq = sequence(a, b);
     int end[2];                                       // slots a tile's rows see
     end[0] = tile_end(a, seq, r0, 128);
-    end[1] = tile_end(a, seq, r0 + 128, 128);
+    end[1] = dealt ? end[0] : tile_end(a, seq, r0 + 128, 128);
     const int all = (max(end[0], end[1]) + kStep - 1) / kStep;
-    const int j0 = static_cast<int>(static_cast<long long>(all) * split / a.splits), j1 = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits);
+    // (a short sequence is cut into fewer ranges than the plan has: what a CTA costs besides its steps is worth several)
+    const int ranges = max(1, min(a.splits, all / kMinSteps));
+    const int j0 = static_cast<int>(static_cast<long long>(all) * min(split, ranges) / ranges);
+    const int j1 = static_cast<int>(static_cast<long long>(all) * min(split + 1, ranges) / ranges);
     const int kv_end = max(end[0], end[1]);
     int n_t[2];                                       // a tile's steps: j0 .. n_t - 1
     n_t[0] = min(j1, (end[0] + kStep - 1) / kStep);
@@ -513,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
     if (j0 >= j1) {                                   // nothing to see: the whole CTA alike
         const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
-        if (row >= kRows || r0 + row >= a.rows) return;
-        if (a.splits > 1) {
+        if (row >= kRows || (dealt ? (row & 127) : r0 + row) >= a.rows) return;
+        if (a.splits > 1 || dealt) {
             if (half == 0) reinterpret_cast<float2 *>(a.part_ml)[item * kRows + row] = make_float2(-INFINITY, 0.0f);
         } else {
             uint4 *O = static_cast<uint4 *>(a.O) + (out0 + r0 + row) * (D / 8) + half * (D / 16);
@@ -563,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             constexpr uint32_t idS = idesc_f16(128, 128, BF16 && SC == 0, false, false);
             constexpr uint32_t idPV = idesc_f16(128, D, BF16, false, true);
             auto issue_s = [&](const int t, int st) {
-                const uint32_t q_addr = smem_u32(s.q[t][0]), k_addr = smem_u32(s.k[st][0]);
+                const uint32_t q_addr = smem_u32(s.q[dealt ? 0 : t][0]), k_addr = smem_u32(s.k[st][0]);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
@@ -571,40 +582,73 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 }
                 umma_commit(&s.s_full[t]);
             };
+            // O_t += P_t V of a step, the tile's u-th, half by half
+            auto issue_pv = [&](const int t, int u, int st, bool last) -> bool {
+                const uint32_t v_addr = smem_u32(s.v[st][0]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!mbar_wait(&s.p_full[t][h], u & 1, abort_flag, &g_ext_err, 4)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (u > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(&s.o_full[t]);
+                }
+                if (last) umma_commit(&s.o_done[t]);
+                return true;
+            };
+            const int n = j1 - j0;
             bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&s.k_full[0], 0, abort_flag, &g_ext_err, 2);
-            if (ok) {
-                tc_fence_after();
-                if (j0 < n_t[0]) issue_s(0, 0);
-                if (j0 < n_t[1]) issue_s(1, 0);
-                umma_commit(&s.k_free[0]);
-            }
             // As in the forward kernel a tile's next S follows its PV in issue order and overwrites the P that the
             // PV reads: the tensor pipe runs MMAs in that order.
-            for (int j = j0; j < j1 && ok; ++j) {
-                const int i = j - j0, st = i & 1, nst = st ^ 1;
-                if (!(ok = mbar_wait(&s.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
-                // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
-                if (j + 1 < j1 && !(ok = mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
-                const uint32_t v_addr = smem_u32(s.v[st][0]);
-                auto tile_step = [&](const int t) -> bool {
-                    if (j >= n_t[t]) return true;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!mbar_wait(&s.p_full[t][h], i & 1, abort_flag, &g_ext_err, 4)) return false;
+            if (dealt) {
+                // step i is group i & 1's: its S once that group's last PV has been issued
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(0, 0);
+                    umma_commit(&s.k_free[0]);
+                }
+                if (ok && n > 1 && (ok = mbar_wait(&s.k_full[1], 0, abort_flag, &g_ext_err, 2))) {
+                    tc_fence_after();
+                    issue_s(1, 1);
+                    umma_commit(&s.k_free[1]);
+                }
+                auto step = [&](const int t, int i) -> bool {
+                    if (!mbar_wait(&s.v_full[t], (i >> 1) & 1, abort_flag, &g_ext_err, 3)) return false;
+                    if (!issue_pv(t, i >> 1, t, i + 2 >= n)) return false;
+                    umma_commit(&s.v_free[t]);
+                    if (i + 2 < n) {
+                        if (!mbar_wait(&s.k_full[t], ((i + 2) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
                         tc_fence_after();
-#pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (i > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&s.o_full[t]);
+                        issue_s(t, t);
+                        umma_commit(&s.k_free[t]);
                     }
-                    if (j + 1 == n_t[t]) umma_commit(&s.o_done[t]);
-                    if (t == 1 || j >= n_t[1]) umma_commit(&s.v_free[st]);
-                    if (j + 1 < n_t[t]) issue_s(t, nst);
                     return true;
                 };
-                ok = tile_step(0) && tile_step(1);
-                if (!ok) break;
-                if (j + 1 < j1) umma_commit(&s.k_free[nst]);
+                for (int i = 0; i < n && ok; i += 2) ok = step(0, i) && (i + 1 >= n || step(1, i + 1));
+            } else {
+                if (ok) {
+                    tc_fence_after();
+                    if (j0 < n_t[0]) issue_s(0, 0);
+                    if (j0 < n_t[1]) issue_s(1, 0);
+                    umma_commit(&s.k_free[0]);
+                }
+                for (int j = j0; j < j1 && ok; ++j) {
+                    const int i = j - j0, st = i & 1, nst = st ^ 1;
+                    if (!(ok = mbar_wait(&s.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
+                    // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
+                    if (j + 1 < j1 && !(ok = mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
+                    auto tile_step = [&](const int t) -> bool {
+                        if (j >= n_t[t]) return true;
+                        if (!issue_pv(t, i, st, j + 1 == n_t[t])) return false;
+                        if (t == 1 || j >= n_t[1]) umma_commit(&s.v_free[st]);
+                        if (j + 1 < n_t[t]) issue_s(t, nst);
+                        return true;
+                    };
+                    ok = tile_step(0) && tile_step(1);
+                    if (!ok) break;
+                    if (j + 1 < j1) umma_commit(&s.k_free[nst]);
+                }
             }
             // every MMA must have finished before the tensor memory is released
             umma_commit(&s.mma_done);
@@ -612,25 +656,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         }
     } else if (warp >= kKeyWarp) {
         regs_dec<kRegsLoad>();
-        const Loader<D, BF16, SC, FP8> load{a, s, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, n_t[warp >= kValueWarp], out0};
+        const Loader<D, BF16, SC, FP8> load{a, s, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, warp >= kValueWarp && dealt ? 0 : n_t[warp >= kValueWarp], out0};
         if (warp < kValueWarp) load.template run<false>();
         else load.template run<true>();
     } else {
         regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------------------ softmax
         const int t = warp >> 2, quarter = warp & 3, lane = static_cast<int>(lane_id());
-        const int row = 128 * t + 32 * quarter + lane;
+        const int row = (dealt ? 0 : 128 * t) + 32 * quarter + lane;
         const int limit = row_limit(a, seq, r0 + row);               // slots this row sees
         const int steps = t ? n_t[1] : n_t[0];
         const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 256 * t);
         float m = -INFINITY, l = 0.0f;                               // reference of O and l; l
         bool ok = steps <= j0 || mbar_wait_warp(&s.q_full, 0, abort_flag, &g_ext_err, 11);
         const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
-        for (int j = j0; j < steps && ok; ++j) {
-            const int i = j - j0, at = i & 3;
+        const int deal = dealt ? 1 : 0, first = dealt ? j0 + t : j0;
+        for (int j = first; j < steps && ok; j += 1 + deal) {
+            const int i = j - j0, u = i >> deal, at = i & 3;         // u: of this group's steps
             // What the step's scales say is read ahead of its S, not a group at a time: shared memory answers slowly beside
             // the products' operands and the loaders' stores.
-            if (!(ok = wait_either(&s.k_full[i & 1], (i >> 1) & 1, &s.s_full[t], i & 1, abort_flag))) break;
+            if (!(ok = wait_either(&s.k_full[i & 1], (i >> 1) & 1, &s.s_full[t], u & 1, abort_flag))) break;
             const uint32_t holes = s.holes[at];
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
@@ -664,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 lv4 = lds128(smem_u32(&s.lv[at][0])); lv4n = lds128(smem_u32(&s.lv[at][4]));
                 rv4 = lds128(smem_u32(&s.rv[at][0])); rv4n = lds128(smem_u32(&s.rv[at][4]));
             }
-            if (!(ok = mbar_wait_warp(&s.s_full[t], i & 1, abort_flag, &g_ext_err, 7))) break;
+            if (!(ok = mbar_wait_warp(&s.s_full[t], u & 1, abort_flag, &g_ext_err, 7))) break;
             tc_fence_after();
             // Half h of the step, 64 slots: p' = 2^(x - ref), packed, and their l; the largest sum of 16 of them
             uint32_t pk[32];
@@ -748,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 const float to = moves ? mx : m, alpha = moves ? ex2_approx(m - to) : 1.0f;    // (m = -inf: 0)
                 m = to;
                 l *= alpha;
-                if (i == 0 && h == 0) return true;
+                if (u == 0 && h == 0) return true;
                 // The half before has to be in O.  (s_full says that of all halves of the steps before, so the
                 // barrier is in the phase of the half before or in the next.)
                 if (!mbar_wait_warp(&s.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
@@ -821,16 +866,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             }
             if (!ok) break;
         }
-        if (ok && steps > j0) ok = mbar_wait_warp(&s.o_done[t], 0, abort_flag, &g_ext_err, 9);
+        const bool any = steps > first;
+        if (ok && any) ok = mbar_wait_warp(&s.o_done[t], 0, abort_flag, &g_ext_err, 9);
         tc_fence_after();
         const bool there = r0 + row < a.rows;
         const bool empty = limit == 0 || l == 0.0f;                  // saw nothing (a NaN is no 0)
-        const bool part = a.splits > 1;
+        const bool part = a.splits > 1 || dealt;
+        const size_t part_row = item * kRows + (dealt ? 128 * t : 0) + row;
         if (ok && !*abort_flag) {
             const float inv = empty ? 0.0f : 1.0f / l;
             if (there) {
                 const float ref = m - kShift;
-                if (part) reinterpret_cast<float2 *>(a.part_ml)[item * kRows + row] = empty ? make_float2(-INFINITY, 0.0f) : make_float2(ref, l);
+                if (part) reinterpret_cast<float2 *>(a.part_ml)[part_row] = empty ? make_float2(-INFINITY, 0.0f) : make_float2(ref, l);
                 else a.L[out0 + r0 + row] = empty ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
             }
             // V values that are not finite and were taken out of the products: added for the rows that see them
@@ -840,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 uint32_t o[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
-                if (steps > j0) {
+                if (any) {
                     tmem_ld16(lane_base + 128 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
                     tmem_ld16(lane_base + 128 + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
                     tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[16]>(&o[0]));
@@ -872,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 if (!there) continue;
                 if (part) {
                     if (empty) continue;                             // not read
-                    float4 *to = reinterpret_cast<float4 *>(a.part_O + (item * kRows + row) * D + c);
+                    float4 *to = reinterpret_cast<float4 *>(a.part_O + part_row * D + c);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 } else {
@@ -899,9 +946,11 @@ __global__ void __launch_bounds__(256) extend_join_kernel(const __grid_constant_
     if (row >= total) return;
     const size_t bh = row / a.rows;
     const int r = static_cast<int>(row - bh * a.rows), tile = r / kRows;
-    const size_t first = ((bh * a.tiles + tile) * a.splits) * kRows + (r - tile * kRows);   // part k: + k * kRows
+    const bool dealt = a.rows <= 128;                                // two parts a CTA
+    const int parts = dealt ? 2 * a.splits : a.splits, stride = dealt ? 128 : kRows;
+    const size_t first = ((bh * a.tiles + tile) * a.splits) * kRows + (r - tile * kRows);   // part k: + k * stride
     float2 ml = make_float2(-INFINITY, 0.0f);
-    if (lane < a.splits) ml = reinterpret_cast<const float2 *>(a.part_ml)[first + static_cast<size_t>(lane) * kRows];
+    if (lane < parts) ml = reinterpret_cast<const float2 *>(a.part_ml)[first + static_cast<size_t>(lane) * stride];
     float M = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -911,10 +960,10 @@ __global__ void __launch_bounds__(256) extend_join_kernel(const __grid_constant_
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     constexpr int V = D / 32;                                        // channels a lane: 2 or 4
     float o[V] = {};
-    for (int k = 0; k < a.splits; ++k) {
+    for (int k = 0; k < parts; ++k) {
         const float f = __shfl_sync(0xffffffffu, mine, k), lk = __shfl_sync(0xffffffffu, ml.y, k);
         if (lk == 0.0f) continue;                                    // saw nothing: not written
-        const float *from = a.part_O + (first + static_cast<size_t>(k) * kRows) * D + lane * V;
+        const float *from = a.part_O + (first + static_cast<size_t>(k) * stride) * D + lane * V;
         if constexpr (V == 4) {
             const float4 x = *reinterpret_cast<const float4 *>(from);
             o[0] += f * x.x; o[1] += f * x.y; o[2] += f * x.z; o[3] += f * x.w;
@@ -941,21 +990,21 @@ static Plan plan(const sage_kv &c, int Hq, int T) {
     const long long rows = static_cast<long long>(Hq / c.H) * T;
     p.tiles = static_cast<int>((rows + kRows - 1) / kRows);
     const long long items = static_cast<long long>(c.B) * c.H * p.tiles;
-    // The slots are cut where CTAs are fewer than SMs: into as many ranges as make the last wave fullest, at
-    // least four steps of the capacity each.
+    // The slots are cut where CTAs are fewer than SMs: into as many ranges as end first, by waves of CTAs and the steps of
+    // each, if every sequence fills its capacity.
     const long long steps = (static_cast<long long>(c.max_pages) * c.page + kStep - 1) / kStep;
     p.splits = 1;
     if (items < kSMs) {
-        double best = 1.0;
-        for (int k = 2; k <= kExtMaxSplits && steps / k >= 4; ++k) {
-            const double cost = static_cast<double>((items * k + kSMs - 1) / kSMs) / k;
-            if (cost < best * 0.97) {
+        double best = 1e30;
+        for (int k = 1; k <= kExtMaxSplits && (k == 1 || steps / k >= kMinSteps); ++k) {
+            const double cost = static_cast<double>((items * k + kSMs - 1) / kSMs) * (static_cast<double>(steps) / k + kCtaSteps);
+            if (cost < best) {
                 best = cost;
                 p.splits = k;
             }
         }
     }
-    const size_t parts = p.splits > 1 ? static_cast<size_t>(items) * p.splits * kRows : 0;
+    const size_t parts = p.splits > 1 || rows <= 128 ? static_cast<size_t>(items) * p.splits * kRows : 0;
     p.off_ml = parts * c.d * sizeof(float);
     p.bytes = p.off_ml + parts * 2 * sizeof(float);
     return p;
@@ -980,7 +1029,7 @@ static cudaError_t launch_k(const Args &a, cudaStream_t st) {
     const long long grid = static_cast<long long>(a.c.B) * a.c.H * a.tiles * a.splits;
     kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.splits == 1) return e;
+    if (e != cudaSuccess || (a.splits == 1 && a.rows > 128)) return e;
     const size_t rows = static_cast<size_t>(a.c.B) * a.c.H * a.rows;
     extend_join_kernel<D, BF16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a);
     return cudaGetLastError();
