@@ -277,10 +277,10 @@ __device__ __forceinline__ int seq_len(const DecodeArgs &a, int b) {
     }
     return n;
 }
-// the slots that row r of a kv head sees (several tokens only)
-__device__ __forceinline__ int row_limit(const DecodeArgs &a, int b, int r, int len) {
+// the slots that row r of a kv head sees (several tokens only): its sequence's first new slot, new tokens and slots
+__device__ __forceinline__ int row_limit(const DecodeArgs &a, int r, int start, int count, int len) {
     const int t = r % a.T;
-    return t < new_tokens(a, b) ? min(kv_len(a.c, a.lens, b, &g_decode_err) + t + 1, len) : 0;
+    return t < count ? min(start + t + 1, len) : 0;
 }
 
 // ---- the cut of the work ---------------------------------------------------------------------
@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & (S::ALIGN - 1));
     __shared__ float s_m[kDecWarps][MR], s_l[kDecWarps][MR];
     __shared__ float s_part[2][MR], s_f[kDecCluster][MR];        // ONE: a CTA's M and l; factors of the cluster's
-    __shared__ int s_not_finite;                                 // several tokens: a V was taken out of the products
-    (void)s_part; (void)s_f; (void)s_not_finite;
+    __shared__ int s_not_finite, s_limit[MR];                    // ROWS: a V was taken out of the products; slots a row sees
+    (void)s_part; (void)s_f; (void)s_not_finite; (void)s_limit;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -460,6 +460,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 
     // the run's pairs, one after the other
     int len, tiles, t0, t1, hk, head0, heads, tok0, ng, edge;
+    [[maybe_unused]] int first_new = 0, count = 0;               // ROWS: of the pair's sequence
     // The next pair of the run with a tile to do, from unit u on; u moves past its units.  False at
     // the run's end.
     auto find = [&]() {
@@ -496,7 +497,11 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         heads = min(MR, a.G - ch * MR);
         // the last granules, where a slot may be hidden from a row: those with fewer than `edge` slots to the end
         edge = S::GRAN;
-        if constexpr (ROWS) edge = S::GRAN + max(0, len - 1 - kv_len(a.c, a.lens, b, &g_decode_err));
+        if constexpr (ROWS) {
+            first_new = kv_len(a.c, a.lens, b, &g_decode_err);
+            count = new_tokens(a, b);
+            edge = S::GRAN + max(0, len - 1 - first_new);
+        }
         // granules of this warp: tokens tau * TILE + warp * GRAN, tau in [t0, t1), while below len
         tok0 = t0 * S::TILE + warp * S::GRAN;
         ng = tok0 >= len ? 0 : min(t1 - t0, (len - tok0 + S::TILE - 1) / S::TILE);
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) limit[nh][e] = row_limit(a, b, head0 - hk * a.G + nh * 8 + 2 * q + e, len) - tok;
+                    for (int e = 0; e < 2; ++e) limit[nh][e] = row_limit(a, head0 - hk * a.G + nh * 8 + 2 * q + e, first_new, count, len) - tok;
 #pragma unroll
                 for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
@@ -921,8 +926,11 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
         const int place = run_first && t0 > 0 ? 0 : 1;
         const size_t out0 = static_cast<size_t>(b) * a.Hq + head0;
         const int outs = heads;
-        // (of this pair, for values that are not finite: its sequence, kv head, first row, and the slots of its tiles)
-        [[maybe_unused]] const int pb = b, pk = hk, prow = head0 - hk * a.G, plen = len, pfrom = max(t0 * S::TILE, edge >= len ? 0 : len - edge), pto = t1 * S::TILE;
+        // (of this pair, for values that are not finite: its sequence, kv head, and the slots of its tiles)
+        if constexpr (ROWS) {
+            if (tid < MR) s_limit[tid] = row_limit(a, head0 - hk * a.G + tid, first_new, count, len);
+        }
+        [[maybe_unused]] const int pb = b, pk = hk, pfrom = max(t0 * S::TILE, edge >= len ? 0 : len - edge), pto = t1 * S::TILE;
         bool more = false;
         if constexpr (!ONE) {
             more = find();
@@ -978,14 +986,14 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
             }
             if constexpr (ROWS) {
                 // a row behind its sequence's last token has seen what it was not hidden from
-                if (row_limit(a, pb, prow + r, plen) == 0) {
+                if (s_limit[r] == 0) {
                     o0 = o1 = sum = 0.0f;
                     M = -INFINITY;
                 }
             }
             if constexpr (ROWS && KIND != 2) {
                 if (s_not_finite) {
-                    const int to = min(row_limit(a, pb, prow + r, plen), pto);
+                    const int to = min(s_limit[r], pto);
                     for (int t = pfrom; t < to; ++t) {
                         const int p = kv_page(a.c, pb, t, &g_decode_err);
                         if (p < 0) continue;
