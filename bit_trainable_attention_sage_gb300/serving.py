@@ -446,7 +446,8 @@ def sage_kv_fork(cache: KvCache, parent: torch.Tensor, lens: torch.Tensor, *, ou
     """Sequence b goes on as a copy of sequence ``parent[b]``, as all were before, of lens[parent[b]] slots (-1: it
     ends).  Full pages are shared, the rows of the page in use copied to a page of its own; pages of no
     sequence are free again.  Returns the new lengths (B) int32.  Sequences that then grow need
-    sage_kv_resize first.  Not for caches with score or pos."""
+    sage_kv_resize first; one that is cut back into a page that others share must not be appended to.  Not for
+    caches with score or pos."""
     if cache.score is not None or cache.pos is not None:
         raise ValueError("sage_kv_fork: a cache with score or pos is evicted from, its pages cannot be shared")
     return _pages_call("sage_kv_fork", cache, (("parent", parent), ("lens", lens)), cache.B, out, workspace, stream)

@@ -509,7 +509,8 @@ SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, i
  * entry that is no page left alone: SAGE_ERR_INDEX (from sage_kv_compact where pages move).  A pool without a free page: SAGE_ERR_PAGES.
  * Workspace: sage_pages_workspace_bytes(c), 16-byte aligned.  No call allocates, and all can be captured.
  * What writes a page writes it for every sequence that shares it: sage_kv_append goes behind the
- * shared ones where lengths come from sage_kv_fork, eviction is not for shared pages.
+ * shared ones where lengths come from sage_kv_fork and grow from there (a sequence that is cut back into a
+ * page that others share must not be appended to), eviction is not for shared pages.
  *
  * sage_kv_resize -- every sequence gets or gives back pages at its row's end, until it holds those of
  *   want[b] slots (0: it ends).  Pages that are given back are free again where nobody else names
