@@ -310,3 +310,43 @@ def test_a_conversation():
         check_extend(q, O, L, lens, count, [x[:, :n + c] for x, n, c in zip(Kd, lens, count)], [x[:, :n + c] for x, n, c in zip(Vd, lens, count)], H, Hq // H * T <= 32)
         lens = [n + t for n, t in zip(lens, take)]          # (drafts that are taken back are overwritten)
     assert sg.sage_device_status() == 0
+
+
+@pytest.mark.parametrize("kind,dtype,d,page,block", [FORMS[0], FORMS[1], FORMS[4]])
+@pytest.mark.parametrize("T,start", [(5000, 0), (3001, 1777)])
+def test_long_prompts(kind, dtype, d, page, block, T, start):
+    """Rows here and there of a long prompt of grouped heads, tiles that end inside a head, against 64 bits on the GPU."""
+    sg = _sg()
+    H, Hq, n = 2, 10, start + T
+    K, V = (torch.randn(1, H, n, d).to(dtype).cuda() for _ in range(2))
+    Q = torch.randn(1, Hq, T, d).to(dtype).cuda()
+    cache = sg.make_kv_cache(1, H, d, n, dtype=DT[kind], page=page, block=block)
+    sg.sage_kv_append(cache, K, V, ints([0]))
+    O, L = sg.sage_attn_extend(Q, cache, ints([start]))
+    assert sg.sage_device_status() == 0
+    Kd, Vd = (torch.from_numpy(x[0]).cuda() for x in values_of(cache, n))
+    rows = torch.tensor(sorted({0, 1, 127, 128, 255, 256, 257, T // 2, T - 2, T - 1, 1234, 2999}), device="cuda")
+    eps = torch.finfo(dtype).eps / 2
+    for h in range(Hq):
+        s = Q[0, h, rows].double() @ Kd[h // 5].T / d ** 0.5
+        s.masked_fill_(torch.arange(n, device="cuda") > start + rows.unsqueeze(1), float("-inf"))
+        p = s.softmax(-1)
+        want, pv = p @ Vd[h // 5], p @ Vd[h // 5].abs()
+        # half a step for the probabilities, half for the output; logits and sums as in check_extend, below 2^-9 here; fp16: what
+        # falls below 2^-36 of the largest weight
+        bound = (eps + 2.0 ** -9) * pv + eps * want.abs() + n * 2.0 ** -36 * 2.0 ** 9 * Vd.abs().max() + 2.0 ** -25
+        assert bool(((O[0, h, rows].double() - want).abs() <= bound).all()), h
+        assert bool(((L[0, h, rows].double() - s.logsumexp(-1)).abs() <= 1e-4).all()), h
+
+
+@pytest.mark.parametrize("B,T,Hq", [(300, 2, 4), (180, 40, 2), (3, 3, 140), (2, 1, 66)])
+def test_many_sequences_and_heads(B, T, Hq):
+    sg = _sg()
+    start = [(37 * b) % 200 for b in range(B)]
+    count = [T if b % 3 else max(0, T - 1) for b in range(B)]
+    cache, K, V = cache_of("int8", B, 2, 64, 32, 32, [s + c for s, c in zip(start, count)], seed=8)
+    Q = torch.randn(B, Hq, T, 64).bfloat16().cuda()
+    out, lse = torch.full_like(Q, 7.0), torch.full((B, Hq, T), 7.0, device="cuda")
+    O, L = sg.sage_attn_extend(Q, cache, ints(start), count=ints(count), out=out, lse=lse)
+    assert O is out and L is lse and sg.sage_device_status() == 0
+    check_extend(Q, O, L, start, count, K, V, 2, both(T, Hq))

@@ -334,3 +334,24 @@ def test_another_stream():
     assert slots.tolist() == model.resize([40, 1, 17]) and lens.tolist() == model.fork([0, 0, 2], [40, 1, 17])
     model.compact()
     model.check(cache)
+
+
+def test_a_shared_pool_with_scores():
+    """Resize and compact beside scores: rows of scores are the sequences' own, and eviction goes on as before."""
+    sg = _sg()
+    B, H, d = 3, 2, 64
+    cache = sg.make_kv_cache(B, H, d, 128, dtype=torch.int8, page=16, score=True, pages=30)
+    alone = sg.make_kv_cache(B, H, d, 128, dtype=torch.int8, page=16, score=True)
+    lens = ints([100, 33, 64])
+    assert sg.sage_kv_resize(cache, lens).tolist() == [112, 48, 64]
+    assert sg.sage_kv_resize(cache, ints([100, 0, 64])).tolist() == [112, 0, 64]
+    assert int(sg.sage_kv_compact(cache)) == 11 and sg.sage_kv_resize(cache, lens).tolist() == [112, 48, 64]
+    k, v = (torch.randn(B, H, 100, d).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(B, 4, 1, d).bfloat16().cuda()
+    for c in (cache, alone):
+        sg.sage_kv_append(c, k, v, ints([0] * B), count=lens)
+    out = [(*sg.sage_attn_decode(q, c, lens, score=True), sg.sage_kv_evict(c, lens, lens, budget=40, recent=8)) for c in (cache, alone)]
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and torch.equal(cache.score, alone.score) and torch.equal(cache.pos, alone.pos)
+    assert sg.sage_kv_resize(cache, out[0][2]).tolist() == [48, 48, 48] and int(sg.sage_kv_compact(cache)) == 9
+    a, b = (sg.sage_attn_decode(q, c, out[0][2]) for c in (cache, alone))
+    assert torch.equal(a[0], b[0]) and sg.sage_device_status() == 0
