@@ -242,7 +242,12 @@ class KvCache:
                                           _ptr(sK), _ptr(sV), table.data_ptr(), _ptr(score), _ptr(pos))) for t in types}
         self._bytes = {}        # workspace sizes by what they depend on
         # the page calls' workspace: they all write table, refs and held, so that no two may run at once anyway
-        self._pages_ws = None if refs is None else _workspace(lib().sage_pages_workspace_bytes(next(iter(self._c.values()))), dev)
+        # (with what every such call passes, looked up once: their time is mostly the host's)
+        self._any = next(iter(self._c.values()))
+        self._pages = None
+        if refs is not None:
+            ws = self._pages_ws = _workspace(lib().sage_pages_workspace_bytes(self._any), dev)
+            self._pages = refs.data_ptr(), held.data_ptr(), (ws.data_ptr(), ws.numel())
 
     def _struct(self, t: torch.Tensor, what: str):
         """The struct for a call on 16-bit tensors like ``t``."""
@@ -414,10 +419,11 @@ def sage_kv_evict(cache: KvCache, lens: torch.Tensor, seen: torch.Tensor, *, bud
 def _pages_call(name: str, cache: KvCache, ins, size: int, out, workspace, stream) -> torch.Tensor:
     """sage_kv_resize, sage_kv_fork or sage_kv_compact: int32 inputs by name, an int32 output of ``size``."""
     dev = cache.device
-    if cache.refs is None:
+    if cache._pages is None:
         raise ValueError(f"{name} needs a cache with refs and held (make_kv_cache(..., pages=))")
+    shape = cache.held.shape
     for what, t in ins:
-        _need(t, what, torch.int32, cache.held.shape, dev)
+        _need(t, what, torch.int32, shape, dev)
     if _elsewhere(stream, dev):
         with _on(stream, dev):
             return _pages_call(name, cache, ins, size, out, workspace, None)
@@ -425,12 +431,11 @@ def _pages_call(name: str, cache: KvCache, ins, size: int, out, workspace, strea
         out = torch.empty(size, dtype=torch.int32, device=dev)
     else:
         _need(out, "out", torch.int32, (size,), dev)
-    if workspace is None:
-        workspace = cache._pages_ws
-    else:
+    refs, held, ws = cache._pages
+    if workspace is not None:
         _workspace_ok(workspace, dev)
-    st = getattr(lib(), name)(next(iter(cache._c.values())), cache.refs.data_ptr(), cache.held.data_ptr(), *[t.data_ptr() for _, t in ins],
-                              out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current(dev))
+        ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = getattr(lib(), name)(cache._any, refs, held, *[t.data_ptr() for _, t in ins], out.data_ptr(), *ws, _current(dev))
     _check(name, st)
     return out
 
