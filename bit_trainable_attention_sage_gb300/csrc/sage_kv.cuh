@@ -25,6 +25,13 @@ __device__ __forceinline__ int cluster_word(const int *p, int rank) {
     return v;
 }
 
+__device__ __forceinline__ long long cluster_long(const long long *p, int rank) {
+    uint32_t at;
+    long long v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ float cluster_float(const float *p, int rank) {
     return __int_as_float(cluster_word(reinterpret_cast<const int *>(p), rank));
 }

@@ -37,7 +37,8 @@ struct Args {
     int *list;               // (pages): resize, fork: free pages in order; compact: free pages below the used number
     int *from;               // (pages): compact: pages that move, at their places in the order of the used ones
     int *map;                // (pages): compact: new page of a page that moves
-    int *need;               // (B): resize: first place in the list
+    PageSum *first;          // (B): resize: first place in the list
+    int *need;               // (B): fork: place in the list (-1: none)
     int *children, *heir;    // (B): fork
     int *held0;              // (B): fork: held as it was
     int *copy;               // (B, 3): fork: source page, destination page (-1: none), rows
@@ -47,43 +48,65 @@ struct Args {
 
 __device__ __forceinline__ int cluster_rank() { return blockIdx.x; }     // the grid is one cluster
 
-// The sums of x and y over the cluster's threads before this one, and over all of them.  (Read by other CTAs until the
-// next barrier of the cluster.)
-struct Prefix {
-    int before[2], total[2];
+// The sums of x and y over the cluster's threads before this one, and over all of them.  x: pages that sequences
+// want, which together can be more than 32 bits hold; y: things of the pool or sequences.  (Read by other CTAs until
+// the next barrier of the cluster.)
+struct Totals {
+    PageSum x;
+    int y;
 };
-__device__ __forceinline__ Prefix prefix(int x, int y, int (&s_total)[2], int (&s_warp)[2][kWarps]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine[2] = {x, y};
+struct Prefix {
+    Totals before, total;
+};
+struct WarpTotals {
+    PageSum x[kWarps];
+    int y[kWarps];
+};
+__device__ __forceinline__ Prefix prefix(PageSum x, int y, Totals &s_total, WarpTotals &s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Prefix p{};
+    PageSum ix = x;
+    int iy = y;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        int incl = mine[k];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
+    for (int o = 1; o < 32; o <<= 1) {
+        const PageSum ux = __shfl_up_sync(0xffffffffu, ix, o);
+        const int uy = __shfl_up_sync(0xffffffffu, iy, o);
+        if (lane >= o) {
+            ix += ux;
+            iy += uy;
         }
-        if (lane == 31) s_warp[k][warp] = incl;
-        p.before[k] = incl - mine[k];
     }
+    if (lane == 31) {
+        s_warp.x[warp] = ix;
+        s_warp.y[warp] = iy;
+    }
+    p.before = Totals{ix - x, iy - y};
     __syncthreads();
-    if (warp < 2) {
-        const int sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[warp][lane] : 0);
-        if (lane == 0) s_total[warp] = sum;
+    if (warp == 0) {
+        PageSum sum = lane < kWarps ? s_warp.x[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_total.x = sum;
+    } else if (warp == 1) {
+        const int sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp.y[lane] : 0);
+        if (lane == 0) s_total.y = sum;
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) p.before[k] += w < warp ? s_warp[k][w] : 0;
+    for (int w = 0; w < kWarps; ++w) {
+        p.before.x += w < warp ? s_warp.x[w] : 0;
+        p.before.y += w < warp ? s_warp.y[w] : 0;
+    }
     cluster_sync();
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int n = cluster_word(&s_total[k], r);
-            if (r < cluster_rank()) p.before[k] += n;
-            p.total[k] += n;
+    for (int r = 0; r < kCluster; ++r) {
+        const Totals n{cluster_long(&s_total.x, r), cluster_word(&s_total.y, r)};
+        if (r < cluster_rank()) {
+            p.before.x += n.x;
+            p.before.y += n.y;
         }
+        p.total.x += n.x;
+        p.total.y += n.y;
+    }
     return p;
 }
 
@@ -123,7 +146,7 @@ __device__ __forceinline__ int free_pages(const Args &a, int &begin, int &end) {
     return n;
 }
 // They, n of them, to their places in the list, as far as it is wanted.
-__device__ __forceinline__ void list_free(const Args &a, int begin, int end, int n, int at, int wanted) {
+__device__ __forceinline__ void list_free(const Args &a, int begin, int end, int n, int at, PageSum wanted) {
     for (int p = begin; p < end && n > 0 && at < wanted; ++p)
         if (__ldcg(a.refs + p) == 0) {
             a.list[at++] = p;
@@ -133,7 +156,8 @@ __device__ __forceinline__ void list_free(const Args &a, int begin, int end, int
 
 // ---- resize --------------------------------------------------------------------------------------
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) resize_kernel(const __grid_constant__ Args a) {
-    __shared__ int s_total[2][2], s_warp[2][kWarps];
+    __shared__ Totals s_total[2];
+    __shared__ WarpTotals s_warp;
     const int lane = threadIdx.x & 31, warp = cluster_rank() * kWarps + (threadIdx.x >> 5);
     // pages that are no longer wanted go back, a warp a sequence
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
@@ -146,30 +170,32 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) res
         }
     }
     // the places in the list of free pages of those that grow; in most steps of a decoding loop none does
-    int begin, end, n = 0;
+    int begin, end;
+    PageSum n = 0;
     part_of(a.c.B, begin, end);
-    for (int b = begin; b < end; ++b) n += max(0, pages_of(a, __ldg(a.want + b)) - held_of(a, b));
+    for (int b = begin; b < end; ++b) n += pages_more(pages_of(a, __ldg(a.want + b)), held_of(a, b));
     const Prefix grow = prefix(n, 0, s_total[0], s_warp);            // (a barrier of the cluster: the counts are down)
     int free = 0;
-    if (grow.total[0] > 0) {                                         // the whole cluster alike
-        int at = grow.before[0], p0, p1;
+    if (grow.total.x > 0) {                                          // the whole cluster alike
+        PageSum at = grow.before.x;
+        int p0, p1;
         for (int b = begin; b < end; ++b) {
-            a.need[b] = at;
-            at += max(0, pages_of(a, __ldg(a.want + b)) - held_of(a, b));
+            a.first[b] = at;
+            at += pages_more(pages_of(a, __ldg(a.want + b)), held_of(a, b));
         }
         const int mine = free_pages(a, p0, p1);
         __syncthreads();                                             // s_warp has been read
-        const Prefix f = prefix(mine, 0, s_total[1], s_warp);
-        list_free(a, p0, p1, mine, f.before[0], grow.total[0]);
-        free = f.total[0];
+        const Prefix f = prefix(0, mine, s_total[1], s_warp);
+        list_free(a, p0, p1, mine, f.before.y, grow.total.x);
+        free = f.total.y;
     }
     cluster_sync();                                                  // (in either case: no CTA leaves while its sums are read)
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
         const int m = held_of(a, b), k = pages_of(a, __ldg(a.want + b));
         int got = 0;
         if (k > m) {
-            const int first = __ldcg(a.need + b);
-            got = max(0, min(k - m, free - first));
+            const PageSum first = __ldcg(a.first + b);               // below `free`, a count of pages, where got > 0
+            got = pages_got(k - m, first, free);
             if (got < k - m && lane == 0) atomicOr(&g_pages_err, 2u);
             for (int i = lane; i < got; i += 32) {
                 const int p = __ldcg(a.list + first + i);
@@ -204,7 +230,8 @@ __device__ __forceinline__ int slots_of(const Args &a, int q, int held) {
 }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ Args a) {
-    __shared__ int s_total[2], s_warp[2][kWarps];
+    __shared__ Totals s_total;
+    __shared__ WarpTotals s_warp;
     __shared__ int s_children[kSmall], s_heir[kSmall];
     const int lane = threadIdx.x & 31, warp = cluster_rank() * kWarps + (threadIdx.x >> 5);
     // How many go on from each sequence, and which of them keeps its last pages: itself, or else the first.  Each CTA
@@ -255,10 +282,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
     for (int b = begin; b < end; ++b) n += copies(b);
     const int mine = free_pages(a, p0, p1);
     const Prefix f = prefix(n, mine, s_total, s_warp);
-    int place = f.before[0];
+    int place = static_cast<int>(f.before.x);                        // (at most one a sequence)
     for (int b = begin; b < end; ++b) a.need[b] = copies(b) ? place++ : -1;
-    list_free(a, p0, p1, mine, f.before[1], f.total[0]);
-    const int free = f.total[1];
+    list_free(a, p0, p1, mine, f.before.y, f.total.x);
+    const int free = f.total.y;
     cluster_sync();
     // the new rows
     for (int b = warp; b < a.c.B; b += kCluster * kWarps) {
@@ -339,15 +366,16 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const __grid_co
 // ---- compact ---------------------------------------------------------------------------------------
 // The i-th of the used pages from place U on (U: how many are used) moves to the i-th free page below U.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ Args a) {
-    __shared__ int s_total[2], s_warp[2][kWarps];
+    __shared__ Totals s_total;
+    __shared__ WarpTotals s_warp;
     int begin, end, n = 0;
     part_of(a.c.pages, begin, end);
     for (int p = begin; p < end; ++p) n += __ldcg(a.refs + p) != 0;
-    const Prefix used = prefix(n, 0, s_total, s_warp);
-    const int U = used.total[0];
+    const Prefix used = prefix(0, n, s_total, s_warp);
+    const int U = used.total.y;
     // `at` used pages lie before p: a free p below U is free page p - at of them; a used one from U on has
     // place `at` in the order of all, of which the last ones move
-    int at = used.before[0];
+    int at = used.before.y;
     for (int p = begin; p < end; ++p) {
         const bool there = __ldcg(a.refs + p) != 0;
         if (p == U) a.count[1] = U - at;                             // moves: free pages below U
@@ -408,7 +436,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_copy_kernel(const __grid
 // ---- host ------------------------------------------------------------------------------------------
 // Places in the workspace, in ints; the last is its size.
 struct Places {
-    size_t list, from, map, need, children, heir, held0, copy, old, count, all;
+    size_t list, from, map, first, need, children, heir, held0, copy, old, count, all;
 };
 static Places places(const sage_kv &c) {
     Places p;
@@ -421,6 +449,7 @@ static Places places(const sage_kv &c) {
     p.list = take(c.pages);
     p.from = take(c.pages);
     p.map = take(c.pages);
+    p.first = take(2 * static_cast<size_t>(c.B));
     p.need = take(c.B);
     p.children = take(c.B);
     p.heir = take(c.B);
@@ -439,7 +468,7 @@ static Args args(const sage_kv &c, int *refs, int *held, int *out, void *workspa
     a.c = kv_view(c);
     a.table = const_cast<int *>(c.table);
     a.refs = refs; a.held = held; a.out = out;
-    a.list = w + p.list; a.from = w + p.from; a.map = w + p.map; a.need = w + p.need; a.children = w + p.children; a.heir = w + p.heir;
+    a.list = w + p.list; a.from = w + p.from; a.map = w + p.map; a.first = reinterpret_cast<PageSum *>(w + p.first); a.need = w + p.need; a.children = w + p.children; a.heir = w + p.heir;
     a.held0 = w + p.held0; a.copy = w + p.copy; a.count = w + p.count; a.old = w + p.old;
     return a;
 }
