@@ -199,8 +199,9 @@ class KvCache:
     pos (same, int32) are there for sage_attn_decode(score=True) and sage_kv_evict (not with scales of
     blocks).  refs (pages) and held (B) int32, both or none, are there for a pool that sequences share
     (sage_kv_resize, sage_kv_fork, sage_kv_compact): how many table entries name each page, and how many of each
-    row's entries are its pages; these calls write them and table, by a workspace that the object holds.  The tensors are fixed for the life of the object; their contents are the caller's and
-    the calls'."""
+    row's entries are its pages; these calls write them and table, by a workspace that the object holds (calls that are
+    captured into a graph take theirs from the graph's memory, so that a graph can outlive the object).  The tensors are
+    fixed for the life of the object; their contents are the caller's and the calls'."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, *, sK=None, sV=None, score=None, pos=None, refs=None,
                  held=None):
@@ -248,6 +249,7 @@ class KvCache:
         if refs is not None:
             ws = self._pages_ws = _workspace(lib().sage_pages_workspace_bytes(self._any), dev)
             self._pages = refs.data_ptr(), held.data_ptr(), (ws.data_ptr(), ws.numel())
+            self._pages_streams = {_current(dev)}       # that the allocator knows to use the workspace
 
     def _struct(self, t: torch.Tensor, what: str):
         """The struct for a call on 16-bit tensors like ``t``."""
@@ -432,10 +434,17 @@ def _pages_call(name: str, cache: KvCache, ins, size: int, out, workspace, strea
     else:
         _need(out, "out", torch.int32, (size,), dev)
     refs, held, ws = cache._pages
+    current = _current(dev)
     if workspace is not None:
         _workspace_ok(workspace, dev)
         ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = getattr(lib(), name)(cache._any, refs, held, *[t.data_ptr() for _, t in ins], out.data_ptr(), *ws, _current(dev))
+    elif torch._C._cuda_isCurrentStreamCapturing():
+        workspace = _workspace(ws[1], dev)      # the graph's: a replay finds it when the cache is gone
+        ws = workspace.data_ptr(), ws[1]
+    elif current not in cache._pages_streams:
+        cache._pages_ws.record_stream(torch.cuda.current_stream(dev))      # not given away while this call is pending
+        cache._pages_streams.add(current)
+    st = getattr(lib(), name)(cache._any, refs, held, *[t.data_ptr() for _, t in ins], out.data_ptr(), *ws, current)
     _check(name, st)
     return out
 
