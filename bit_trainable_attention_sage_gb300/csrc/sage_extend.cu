@@ -25,10 +25,13 @@
 // from a tile's last P to its next S.  In 8 bits 3900: the loaders share schedulers and instruction cache with the softmax.
 // TMEM: columns 256 t + [0, 128) S_t and P_t, 256 t + 128 + [0, d) O_t.
 //
-// Scales.  Codes are exact in fp16 and bf16, so a logit is acc * (sK log2(e) / sqrt(d)); with one scale a
-// block that is one factor for 16 or more columns, and the maximum of a group's products is scaled once.  V's
-// scale goes into the exponent: p' = 2^(x + log2 sV - m), m the running maximum of x + log2 sV, feeds the
-// second product and keeps its largest value near 1 whatever the scales are; l sums p' / sV.
+// Scales.  Codes are exact in fp16 and bf16, so a logit x is acc * (sK log2(e) / sqrt(d)); with one scale a
+// block that is one factor for 16 or more columns.  q = 2^(x - m) goes into l, and p' = q sV feeds the second product,
+// where m follows the running maximum of x + log2 sV, so that the largest p' stays near 1 whatever the scales are.  For
+// m a scale counts as at least 2^-60, so that q stays below 2^80 (and as at most 2^20 in bf16, whose p' can grow): l
+// then loses nothing above 2^-46 of a row's largest weight, and no scale, however small or not finite, reaches it.
+// A scale a row is multiplied on; scales of blocks go into the exponent with x, in the rare steps with one outside
+// [2^-60, 2^20] or with hidden slots by a pass over S of their own.
 // Roundings: p' is rounded to Q's type, bf16 (8 bits) or fp16 (11 bits, the running maximum's at 2^11, so that
 // they are all there down to 2^-25 of it and gone below 2^-36, which shows only in outputs that fp16 cannot hold
 // either): half a step of the output's own type each, and they average over the slots.  K's codes meet Q in fp16
@@ -83,15 +86,31 @@ struct Smem {
     alignas(1024) uint8_t k[2][D / 64][128 * 128];   // two stages: step j's rows in stage j & 1
     alignas(1024) uint8_t v[2][D / 64][128 * 128];
     // of step j in place j & 3 (a place is written again when the step before the last has been read):
-    // factor of the products, log2 of V's scale and its reciprocal, a slot or a group of 16 slots each
-    alignas(16) float kc[4][128], lv[4][128], rv[4][128];
+    // factor of the products, V's scale and its log2 as the reference follows it, a slot or a group of 16 slots each;
+    // the scales' reciprocals, a group
+    alignas(16) float kc[4][128], sv[4][128], lv[4][128], rv[4][8];
     float qs[256];                                   // the rows' factors of Q (8-bit pools, Q in bf16)
-    uint32_t holes[4];                               // groups of 16 slots whose page is none
+    uint32_t holes[4];                               // groups of 16 slots whose page is none; kOdd: scales of V out of the ordinary
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
     uint64_t s_full[2], p_full[2][2], o_full[2], o_done[2];   // p_full[tile][half of the step]; o_full: a half's PV, o_done: a tile's last
     uint32_t tmem_base;
     int abort_flag, not_finite;
 };
+
+// log2 of V's scale as the reference follows it.  Held to 2^-60, so that the probabilities before their scales stay
+// below 2^80, and in bf16, where P itself can grow, to 2^20, so that they stay above 2^-126 where they count; a scale
+// that is not finite reaches O by itself.
+constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p20f;
+template <bool BF16>
+__device__ __forceinline__ float followed_log2(float sv) {
+    const float x = fabsf(sv);
+    if (!(x > 0.0f && x < INFINITY)) return 0.0f;
+    const float l = fmaxf(log2f(x), -60.0f);
+    return BF16 ? fminf(l, 20.0f) : l;
+}
+// Scales of groups of 16 go into the exponent as they are where all of a step are 0 or from 2^-60 to 2^20.
+constexpr uint32_t kOdd = 4u;                        // in the word of a step's holes
+__device__ __forceinline__ bool ordinary(float sv) { return sv == 0.0f || (sv >= kLeastScale && sv <= kMostScale); }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
@@ -350,9 +369,9 @@ struct Loader {
             const int at = i & 3;
             if (SC == 1 || (SC == 2 && tid < 8)) {
                 s.kc[at][tid] = sk * a.sl2;
-                // no value is lost with a scale of 0 (its codes are): a NaN stays one
-                s.lv[at][tid] = sv == 0.0f ? 0.0f : log2f(sv);
-                s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;
+                s.sv[at][tid] = sv;
+                s.lv[at][tid] = followed_log2<BF16>(sv);
+                if (SC == 2) s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;   // (not read where a scale is odd)
             }
             if constexpr (SC == 1) {
                 // slots 32 w .. of warp w: two groups
@@ -363,8 +382,9 @@ struct Loader {
                 }
             } else if (tid < 32) {
                 const uint32_t h = __ballot_sync(0xffffffffu, hole);
+                const bool odd = SC == 2 && __any_sync(0xffffffffu, !ordinary(sv));
                 // groups 2 w and 2 w + 1 in byte w, as above
-                if (lane == 0) s.holes[at] = (h & 3u) | ((h >> 2) & 3u) << 8 | ((h >> 4) & 3u) << 16 | ((h >> 6) & 3u) << 24;
+                if (lane == 0) s.holes[at] = (h & 3u) | ((h >> 2) & 3u) << 8 | ((h >> 4) & 3u) << 16 | ((h >> 6) & 3u) << 24 | (odd ? kOdd : 0u);
             }
         };
         if constexpr (SC != 0) {
@@ -685,15 +705,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
             uint32_t raw[2][16];                                     // S, 16 slots a group, a group ahead
-            // x of slots k .. k + 3 of the step (hidden ones: -inf)
-            auto four = [&](const uint32_t *r, int k, float (&v)[4]) {
+            // Logits of slots k .. k + 3 of the step (hidden ones: -inf), `scaled`: and V's scales on them.
+            auto four = [&](const uint32_t *r, int k, float (&v)[4], auto scaled) {
                 float4 kc = make_float4(a.sl2, a.sl2, a.sl2, a.sl2), lv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if constexpr (SC == 1) {
                     kc = lds128(smem_u32(&s.kc[at][k]));
-                    lv = lds128(smem_u32(&s.lv[at][k]));
+                    if (decltype(scaled)::value) lv = lds128(smem_u32(&s.lv[at][k]));
                 } else if constexpr (SC == 2) {
                     kc.x = kc.y = kc.z = kc.w = s.kc[at][k / 16];
-                    lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
+                    if (decltype(scaled)::value) lv.x = lv.y = lv.z = lv.w = s.lv[at][k / 16];
                 }
                 if constexpr (BF16 && SC != 0) {
                     kc.x *= qs; kc.y *= qs; kc.z *= qs; kc.w *= qs;
@@ -713,14 +733,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 kc4 = lds128(smem_u32(&s.kc[at][0])); kc4n = lds128(smem_u32(&s.kc[at][4]));
                 lv4 = lds128(smem_u32(&s.lv[at][0])); lv4n = lds128(smem_u32(&s.lv[at][4]));
                 rv4 = lds128(smem_u32(&s.rv[at][0])); rv4n = lds128(smem_u32(&s.rv[at][4]));
+                if (!whole) {                                        // prepare() puts the factors on
+                    kc4 = kc4n = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    lv4 = lv4n = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
             }
+            [[maybe_unused]] const float qs4 = whole ? qs : 1.0f;
             if (!(ok = mbar_wait_warp(&s.s_full[t], u & 1, abort_flag, &g_ext_err, 7))) break;
             tc_fence_after();
-            // Half h of the step, 64 slots: p' = 2^(x - ref), packed, and their l; the largest sum of 16 of them
+            // Half h of the step, 64 slots: p' = 2^(x - ref) sV, packed, and their l, sums of 2^(x - ref); the largest sum of
+            // 16 p', or infinity.  Scales of groups go into the exponent, and a group's sum times its scale's reciprocal is
+            // its part of l.
             uint32_t pk[32];
             float add;
             auto probabilities = [&](const int h, float ref, auto plain) -> float {
                 constexpr bool PLAIN = decltype(plain)::value;       // no slot is hidden
+                static_assert(PLAIN || SC != 2, "prepare() has been there");
+                constexpr bool SCALED = SC == 1;                     // p' = q sV after q = 2^(x - ref)
                 const uint32_t from = lane_base + 64 * h;
                 float most = 0.0f;
                 [[maybe_unused]] float sums[4];
@@ -734,50 +763,63 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     f2 sum{0.0f, 0.0f};
                     [[maybe_unused]] f2 l2{0.0f, 0.0f};
                     f2 f{a.sl2, a.sl2}, off{-ref, -ref};
-                    if constexpr (SC == 2 && PLAIN) {
-                        f.x = f.y = (g == 0 ? kc4.x : g == 1 ? kc4.y : g == 2 ? kc4.z : kc4.w) * qs;
+                    if constexpr (SC == 2) {
+                        f.x = f.y = (g == 0 ? kc4.x : g == 1 ? kc4.y : g == 2 ? kc4.z : kc4.w) * (BF16 ? qs4 : 1.0f);
                         off.x = off.y = (g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w) - ref;
                     }
-                    if constexpr (SC == 1 || !PLAIN) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            float v[4];
-                            four(&r[k], 64 * h + 16 * g + k, v);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) r[k + e] = __float_as_uint(v[e]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        const f2 r2{__uint_as_float(r[k]), __uint_as_float(r[k + 1])};
-                        const f2 x2 = SC == 1 || !PLAIN ? add2(r2, off) : fma2(r2, f, off);
-                        const f2 p{ex2_approx(x2.x), ex2_approx(x2.y)};
-                        sum = add2(sum, p);
-                        if constexpr (SC == 1) {
-                            const f2 rv{s.rv[at][64 * h + 16 * g + k], s.rv[at][64 * h + 16 * g + k + 1]};
-                            if constexpr (PLAIN) {
-                                l2 = fma2(p, rv, l2);
-                            } else {                                 // (a hidden slot's reciprocal may be anything)
-                                l2.x += p.x == 0.0f ? 0.0f : p.x * rv.x;
-                                l2.y += p.y == 0.0f ? 0.0f : p.y * rv.y;
+                    for (int k = 0; k < 16; k += 4) {
+                        const int col = 64 * h + 16 * g + k;
+                        f2 x[2];
+                        [[maybe_unused]] float v[4];
+                        if constexpr (PLAIN) {
+                            [[maybe_unused]] float4 kc;
+                            if constexpr (SC == 1) {
+                                kc = lds128(smem_u32(&s.kc[at][col]));
+                                if constexpr (BF16) {
+                                    kc.x *= qs; kc.y *= qs; kc.z *= qs; kc.w *= qs;
+                                }
                             }
+                            x[0] = fma2(f2{__uint_as_float(r[k]), __uint_as_float(r[k + 1])}, SC == 1 ? f2{kc.x, kc.y} : f, off);
+                            x[1] = fma2(f2{__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])}, SC == 1 ? f2{kc.z, kc.w} : f, off);
+                        } else {
+                            four(&r[k], col, v, std::false_type());
+                            x[0] = add2(f2{v[0], v[1]}, off);
+                            x[1] = add2(f2{v[2], v[3]}, off);
                         }
-                        pk[8 * g + k / 2] = pack2<BF16>(p.x, p.y);
+                        [[maybe_unused]] float4 sv;
+                        if constexpr (SCALED) sv = lds128(smem_u32(&s.sv[at][col]));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            f2 p{ex2_approx(x[e].x), ex2_approx(x[e].y)};
+                            if constexpr (SCALED) {
+                                l2 = add2(l2, p);
+                                p = mul2(p, e ? f2{sv.z, sv.w} : f2{sv.x, sv.y});
+                                if constexpr (!PLAIN) {              // (a hidden slot's scale may be anything)
+                                    if (v[2 * e] == -INFINITY) p.x = 0.0f;
+                                    if (v[2 * e + 1] == -INFINITY) p.y = 0.0f;
+                                }
+                            }
+                            sum = add2(sum, p);
+                            pk[8 * g + k / 2 + e] = pack2<BF16>(p.x, p.y);
+                        }
                     }
                     const float both = sum.x + sum.y;
                     most = fmaxf(most, both);
-                    if constexpr (SC == 1) add += l2.x + l2.y;
+                    if constexpr (SCALED) add += l2.x + l2.y;
                     else if constexpr (SC == 2) sums[g] = both;
                     else add += both;
                 }
                 if constexpr (SC == 2) {
                     const float rvs[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) add += !PLAIN && sums[g] == 0.0f ? 0.0f : sums[g] * rvs[g];
+                    for (int g = 0; g < 4; ++g) add += sums[g] * rvs[g];
                 }
+                // (slots of little scale, far above the reference: it has to follow before their q overflows)
+                if constexpr (SC == 1 && PLAIN) most = add > 0x1p90f ? INFINITY : most;
                 return most;
             };
-            // The reference follows half h's largest x = acc kc + lv where it lags.  False: a wait gave up.
+            // The reference follows half h's largest x + lv where it lags.  False: a wait gave up.
             auto follow = [&](const int h, float most) __attribute__((always_inline)) -> bool {
                 float mx = -INFINITY;
 #pragma unroll 1
@@ -788,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         float v[4];
-                        four(r + k, 16 * g + k, v);
+                        four(r + k, 16 * g + k, v, std::true_type());
                         mx = max3f(mx, v[0], v[1]);
                         mx = max3f(mx, v[2], v[3]);
                     }
@@ -815,6 +857,32 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 tmem_wait_st();
                 return true;
             };
+            // Scales of groups, a step with hidden slots or odd scales: half h's logits take their factors here, a group at a
+            // time, and go back to TMEM with V's scales on them, hidden ones as -inf, for the code of the whole steps.  Their part
+            // of l.
+            [[maybe_unused]] auto prepare = [&](const int h, float ref) __attribute__((always_inline)) -> float {
+                float part = 0.0f;
+#pragma unroll 1
+                for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                    uint32_t(&r)[16] = raw[0];
+                    tmem_ld16(lane_base + 16 * g, r);
+                    tmem_wait_ld_regs(r);
+                    const float sv = s.sv[at][g], lv = sv == 0.0f ? s.lv[at][g] : log2f(sv);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        float v[4];
+                        four(r + k, 16 * g + k, v, std::false_type());
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            part += ex2_approx(v[e] - ref);
+                            r[k + e] = __float_as_uint(v[e] == -INFINITY ? v[e] : v[e] + lv);
+                        }
+                    }
+                    tmem_st16(lane_base + 16 * g, r);
+                }
+                tmem_wait_st();
+                return part;
+            };
             // Most halves keep the reference that they find: the row's largest x then lies so little above it that no p'
             // exceeds kMost, which the sums of 16 show without a maximum.
             auto half_step = [&](const int h) __attribute__((always_inline)) -> bool {
@@ -822,19 +890,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 float most = 0.0f;
                 if constexpr (SC == 2) {
                     // (at most twice round)
+                    float ref = m - kShift, part = 0.0f;
                     bool sure = false;
 #pragma unroll 1
                     for (;;) {
                         if (known) {
-                            most = probabilities(h, m - kShift, std::true_type());
+                            most = probabilities(h, ref, std::true_type());
                             if (sure || !__any_sync(0xffffffffu, most > kMost)) break;
                         }
                         if (!follow(h, most)) return false;
-                        known = sure = whole && !__any_sync(0xffffffffu, m == -INFINITY);
-                        if (known) continue;
-                        probabilities(h, m == -INFINITY ? 0.0f : m - kShift, std::false_type());   // (nothing seen yet: all terms are 0)
-                        break;
+                        ref = m == -INFINITY ? 0.0f : m - kShift;    // (nothing seen yet: all terms are 0)
+                        if (!whole) part = prepare(h, ref);
+                        known = sure = true;
                     }
+                    l += whole ? add : part;
                 } else {
                     if (known) {
                         most = probabilities(h, m - kShift, std::true_type());
@@ -846,8 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         if (whole) probabilities(h, ref, std::true_type());
                         else probabilities(h, ref, std::false_type());
                     }
+                    l += add;
                 }
-                l += add;
                 // ---- to TMEM over slots of S that have been read: 32 columns a half, behind which half 1 finds its own
                 tmem_st32(lane_base + 32 * h, pk);
                 tmem_wait_st();
