@@ -98,14 +98,15 @@ struct Smem {
 };
 
 // log2 of V's scale as the reference follows it.  Held to 2^-60, so that the probabilities before their scales stay
-// below 2^80, and in bf16, where P itself can grow, to 2^20, so that they stay above 2^-126 where they count; a scale
-// that is not finite reaches O by itself.
+// below 2^80, and in bf16, where P itself can grow, to 2^20, so that they stay above 2^-126 where they count.  A scale of 0
+// counts as 2^-60 too (its codes are 0): a slot of no value, however large its weight, does not hold the reference above
+// those that have one.  A scale that is not finite reaches O by itself.
 constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p20f;
 template <bool BF16>
 __device__ __forceinline__ float followed_log2(float sv) {
     const float x = fabsf(sv);
-    if (!(x > 0.0f && x < INFINITY)) return 0.0f;
-    const float l = fmaxf(log2f(x), -60.0f);
+    if (!(x < INFINITY)) return 0.0f;
+    const float l = x < kLeastScale ? -60.0f : log2f(x);
     return BF16 ? fminf(l, 20.0f) : l;
 }
 // Scales of groups of 16 go into the exponent as they are where all of a step are 0 or from 2^-60 to 2^20.
@@ -371,7 +372,7 @@ struct Loader {
                 s.kc[at][tid] = sk * a.sl2;
                 s.sv[at][tid] = sv;
                 s.lv[at][tid] = followed_log2<BF16>(sv);
-                if (SC == 2) s.rv[at][tid] = sv == 0.0f ? 1.0f : 1.0f / sv;   // (not read where a scale is odd)
+                if (SC == 2) s.rv[at][tid] = 1.0f / (sv == 0.0f ? kLeastScale : sv);   // (not read where a scale is odd)
             }
             if constexpr (SC == 1) {
                 // slots 32 w .. of warp w: two groups
