@@ -32,11 +32,14 @@
 // then loses nothing above 2^-46 of a row's largest weight, and no scale, however small or not finite, reaches it.
 // A scale a row is multiplied on; scales of blocks go into the exponent with x, in the rare steps with one outside
 // [2^-60, 2^20] or with hidden slots by a pass over S of their own.
-// Roundings: p' is rounded to Q's type, bf16 (8 bits) or fp16 (11 bits, the running maximum's at 2^11, so that
-// they are all there down to 2^-25 of it and gone below 2^-36, which shows only in outputs that fp16 cannot hold
-// either): half a step of the output's own type each, and they average over the slots.  K's codes meet Q in fp16
-// (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.  Sums, statistics
-// and O are float32.
+// Roundings: p' is rounded to Q's type, half a step of the output's own type each, and they average over the slots: bf16
+// (8 bits, of any size), or fp16, the running maximum's at 2^11, so that all 11 bits are there down to 2^-25 of it and
+// below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of those.  Where what fp16 may
+// have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest output, its CTA walks the slots
+// twice more, under the references that the first walk left: once for the small p', 2^24 times, and once for the others.
+// That CTA takes three times as long; the largest V of a 16-bit pool is found beside the first walk.
+// K's codes meet Q in fp16 (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.
+// Sums, statistics and O are float32.
 //
 // Up to 128 rows a kv head there is one tile: its steps go to the two softmax groups in turn, so that one's MMAs
 // run beside the other's softmax here too, and the two parts are joined like ranges.
@@ -64,6 +67,7 @@ constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsControl = 64;
 constexpr int kRows = 256;                  // of a CTA
 constexpr int kStep = 128;                  // slots a step
 constexpr int kExtMaxSplits = 16;
+constexpr int kWalks = 3;                   // over the slots: one, and where fp16 may have lost too much two more
 constexpr int kMinSteps = 8;                // of a range of slots
 constexpr int kCtaSteps = 6;                // what a CTA costs besides its steps, in steps (512 tokens over 65536: 9 ranges 229 us, 14 242)
 
@@ -80,6 +84,12 @@ struct Args {
     float *part_O, *part_ml;                // splits > 1 or one tile: (items, splits, 256, d), (items, splits, 256, 2)
 };
 
+// Barriers of one walk over the slots.
+struct Bars {
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_done[2];   // p_full[tile][half of the step]; o_full: a half's PV, o_done: a tile's last
+};
+
 template <int D>
 struct Smem {
     alignas(1024) uint8_t q[2][D / 64][128 * 128];   // [tile][64 channels][row][128 bytes], 128-byte swizzle
@@ -91,10 +101,10 @@ struct Smem {
     alignas(16) float kc[4][128], sv[4][128], lv[4][128], rv[4][8];
     float qs[256];                                   // the rows' factors of Q (8-bit pools, Q in bf16)
     uint32_t holes[4];                               // groups of 16 slots whose page is none; kOdd: scales of V out of the ordinary
-    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], mma_done;
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_done[2];   // p_full[tile][half of the step]; o_full: a half's PV, o_done: a tile's last
-    uint32_t tmem_base;
-    int abort_flag, not_finite;
+    uint64_t q_full;
+    Bars bars[kWalks];
+    uint32_t tmem_base, v_most;                      // v_most: the largest |V| of the CTA's slots, its bits (16-bit pools, fp16)
+    int abort_flag, not_finite, ask, again;
 };
 
 // log2 of V's scale as the reference follows it.  Held to 2^-60, so that the probabilities before their scales stay
@@ -156,6 +166,13 @@ __device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
     if constexpr (FP8) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
     else if constexpr (BF16) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
     else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
+}
+
+// max(|a|, |b|) of two pairs of fp16, under some sign
+__device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // Place of 16-byte chunk c of row r in an operand of 64-channel parts.
@@ -270,6 +287,8 @@ template <int D, bool BF16, int SC, bool FP8>
 struct Loader {
     const Args &a;
     Smem<D> &s;
+    Bars &z;
+    int walk;
     int b, hk, j0, j1, kv_end, mixed, tid, r0, n_q;
     size_t out0;
 
@@ -327,7 +346,7 @@ struct Loader {
         const int lane = tid & 31;
         const int rr = tid / CPR, cc = tid % CPR;                    // rows rr + i RPI, chunk cc
         const void *pool = VALUES ? a.c.V : a.c.K;
-        uint64_t *full = VALUES ? s.v_full : s.k_full, *free = VALUES ? s.v_free : s.k_free;
+        uint64_t *full = VALUES ? z.v_full : z.k_full, *free = VALUES ? z.v_free : z.k_free;
         // Pages are asked for two steps ahead, by lane g of every warp (mod 8) for its step's group g of 16 slots,
         // and become the group's first row of the pool, kNone where it has no page, a step ahead.
         const int *table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
@@ -434,7 +453,7 @@ struct Loader {
             if (!VALUES) load_scales(j0);
             load(j0, 0);
             load(j0, 1);
-            query(VALUES);
+            if (walk == 0) query(VALUES);
 #pragma unroll 1
             for (int j = j0; j < j1; ++j) {
                 const int i = j - j0;
@@ -480,7 +499,8 @@ struct Loader {
             look(j0 + 1);
             load(j0);
             if (!VALUES) load_scales(j0);
-            query(VALUES);
+            if (walk == 0) query(VALUES);
+            [[maybe_unused]] uint32_t most = 0;                      // |V|, pairs of fp16
             for (int j = j0; j < j1; ++j) {
                 const int i = j - j0, st = i & 1;
                 if (!VALUES) store_scales(i);
@@ -506,6 +526,19 @@ struct Loader {
                     load(j + 1);
                     if (!VALUES) load_scales(j + 1);
                 }
+                if constexpr (VALUES && !BF16) {
+                    // the largest |V|, from the chunks this thread has copied itself, while the next step's are on their way
+                    if (walk == 0) {
+#pragma unroll 4
+                        for (int y = 0; y < ITS; ++y) {
+                            const uint4 w = lds128u(smem_u32(s.v[st][0]) + chunk_at(rr + y * RPI, cc));
+                            most = larger_halves(larger_halves(most, w.x), larger_halves(larger_halves(w.y, w.z), w.w));
+                        }
+                    }
+                }
+            }
+            if constexpr (VALUES && !BF16) {
+                if (walk == 0) atomicMax(&s.v_most, min(max(most & 0x7FFFu, most >> 16 & 0x7FFFu), 0x7BFFu));
             }
             cp_wait<0>();                                            // no copy outlives the CTA's shared memory
         }
@@ -519,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     Smem<D> &s = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // Results are referred to 2^kShift of the running maximum, which lags by up to 2^kSlack.
     constexpr float kSlack = 4.0f, kShift = BF16 ? 0.0f : 11.0f, kMost = BF16 ? 0x1p15f : 65504.0f;
+    // fp16: below kLow a p' has fewer than 11 bits.
+    [[maybe_unused]] constexpr float kLow = 0x1p-14f, kLift = 0x1p24f;
     const int warp = threadIdx.x >> 5;
     const int BH = a.c.B * a.c.H;
     // item: tiles with many slots first, all heads of a rank after one another
@@ -569,20 +604,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         s.abort_flag = 0;
         s.not_finite = 0;
+        s.ask = s.again = 0;
+        s.v_most = 0;
         mbar_init(&s.q_full, 8);
-        for (int st = 0; st < 2; ++st) {
-            mbar_init(&s.k_full[st], 4);
-            mbar_init(&s.k_free[st], 1);
-            mbar_init(&s.v_full[st], 4);
-            mbar_init(&s.v_free[st], 1);
-        }
-        mbar_init(&s.mma_done, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&s.s_full[t], 1);
-            mbar_init(&s.p_full[t][0], 4);
-            mbar_init(&s.p_full[t][1], 4);
-            mbar_init(&s.o_full[t], 1);
-            mbar_init(&s.o_done[t], 1);
+        for (int w = 0; w < (BF16 ? 1 : kWalks); ++w) {
+            Bars &z = s.bars[w];
+            mbar_init(&z.mma_done, 1);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&z.k_full[t], 4);
+                mbar_init(&z.k_free[t], 1);
+                mbar_init(&z.v_full[t], 4);
+                mbar_init(&z.v_free[t], 1);
+                mbar_init(&z.s_full[t], 1);
+                mbar_init(&z.p_full[t][0], 4);
+                mbar_init(&z.p_full[t][1], 4);
+                mbar_init(&z.o_full[t], 1);
+                mbar_init(&z.o_done[t], 1);
+            }
         }
         fence_barrier_init();
     }
@@ -592,9 +630,35 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
     // step j is the (j - j0)th: stage (j - j0) & 1, its barriers' phase ((j - j0) >> 1) & 1
+    // All warps, at the end of a walk: whether there is another one.  `bearable`: the largest |V| (8 bits: code) with which
+    // fp16 can not have lost too much of this thread's row.
+    auto all_warps = [&]() {
+        __syncwarp();
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        tc_fence_after();
+    };
+    auto another = [&](int walk, float bearable) -> bool {
+        if constexpr (BF16) {
+            return false;
+        } else {
+            if (walk + 1 == kWalks) return false;
+            constexpr float top = SC == 0 ? 65504.0f : FP8 ? 448.0f : 127.0f;
+            if (walk == 0 && bearable < top) s.ask = 1;
+            all_warps();
+            if (*static_cast<volatile int *>(&s.ask) == 0) return false;
+            if (SC != 0 || walk > 0) return SC != 0 || *static_cast<volatile int *>(&s.again) != 0;
+            const uint32_t v = *static_cast<volatile uint32_t *>(&s.v_most);
+            if (bearable < __half2float(__ushort_as_half(static_cast<unsigned short>(v)))) s.again = 1;
+            all_warps();
+            return *static_cast<volatile int *>(&s.again) != 0;
+        }
+    };
 
     if (warp >= kMmaWarp) {
         regs_dec<kRegsControl>();
+        for (int walk = 0;; ++walk) {
+        Bars &z = s.bars[walk];
         if (warp == kMmaWarp && elect_one()) {
             // ------------------------------------------------------------------ MMA issuer
             constexpr uint32_t idS = idesc_f16(128, 128, BF16 && SC == 0, false, false);
@@ -606,25 +670,25 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
                     umma_ss(tmem + 256 * t, sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0);
                 }
-                umma_commit(&s.s_full[t]);
+                umma_commit(&z.s_full[t]);
             };
             // O_t += P_t V of a step, the tile's u-th, half by half
             auto issue_pv = [&](const int t, int u, int st, bool last) -> bool {
                 const uint32_t v_addr = smem_u32(s.v[st][0]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!mbar_wait(&s.p_full[t][h], u & 1, abort_flag, &g_ext_err, 4)) return false;
+                    if (!mbar_wait(&z.p_full[t][h], u & 1, abort_flag, &g_ext_err, 4)) return false;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (u > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&s.o_full[t]);
+                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (walk == 2 || u > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(&z.o_full[t]);
                 }
-                if (last) umma_commit(&s.o_done[t]);
+                if (last) umma_commit(&z.o_done[t]);
                 return true;
             };
             const int n = j1 - j0;
-            bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&s.k_full[0], 0, abort_flag, &g_ext_err, 2);
+            bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&z.k_full[0], 0, abort_flag, &g_ext_err, 2);
             // As in the forward kernel a tile's next S follows its PV in issue order and overwrites the P that the
             // PV reads: the tensor pipe runs MMAs in that order.
             if (dealt) {
@@ -632,22 +696,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 if (ok) {
                     tc_fence_after();
                     issue_s(0, 0);
-                    umma_commit(&s.k_free[0]);
+                    umma_commit(&z.k_free[0]);
                 }
-                if (ok && n > 1 && (ok = mbar_wait(&s.k_full[1], 0, abort_flag, &g_ext_err, 2))) {
+                if (ok && n > 1 && (ok = mbar_wait(&z.k_full[1], 0, abort_flag, &g_ext_err, 2))) {
                     tc_fence_after();
                     issue_s(1, 1);
-                    umma_commit(&s.k_free[1]);
+                    umma_commit(&z.k_free[1]);
                 }
                 auto step = [&](const int t, int i) -> bool {
-                    if (!mbar_wait(&s.v_full[t], (i >> 1) & 1, abort_flag, &g_ext_err, 3)) return false;
+                    if (!mbar_wait(&z.v_full[t], (i >> 1) & 1, abort_flag, &g_ext_err, 3)) return false;
                     if (!issue_pv(t, i >> 1, t, i + 2 >= n)) return false;
-                    umma_commit(&s.v_free[t]);
+                    umma_commit(&z.v_free[t]);
                     if (i + 2 < n) {
-                        if (!mbar_wait(&s.k_full[t], ((i + 2) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
+                        if (!mbar_wait(&z.k_full[t], ((i + 2) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
                         tc_fence_after();
                         issue_s(t, t);
-                        umma_commit(&s.k_free[t]);
+                        umma_commit(&z.k_free[t]);
                     }
                     return true;
                 };
@@ -657,34 +721,39 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     tc_fence_after();
                     if (j0 < n_t[0]) issue_s(0, 0);
                     if (j0 < n_t[1]) issue_s(1, 0);
-                    umma_commit(&s.k_free[0]);
+                    umma_commit(&z.k_free[0]);
                 }
                 for (int j = j0; j < j1 && ok; ++j) {
                     const int i = j - j0, st = i & 1, nst = st ^ 1;
-                    if (!(ok = mbar_wait(&s.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
+                    if (!(ok = mbar_wait(&z.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
                     // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
-                    if (j + 1 < j1 && !(ok = mbar_wait(&s.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
+                    if (j + 1 < j1 && !(ok = mbar_wait(&z.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
                     auto tile_step = [&](const int t) -> bool {
                         if (j >= n_t[t]) return true;
                         if (!issue_pv(t, i, st, j + 1 == n_t[t])) return false;
-                        if (t == 1 || j >= n_t[1]) umma_commit(&s.v_free[st]);
+                        if (t == 1 || j >= n_t[1]) umma_commit(&z.v_free[st]);
                         if (j + 1 < n_t[t]) issue_s(t, nst);
                         return true;
                     };
                     ok = tile_step(0) && tile_step(1);
                     if (!ok) break;
-                    if (j + 1 < j1) umma_commit(&s.k_free[nst]);
+                    if (j + 1 < j1) umma_commit(&z.k_free[nst]);
                 }
             }
             // every MMA must have finished before the tensor memory is released
-            umma_commit(&s.mma_done);
-            mbar_wait_drain(&s.mma_done, 0, &g_ext_err, 5);
+            umma_commit(&z.mma_done);
+            mbar_wait_drain(&z.mma_done, 0, &g_ext_err, 5);
+        }
+        if (!another(walk, INFINITY)) break;
         }
     } else if (warp >= kKeyWarp) {
         regs_dec<kRegsLoad>();
-        const Loader<D, BF16, SC, FP8> load{a, s, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, warp >= kValueWarp && dealt ? 0 : n_t[warp >= kValueWarp], out0};
+        for (int walk = 0;; ++walk) {
+        const Loader<D, BF16, SC, FP8> load{a, s, s.bars[walk], walk, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, warp >= kValueWarp && dealt ? 0 : n_t[warp >= kValueWarp], out0};
         if (warp < kValueWarp) load.template run<false>();
         else load.template run<true>();
+        if (!another(walk, INFINITY)) break;
+        }
     } else {
         regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------------------ softmax
@@ -697,11 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         bool ok = steps <= j0 || mbar_wait_warp(&s.q_full, 0, abort_flag, &g_ext_err, 11);
         const float qs = BF16 && SC != 0 ? s.qs[row] : 1.0f;
         const int deal = dealt ? 1 : 0, first = dealt ? j0 + t : j0;
+        const bool any = steps > first;
+        Bars &z = s.bars[0];
         for (int j = first; j < steps && ok; j += 1 + deal) {
             const int i = j - j0, u = i >> deal, at = i & 3;         // u: of this group's steps
             // What the step's scales say is read ahead of its S, not a group at a time: shared memory answers slowly beside
             // the products' operands and the loaders' stores.
-            if (!(ok = wait_either(&s.k_full[i & 1], (i >> 1) & 1, &s.s_full[t], u & 1, abort_flag))) break;
+            if (!(ok = wait_either(&z.k_full[i & 1], (i >> 1) & 1, &z.s_full[t], u & 1, abort_flag))) break;
             const uint32_t holes = s.holes[at];
             const int seen = limit > 0 ? limit - j * kStep : kStep;  // of this step's slots, from the first; rows that are none take all
             const bool whole = holes == 0u && !__any_sync(0xffffffffu, seen < kStep);
@@ -740,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 }
             }
             [[maybe_unused]] const float qs4 = whole ? qs : 1.0f;
-            if (!(ok = mbar_wait_warp(&s.s_full[t], u & 1, abort_flag, &g_ext_err, 7))) break;
+            if (!(ok = mbar_wait_warp(&z.s_full[t], u & 1, abort_flag, &g_ext_err, 7))) break;
             tc_fence_after();
             // Half h of the step, 64 slots: p' = 2^(x - ref) sV, packed, and their l, sums of 2^(x - ref); the largest sum of
             // 16 p', or infinity.  Scales of groups go into the exponent, and a group's sum times its scale's reciprocal is
@@ -844,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 if (u == 0 && h == 0) return true;
                 // The half before has to be in O.  (s_full says that of all halves of the steps before, so the
                 // barrier is in the phase of the half before or in the next.)
-                if (!mbar_wait_warp(&s.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
+                if (!mbar_wait_warp(&z.o_full[t], h ^ 1, abort_flag, &g_ext_err, 8)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
@@ -923,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[t][h]);
+                if (lane == 0) mbar_arrive(&z.p_full[t][h]);
                 if constexpr (SC == 2) {
                     kc4 = kc4n;
                     lv4 = lv4n;
@@ -941,9 +1012,87 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             }
             if (!ok) break;
         }
-        const bool any = steps > first;
-        if (ok && any) ok = mbar_wait_warp(&s.o_done[t], 0, abort_flag, &g_ext_err, 9);
+        if (ok && any) ok = mbar_wait_warp(&z.o_done[t], 0, abort_flag, &g_ext_err, 9);
         tc_fence_after();
+        if constexpr (!BF16) {
+            // Each p' was off by at most half of fp16's smallest step, 2^-25, besides its rounding.  Where that, times the
+            // slots and the largest V, may be above 2^-12 of the row's largest output, the CTA walks twice more under the
+            // references that it has now, for the p' below kLow, 2^24 times, and for the others.  (Loops of their own: within
+            // the first walk's they cost it a fifth of its time.)
+            float bearable = INFINITY;
+            if (ok && any) {                                         // (whole warps)
+                float top = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(lane_base + 128 + c, o);
+                    tmem_wait_ld_regs(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float x = fabsf(__uint_as_float(o[k]));
+                        top = x < INFINITY ? fmaxf(top, x) : top;
+                    }
+                }
+                const int slots = min(limit, j1 * kStep) - j0 * kStep;
+                if (slots > 0) bearable = top * 0x1p13f / static_cast<float>(slots);
+            }
+            const float ref = m == -INFINITY ? 0.0f : m - kShift;
+            for (int walk = 1; another(walk - 1, bearable); ++walk) {
+                Bars &z = s.bars[walk];
+                for (int j = first; j < steps && ok; j += 1 + deal) {
+                    const int i = j - j0, u = i >> deal, at = i & 3;
+                    if (!(ok = wait_either(&z.k_full[i & 1], (i >> 1) & 1, &z.s_full[t], u & 1, abort_flag))) break;
+                    const uint32_t holes = s.holes[at];
+                    const int seen = limit > 0 ? limit - j * kStep : kStep;
+                    if (!(ok = mbar_wait_warp(&z.s_full[t], u & 1, abort_flag, &g_ext_err, 12))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kStep; c += 32) {            // 32 slots at a time, two groups
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t r[16];
+                            tmem_ld16(lane_base + c + 16 * g, r);
+                            tmem_wait_ld_regs(r);
+                            const bool none = (holes >> (c / 4 + g)) & 1u;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int col = c + 16 * g + k, place = SC == 1 ? col : col / 16;
+                                float p = ex2_approx(__uint_as_float(r[k]) * (SC == 0 ? a.sl2 : s.kc[at][place]) - ref);
+                                if constexpr (SC != 0) p *= s.sv[at][place];
+                                if (none || col >= seen) p = 0.0f;
+                                if (p > kMost && p < 65536.0f) p = kMost;    // (rounded otherwise than in the first walk)
+                                const bool low = fabsf(p) < kLow;            // (not a NaN)
+                                r[k] = low == (walk == 1) ? __float_as_uint(low ? p * kLift : p) : 0u;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) pk[8 * g + k / 2] = pack2<BF16>(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                        }
+                        tmem_st16(lane_base + c / 2, pk);
+                        if (c % 64 == 32) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&z.p_full[t][c / 64]);
+                        }
+                    }
+                }
+                if (ok && any) ok = mbar_wait_warp(&z.o_done[t], 0, abort_flag, &g_ext_err, 13);
+                tc_fence_after();
+                if (walk == 1 && ok && any) {                        // to the others' units
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(lane_base + 128 + c, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (1.0f / kLift));
+                        tmem_st16(lane_base + 128 + c, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+        }
         const bool there = r0 + row < a.rows;
         const bool empty = limit == 0 || l == 0.0f;                  // saw nothing (a NaN is no 0)
         const bool part = a.splits > 1 || dealt;

@@ -473,8 +473,9 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
  * whose logits become -infinity; where one becomes +infinity or NaN, O is NaN and L no finite number.
  * Sums and statistics are float32.  Up to 32 rows a kv head (Hq / H * T) the probabilities keep 16
  * bits or more, as in sage_attn_decode.  Above that p sV enters the second product rounded to Q's
- * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and
- * nothing below 2^-36 of it.
+ * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and steps of
+ * 2^-35 of it below that.  Where such steps could move an output by more than 2^-12 of its row's largest (the weight lies
+ * on slots of little value), 11 bits down to 2^-49 and steps of 2^-59, at three times the time for those rows.
  * Results do not depend on the order in which the GPU runs its blocks; their last bits do on the
  * capacity, and up to 32 rows on the other sequences' lengths.  O and L may not overlap the inputs
  * or the cache.  The workspace must be 256-byte aligned; where the query says 0 it may be anything. */

@@ -80,3 +80,89 @@ def test_values_of_zero(kind, block, T, Hq, dtype, lead, at):
     O, L = sg.sage_attn_extend(Q, cache, ints([n0]))
     assert sg.sage_device_status() == 0
     check_rows(Q, O, L, n0, Kd[0], Vd[0], Hq // 2 * T <= 32)
+
+
+def run(kind, dtype, block, T, Hq, n0, sinks, lead, size, *, d=64, change=None, seed=3):
+    sg = _sg()
+    K, V = made(n0 + T, d, sinks, lead, seed, size, dtype)
+    V[:, :, sinks] = 0
+    Q = queries(Hq, T, d, dtype, seed + 1)
+    if change:
+        change(K, V, Q)
+    cache, Kd, Vd = appended(kind, d, 64, block, K, V)
+    O, L = sg.sage_attn_extend(Q, cache, ints([n0]))
+    assert sg.sage_device_status() == 0
+    check_rows(Q, O, L, n0, Kd[0], Vd[0], Hq // 2 * T <= 32)
+    return O
+
+
+# a 16-bit pool, a scale a row, scales of blocks in which the sink is one row of many
+POOLS = [("fp16", 0), ("int8", 0), ("int8", 16), ("fp8", 64)]
+
+
+@pytest.mark.parametrize("kind,block", POOLS)
+@pytest.mark.parametrize("T,Hq", [FEW, ONE, MANY])
+@pytest.mark.parametrize("lead", [12.0, 18.0, 25.65, 33.0])
+@pytest.mark.parametrize("n0", [200, 4096])
+def test_one_slot_takes_the_weight(kind, block, T, Hq, lead, n0):
+    """All others together carry an ordinary fp16 number, each far below 2^-25 of the largest probability."""
+    O = run(kind, torch.float16, block, T, Hq, n0, slice(7, 8), lead, 6e4 / 1.75)
+    if lead < 26 and n0 == 4096:
+        assert bool((O > 1e-4).all())
+
+
+@pytest.mark.parametrize("kind,block", POOLS)
+@pytest.mark.parametrize("T,Hq", [ONE, MANY])
+@pytest.mark.parametrize("carries", [1.0, 2.0 ** -6, 2.0 ** -14])
+def test_the_slot_carries_little(kind, block, T, Hq, carries):
+    """The slot with the weight has small values, or one value alone."""
+    def small(K, V, Q):
+        V[:, 0, 7] = carries
+        V[:, 1, 7, 5] = carries
+    run(kind, torch.float16, block, T, Hq, 3000, slice(7, 8), 25.65, 3e4, change=small)
+
+
+@pytest.mark.parametrize("kind,block", POOLS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,Hq,n0", [(40, 2, 20000), (700, 6, 1000), (129, 2, 0), (256, 4, 256)])
+def test_rows_that_need_it_among_rows_that_do_not(kind, block, d, T, Hq, n0):
+    """Ranges of slots, tiles of several heads, and rows whose slot with the weight is another, or none."""
+    def some(K, V, Q):
+        Q[:, :, 1::3, 0] = 0.0
+        Q[:, :, 2::3, 0] = -4.0
+        K[:, :, n0 + 5::17, 0] = -25.0 * d ** 0.5 / 4
+    run(kind, torch.float16, block, T, Hq, n0, slice(3, 4), 25.65, 2e4, d=d, change=some)
+
+
+@pytest.mark.parametrize("T,Hq", [ONE, MANY])
+def test_ragged_and_replayed(T, Hq):
+    """Counts, a sequence without slots, and a graph whose replay needs the further walks where its capture did not."""
+    sg = _sg()
+    n0, d = 500, 64
+    K, V = made(n0 + T, d, slice(9, 10), 25.65, 5, 3e4, torch.float16)
+    V[:, :, 9] = 0
+    cache = sg.make_kv_cache(3, 2, d, n0 + T, dtype=torch.float16, page=64)
+    K3, V3 = (x.expand(3, -1, -1, -1).contiguous() for x in (K, V))
+    sg.sage_kv_append(cache, K3, V3, ints([0] * 3))
+    start, count = [n0, 0, 30], [T, 0, T - 3]
+    Q = queries(Hq, T, d, torch.float16, 6).expand(3, -1, -1, -1).contiguous()
+    easy = Q.clone()
+    easy[..., 0] = 0
+    held = easy.clone()
+    s, c = ints(start), ints(count)
+    sg.sage_attn_extend(held, cache, s, count=c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O, L = sg.sage_attn_extend(held, cache, s, count=c)
+    for x in (easy, Q, easy):
+        held.copy_(x)
+        graph.replay()
+        again = sg.sage_attn_extend(x, cache, s, count=c)
+        assert torch.equal(O, again[0]) and torch.equal(L, again[1])
+        Kd, Vd = (y[0].double().cpu().numpy() for y in (K, V))
+        for b in (0, 2):
+            n = count[b]
+            check_rows(x[b:b + 1, :, :n], O[b:b + 1, :, :n], L[b:b + 1, :, :n], start[b], Kd[:, :start[b] + n], Vd[:, :start[b] + n], False)
+        assert bool((O[1] == 0).all()) and bool((O[2, :, T - 3:] == 0).all()) and bool(L[1].isneginf().all())
+    assert sg.sage_device_status() == 0
