@@ -317,8 +317,8 @@ struct Loader {
                 const int row = r0 + 128 * t + r;
                 uint4 w = row < a.rows ? __ldg(Q + static_cast<size_t>(row) * QC + tid % QC) : make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (BF16 && SC != 0) {
-                    // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15), and what is
-                    // below 2^-39 of it loses bits
+                    // to fp16 under a power of two a row: the largest value lands in [2^14, 2^15); the 8 bits of others are
+                    // all there down to 2^-31 of it (fp16's steps end at 2^-24), and from 2^-39 on they are gone
                     float2 f[4];
                     float mx = 0.0f;
 #pragma unroll

@@ -291,7 +291,8 @@ def sage_kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, start: torc
     cache, in its form.  ``mu`` (B,H,d) float32 (8-bit caches): K-smoothing, codes of K - mu.
     ``pos`` (B) int32: position in the text of each sequence's first new token (None: its slot).
     With scales of blocks a block's scale grows with its rows (the codes before start[b] follow), and
-    what it holds behind the last new token is lost.
+    what it holds behind the last new token is lost.  It does not shrink when tokens are taken back (a start
+    below an earlier call's end), until a call begins the block anew.
     Scores of the new slots are 0: decoding adds to them, weights of a prompt's own queries are the
     caller's to write to cache.score."""
     shape, dev = K.shape, cache.device

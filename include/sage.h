@@ -434,7 +434,9 @@ typedef struct sage_kv {
  * start[b]) takes the larger of its scale and theirs; where that grows, the codes of its rows before
  * start[b] become the nearest (ties to even) of fl32(code * fl32(delta_old / delta)).  What the
  * block holds behind the call's last row is lost.  A NaN or an infinity makes the scale of its whole
- * block NaN or infinite.
+ * block NaN or infinite.  Rows that are taken back (a start below an earlier call's end: rejected drafts) leave
+ * their block the scale that they gave it, a NaN too, until a call begins the block anew; the codes of the
+ * rows that stay have been rounded again under it.
  * Where the cache has score: score[slot] = 0 (only sage_attn_decode adds to it: weights of a prompt's
  * own queries are the caller's to write there).  Where it has pos: pos[slot] = pos0[b] + t, with
  * pos0 NULL: the slot itself. */
@@ -473,9 +475,11 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
  * whose logits become -infinity; where one becomes +infinity or NaN, O is NaN and L no finite number.
  * Sums and statistics are float32.  Up to 32 rows a kv head (Hq / H * T) the probabilities keep 16
  * bits or more, as in sage_attn_decode.  Above that p sV enters the second product rounded to Q's
- * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and steps of
- * 2^-35 of it below that.  Where such steps could move an output by more than 2^-12 of its row's largest (the weight lies
- * on slots of little value), 11 bits down to 2^-49 and steps of 2^-59, at three times the time for those rows.
+ * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and
+ * steps of 2^-35 of it below that.  Where such steps could move an output by more than 2^-12 of its row's
+ * largest (the weight lies on slots of little value), 11 bits down to 2^-49 and steps of 2^-59, at three
+ * times the time for those rows.  Q in bf16 meets 8-bit keys there in fp16 under a power of two a row: its
+ * values below 2^-31 of a row's largest lose bits, those below 2^-39 are gone.
  * Results do not depend on the order in which the GPU runs its blocks; their last bits do on the
  * capacity, and up to 32 rows on the other sequences' lengths.  O and L may not overlap the inputs
  * or the cache.  The workspace must be 256-byte aligned; where the query says 0 it may be anything. */
