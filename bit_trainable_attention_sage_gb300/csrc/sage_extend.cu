@@ -37,7 +37,7 @@
 // below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of those.  Where what fp16 may
 // have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest output, its CTA walks the slots
 // twice more, under the references that the first walk left: once for the small p', 2^24 times, and once for the others.
-// That CTA takes three times as long; the largest V of a 16-bit pool is found beside the first walk.
+// That takes 3.3 times as long where every row needs it (chunk over an fp16 pool 390 -> 1288 us); the largest V of a 16-bit pool is found beside the first walk.
 // K's codes meet Q in fp16 (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.
 // Sums, statistics and O are float32.
 //
@@ -166,6 +166,13 @@ __device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
     if constexpr (FP8) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
     else if constexpr (BF16) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
     else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
+}
+
+// To fp16, 65504 at most (a NaN stays one).
+__device__ __forceinline__ uint32_t pack_finite(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 // max(|a|, |b|) of two pairs of fp16, under some sign
@@ -1039,34 +1046,44 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             const float ref = m == -INFINITY ? 0.0f : m - kShift;
             for (int walk = 1; another(walk - 1, bearable); ++walk) {
                 Bars &z = s.bars[walk];
+                const float for_low = walk == 1 ? kLift : 0.0f, for_others = walk == 1 ? 0.0f : 1.0f;
                 for (int j = first; j < steps && ok; j += 1 + deal) {
                     const int i = j - j0, u = i >> deal, at = i & 3;
                     if (!(ok = wait_either(&z.k_full[i & 1], (i >> 1) & 1, &z.s_full[t], u & 1, abort_flag))) break;
                     const uint32_t holes = s.holes[at];
                     const int seen = limit > 0 ? limit - j * kStep : kStep;
+                    const bool whole = (holes & ~kOdd) == 0u && !__any_sync(0xffffffffu, seen < kStep);
                     if (!(ok = mbar_wait_warp(&z.s_full[t], u & 1, abort_flag, &g_ext_err, 12))) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < kStep; c += 32) {            // 32 slots at a time, two groups
-                        uint32_t pk[16];
+                        uint32_t r[2][16], pk[16];
+                        tmem_ld16(lane_base + c, r[0]);
+                        tmem_ld16(lane_base + c + 16, r[1]);
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            uint32_t r[16];
-                            tmem_ld16(lane_base + c + 16 * g, r);
-                            tmem_wait_ld_regs(r);
-                            const bool none = (holes >> (c / 4 + g)) & 1u;
+                            tmem_wait_ld_regs(r[g]);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
                                 const int col = c + 16 * g + k, place = SC == 1 ? col : col / 16;
-                                float p = ex2_approx(__uint_as_float(r[k]) * (SC == 0 ? a.sl2 : s.kc[at][place]) - ref);
+                                float p = ex2_approx(fmaf(__uint_as_float(r[g][k]), SC == 0 ? a.sl2 : s.kc[at][place], -ref));
                                 if constexpr (SC != 0) p *= s.sv[at][place];
-                                if (none || col >= seen) p = 0.0f;
-                                if (p > kMost && p < 65536.0f) p = kMost;    // (rounded otherwise than in the first walk)
-                                const bool low = fabsf(p) < kLow;            // (not a NaN)
-                                r[k] = low == (walk == 1) ? __float_as_uint(low ? p * kLift : p) : 0u;
+                                r[g][k] = __float_as_uint(p);
+                            }
+                            if (!whole) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (((holes >> (c / 4 + g)) & 1u) || c + 16 * g + k >= seen) r[g][k] = 0u;
                             }
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) pk[8 * g + k / 2] = pack2<BF16>(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                            for (int k = 0; k < 16; ++k) {
+                                // (rounded otherwise than in the first walk a p' can lie just above what that allowed; one that is
+                                // infinite, of a scale that is, leaves a NaN)
+                                const float p = __uint_as_float(r[g][k]), f = fabsf(p) < kLow ? for_low : for_others;
+                                r[g][k] = __float_as_uint(SC == 0 ? p * f : fmaf(p, f, p * 0.0f));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) pk[8 * g + k / 2] = pack_finite(__uint_as_float(r[g][k]), __uint_as_float(r[g][k + 1]));
                         }
                         tmem_st16(lane_base + c / 2, pk);
                         if (c % 64 == 32) {

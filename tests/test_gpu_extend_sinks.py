@@ -166,3 +166,31 @@ def test_ragged_and_replayed(T, Hq):
             check_rows(x[b:b + 1, :, :n], O[b:b + 1, :, :n], L[b:b + 1, :, :n], start[b], Kd[:, :start[b] + n], Vd[:, :start[b] + n], False)
         assert bool((O[1] == 0).all()) and bool((O[2, :, T - 3:] == 0).all()) and bool(L[1].isneginf().all())
     assert sg.sage_device_status() == 0
+
+
+@pytest.mark.parametrize("kind,block", POOLS)
+@pytest.mark.parametrize("T,Hq", [ONE, MANY])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_show(kind, block, T, Hq, value):
+    """Beside a slot that takes the weight: rows that see such a value or scale show it, the others are as they would be
+    without it, and L does not depend on it."""
+    sg = _sg()
+    n0, d, s = 700, 64, 700 + T // 2
+    K, V = made(n0 + T, d, slice(7, 8), 25.65, 9, 3e4, torch.float16)
+    V[:, :, 7] = 0
+    Q = queries(Hq, T, d, torch.float16, 10)
+    cache, Kd, Vd = appended(kind, d, 64, block, K, V)
+    good_O, good_L = sg.sage_attn_extend(Q, cache, ints([n0]))
+    check_rows(Q, good_O, good_L, n0, Kd[0], Vd[0], False)
+    p, off, size = int(cache.table[0, s // 64]), s % 64, block or 1
+    if cache.sV is None:
+        cache.V[p, 1, off, 3] = value
+    else:
+        cache.sV[p, 1, off // size] = value
+    O, L = sg.sage_attn_extend(Q, cache, ints([n0]))
+    G, before = Hq // 2, max(0, s // size * size - n0)
+    assert torch.equal(O[:, :G], good_O[:, :G]) and torch.allclose(L, good_L, rtol=1e-6, atol=1e-5)
+    reached = O[:, G:, T // 2:] if cache.sV is not None else O[:, G:, T // 2:, 3]
+    assert not reached.isfinite().any()
+    assert torch.allclose(O[:, G:, :before].float(), good_O[:, G:, :before].float(), rtol=2.0 ** -9, atol=2.0 ** -20)
+    assert sg.sage_device_status() == 0
