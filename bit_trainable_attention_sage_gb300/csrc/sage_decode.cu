@@ -110,17 +110,10 @@ template <int DST, int SRC>
 __device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 4 : 0;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -172,48 +165,6 @@ __device__ __forceinline__ void load_half(uint32_t k_dst, uint32_t v_dst, const 
     (cp_async16_at<I * 512, I * 512>(v_dst ^ (chunk_at<D, KIND>(I * RPI, 0) - I * 512u), v), ...);
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
-
-// Bytes (0,1) and (2,3) of w as fp16 pairs.  INT8: byte ^ 0x80 under 0x64 is 1024 + 128 + code
-// in fp16, less 1152 the code; E4M3 by the conversion instruction.  All exact.
-template <int KIND>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (KIND == 2) {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
-        const uint32_t k = 0x64806480u;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(k));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(k));
-    } else {
-        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
-        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-    }
-}
-
-// The same as bf16 pairs.  INT8: the low seven bits under 0x43 are 128 + them in bf16, the sign under 0x43
-// 128 or 256; their difference is the code.  E4M3 through float32.  All exact.
-template <int KIND>
-__device__ __forceinline__ void widen4_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (KIND == 2) {
-        const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
-    } else {
-        widen4<KIND>(w, lo, hi);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
-        lo = *reinterpret_cast<const uint32_t *>(&x);
-        hi = *reinterpret_cast<const uint32_t *>(&y);
-    }
-}
-
-// Which 16-bit values (E4M3 codes) of a word are not finite, as a mask of their bits.
-template <int KIND>
-__device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
-    if constexpr (KIND == 3) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    else if constexpr (KIND == 1) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
-    else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
-}
 // A pool's values i and i + 1 (E4M3: codes).
 template <int KIND>
 __device__ __forceinline__ float2 value_pair(const void *pool, size_t i) {
@@ -696,8 +647,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t ka[4];
-                            widen4<KIND>(w0[i], ka[0], ka[2]);
-                            widen4<KIND>(w1[i], ka[1], ka[3]);
+                            widen4<false, KIND == 3>(w0[i], ka[0], ka[2]);
+                            widen4<false, KIND == 3>(w1[i], ka[1], ka[3]);
 #pragma unroll
                             for (int nh = 0; nh < NH; ++nh)
                                 mma16816<false>(s[hf][nh], ka, qb[nh][4 * jj + i][0], qb[nh][4 * jj + i][1]);
@@ -747,8 +698,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
                     for (int i = lane; i < S::GRAN * S::ROW / 16; i += 32) {
                         uint4 *at = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(vst)) + i;
                         const uint4 w = *at;
-                        const uint32_t m0 = not_finite_mask<KIND>(w.x), m1 = not_finite_mask<KIND>(w.y);
-                        const uint32_t m2 = not_finite_mask<KIND>(w.z), m3 = not_finite_mask<KIND>(w.w);
+                        const uint32_t m0 = not_finite_mask<KIND == 1, KIND == 3>(w.x), m1 = not_finite_mask<KIND == 1, KIND == 3>(w.y);
+                        const uint32_t m2 = not_finite_mask<KIND == 1, KIND == 3>(w.z), m3 = not_finite_mask<KIND == 1, KIND == 3>(w.w);
                         if (m0 | m1 | m2 | m3) *at = make_uint4(w.x & ~m0, w.y & ~m1, w.z & ~m2, w.w & ~m3);
                         bad |= m0 | m1 | m2 | m3;
                     }
@@ -904,10 +855,10 @@ __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, KIND, MR>::CTAS) d
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
                             uint32_t va[2][4];
-                            widen4_bf16<KIND>(prmt(x[0][i], x[1][i], 0x5140), va[0][0], va[0][1]);
-                            widen4_bf16<KIND>(prmt(x[2][i], x[3][i], 0x5140), va[0][2], va[0][3]);
-                            widen4_bf16<KIND>(prmt(x[0][i], x[1][i], 0x7362), va[1][0], va[1][1]);
-                            widen4_bf16<KIND>(prmt(x[2][i], x[3][i], 0x7362), va[1][2], va[1][3]);
+                            widen4<true, KIND == 3>(prmt(x[0][i], x[1][i], 0x5140), va[0][0], va[0][1]);
+                            widen4<true, KIND == 3>(prmt(x[2][i], x[3][i], 0x5140), va[0][2], va[0][3]);
+                            widen4<true, KIND == 3>(prmt(x[0][i], x[1][i], 0x7362), va[1][0], va[1][1]);
+                            widen4<true, KIND == 3>(prmt(x[2][i], x[3][i], 0x7362), va[1][2], va[1][3]);
                             pv(2 * i, va[0]);
                             pv(2 * i + 1, va[1]);
                         }

@@ -20,9 +20,10 @@
 //               beside the other 64's softmax; O stays in TMEM over the whole walk and is rescaled only where a
 //               row's reference, its largest logit when it last moved, lags too far behind.
 // Measured (INT8 with scales of blocks / bf16 pool, 2 sequences of 2048 new tokens over 6144, 32 query heads on 8, d = 128):
-// 500 / 381 us, 963 / 1262 TFLOP/s of the 1903 that a library product reaches.  A step of 128 slots takes 3050 cycles over a
+// 508 / 387 us, 947 / 1243 TFLOP/s of the 1903 that a library product reaches.  A step of 128 slots takes 3050 cycles over a
 // bf16 pool where the MMAs alone take 2540 (their operands fill shared memory's bandwidth): what is left is the chain
 // from a tile's last P to its next S.  In 8 bits 3900: the loaders share schedulers and instruction cache with the softmax.
+// And the last wave: these 512 CTAs of 50 to 64 steps are 192 steps an SM, and the SM that ends last has 224.
 // TMEM: columns 256 t + [0, 128) S_t and P_t, 256 t + 128 + [0, d) O_t.
 //
 // Scales.  Codes are exact in fp16 and bf16, so a logit x is acc * (sK log2(e) / sqrt(d)); with one scale a
@@ -37,7 +38,8 @@
 // below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of those.  Where what fp16 may
 // have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest output, its CTA walks the slots
 // twice more, under the references that the first walk left: once for the small p', 2^24 times, and once for the others.
-// That takes 3.3 times as long where every row needs it (chunk over an fp16 pool 390 -> 1288 us); the largest V of a 16-bit pool is found beside the first walk.
+// That takes 3.3 times as long where every row needs it (chunk over an fp16 pool 390 -> 1288 us); the largest V of a
+// 16-bit pool is found beside the first walk.
 // K's codes meet Q in fp16 (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.
 // Sums, statistics and O are float32.
 //
@@ -123,33 +125,6 @@ __device__ __forceinline__ float followed_log2(float sv) {
 constexpr uint32_t kOdd = 4u;                        // in the word of a step's holes
 __device__ __forceinline__ bool ordinary(float sv) { return sv == 0.0f || (sv >= kLeastScale && sv <= kMostScale); }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
-
-// Four codes as two pairs of fp16 (K) or of Q's type (V).  All exact.
-//   fp16: INT8: byte ^ 0x80 under 0x64 is 1024 + 128 + code, less 1152 the code; E4M3 by the conversion instruction.
-//   bf16: INT8: the low seven bits under 0x43 are 128 + them, the sign under 0x43 128 or 256; E4M3 through float32.
-template <bool BF16, bool FP8>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (FP8) {
-        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
-        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-        if constexpr (BF16) {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-            const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
-            lo = *reinterpret_cast<const uint32_t *>(&x);
-            hi = *reinterpret_cast<const uint32_t *>(&y);
-        }
-    } else if constexpr (BF16) {
-        const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
-    } else {
-        const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, 0x64646464u, 0x4140)), "r"(k));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, 0x64646464u, 0x4342)), "r"(k));
-    }
-}
-
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (BF16) {
@@ -158,14 +133,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     } else {
         return pack_half2(lo, hi);
     }
-}
-
-// Which 16-bit values (E4M3 codes) of a word are not finite, as a mask of their bits.
-template <bool BF16, bool FP8>
-__device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
-    if constexpr (FP8) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    else if constexpr (BF16) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
-    else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
 }
 
 // To fp16, 65504 at most (a NaN stays one).
@@ -186,17 +153,6 @@ __device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");

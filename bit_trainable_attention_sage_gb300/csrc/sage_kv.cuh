@@ -1,6 +1,6 @@
-// sage_kv.cuh -- what the cache kernels (sage_kv.cu, sage_decode.cu) share: the device view of a
-// paged key-value cache, the lookup of a slot's row with its bounds checks, and the checks of the
-// C entry points.
+// sage_kv.cuh -- what the cache kernels (sage_kv.cu, sage_decode.cu, sage_extend.cu, sage_pages.cu) share: the device view
+// of a paged key-value cache, the lookup of a slot's row with its bounds checks, codes widened to 16 bits, copies to
+// shared memory, and the checks of the C entry points.
 #pragma once
 
 #include "sage_device.cuh"
@@ -42,6 +42,54 @@ __device__ __forceinline__ int4 cluster_words(const int *p, int rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+
+// ---- copies to shared memory that a thread does not wait for ------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;            // 0: the 16 bytes are zeroed and nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ---- codes in 16 bits -------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Four codes as two pairs of fp16 or bf16.  All exact.
+//   fp16: INT8: byte ^ 0x80 under 0x64 is 1024 + 128 + code, less 1152 the code; E4M3 by the conversion instruction.
+//   bf16: INT8: the low seven bits under 0x43 are 128 + them, the sign under 0x43 128 or 256; E4M3 through float32.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FP8) {
+        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+        if constexpr (BF16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+            lo = *reinterpret_cast<const uint32_t *>(&x);
+            hi = *reinterpret_cast<const uint32_t *>(&y);
+        }
+    } else if constexpr (BF16) {
+        const uint32_t u = w & 0x7F7F7F7Fu, s = w & 0x80808080u, k = 0x43434343u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, k, 0x4140)), "r"(prmt(s, k, 0x4140)));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, k, 0x4342)), "r"(prmt(s, k, 0x4342)));
+    } else {
+        const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(prmt(u, 0x64646464u, 0x4140)), "r"(k));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(prmt(u, 0x64646464u, 0x4342)), "r"(k));
+    }
+}
+
+// Which 16-bit values (E4M3 codes) of a word are not finite, as a mask of their bits.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
+    if constexpr (FP8) return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    else if constexpr (BF16) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+    else return __vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
 }
 
 struct KvView {
