@@ -34,7 +34,7 @@
 // A scale a row is multiplied on; scales of blocks go into the exponent with x, in the rare steps with one outside
 // [2^-60, 2^20] or with hidden slots by a pass over S of their own.
 // Roundings: p' is rounded to Q's type, half a step of the output's own type each, and they average over the slots: bf16
-// (8 bits, of any size), or fp16, the running maximum's at 2^11, so that all 11 bits are there down to 2^-25 of it and
+// (8 bits, down to 2^-100 of the row's largest), or fp16, the running maximum's at 2^11, so that all 11 bits are there down to 2^-25 of it and
 // below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of those.  Where what fp16 may
 // have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest output, its CTA walks the slots
 // twice more, under the references that the first walk left: once for the small p', 2^24 times, and once for the others.

@@ -471,15 +471,17 @@ SAGE_API int sage_attn_decode(const sage_kv *c, int Hq, const void *Q, const int
  * Out: O (B,Hq,T,d), L (B,Hq,T) float32.
  * What a token does not see does not reach it, whatever it holds.  A NaN in a visible K or its scale
  * makes O and L NaN, an infinity or a NaN in a visible V the channels of O that it reaches infinite
- * or NaN, in its scale all of them; L does not depend on V.  An infinity in K or its scale takes the slots out
- * whose logits become -infinity; where one becomes +infinity or NaN, O is NaN and L no finite number.
+ * or NaN, in its scale all of them; L does not depend on V.  An infinity in K or its scale takes the
+ * slots out whose logits become -infinity; where one becomes +infinity or NaN, O is NaN and L no finite
+ * number.
  * Sums and statistics are float32.  Up to 32 rows a kv head (Hq / H * T) the probabilities keep 16
  * bits or more, as in sage_attn_decode.  Above that p sV enters the second product rounded to Q's
- * type: bf16 keeps 8 bits of each however small, fp16 11 bits down to 2^-25 of the row's largest and
- * steps of 2^-35 of it below that.  Where such steps could move an output by more than 2^-12 of its row's
- * largest (the weight lies on slots of little value), 11 bits down to 2^-49 and steps of 2^-59, at three
- * times the time for those rows.  Q in bf16 meets 8-bit keys there in fp16 under a power of two a row: its
- * values below 2^-31 of a row's largest lose bits, those below 2^-39 are gone.
+ * type.  bf16 keeps 8 bits of each down to 2^-100 of the row's largest (where an sV below 2^-60 counts
+ * as that).  fp16 keeps 11 bits down to 2^-25 of it and steps of 2^-35 below; where such steps could move
+ * an output by more than 2^-12 of its row's largest (the weight lies on slots of little value), 11 bits
+ * down to 2^-49 and steps of 2^-59, at three times the time for those rows.  Q in bf16 meets 8-bit keys
+ * there in fp16 under a power of two a row: its values below 2^-31 of a row's largest lose bits, those
+ * below 2^-39 are gone.
  * Results do not depend on the order in which the GPU runs its blocks; their last bits do on the
  * capacity, and up to 32 rows on the other sequences' lengths.  O and L may not overlap the inputs
  * or the cache.  The workspace must be 256-byte aligned; where the query says 0 it may be anything. */
