@@ -34,12 +34,12 @@
 // A scale a row is multiplied on; scales of blocks go into the exponent with x, in the rare steps with one outside
 // [2^-60, 2^20] or with hidden slots by a pass over S of their own.
 // Roundings: p' is rounded to Q's type, half a step of the output's own type each, and they average over the slots: bf16
-// (8 bits, down to 2^-100 of the row's largest), or fp16, the running maximum's at 2^11, so that all 11 bits are there down to 2^-25 of it and
-// below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of those.  Where what fp16 may
-// have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest output, its CTA walks the slots
-// twice more, under the references that the first walk left: once for the small p', 2^24 times, and once for the others.
-// That takes 3.3 times as long where every row needs it (chunk over an fp16 pool 390 -> 1288 us); the largest V of a
-// 16-bit pool is found beside the first walk.
+// (8 bits, down to 2^-100 of the row's largest), or fp16, the running maximum's at 2^11, so that all 11 bits are there
+// down to 2^-25 of it and below in steps of 2^-35.  A row whose weight lies on slots of little value can be made of
+// those.  Where what fp16 may have lost (half a step a slot, times the largest V) exceeds 2^-12 of a row's largest
+// output, its CTA walks the slots twice more, under the references that the first walk left: once for the small p',
+// 2^24 times, and once for the others.  That takes 3.3 times as long where every row needs it (chunk over an fp16 pool
+// 390 -> 1288 us); the largest V of a 16-bit pool is found beside the first walk.
 // K's codes meet Q in fp16 (4 of them take 5 or 2 instructions, to bf16 8 or 10), Q in bf16 under a power of two a row.
 // Sums, statistics and O are float32.
 //
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
     // step j is the (j - j0)th: stage (j - j0) & 1, its barriers' phase ((j - j0) >> 1) & 1
-    // All warps, at the end of a walk: whether there is another one.  `bearable`: the largest |V| (8 bits: code) with which
-    // fp16 can not have lost too much of this thread's row.
+    // All warps of the CTA, each at the end of a walk, also of one that gave up: whether there is another one.
+    // `bearable`: the largest |V| (8 bits: code) with which fp16 cannot have lost too much of this thread's row.
     auto all_warps = [&]() {
         __syncwarp();
         tc_fence_before();
@@ -621,101 +621,102 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     if (warp >= kMmaWarp) {
         regs_dec<kRegsControl>();
         for (int walk = 0;; ++walk) {
-        Bars &z = s.bars[walk];
-        if (warp == kMmaWarp && elect_one()) {
-            // ------------------------------------------------------------------ MMA issuer
-            constexpr uint32_t idS = idesc_f16(128, 128, BF16 && SC == 0, false, false);
-            constexpr uint32_t idPV = idesc_f16(128, D, BF16, false, true);
-            auto issue_s = [&](const int t, int st) {
-                const uint32_t q_addr = smem_u32(s.q[dealt ? 0 : t][0]), k_addr = smem_u32(s.k[st][0]);
+            Bars &z = s.bars[walk];
+            if (warp == kMmaWarp && elect_one()) {
+                // ------------------------------------------------------------------ MMA issuer
+                constexpr uint32_t idS = idesc_f16(128, 128, BF16 && SC == 0, false, false);
+                constexpr uint32_t idPV = idesc_f16(128, D, BF16, false, true);
+                auto issue_s = [&](const int t, int st) {
+                    const uint32_t q_addr = smem_u32(s.q[dealt ? 0 : t][0]), k_addr = smem_u32(s.k[st][0]);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-                    umma_ss(tmem + 256 * t, sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0);
-                }
-                umma_commit(&z.s_full[t]);
-            };
-            // O_t += P_t V of a step, the tile's u-th, half by half
-            auto issue_pv = [&](const int t, int u, int st, bool last) -> bool {
-                const uint32_t v_addr = smem_u32(s.v[st][0]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!mbar_wait(&z.p_full[t][h], u & 1, abort_flag, &g_ext_err, 4)) return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                        umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (walk == 2 || u > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&z.o_full[t]);
-                }
-                if (last) umma_commit(&z.o_done[t]);
-                return true;
-            };
-            const int n = j1 - j0;
-            bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&z.k_full[0], 0, abort_flag, &g_ext_err, 2);
-            // As in the forward kernel a tile's next S follows its PV in issue order and overwrites the P that the
-            // PV reads: the tensor pipe runs MMAs in that order.
-            if (dealt) {
-                // step i is group i & 1's: its S once that group's last PV has been issued
-                if (ok) {
-                    tc_fence_after();
-                    issue_s(0, 0);
-                    umma_commit(&z.k_free[0]);
-                }
-                if (ok && n > 1 && (ok = mbar_wait(&z.k_full[1], 0, abort_flag, &g_ext_err, 2))) {
-                    tc_fence_after();
-                    issue_s(1, 1);
-                    umma_commit(&z.k_free[1]);
-                }
-                auto step = [&](const int t, int i) -> bool {
-                    if (!mbar_wait(&z.v_full[t], (i >> 1) & 1, abort_flag, &g_ext_err, 3)) return false;
-                    if (!issue_pv(t, i >> 1, t, i + 2 >= n)) return false;
-                    umma_commit(&z.v_free[t]);
-                    if (i + 2 < n) {
-                        if (!mbar_wait(&z.k_full[t], ((i + 2) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
-                        tc_fence_after();
-                        issue_s(t, t);
-                        umma_commit(&z.k_free[t]);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+                        umma_ss(tmem + 256 * t, sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0);
                     }
+                    umma_commit(&z.s_full[t]);
+                };
+                // O_t += P_t V of a step, the tile's u-th, half by half
+                auto issue_pv = [&](const int t, int u, int st, bool last) -> bool {
+                    const uint32_t v_addr = smem_u32(s.v[st][0]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!mbar_wait(&z.p_full[t][h], u & 1, abort_flag, &g_ext_err, 4)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            umma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, sdesc_sw128(v_addr + 16 * kk * 128, 16384, 1024), idPV, (walk == 2 || u > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&z.o_full[t]);
+                    }
+                    if (last) umma_commit(&z.o_done[t]);
                     return true;
                 };
-                for (int i = 0; i < n && ok; i += 2) ok = step(0, i) && (i + 1 >= n || step(1, i + 1));
-            } else {
-                if (ok) {
-                    tc_fence_after();
-                    if (j0 < n_t[0]) issue_s(0, 0);
-                    if (j0 < n_t[1]) issue_s(1, 0);
-                    umma_commit(&z.k_free[0]);
-                }
-                for (int j = j0; j < j1 && ok; ++j) {
-                    const int i = j - j0, st = i & 1, nst = st ^ 1;
-                    if (!(ok = mbar_wait(&z.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
-                    // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
-                    if (j + 1 < j1 && !(ok = mbar_wait(&z.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
-                    auto tile_step = [&](const int t) -> bool {
-                        if (j >= n_t[t]) return true;
-                        if (!issue_pv(t, i, st, j + 1 == n_t[t])) return false;
-                        if (t == 1 || j >= n_t[1]) umma_commit(&z.v_free[st]);
-                        if (j + 1 < n_t[t]) issue_s(t, nst);
+                const int n = j1 - j0;
+                bool ok = mbar_wait(&s.q_full, 0, abort_flag, &g_ext_err, 1) && mbar_wait(&z.k_full[0], 0, abort_flag, &g_ext_err, 2);
+                // As in the forward kernel a tile's next S follows its PV in issue order and overwrites the P that the
+                // PV reads: the tensor pipe runs MMAs in that order.
+                if (dealt) {
+                    // step i is group i & 1's: its S once that group's last PV has been issued
+                    if (ok) {
+                        tc_fence_after();
+                        issue_s(0, 0);
+                        umma_commit(&z.k_free[0]);
+                    }
+                    if (ok && n > 1 && (ok = mbar_wait(&z.k_full[1], 0, abort_flag, &g_ext_err, 2))) {
+                        tc_fence_after();
+                        issue_s(1, 1);
+                        umma_commit(&z.k_free[1]);
+                    }
+                    auto step = [&](const int t, int i) -> bool {
+                        if (!mbar_wait(&z.v_full[t], (i >> 1) & 1, abort_flag, &g_ext_err, 3)) return false;
+                        if (!issue_pv(t, i >> 1, t, i + 2 >= n)) return false;
+                        umma_commit(&z.v_free[t]);
+                        if (i + 2 < n) {
+                            if (!mbar_wait(&z.k_full[t], ((i + 2) >> 1) & 1, abort_flag, &g_ext_err, 2)) return false;
+                            tc_fence_after();
+                            issue_s(t, t);
+                            umma_commit(&z.k_free[t]);
+                        }
                         return true;
                     };
-                    ok = tile_step(0) && tile_step(1);
-                    if (!ok) break;
-                    if (j + 1 < j1) umma_commit(&z.k_free[nst]);
+                    for (int i = 0; i < n && ok; i += 2) ok = step(0, i) && (i + 1 >= n || step(1, i + 1));
+                } else {
+                    if (ok) {
+                        tc_fence_after();
+                        if (j0 < n_t[0]) issue_s(0, 0);
+                        if (j0 < n_t[1]) issue_s(1, 0);
+                        umma_commit(&z.k_free[0]);
+                    }
+                    for (int j = j0; j < j1 && ok; ++j) {
+                        const int i = j - j0, st = i & 1, nst = st ^ 1;
+                        if (!(ok = mbar_wait(&z.v_full[st], (i >> 1) & 1, abort_flag, &g_ext_err, 3))) break;
+                        // (the next K too, which has been there for long: nothing then stands between a tile's PV and its next S)
+                        if (j + 1 < j1 && !(ok = mbar_wait(&z.k_full[nst], ((i + 1) >> 1) & 1, abort_flag, &g_ext_err, 2))) break;
+                        auto tile_step = [&](const int t) -> bool {
+                            if (j >= n_t[t]) return true;
+                            if (!issue_pv(t, i, st, j + 1 == n_t[t])) return false;
+                            if (t == 1 || j >= n_t[1]) umma_commit(&z.v_free[st]);
+                            if (j + 1 < n_t[t]) issue_s(t, nst);
+                            return true;
+                        };
+                        ok = tile_step(0) && tile_step(1);
+                        if (!ok) break;
+                        if (j + 1 < j1) umma_commit(&z.k_free[nst]);
+                    }
                 }
+                // every MMA must have finished before the tensor memory is released
+                umma_commit(&z.mma_done);
+                mbar_wait_drain(&z.mma_done, 0, &g_ext_err, 5);
             }
-            // every MMA must have finished before the tensor memory is released
-            umma_commit(&z.mma_done);
-            mbar_wait_drain(&z.mma_done, 0, &g_ext_err, 5);
-        }
-        if (!another(walk, INFINITY)) break;
+            if (!another(walk, INFINITY)) break;
         }
     } else if (warp >= kKeyWarp) {
         regs_dec<kRegsLoad>();
         for (int walk = 0;; ++walk) {
-        const Loader<D, BF16, SC, FP8> load{a, s, s.bars[walk], walk, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0, warp >= kValueWarp && dealt ? 0 : n_t[warp >= kValueWarp], out0};
-        if (warp < kValueWarp) load.template run<false>();
-        else load.template run<true>();
-        if (!another(walk, INFINITY)) break;
+            const Loader<D, BF16, SC, FP8> load{a, s, s.bars[walk], walk, b, hk, j0, j1, kv_end, mixed, static_cast<int>(threadIdx.x) & 127, r0,
+                                                warp >= kValueWarp && dealt ? 0 : n_t[warp >= kValueWarp], out0};
+            if (warp < kValueWarp) load.template run<false>();
+            else load.template run<true>();
+            if (!another(walk, INFINITY)) break;
         }
     } else {
         regs_inc<kRegsSoftmax>();

@@ -514,7 +514,8 @@ SAGE_API int sage_kv_evict(const sage_kv *c, const int *lens, const int *seen, i
  * Free pages are given in ascending order, to sequences in ascending order: results depend on the
  * inputs alone.  refs, held and all int32 inputs need 4-byte alignment; out may not overlap an input.
  * An input out of range is held to it, or a parent out of range read as the sequence itself, and an
- * entry that is no page left alone: SAGE_ERR_INDEX (from sage_kv_compact where pages move).  A pool without a free page: SAGE_ERR_PAGES.
+ * entry that is no page is not followed: SAGE_ERR_INDEX (from sage_kv_compact where pages move).  A pool
+ * without a free page: SAGE_ERR_PAGES.
  * Workspace: sage_pages_workspace_bytes(c), 16-byte aligned.  No call allocates, and all can be captured.
  * What writes a page writes it for every sequence that shares it: sage_kv_append goes behind the
  * shared ones where lengths come from sage_kv_fork and grow from there (a sequence that is cut back into a
